@@ -378,6 +378,93 @@ LF_API lf_status lf_generate_noalloc(const lf_config *cfg, const lf_weights *w, 
                                      int32_t n_prompt, int32_t n_steps, const lf_sampling *sp, uint64_t seed,
                                      int32_t *out_tokens_dev, void *stream);
 
+/* ---- KV cache in 4 bits
+ *
+ * Operators on a cache that holds K and V of one layer as 4-bit floats, for
+ * programs whose context would not fit, or would stream too slowly, in FP16
+ * (4.5 bits per value, 3.6 times less).  They need no handle; their kernels run
+ * on `stream` of the current device, and every buffer belongs to the caller.
+ *
+ * Format: a row of head_dim values is cut into blocks of 16.  A block whose
+ * largest magnitude is A is stored as one scale s = E4M3(A / 6) and 16 codes
+ * E2M1(x / s) (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6), both to nearest with ties
+ * to even; it stands for the values s * code, which are exact in FP16 and BF16.
+ * A is at most 6 * 448 = 2,688 (more saturates); blocks with A < 6 * 2^-10
+ * become zeros (below 6 * 2^-6 the scale's own steps grow coarse).  Infinities
+ * saturate and NaN is stored as 0: what lf_kv4_append writes is always finite. */
+
+#define LF_F16 0
+#define LF_BF16 1
+#define LF_F32 2
+
+typedef struct {
+    int32_t n_kv_heads;      /* 1 .. 1024 */
+    int32_t head_dim;        /* 64 or 128 */
+    int32_t max_seq;         /* capacity in positions */
+    /* device buffers, each 16-byte aligned and position-major per KV head:
+     * codes uint8 [n_kv_heads, max_seq, head_dim / 2], element 2i in the low
+     * nibble of byte i; scales uint8 (E4M3) [n_kv_heads, max_seq, head_dim / 16] */
+    void *k_codes, *k_scales, *v_codes, *v_scales;
+} lf_kv4;
+
+/* A tensor [n][heads][head_dim] in device memory: element (t, h, i) at
+ * data + t * token_stride + h * head_stride + i (strides in elements, >= 0, so
+ * that a slice of a fused projection or a [heads][n][head_dim] tensor needs no
+ * copy).  data must be 16-byte aligned and both strides whole multiples of 16
+ * bytes.  A tensor that is written must not overlap itself. */
+typedef struct {
+    void *data;
+    int32_t dtype;           /* LF_F16, LF_BF16 or LF_F32 */
+    int64_t token_stride, head_stride;
+} lf_rows;
+
+/* Quantise rows k and v [n][n_kv_heads][head_dim] (one dtype) into positions
+ * pos .. pos + n - 1; other positions keep their bytes.  n = 0 does nothing.
+ * Errors: INVALID_ARG (NULL, alignment, negative sizes, differing dtypes),
+ * NOT_SUPPORTED (head_dim, n_kv_heads, dtype), CAPACITY (pos + n > max_seq), CUDA. */
+LF_API lf_status lf_kv4_append(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int32_t n, int32_t pos,
+                               void *stream);
+
+/* The values of positions pos .. pos + n - 1 into k and v
+ * [n][n_kv_heads][head_dim] (one dtype; exact in all three).  Errors as for
+ * lf_kv4_append. */
+LF_API lf_status lf_kv4_read(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int32_t n, int32_t pos,
+                             void *stream);
+
+/* Attention of n query rows at positions pos .. pos + n - 1 over the cache:
+ * query head h of row t reads KV head h / (n_heads / n_kv_heads) and attends to
+ * the positions j with j <= pos + t, j < length and, for window > 0,
+ * j > pos + t - window:
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K[j]) V[j],
+ * a row that sees no position gives zeros.  Positions that no row sees are not
+ * read.  Scores, softmax and sums are FP32; with q in FP16 or BF16 the
+ * probabilities are rounded to FP16 before they meet V, with q in FP32 the
+ * products carry FP32-level operands.  q must be finite. */
+typedef struct {
+    lf_rows q, out;          /* [n][n_heads][head_dim], one dtype; out must not overlap q */
+    int32_t n_heads;         /* a multiple of n_kv_heads */
+    int32_t n;               /* query rows; 0 does nothing */
+    int32_t pos;             /* position of row 0, >= 0 */
+    int32_t length;          /* positions the cache holds, 0 .. max_seq */
+    int32_t window;          /* 0: no window */
+    float scale;             /* 0 selects 1 / sqrt(head_dim) */
+} lf_kv4_query;
+
+/* Scratch bytes that lf_kv4_attend needs for this query on the current device
+ * (0 for many); the tensors' data pointers are not looked at. */
+LF_API lf_status lf_kv4_workspace(const lf_kv4 *c, const lf_kv4_query *q, int64_t *bytes);
+
+/* workspace: device scratch, 16-byte aligned, of at least the bytes that
+ * lf_kv4_workspace names (NULL where it names 0).  It need not be initialised,
+ * and holds nothing between calls; calls that may run at the same time need
+ * one each.  Errors: INVALID_ARG (NULL, alignment, negative sizes, a scale
+ * that is not finite, differing dtypes, out = q, a workspace that is too
+ * small), NOT_SUPPORTED (head_dim, n_kv_heads, dtype, n_heads no multiple of
+ * n_kv_heads, n * n_heads / n_kv_heads above 2^28), CAPACITY (length >
+ * max_seq), CUDA. */
+LF_API lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *workspace, int64_t workspace_bytes,
+                               void *stream);
+
 /* Static string naming a status code. */
 LF_API const char *lf_error_string(lf_status s);
 

@@ -10,6 +10,8 @@ from __future__ import annotations
 import ctypes as C
 import os
 
+from .kv4 import KV4Cache, lf_kv4, lf_kv4_query, lf_rows
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "liblf.so")
 
@@ -25,7 +27,8 @@ TRACE_STAMPS = 9
 # Every symbol include/lf.h declares.
 EXPORTS = ("lf_create", "lf_destroy", "lf_prefill", "lf_decode", "lf_generate", "lf_sync", "lf_reset",
            "lf_set_schedule", "lf_get_info", "lf_error_string", "lf_abi_version", "lf_generate_noalloc",
-           "lf_enable_trace", "lf_read_trace", "lf_sync_latency")
+           "lf_enable_trace", "lf_read_trace", "lf_sync_latency", "lf_kv4_append", "lf_kv4_read", "lf_kv4_workspace",
+           "lf_kv4_attend")
 
 
 class LFError(RuntimeError):
@@ -100,6 +103,12 @@ def lib() -> C.CDLL:
         L.lf_read_trace.restype = C.c_int
         L.lf_sync_latency.argtypes = [C.c_int32, C.c_int32, C.c_int32, C.POINTER(C.c_double)]
         L.lf_sync_latency.restype = C.c_int
+        L.lf_kv4_append.argtypes = [C.POINTER(lf_kv4), C.POINTER(lf_rows), C.POINTER(lf_rows), C.c_int32, C.c_int32, vp]
+        L.lf_kv4_read.argtypes = L.lf_kv4_append.argtypes
+        L.lf_kv4_workspace.argtypes = [C.POINTER(lf_kv4), C.POINTER(lf_kv4_query), C.POINTER(C.c_int64)]
+        L.lf_kv4_attend.argtypes = [C.POINTER(lf_kv4), C.POINTER(lf_kv4_query), vp, C.c_int64, vp]
+        for name in ("lf_kv4_append", "lf_kv4_read", "lf_kv4_workspace", "lf_kv4_attend"):
+            getattr(L, name).restype = C.c_int
         for name in ("lf_create", "lf_prefill", "lf_decode", "lf_generate", "lf_sync", "lf_reset",
                      "lf_set_schedule", "lf_get_info"):
             getattr(L, name).restype = C.c_int

@@ -1,0 +1,638 @@
+// lf_kv4.cu -- a KV cache held in 4 bits: rows quantised as they are written,
+// read back, and attended to without a wider copy.
+//
+// Format.  A row of head_dim values is cut into blocks of 16.  A block with
+// largest magnitude A is stored as the scale s = E4M3(A / 6) and the codes
+// c_i = E2M1(x_i / s), both rounded to nearest, ties to even; its values are
+// s c_i.  s has 4 significant bits and c_i two, so every value has at most 6
+// and lies in 2^-10 .. 2,688: exact in FP16 and BF16.  The products of the
+// attention therefore see the cache's values themselves, and dequantising
+// costs no accuracy.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "../../include/lf.h"
+#include "lf_kv4.h"
+#include "lf_kv4.cuh"
+#include "lf_internal.cuh"
+#include "lf_ptx.cuh"
+
+namespace lfq {
+
+// ---------------------------------------------------------------- append and read
+
+// One thread per block of 16 values.  Non-finite inputs: an infinity counts as
+// the largest finite value (the block then saturates), a NaN as 0, so that the
+// cache holds finite values only and a masked position can never reach a result.
+template <class T>
+__global__ void __launch_bounds__(256) append_rows(Cache c, Rows k, Rows v, int n, int pos)
+{
+    const int bpr = c.hd / 16;
+    const Rows &in = blockIdx.y ? v : k;
+    uint8_t *codes = blockIdx.y ? c.vc : c.kc, *scales = blockIdx.y ? c.vs : c.ks;
+    const long long total = (long long)n * c.Hkv * bpr;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const int b = (int)(i % bpr);
+    const long long r = i / bpr;
+    const int h = (int)(r % c.Hkv);
+    const long long t = r / c.Hkv;
+    float x[16];
+    load16<T>(static_cast<const T *>(in.p) + t * in.ts + h * in.hs + b * 16, x);
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        x[j] = x[j] != x[j] ? 0.f : fminf(fmaxf(x[j], -3.402823466e38f), 3.402823466e38f);
+        amax = fmaxf(amax, fabsf(x[j]));
+    }
+    const unsigned s8 = __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f), __NV_SATFINITE, __NV_E4M3);
+    const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3)));
+    unsigned w[2] = {0u, 0u};
+    if (s > 0.f) {   // a block below E4M3's range (A < 6 * 2^-10) is stored as zeros
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j / 4] |= e2m1x2(__fdiv_rn(x[2 * j], s), __fdiv_rn(x[2 * j + 1], s)) << (8 * (j % 4));
+    }
+    const size_t row = (size_t)h * c.cap + (size_t)pos + (size_t)t;
+    *reinterpret_cast<uint2 *>(codes + row * code_bytes(c.hd) + b * 8) = make_uint2(w[0], w[1]);
+    scales[row * scale_bytes(c.hd) + b] = (uint8_t)s8;
+}
+
+template <class T>
+__global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n, int pos)
+{
+    const int bpr = c.hd / 16;
+    const Rows &out = blockIdx.y ? v : k;
+    const uint8_t *codes = blockIdx.y ? c.vc : c.kc, *scales = blockIdx.y ? c.vs : c.ks;
+    const long long total = (long long)n * c.Hkv * bpr;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const int b = (int)(i % bpr);
+    const long long r = i / bpr;
+    const int h = (int)(r % c.Hkv);
+    const long long t = r / c.Hkv;
+    const size_t row = (size_t)h * c.cap + (size_t)pos + (size_t)t;
+    const uint2 w = *reinterpret_cast<const uint2 *>(codes + row * code_bytes(c.hd) + b * 8);
+    const unsigned s2 = e4m3_h2_same(scales[row * scale_bytes(c.hd) + b]);
+    unsigned hv[8];
+    e2m1x8_h2(w.x, hv[0], hv[1], hv[2], hv[3]);
+    e2m1x8_h2(w.y, hv[4], hv[5], hv[6], hv[7]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) hv[j] = hmul2(hv[j], s2);
+    store16<T>(static_cast<T *>(out.p) + t * out.ts + h * out.hs + b * 16, hv);
+}
+
+// ---------------------------------------------------------------- attention, few rows
+
+// A tile of 8 NT query rows of one KV head against the positions of one split.
+//
+// The contraction runs on warp-level tensor-core products (m16n8k16, FP16
+// operands, FP32 sums) whose operands come straight from the cache's bytes in
+// global memory, with no pass through shared memory: the order of the
+// contracted index is free, so each lane takes the bytes that lie together.
+//   S^T = K Q^T   A = 16 positions x 16 dims of K.  Lane (g, t) holds dims
+//                 [HD/4 t, HD/4 (t+1)) of two positions: one wide load each;
+//                 k-step s uses 4 of them.
+//   O^T = V^T P^T A = 16 dims x 16 positions of V.  Lane (g, t) holds dims
+//                 [HD/8 g, HD/8 (g+1)) of the positions 4t .. 4t + 3; the codes of
+//                 two positions are woven nibble by nibble, so that one
+//                 conversion yields the pair of positions the product wants.
+// The position of row i of a 16-position slab is 4 (i / 2) + i % 2 for i < 8
+// and 2 more for i + 8, the same in both products, so that the scores become
+// the second product's operand by one 8x8 transpose in registers.
+//
+// The softmax is online: per chunk of 16 SL positions the running reference m
+// (the largest score less P_EXP, so that the largest P is 2^P_EXP) and sum l of
+// a row in FP32, exponentials to base 2.  P is rounded to FP16: relative error
+// 2^-11, below that of a half-precision output, down to 2^-(14 + P_EXP) of the
+// row's largest, where FP16 runs out of exponents.  With FP32 queries (SPLIT) q
+// and P are split into an FP16 head and remainder and the products are formed
+// twice, which leaves errors near 2^-22.
+template <int HD, int NT, bool SPLIT>
+struct RowCfg {
+    static constexpr int NW = 8;                       // warps
+    static constexpr int RT = 8 * NT;                  // query rows
+    static constexpr int KS = HD / 16;                 // k-steps of S, m-tiles of O
+    static constexpr int QW = SPLIT ? 4 : 2;           // words per q fragment
+    static constexpr int SMEM = NT * KS * 32 * QW * 4 + (2 * NW + 1) * RT * 4 + NW * RT * HD * 4;
+};
+constexpr float P_EXP = 15.f;
+constexpr int SL = 2;                                  // 16-position slabs per softmax step
+constexpr int CH = 16 * SL;
+
+template <int HD, int NT, bool SPLIT>
+__global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
+{
+    using C = RowCfg<HD, NT, SPLIT>;
+    constexpr int NW = C::NW, RT = C::RT, KS = C::KS;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    unsigned *qf = reinterpret_cast<unsigned *>(smem_raw);              // [NT][KS][32][QW]
+    float *rs = reinterpret_cast<float *>(qf + NT * KS * 32 * C::QW);   // [RT] score factor of a row
+    float *wm = rs + RT, *wl = wm + NW * RT;                            // [NW][RT]
+    float *wo = wl + NW * RT;                                           // [NW][RT][HD]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int kvh = blockIdx.y, split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
+    const int r0 = tile * RT, rows = min(RT, a.n * a.G - r0);
+
+    // ---- q: row r as an FP16 B operand, scaled by a power of two for BF16 and FP32 (their
+    // range is wider than FP16's), which the row's score factor takes back
+    for (int r = warp; r < RT; r += NW) {
+        float x[HD / 32];
+        const int tt = (r0 + r) / a.G, hh = kvh * a.G + (r0 + r) % a.G;
+        const bool live = r < rows;
+        load_q<HD>(a.q, live, tt, hh, lane, x);
+        float f = 1.f;
+        if (a.q.dtype != F16) f = range_factor(warp_amax<HD / 32>(x));
+        if (lane == 0) rs[r] = a.scale * 1.4426950408889634f / f;
+        // dims HD/32 lane ..: element d of the row belongs to lane t = d / (HD/4), k-step (d % (HD/4)) / 4
+#pragma unroll
+        for (int j = 0; j < HD / 32; j += 2) {
+            const int d = lane * (HD / 32) + j, qt = d / (HD / 4), k = d % (HD / 4) / 4, w = d % 4 / 2;
+            unsigned *dst = qf + (((r / 8) * KS + k) * 32 + (r % 8) * 4 + qt) * C::QW;
+            __half h0, m0, h1, m1;
+            lfk::split_h(x[j] * f, h0, m0);
+            lfk::split_h(x[j + 1] * f, h1, m1);
+            dst[w] = lfk::pack_h2(h0, h1);
+            if (SPLIT) dst[2 + w] = lfk::pack_h2(m0, m1);
+        }
+    }
+    __syncthreads();
+
+    // ---- this lane's rows 2t, 2t+1 of each n-tile: visible keys and score factors
+    int khi[NT][2], klo[NT][2];
+    float f[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * i + 2 * t + e, tt = (r0 + min(r, rows - 1)) / a.G;
+            khi[i][e] = key_hi(a.pos, tt, a.len);
+            klo[i][e] = key_lo(a.pos, tt, a.win);
+            f[i][e] = rs[r];
+        }
+    // positions of this CTA: the split's, cut to what the tile's rows see
+    const int t_first = r0 / a.G, t_last = (r0 + rows - 1) / a.G;
+    const int lo_t = key_lo(a.pos, t_first, a.win), hi_t = key_hi(a.pos, t_last, a.len);
+    const int p0 = max(a.lo + split * a.per, lo_t / CH * CH), p1 = min(a.lo + (split + 1) * a.per, hi_t);
+    // inside [all_lo, all_hi) every row sees every position
+    const int all_lo = key_lo(a.pos, t_last, a.win), all_hi = key_hi(a.pos, t_first, a.len);
+
+    float m[NT][2], l[NT][2], o[NT][KS][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        m[i][0] = m[i][1] = -INFINITY;
+        l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) o[i][k][0] = o[i][k][1] = o[i][k][2] = o[i][k][3] = 0.f;
+    }
+    const size_t row0 = (size_t)kvh * a.c.cap;
+    const uint8_t *kc = a.c.kc + row0 * code_bytes(HD) + t * (HD / 8);
+    const uint8_t *ks = a.c.ks + row0 * scale_bytes(HD) + t * (HD / 64);
+    const uint8_t *vc = a.c.vc + row0 * code_bytes(HD) + g * (HD / 16);
+    const uint8_t *vs = a.c.vs + row0 * scale_bytes(HD) + g * (HD / 16) / 8;
+    const int sg = 4 * (g >> 1) + (g & 1);                 // slab position of rows g (and + 2: of g + 8)
+
+    for (int p = p0 + warp * CH; p < p1; p += NW * CH) {
+        KRaw<HD> kr[SL][2];
+        VRaw<HD> vr[SL][4];
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const size_t r = (size_t)max(min(p + 16 * s + sg + 2 * e, p1 - 1), lo_t);   // outside: a seen row, masked below
+                kr[s][e].load(kc + r * code_bytes(HD), ks + r * scale_bytes(HD));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const size_t r = (size_t)max(min(p + 16 * s + 4 * t + e, p1 - 1), lo_t);
+                vr[s][e].load(vc + r * code_bytes(HD), vs + r * scale_bytes(HD));
+            }
+        }
+        // ---- scores
+        float st[SL][NT][4];
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) st[s][i][0] = st[s][i][1] = st[s][i][2] = st[s][i][3] = 0.f;
+            unsigned ka[KS][2], kb[KS][2];
+            kr[s][0].values(ka);
+            kr[s][1].values(kb);
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const unsigned *q = qf + ((i * KS + k) * 32 + lane) * C::QW;
+                    if (SPLIT) {
+                        const uint4 b = *reinterpret_cast<const uint4 *>(q);
+                        lfk::mma16816(st[s][i], ka[k][0], kb[k][0], ka[k][1], kb[k][1], b.x, b.y);
+                        lfk::mma16816(st[s][i], ka[k][0], kb[k][0], ka[k][1], kb[k][1], b.z, b.w);
+                    } else {
+                        const uint2 b = *reinterpret_cast<const uint2 *>(q);
+                        lfk::mma16816(st[s][i], ka[k][0], kb[k][0], ka[k][1], kb[k][1], b.x, b.y);
+                    }
+                }
+        }
+        // ---- scale, mask, running maximum
+        const bool whole = p >= all_lo && p + CH <= min(all_hi, p1);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int s = 0; s < SL; ++s)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float &x = st[s][i][2 * u + e];
+                        x *= f[i][e];
+                        const int key = p + 16 * s + sg + 2 * u;
+                        if (!whole && !(key >= klo[i][e] && key < min(khi[i][e], p1))) x = -INFINITY;
+                        mx = fmaxf(mx, x);
+                    }
+#pragma unroll
+                for (int sh = 4; sh <= 16; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                const float mn = fmaxf(m[i][e], mx - P_EXP), ref = mn == -INFINITY ? 0.f : mn;
+                const float alpha = ex2(m[i][e] - ref);    // 0 while nothing was seen
+                m[i][e] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int s = 0; s < SL; ++s)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float &x = st[s][i][2 * u + e];
+                        x = ex2(x - ref);
+                        sum += x;
+                    }
+                l[i][e] = fmaf(l[i][e], alpha, sum);
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    o[i][k][e] *= alpha;
+                    o[i][k][2 + e] *= alpha;
+                }
+            }
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+            unsigned pb[NT][2], pr[NT][2];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    __half h0, m0, h1, m1;
+                    lfk::split_h(st[s][i][2 * u], h0, m0);
+                    lfk::split_h(st[s][i][2 * u + 1], h1, m1);
+                    pb[i][u] = lfk::movm_t(lfk::pack_h2(h0, h1));
+                    if (SPLIT) pr[i][u] = lfk::movm_t(lfk::pack_h2(m0, m1));
+                }
+            unsigned va[KS][2], vb[KS][2];                 // positions 4t, 4t+1 and 4t+2, 4t+3
+            weave<HD>(vr[s][0], vr[s][1], va);
+            weave<HD>(vr[s][2], vr[s][3], vb);
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    lfk::mma16816(o[i][k], va[k][0], va[k][1], vb[k][0], vb[k][1], pb[i][0], pb[i][1]);
+                    if (SPLIT) lfk::mma16816(o[i][k], va[k][0], va[k][1], vb[k][0], vb[k][1], pr[i][0], pr[i][1]);
+                }
+        }
+    }
+
+    // ---- the warps' states, joined: O = sum 2^(m_w - M) O_w over l likewise
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * i + 2 * t + e;
+            float s = l[i][e];
+#pragma unroll
+            for (int sh = 4; sh <= 16; sh <<= 1) s += __shfl_xor_sync(0xffffffffu, s, sh);
+            if (g == 0) {
+                wm[warp * RT + r] = m[i][e];
+                wl[warp * RT + r] = s;
+            }
+            float *dst = wo + ((size_t)warp * RT + r) * HD + g * (HD / 8);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                dst[2 * k] = o[i][k][e];
+                dst[2 * k + 1] = o[i][k][2 + e];
+            }
+        }
+    __syncthreads();
+    float *part = a.part ? a.part + ((size_t)(kvh * a.tiles + tile) * a.splits + split) * RT * (HD + 2) : nullptr;
+    for (int i = threadIdx.x; i < rows * (HD / 4); i += NW * 32) {
+        const int r = i / (HD / 4), d = i % (HD / 4) * 4;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * RT + r]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float x = ex2(wm[w * RT + r] - ref);
+            const float4 v = *reinterpret_cast<const float4 *>(wo + ((size_t)w * RT + r) * HD + d);
+            L = fmaf(wl[w * RT + r], x, L);
+            acc.x = fmaf(v.x, x, acc.x);
+            acc.y = fmaf(v.y, x, acc.y);
+            acc.z = fmaf(v.z, x, acc.z);
+            acc.w = fmaf(v.w, x, acc.w);
+        }
+        if (part) {
+            *reinterpret_cast<float2 *>(part + (size_t)r * (HD + 2) + d) = make_float2(acc.x, acc.y);
+            *reinterpret_cast<float2 *>(part + (size_t)r * (HD + 2) + d + 2) = make_float2(acc.z, acc.w);
+            if (d == 0) *reinterpret_cast<float2 *>(part + (size_t)r * (HD + 2) + HD) = make_float2(M, L);
+        } else {
+            const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);   // a row that saw nothing is 0; NaN stays
+            const int tt = (r0 + r) / a.G, hh = kvh * a.G + (r0 + r) % a.G;
+            store4(a.o, (size_t)tt * a.o.ts + (size_t)hh * a.o.hs + d, acc.x * inv, acc.y * inv, acc.z * inv,
+                   acc.w * inv);
+        }
+    }
+}
+
+// Joins the splits of a row: one block of HD / 4 threads per query row and KV head.
+__global__ void __launch_bounds__(32) attn_join(const __grid_constant__ Attn a)
+{
+    const int hd = a.c.hd, row = blockIdx.x, kvh = blockIdx.y, d = threadIdx.x * 4;
+    const float *part = a.part + ((size_t)(kvh * a.tiles + row / a.rt) * a.splits * a.rt + row % a.rt) * (hd + 2);
+    const size_t step = (size_t)a.rt * (hd + 2);
+    float M = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, part[s * step + hd]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < a.splits; ++s) {
+        const float2 ml = *reinterpret_cast<const float2 *>(part + s * step + hd);
+        const float2 u = *reinterpret_cast<const float2 *>(part + s * step + d);
+        const float2 v = *reinterpret_cast<const float2 *>(part + s * step + d + 2);
+        const float x = ex2(ml.x - ref);
+        L = fmaf(ml.y, x, L);
+        acc.x = fmaf(u.x, x, acc.x);
+        acc.y = fmaf(u.y, x, acc.y);
+        acc.z = fmaf(v.x, x, acc.z);
+        acc.w = fmaf(v.y, x, acc.w);
+    }
+    const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);
+    const int tt = row / a.G, hh = kvh * a.G + row % a.G;
+    store4(a.o, (size_t)tt * a.o.ts + (size_t)hh * a.o.hs + d, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+}
+
+// ---------------------------------------------------------------- launches
+
+size_t plan_attn(Attn &a, int sms)
+{
+    const int rows = a.n * a.G;
+    a.rt = rows <= 8 ? 8 : 16;
+    a.tiles = (rows + a.rt - 1) / a.rt;
+    a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
+    const int hi = key_hi(a.pos, a.n - 1, a.len);
+    const int chunks = std::max(1, (hi - a.lo + CH - 1) / CH);
+    // one CTA per SM, each warp at least one chunk
+    const long long ctas = (long long)a.tiles * a.c.Hkv;
+    int splits = (int)std::max<long long>(1, sms / ctas);
+    splits = std::min(splits, (chunks + 7) / 8);
+    const int per = (chunks + splits - 1) / splits;
+    a.splits = (chunks + per - 1) / per;
+    a.per = per * CH;
+    return a.splits > 1 ? (size_t)a.c.Hkv * a.tiles * a.splits * a.rt * (a.c.hd + 2) : 0;
+}
+
+template <template <class> class F, class... A>
+static cudaError_t by_dtype(int dtype, A... args)
+{
+    switch (dtype) {
+    case F16: return F<__half>::run(args...);
+    case BF16: return F<__nv_bfloat16>::run(args...);
+    default: return F<float>::run(args...);
+    }
+}
+
+static dim3 block_grid(const Cache &c, int n)
+{
+    return dim3((unsigned)(((long long)n * c.Hkv * (c.hd / 16) + 255) / 256), 2);
+}
+template <class T>
+struct RunAppend {
+    static cudaError_t run(Cache c, Rows k, Rows v, int n, int pos, cudaStream_t s)
+    {
+        append_rows<T><<<block_grid(c, n), 256, 0, s>>>(c, k, v, n, pos);
+        return cudaGetLastError();
+    }
+};
+template <class T>
+struct RunRead {
+    static cudaError_t run(Cache c, Rows k, Rows v, int n, int pos, cudaStream_t s)
+    {
+        read_rows<T><<<block_grid(c, n), 256, 0, s>>>(c, k, v, n, pos);
+        return cudaGetLastError();
+    }
+};
+cudaError_t launch_append(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s)
+{
+    return by_dtype<RunAppend>(k.dtype, c, k, v, n, pos, s);
+}
+cudaError_t launch_read(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s)
+{
+    return by_dtype<RunRead>(k.dtype, c, k, v, n, pos, s);
+}
+
+template <int HD, int NT, bool SPLIT>
+static cudaError_t run_rows(const Attn &a, cudaStream_t s)
+{
+    constexpr int smem = RowCfg<HD, NT, SPLIT>::SMEM;
+    static bool ready[64] = {};   // the attribute is per device; setting it again is harmless
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !ready[dev]) {
+        e = cudaFuncSetAttribute(attn_rows<HD, NT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready[dev] = true;
+    }
+    attn_rows<HD, NT, SPLIT><<<dim3((unsigned)(a.tiles * a.splits), (unsigned)a.c.Hkv), 256, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn(const Attn &a, cudaStream_t s)
+{
+    const bool split = a.q.dtype == F32;
+    cudaError_t e;
+    if (a.c.hd == 128)
+        e = a.rt == 8 ? (split ? run_rows<128, 1, true>(a, s) : run_rows<128, 1, false>(a, s))
+                      : (split ? run_rows<128, 2, true>(a, s) : run_rows<128, 2, false>(a, s));
+    else
+        e = a.rt == 8 ? (split ? run_rows<64, 1, true>(a, s) : run_rows<64, 1, false>(a, s))
+                      : (split ? run_rows<64, 2, true>(a, s) : run_rows<64, 2, false>(a, s));
+    if (e == cudaSuccess && a.splits > 1) {
+        attn_join<<<dim3((unsigned)(a.n * a.G), (unsigned)a.c.Hkv), a.c.hd / 4, 0, s>>>(a);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace lfq
+
+// ---------------------------------------------------------------- C entry points
+
+namespace {
+
+using namespace lfq;
+
+constexpr int kMaxKvHeads = 1024;
+
+lf_status status_of(cudaError_t e)
+{
+    if (e == cudaSuccess) return LF_OK;
+    (void)cudaGetLastError();
+    return e == cudaErrorMemoryAllocation ? LF_ERR_OUT_OF_MEMORY : LF_ERR_CUDA;
+}
+
+bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+lf_status check_cache(const lf_kv4 *c)
+{
+    if (!c || c->n_kv_heads < 1 || c->max_seq < 1) return LF_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return LF_ERR_NOT_SUPPORTED;
+    if (c->n_kv_heads > kMaxKvHeads) return LF_ERR_NOT_SUPPORTED;
+    if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
+        return LF_ERR_INVALID_ARG;
+    return LF_OK;
+}
+
+// Rows [n][heads][hd]: type, alignment, strides; `written`: no two may overlap.
+lf_status check_rows(const lf_rows *r, int n, int heads, int hd, bool written)
+{
+    if (!r) return LF_ERR_INVALID_ARG;
+    if (r->dtype != LF_F16 && r->dtype != LF_BF16 && r->dtype != LF_F32) return LF_ERR_NOT_SUPPORTED;
+    const long long per16 = r->dtype == LF_F32 ? 4 : 8;   // elements in 16 bytes
+    if (!aligned16(r->data) || r->token_stride < 0 || r->head_stride < 0 || r->token_stride % per16 ||
+        r->head_stride % per16)
+        return LF_ERR_INVALID_ARG;
+    const long long most = 1ll << 40;   // elements: keeps every offset far inside 64 bits
+    if (r->token_stride > most || r->head_stride > most) return LF_ERR_INVALID_ARG;
+    if (written) {
+        const long long ts = r->token_stride, hs = r->head_stride;
+        const bool t_ok = n == 1 || ts >= hd, h_ok = heads == 1 || hs >= hd;
+        const bool apart = n == 1 || heads == 1 || ts >= (heads - 1ll) * hs + hd || hs >= (n - 1ll) * ts + hd;
+        if (!t_ok || !h_ok || !apart) return LF_ERR_INVALID_ARG;
+    }
+    return LF_OK;
+}
+
+Cache cache_of(const lf_kv4 *c)
+{
+    return {static_cast<uint8_t *>(c->k_codes), static_cast<uint8_t *>(c->k_scales), static_cast<uint8_t *>(c->v_codes),
+            static_cast<uint8_t *>(c->v_scales), c->n_kv_heads, c->head_dim, c->max_seq};
+}
+Rows rows_of(const lf_rows *r) { return {r->data, r->dtype, r->token_stride, r->head_stride}; }
+
+lf_status check_copy(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int n, int pos, bool written)
+{
+    lf_status st = check_cache(c);
+    if (st != LF_OK) return st;
+    if (n < 0 || pos < 0) return LF_ERR_INVALID_ARG;
+    if ((long long)pos + n > c->max_seq) return LF_ERR_CAPACITY;
+    if (n == 0) return LF_OK;
+    st = check_rows(k, n, c->n_kv_heads, c->head_dim, written);
+    if (st == LF_OK) st = check_rows(v, n, c->n_kv_heads, c->head_dim, written);
+    if (st == LF_OK && k->dtype != v->dtype) st = LF_ERR_INVALID_ARG;
+    return st;
+}
+
+// Device properties that the plan needs, read once per device.
+lf_status sm_count(int *out)
+{
+    static int cached[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return status_of(e);
+    if (dev < 64 && cached[dev]) {
+        *out = cached[dev];
+        return LF_OK;
+    }
+    e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return status_of(e);
+    if (dev < 64) cached[dev] = *out;
+    return LF_OK;
+}
+
+lf_status make_attn(const lf_kv4 *c, const lf_kv4_query *q, Attn *a, size_t *floats)
+{
+    lf_status st = check_cache(c);
+    if (st != LF_OK) return st;
+    if (!q || q->n < 0 || q->n_heads < 1 || q->pos < 0 || q->length < 0 || q->window < 0 || !std::isfinite(q->scale))
+        return LF_ERR_INVALID_ARG;
+    if (q->length > c->max_seq) return LF_ERR_CAPACITY;
+    if (q->n_heads % c->n_kv_heads) return LF_ERR_NOT_SUPPORTED;
+    const int G = q->n_heads / c->n_kv_heads;
+    // rows per KV head and positions stay in 31 bits with room to spare
+    if ((long long)q->n * G > (1ll << 28) || (long long)q->pos + q->n > INT_MAX - 1024) return LF_ERR_NOT_SUPPORTED;
+    a->c = cache_of(c);
+    a->Hq = q->n_heads;
+    a->G = G;
+    a->n = q->n;
+    a->pos = q->pos;
+    a->len = q->length;
+    a->win = q->window;
+    a->scale = q->scale != 0.f ? q->scale : 1.0f / std::sqrt((float)c->head_dim);
+    a->part = nullptr;
+    *floats = 0;
+    if (q->n == 0) return LF_OK;
+    int sms = 0;
+    st = sm_count(&sms);
+    if (st == LF_OK) *floats = plan_attn(*a, sms);
+    return st;
+}
+
+}  // namespace
+
+extern "C" {
+
+lf_status lf_kv4_append(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int32_t n, int32_t pos, void *stream)
+{
+    const lf_status st = check_copy(c, k, v, n, pos, false);
+    if (st != LF_OK || n == 0) return st;
+    return status_of(launch_append(cache_of(c), rows_of(k), rows_of(v), n, pos, static_cast<cudaStream_t>(stream)));
+}
+
+lf_status lf_kv4_read(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int32_t n, int32_t pos, void *stream)
+{
+    const lf_status st = check_copy(c, k, v, n, pos, true);
+    if (st != LF_OK || n == 0) return st;
+    return status_of(launch_read(cache_of(c), rows_of(k), rows_of(v), n, pos, static_cast<cudaStream_t>(stream)));
+}
+
+lf_status lf_kv4_workspace(const lf_kv4 *c, const lf_kv4_query *q, int64_t *bytes)
+{
+    if (!bytes) return LF_ERR_INVALID_ARG;
+    Attn a;
+    size_t floats = 0;
+    const lf_status st = make_attn(c, q, &a, &floats);
+    if (st == LF_OK) *bytes = (int64_t)(floats * sizeof(float));
+    return st;
+}
+
+lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    Attn a;
+    size_t floats = 0;
+    lf_status st = make_attn(c, q, &a, &floats);
+    if (st != LF_OK || a.n == 0) return st;
+    st = check_rows(&q->q, a.n, a.Hq, c->head_dim, false);
+    if (st == LF_OK) st = check_rows(&q->out, a.n, a.Hq, c->head_dim, true);
+    if (st != LF_OK) return st;
+    if (q->q.dtype != q->out.dtype || q->q.data == q->out.data) return LF_ERR_INVALID_ARG;
+    if (floats && (!aligned16(workspace) || workspace_bytes < (int64_t)(floats * sizeof(float)))) return LF_ERR_INVALID_ARG;
+    a.q = rows_of(&q->q);
+    a.o = rows_of(&q->out);
+    a.part = floats ? static_cast<float *>(workspace) : nullptr;
+    return status_of(launch_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

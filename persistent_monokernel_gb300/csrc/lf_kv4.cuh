@@ -1,0 +1,287 @@
+// lf_kv4.cuh -- device pieces of the 4-bit KV cache: conversions between the
+// format's bytes and FP16 pairs, and row loads and stores by element type.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "lf_kv4.h"
+#include "lf_internal.cuh"
+#include "lf_ptx.cuh"
+
+namespace lfq {
+
+// Four bytes of two E2M1 codes each -> FP16 pairs (low nibble first), exact.
+__device__ __forceinline__ void e2m1x8_h2(unsigned w, unsigned &h0, unsigned &h1, unsigned &h2, unsigned &h3)
+{
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h0), "=r"(h1), "=r"(h2), "=r"(h3)
+        : "r"(w));
+}
+// Two FP32 values -> one byte of E2M1 codes (`lo` in the low nibble), to nearest even, saturating at 6.
+__device__ __forceinline__ unsigned e2m1x2(float lo, float hi)
+{
+    unsigned short d;
+    asm("{\n\t.reg .b8 b;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
+        "mov.b16 %0, {b, 0};\n\t}"
+        : "=h"(d)
+        : "f"(hi), "f"(lo));
+    return d;
+}
+// Two E4M3 bytes (low one first) -> an FP16 pair, exact.
+__device__ __forceinline__ unsigned e4m3x2_h2(unsigned b)
+{
+    unsigned d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((unsigned short)b));
+    return d;
+}
+// One E4M3 byte in both halves of a pair.
+__device__ __forceinline__ unsigned e4m3_h2_same(unsigned b) { return e4m3x2_h2(b | (b << 8)); }
+__device__ __forceinline__ unsigned hmul2(unsigned a, unsigned b)
+{
+    unsigned d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// 2^x on the special-function unit (about 2 ulp; exact 0 for -inf).
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---- rows by element type: 16 consecutive values (16-byte aligned)
+template <class T>
+__device__ __forceinline__ void load16(const T *p, float (&x)[16]);
+template <>
+__device__ __forceinline__ void load16<float>(const float *p, float (&x)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p) + j);
+        x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
+    }
+}
+template <>
+__device__ __forceinline__ void load16<__half>(const __half *p, float (&x)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + j);
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[u]));
+            x[8 * j + 2 * u] = f.x, x[8 * j + 2 * u + 1] = f.y;
+        }
+    }
+}
+template <>
+__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + j);
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            x[8 * j + 2 * u] = __uint_as_float(w[u] << 16);
+            x[8 * j + 2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
+        }
+    }
+}
+// 16 cached values as FP16 pairs -> T (exact: at most 6 significant bits)
+template <class T>
+__device__ __forceinline__ void store16(T *p, const unsigned (&h)[8]);
+template <>
+__device__ __forceinline__ void store16<__half>(__half *p, const unsigned (&h)[8])
+{
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+}
+__device__ __forceinline__ float2 h2_f2(unsigned h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
+__device__ __forceinline__ unsigned pack_bf2(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const unsigned *>(&b);
+}
+template <>
+__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16 *p, const unsigned (&h)[8])
+{
+    unsigned w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 f = h2_f2(h[j]);
+        w[j] = pack_bf2(f.x, f.y);
+    }
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+template <>
+__device__ __forceinline__ void store16<float>(float *p, const unsigned (&h)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 a = h2_f2(h[2 * j]), b = h2_f2(h[2 * j + 1]);
+        reinterpret_cast<float4 *>(p)[j] = make_float4(a.x, a.y, b.x, b.y);
+    }
+}
+// Four values at element offset `at` of o (rounded once, to nearest even).
+__device__ __forceinline__ void store4(const Rows &o, size_t at, float a, float b, float c, float d)
+{
+    if (o.dtype == F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(o.p) + at) = make_float4(a, b, c, d);
+    } else {
+        unsigned x, y;
+        if (o.dtype == F16) {
+            const __half2 u = __floats2half2_rn(a, b), v = __floats2half2_rn(c, d);
+            x = *reinterpret_cast<const unsigned *>(&u);
+            y = *reinterpret_cast<const unsigned *>(&v);
+        } else {
+            x = pack_bf2(a, b);
+            y = pack_bf2(c, d);
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o.p) + at) = make_uint2(x, y);
+    }
+}
+// One row of q, HD / 32 consecutive values per lane (zeros for a row that is not there).
+template <int HD>
+__device__ __forceinline__ void load_q(const Rows &q, bool live, int tok, int head, int lane, float (&x)[HD / 32])
+{
+    const size_t at = (size_t)tok * q.ts + (size_t)head * q.hs + lane * (HD / 32);
+#pragma unroll
+    for (int j = 0; j < HD / 32; j += 2) {
+        float2 v = make_float2(0.f, 0.f);
+        if (live) {
+            if (q.dtype == F32) {
+                v = *reinterpret_cast<const float2 *>(static_cast<const float *>(q.p) + at + j);
+            } else {
+                const unsigned w = *reinterpret_cast<const unsigned *>(static_cast<const uint16_t *>(q.p) + at + j);
+                v = q.dtype == F16 ? h2_f2(w) : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            }
+        }
+        x[j] = v.x;
+        x[j + 1] = v.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ float warp_amax(const float (&x)[N])
+{
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = fmaxf(m, fabsf(x[j]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+// A power of two that brings values of largest magnitude m into [1, 2) (into [1, 4)
+// at the top of FP32's range; 1 for zero, subnormal or non-finite m): exact to
+// multiply with and, as the inverse is a power of two, to divide by.
+__device__ __forceinline__ float range_factor(float m)
+{
+    const unsigned e = __float_as_uint(m) >> 23;
+    if (e == 0u || e == 255u) return 1.f;
+    return __uint_as_float((254u - min(e, 253u)) << 23);
+}
+
+// ---- one lane's share of a K row: HD / 4 dims, as KS k-steps of 4 (two pairs each)
+template <int HD>
+struct KRaw;
+template <>
+struct KRaw<128> {
+    uint4 c;
+    unsigned s;
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales)
+    {
+        c = __ldg(reinterpret_cast<const uint4 *>(codes));
+        s = __ldg(reinterpret_cast<const unsigned short *>(scales));
+    }
+    __device__ __forceinline__ void values(unsigned (&v)[8][2]) const
+    {
+        const unsigned w[4] = {c.x, c.y, c.z, c.w};
+        const unsigned s0 = e4m3_h2_same(s & 255u), s1 = e4m3_h2_same(s >> 8);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            e2m1x8_h2(w[j], v[2 * j][0], v[2 * j][1], v[2 * j + 1][0], v[2 * j + 1][1]);
+            const unsigned sc = j < 2 ? s0 : s1;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                v[2 * j + u][0] = hmul2(v[2 * j + u][0], sc);
+                v[2 * j + u][1] = hmul2(v[2 * j + u][1], sc);
+            }
+        }
+    }
+};
+template <>
+struct KRaw<64> {
+    uint2 c;
+    unsigned s;
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales)
+    {
+        c = __ldg(reinterpret_cast<const uint2 *>(codes));
+        s = __ldg(scales);
+    }
+    __device__ __forceinline__ void values(unsigned (&v)[4][2]) const
+    {
+        const unsigned s0 = e4m3_h2_same(s);
+        e2m1x8_h2(c.x, v[0][0], v[0][1], v[1][0], v[1][1]);
+        e2m1x8_h2(c.y, v[2][0], v[2][1], v[3][0], v[3][1]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            v[u][0] = hmul2(v[u][0], s0);
+            v[u][1] = hmul2(v[u][1], s0);
+        }
+    }
+};
+// ---- one lane's share of a V row: HD / 8 dims of one block
+template <int HD>
+struct VRaw;
+template <>
+struct VRaw<128> {
+    uint2 c;
+    unsigned s;
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales)
+    {
+        c = __ldg(reinterpret_cast<const uint2 *>(codes));
+        s = __ldg(scales);
+    }
+    __device__ __forceinline__ unsigned word(int j) const { return j ? c.y : c.x; }
+};
+template <>
+struct VRaw<64> {
+    unsigned c;
+    unsigned s;
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales)
+    {
+        c = __ldg(reinterpret_cast<const unsigned *>(codes));
+        s = __ldg(scales);
+    }
+    __device__ __forceinline__ unsigned word(int) const { return c; }
+};
+// Rows a and b of V woven: v[k][e] = the FP16 pair (a[dim 2k + e], b[dim 2k + e]).
+template <int HD>
+__device__ __forceinline__ void weave(const VRaw<HD> &a, const VRaw<HD> &b, unsigned (&v)[HD / 16][2])
+{
+    const unsigned sc = e4m3x2_h2(a.s | (b.s << 8));
+#pragma unroll
+    for (int j = 0; j < HD / 64; ++j) {
+        const unsigned x = a.word(j), y = b.word(j), m = 0x0f0f0f0fu;
+        const unsigned even = (x & m) | ((y << 4) & ~m), odd = ((x >> 4) & m) | (y & ~m);
+        e2m1x8_h2(even, v[4 * j][0], v[4 * j + 1][0], v[4 * j + 2][0], v[4 * j + 3][0]);
+        e2m1x8_h2(odd, v[4 * j][1], v[4 * j + 1][1], v[4 * j + 2][1], v[4 * j + 3][1]);
+    }
+#pragma unroll
+    for (int k = 0; k < HD / 16; ++k) {
+        v[k][0] = hmul2(v[k][0], sc);
+        v[k][1] = hmul2(v[k][1], sc);
+    }
+}
+
+}  // namespace lfq

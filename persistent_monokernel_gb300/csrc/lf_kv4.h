@@ -1,0 +1,55 @@
+// lf_kv4.h -- internal interface of the 4-bit KV cache operators (lf_kv4.cu):
+// launches used by the C entry points and by the decoder's own 4-bit path.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace lfq {
+
+enum DType { F16 = 0, BF16 = 1, F32 = 2 };
+
+// Bytes of one row of head_dim values: codes (two per byte) and scales (one per 16).
+__host__ __device__ constexpr int code_bytes(int hd) { return hd / 2; }
+__host__ __device__ constexpr int scale_bytes(int hd) { return hd / 16; }
+
+// Cache of one layer: [Hkv][cap] rows of codes and of scales, for K and V.
+struct Cache {
+    uint8_t *kc, *ks, *vc, *vs;
+    int Hkv, hd, cap;
+};
+
+// [n][heads][hd] values at element strides ts (token) and hs (head).
+struct Rows {
+    void *p;
+    int dtype;
+    long long ts, hs;
+};
+
+struct Attn {
+    Cache c;
+    Rows q, o;
+    int Hq, G;              // query heads; per KV head
+    int n, pos;             // query rows at positions pos .. pos + n - 1
+    int len, win;           // keys 0 .. len - 1; window (0: all)
+    float scale;
+    // plan: row tiles of rt query rows (n * G rows per KV head, row r = token r / G,
+    // head r % G), each over `splits` ranges of `per` positions from lo on
+    int rt, tiles, splits, per, lo;
+    float *part;            // [Hkv * tiles * splits][rt][hd + 2], splits > 1
+};
+
+// Keys that query row t (position pos + t) sees: [key_lo, key_hi).
+__host__ __device__ inline int key_hi(int pos, int t, int len) { return pos + t + 1 < len ? pos + t + 1 : len; }
+__host__ __device__ inline int key_lo(int pos, int t, int win)
+{
+    return (win > 0 && pos + t + 1 > win) ? pos + t + 1 - win : 0;
+}
+
+// Fills a's plan for `sms` SMs and returns the workspace floats it needs.
+size_t plan_attn(Attn &a, int sms);
+
+cudaError_t launch_append(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s);
+cudaError_t launch_read(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s);
+cudaError_t launch_attn(const Attn &a, cudaStream_t s);
+
+}  // namespace lfq
