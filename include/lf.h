@@ -451,7 +451,7 @@ typedef struct {
 } lf_kv4_query;
 
 /* Scratch bytes that lf_kv4_attend needs for this query on the current device
- * (0 for many); the tensors' data pointers are not looked at. */
+ * (0 for many); of the tensors only the dtype is looked at. */
 LF_API lf_status lf_kv4_workspace(const lf_kv4 *c, const lf_kv4_query *q, int64_t *bytes);
 
 /* workspace: device scratch, 16-byte aligned, of at least the bytes that
@@ -464,6 +464,11 @@ LF_API lf_status lf_kv4_workspace(const lf_kv4 *c, const lf_kv4_query *q, int64_
  * max_seq), CUDA. */
 LF_API lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *workspace, int64_t workspace_bytes,
                                void *stream);
+
+/* Synchronise `stream` and return LF_OK, or LF_ERR_TIMEOUT if a device-side
+ * wait of an lf_kv4_attend call on the current device ran out since the last
+ * lf_kv4_status (its outputs are then not valid). */
+LF_API lf_status lf_kv4_status(void *stream);
 
 /* Static string naming a status code. */
 LF_API const char *lf_error_string(lf_status s);

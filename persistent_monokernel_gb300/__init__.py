@@ -28,7 +28,7 @@ TRACE_STAMPS = 9
 EXPORTS = ("lf_create", "lf_destroy", "lf_prefill", "lf_decode", "lf_generate", "lf_sync", "lf_reset",
            "lf_set_schedule", "lf_get_info", "lf_error_string", "lf_abi_version", "lf_generate_noalloc",
            "lf_enable_trace", "lf_read_trace", "lf_sync_latency", "lf_kv4_append", "lf_kv4_read", "lf_kv4_workspace",
-           "lf_kv4_attend")
+           "lf_kv4_attend", "lf_kv4_status")
 
 
 class LFError(RuntimeError):
@@ -107,7 +107,8 @@ def lib() -> C.CDLL:
         L.lf_kv4_read.argtypes = L.lf_kv4_append.argtypes
         L.lf_kv4_workspace.argtypes = [C.POINTER(lf_kv4), C.POINTER(lf_kv4_query), C.POINTER(C.c_int64)]
         L.lf_kv4_attend.argtypes = [C.POINTER(lf_kv4), C.POINTER(lf_kv4_query), vp, C.c_int64, vp]
-        for name in ("lf_kv4_append", "lf_kv4_read", "lf_kv4_workspace", "lf_kv4_attend"):
+        L.lf_kv4_status.argtypes = [vp]
+        for name in ("lf_kv4_status", "lf_kv4_append", "lf_kv4_read", "lf_kv4_workspace", "lf_kv4_attend"):
             getattr(L, name).restype = C.c_int
         for name in ("lf_create", "lf_prefill", "lf_decode", "lf_generate", "lf_sync", "lf_reset",
                      "lf_set_schedule", "lf_get_info"):

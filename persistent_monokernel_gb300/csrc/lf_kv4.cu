@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
         }
     // positions of this CTA: the split's, cut to what the tile's rows see
     const int t_first = r0 / a.G, t_last = (r0 + rows - 1) / a.G;
-    const int lo_t = key_lo(a.pos, t_first, a.win), hi_t = key_hi(a.pos, t_last, a.len);
+    const int lo_t = key_lo(a.pos, t_first, a.win), hi_r = key_hi(a.pos, t_last, a.len);
+    const int hi_t = hi_r > lo_t ? hi_r : 0;              // no position at all: an empty range
     const int p0 = max(a.lo + split * a.per, lo_t / CH * CH), p1 = min(a.lo + (split + 1) * a.per, hi_t);
     // inside [all_lo, all_hi) every row sees every position
     const int all_lo = key_lo(a.pos, t_last, a.win), all_hi = key_hi(a.pos, t_first, a.len);
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
             }
         }
     __syncthreads();
-    float *part = a.part ? a.part + ((size_t)(kvh * a.tiles + tile) * a.splits + split) * RT * (HD + 2) : nullptr;
+    float *part = a.part ? a.part + ((size_t)(kvh * a.tiles + tile) * a.splits + split) * RT * (HD + PAD) : nullptr;
     for (int i = threadIdx.x; i < rows * (HD / 4); i += NW * 32) {
         const int r = i / (HD / 4), d = i % (HD / 4) * 4;
         float M = -INFINITY;
@@ -344,9 +345,8 @@ __global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
             acc.w = fmaf(v.w, x, acc.w);
         }
         if (part) {
-            *reinterpret_cast<float2 *>(part + (size_t)r * (HD + 2) + d) = make_float2(acc.x, acc.y);
-            *reinterpret_cast<float2 *>(part + (size_t)r * (HD + 2) + d + 2) = make_float2(acc.z, acc.w);
-            if (d == 0) *reinterpret_cast<float2 *>(part + (size_t)r * (HD + 2) + HD) = make_float2(M, L);
+            *reinterpret_cast<float4 *>(part + (size_t)r * (HD + PAD) + d) = acc;
+            if (d == 0) *reinterpret_cast<float2 *>(part + (size_t)r * (HD + PAD) + HD) = make_float2(M, L);
         } else {
             const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);   // a row that saw nothing is 0; NaN stays
             const int tt = (r0 + r) / a.G, hh = kvh * a.G + (r0 + r) % a.G;
@@ -356,12 +356,14 @@ __global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
     }
 }
 
-// Joins the splits of a row: one block of HD / 4 threads per query row and KV head.
-__global__ void __launch_bounds__(32) attn_join(const __grid_constant__ Attn a)
+// Joins the splits of a row: HD / 4 threads per query row and KV head.
+__global__ void __launch_bounds__(256) attn_join(const __grid_constant__ Attn a)
 {
-    const int hd = a.c.hd, row = blockIdx.x, kvh = blockIdx.y, d = threadIdx.x * 4;
-    const float *part = a.part + ((size_t)(kvh * a.tiles + row / a.rt) * a.splits * a.rt + row % a.rt) * (hd + 2);
-    const size_t step = (size_t)a.rt * (hd + 2);
+    const int hd = a.c.hd, per = 1024 / hd;                 // rows per block
+    const int row = blockIdx.x * per + threadIdx.x / (hd / 4), kvh = blockIdx.y, d = threadIdx.x % (hd / 4) * 4;
+    if (row >= a.n * a.G) return;
+    const float *part = a.part + ((size_t)((size_t)kvh * a.tiles + row / a.rt) * a.splits * a.rt + row % a.rt) * (hd + PAD);
+    const size_t step = (size_t)a.rt * (hd + PAD);
     float M = -INFINITY;
     for (int s = 0; s < a.splits; ++s) M = fmaxf(M, part[s * step + hd]);
     const float ref = M == -INFINITY ? 0.f : M;
@@ -369,14 +371,13 @@ __global__ void __launch_bounds__(32) attn_join(const __grid_constant__ Attn a)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s = 0; s < a.splits; ++s) {
         const float2 ml = *reinterpret_cast<const float2 *>(part + s * step + hd);
-        const float2 u = *reinterpret_cast<const float2 *>(part + s * step + d);
-        const float2 v = *reinterpret_cast<const float2 *>(part + s * step + d + 2);
+        const float4 u = *reinterpret_cast<const float4 *>(part + s * step + d);
         const float x = ex2(ml.x - ref);
         L = fmaf(ml.y, x, L);
         acc.x = fmaf(u.x, x, acc.x);
         acc.y = fmaf(u.y, x, acc.y);
-        acc.z = fmaf(v.x, x, acc.z);
-        acc.w = fmaf(v.y, x, acc.w);
+        acc.z = fmaf(u.z, x, acc.z);
+        acc.w = fmaf(u.w, x, acc.w);
     }
     const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);
     const int tt = row / a.G, hh = kvh * a.G + row % a.G;
@@ -385,22 +386,56 @@ __global__ void __launch_bounds__(32) attn_join(const __grid_constant__ Attn a)
 
 // ---------------------------------------------------------------- launches
 
+// Rows per KV head from which the tiles kernel takes over.
+constexpr int kTileRows = 33;
+
+static void plan_tiles(Attn &a, int sms, int rows, int hi)
+{
+    constexpr int BN = 128;
+    a.rt = a.q.dtype == F32 ? 128 : 256;
+    a.tiles = (rows + a.rt - 1) / a.rt;
+    a.lo = a.lo / BN * BN;
+    const int chunks = std::max(1, (hi - a.lo + BN - 1) / BN);
+    // One CTA per SM at a time.  In units of a chunk's time (about 1.2 us): each wave costs its CTAs' chunks
+    // and about two for their start and end; splits cost the partial states written and read at about 6.5 TB/s
+    // and the join's launch.
+    const long long ctas = (long long)a.tiles * a.c.Hkv;
+    double best = 1e30;
+    a.splits = 1;
+    for (int s = 1; s <= chunks && s <= 64; ++s) {
+        const int per = (chunks + s - 1) / s, n = (chunks + per - 1) / per;
+        const double waves = (double)((ctas * n + sms - 1) / sms);
+        const double join = n > 1 ? 2.0 + 2.0 * rows * a.c.Hkv * n * (a.c.hd + PAD) * 4.0 / 6.5e12 / 1.2e-6 : 0.0;
+        const double cost = waves * (per + 2.0) + join;
+        if (cost < best * 0.98) {
+            best = cost;
+            a.splits = n;
+        }
+    }
+    const int per = (chunks + a.splits - 1) / a.splits;
+    a.splits = (chunks + per - 1) / per;
+    a.per = per * BN;
+}
+
 size_t plan_attn(Attn &a, int sms)
 {
-    const int rows = a.n * a.G;
-    a.rt = rows <= 8 ? 8 : 16;
-    a.tiles = (rows + a.rt - 1) / a.rt;
+    const int rows = a.n * a.G, hi = key_hi(a.pos, a.n - 1, a.len);
     a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
-    const int hi = key_hi(a.pos, a.n - 1, a.len);
-    const int chunks = std::max(1, (hi - a.lo + CH - 1) / CH);
-    // one CTA per SM, each warp at least one chunk
-    const long long ctas = (long long)a.tiles * a.c.Hkv;
-    int splits = (int)std::max<long long>(1, sms / ctas);
-    splits = std::min(splits, (chunks + 7) / 8);
-    const int per = (chunks + splits - 1) / splits;
-    a.splits = (chunks + per - 1) / per;
-    a.per = per * CH;
-    return a.splits > 1 ? (size_t)a.c.Hkv * a.tiles * a.splits * a.rt * (a.c.hd + 2) : 0;
+    if (rows >= kTileRows) {
+        plan_tiles(a, sms, rows, hi);
+    } else {
+        a.rt = rows <= 8 ? 8 : 16;
+        a.tiles = (rows + a.rt - 1) / a.rt;
+        const int chunks = std::max(1, (hi - a.lo + CH - 1) / CH);
+        // one CTA per SM, each warp at least one chunk
+        const long long ctas = (long long)a.tiles * a.c.Hkv;
+        int splits = (int)std::max<long long>(1, sms / ctas);
+        splits = std::min(splits, (chunks + 7) / 8);
+        const int per = (chunks + splits - 1) / splits;
+        a.splits = (chunks + per - 1) / per;
+        a.per = per * CH;
+    }
+    return a.splits > 1 ? (size_t)a.c.Hkv * a.tiles * a.splits * a.rt * (a.c.hd + PAD) : 0;
 }
 
 template <template <class> class F, class... A>
@@ -463,14 +498,17 @@ cudaError_t launch_attn(const Attn &a, cudaStream_t s)
 {
     const bool split = a.q.dtype == F32;
     cudaError_t e;
-    if (a.c.hd == 128)
+    if (a.rt > 16)
+        e = launch_attn_tiles(a, s);
+    else if (a.c.hd == 128)
         e = a.rt == 8 ? (split ? run_rows<128, 1, true>(a, s) : run_rows<128, 1, false>(a, s))
                       : (split ? run_rows<128, 2, true>(a, s) : run_rows<128, 2, false>(a, s));
     else
         e = a.rt == 8 ? (split ? run_rows<64, 1, true>(a, s) : run_rows<64, 1, false>(a, s))
                       : (split ? run_rows<64, 2, true>(a, s) : run_rows<64, 2, false>(a, s));
     if (e == cudaSuccess && a.splits > 1) {
-        attn_join<<<dim3((unsigned)(a.n * a.G), (unsigned)a.c.Hkv), a.c.hd / 4, 0, s>>>(a);
+        const int per = 1024 / a.c.hd;
+        attn_join<<<dim3((unsigned)((a.n * a.G + per - 1) / per), (unsigned)a.c.Hkv), 256, 0, s>>>(a);
         e = cudaGetLastError();
     }
     return e;
@@ -580,6 +618,8 @@ lf_status make_attn(const lf_kv4 *c, const lf_kv4_query *q, Attn *a, size_t *flo
     a->pos = q->pos;
     a->len = q->length;
     a->win = q->window;
+    if (q->q.dtype != LF_F16 && q->q.dtype != LF_BF16 && q->q.dtype != LF_F32) return LF_ERR_NOT_SUPPORTED;
+    a->q = rows_of(&q->q);
     a->scale = q->scale != 0.f ? q->scale : 1.0f / std::sqrt((float)c->head_dim);
     a->part = nullptr;
     *floats = 0;
@@ -629,10 +669,17 @@ lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *workspace,
     if (st != LF_OK) return st;
     if (q->q.dtype != q->out.dtype || q->q.data == q->out.data) return LF_ERR_INVALID_ARG;
     if (floats && (!aligned16(workspace) || workspace_bytes < (int64_t)(floats * sizeof(float)))) return LF_ERR_INVALID_ARG;
-    a.q = rows_of(&q->q);
     a.o = rows_of(&q->out);
     a.part = floats ? static_cast<float *>(workspace) : nullptr;
     return status_of(launch_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+lf_status lf_kv4_status(void *stream)
+{
+    unsigned rec[4];
+    const cudaError_t e = tiles_status(rec, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return status_of(e);
+    return rec[0] ? LF_ERR_TIMEOUT : LF_OK;
 }
 
 }  // extern "C"

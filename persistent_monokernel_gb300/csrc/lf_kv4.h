@@ -6,6 +6,8 @@
 
 namespace lfq {
 
+constexpr int PAD = 4;      // words of a partial row behind O: m, l, and two that keep rows 16-byte aligned
+
 enum DType { F16 = 0, BF16 = 1, F32 = 2 };
 
 // Bytes of one row of head_dim values: codes (two per byte) and scales (one per 16).
@@ -35,7 +37,7 @@ struct Attn {
     // plan: row tiles of rt query rows (n * G rows per KV head, row r = token r / G,
     // head r % G), each over `splits` ranges of `per` positions from lo on
     int rt, tiles, splits, per, lo;
-    float *part;            // [Hkv * tiles * splits][rt][hd + 2], splits > 1
+    float *part;            // [Hkv * tiles * splits][rt][hd + PAD]: O, then m and l; splits > 1
 };
 
 // Keys that query row t (position pos + t) sees: [key_lo, key_hi).
@@ -45,11 +47,15 @@ __host__ __device__ inline int key_lo(int pos, int t, int win)
     return (win > 0 && pos + t + 1 > win) ? pos + t + 1 - win : 0;
 }
 
-// Fills a's plan for `sms` SMs and returns the workspace floats it needs.
+// Fills a's plan for `sms` SMs (a.q.dtype is set) and returns the workspace floats it needs.
 size_t plan_attn(Attn &a, int sms);
 
 cudaError_t launch_append(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s);
 cudaError_t launch_read(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s);
 cudaError_t launch_attn(const Attn &a, cudaStream_t s);
+// Tiles of 128 or 256 query rows on tcgen05 (lf_kv4_tc.cu); launch_attn calls it by the plan's rt.
+cudaError_t launch_attn_tiles(const Attn &a, cudaStream_t s);
+// Error record of that kernel (out[0] = 0: none), read after synchronising s, and cleared.
+cudaError_t tiles_status(unsigned out[4], cudaStream_t s);
 
 }  // namespace lfq

@@ -26,17 +26,24 @@ class lf_kv4_query(C.Structure):
 
 F16, BF16, F32 = 0, 1, 2
 BLOCK = 16          # values that share a scale
-_DTYPES = {}        # torch dtype -> code, filled at first use (the package imports without torch)
+_byref = C.byref
+_torch = _lib = _codes = _raw_stream = _current_device = None
 
 
-def _dtype_code(dt):
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
-    code = _DTYPES.get(dt)
-    if code is None:
-        raise ValueError(f"dtype {dt}: float16, bfloat16 or float32 is needed")
-    return code
+def _load():
+    """torch and the library, once, at the first cache (the package imports without torch)."""
+    global _torch, _lib, _codes, _raw_stream, _current_device
+    import torch
+
+    from . import lib
+    _lib = lib()
+    _codes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+    # the plain functions behind torch.cuda.current_stream and current_device: a decode step's calls
+    # take a few microseconds on the GPU, and a Stream object costs three
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _torch = torch
 
 
 class KV4Cache:
@@ -62,112 +69,105 @@ class KV4Cache:
         return self
 
     def _set(self, k_codes, k_scales, v_codes, v_scales) -> None:
-        import torch
+        if _torch is None:
+            _load()
         if k_codes.dim() != 3:
             raise ValueError("codes are [n_kv_heads, max_seq, head_dim / 2]")
         h, s, half = k_codes.shape
         for t, width in ((k_codes, half), (k_scales, half // 8), (v_codes, half), (v_scales, half // 8)):
-            if not (t.is_cuda and t.dtype == torch.uint8 and t.is_contiguous() and t.device == k_codes.device
+            if not (t.is_cuda and t.dtype == _torch.uint8 and t.is_contiguous() and t.device == k_codes.device
                     and tuple(t.shape) == (h, s, width)):
                 raise ValueError("codes [n_kv_heads, max_seq, head_dim / 2] and scales [n_kv_heads, max_seq, "
                                  "head_dim / 16] must be contiguous CUDA torch.uint8 tensors on one device")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.n_kv_heads, self.max_seq, self.head_dim = h, s, 2 * half
         self.device = k_codes.device
+        self._index = k_codes.get_device()
         self._c = lf_kv4(h, 2 * half, s, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                          v_scales.data_ptr())
-        self._ref = C.byref(self._c)
+        self._ref = _byref(self._c)
 
     @property
     def nbytes(self) -> int:
         return sum(t.numel() for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales))
 
-    def _rows(self, t, heads, n, what) -> lf_rows:
-        shape = t.shape
-        if len(shape) != 3 or shape[2] != self.head_dim or (heads is not None and shape[1] != heads) or \
-                (n is not None and shape[0] != n):
-            raise ValueError(f"{what} is {tuple(shape)}: [n, heads, {self.head_dim}] is needed")
-        if t.device != self.device:
-            raise ValueError(f"{what} is on {t.device}, the cache on {self.device}")
-        ts, hs, es = t.stride()
-        if es != 1:
-            raise ValueError(f"{what}'s last dimension must be contiguous")
+    def _rows(self, t, n, heads, what) -> lf_rows:
+        """lf_rows of t [n, heads, head_dim]."""
+        stride = t.stride()
+        code = _codes.get(t.dtype)
+        if t.shape != (n, heads, self.head_dim) or t.get_device() != self._index or stride[2] != 1 or code is None:
+            raise ValueError(f"{what} is {t.dtype} {tuple(t.shape)}, strides {stride}, on {t.device}: [{n}, {heads}, "
+                             f"{self.head_dim}] float16, bfloat16 or float32 with a contiguous last dimension on "
+                             f"{self.device} is needed")
         # the stride of a dimension of one is never used (and may be anything)
-        return lf_rows(t.data_ptr(), _dtype_code(t.dtype), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
+        return lf_rows(t.data_ptr(), code, stride[0] if n > 1 else 0, stride[1] if heads > 1 else 0)
 
-    def _run(self, call, stream):
-        """call(stream pointer) with the cache's device current; allocations inside belong to the stream."""
-        import torch
+    def _elsewhere(self, call, stream, args):
+        """The call again with the cache's device, and the stream if one is passed, current: what it allocates belongs
+        to that stream."""
         if stream is None:
-            if torch.cuda.current_device() == self.device.index:
-                return call(torch.cuda.current_stream().cuda_stream)
-            with torch.cuda.device(self.device):
-                return call(torch.cuda.current_stream().cuda_stream)
+            with _torch.cuda.device(self.device):
+                return call(*args)
         if stream.device != self.device:
             raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+        with _torch.cuda.stream(stream):
+            return call(*args)
 
     def append(self, k, v, pos: int, stream=None) -> None:
         """Quantise k, v [n, n_kv_heads, head_dim] into positions pos .. pos + n - 1."""
+        if stream is not None or _current_device() != self._index:
+            return self._elsewhere(self.append, stream, (k, v, pos))
         n = k.shape[0]
-        kr, vr = self._rows(k, self.n_kv_heads, None, "k"), self._rows(v, self.n_kv_heads, n, "v")
-
-        def call(sp):
-            _check(_lib().lf_kv4_append(self._ref, C.byref(kr), C.byref(vr), n, int(pos), sp), "lf_kv4_append")
-        self._run(call, stream)
+        kr, vr = self._rows(k, n, self.n_kv_heads, "k"), self._rows(v, n, self.n_kv_heads, "v")
+        status = _lib.lf_kv4_append(self._ref, _byref(kr), _byref(vr), n, pos, _raw_stream(self._index))
+        if status:
+            _fail(status, "lf_kv4_append")
 
     def read(self, pos: int, n: int, dtype=None, out=None, stream=None):
         """(k, v) [n, n_kv_heads, head_dim]: the values of positions pos .. pos + n - 1 (float16 unless `dtype`
         says otherwise; `out` is a pair of tensors to write to)."""
-        import torch
-
-        def call(sp):
-            pair = out
-            if pair is None:
-                pair = tuple(torch.empty(max(0, int(n)), self.n_kv_heads, self.head_dim, dtype=dtype or torch.float16,
-                                         device=self.device) for _ in range(2))
-            kr, vr = (self._rows(t, self.n_kv_heads, max(0, int(n)), w) for t, w in zip(pair, ("k", "v")))
-            _check(_lib().lf_kv4_read(self._ref, C.byref(kr), C.byref(vr), int(n), int(pos), sp), "lf_kv4_read")
-            return pair
-        return self._run(call, stream)
+        if stream is not None or _current_device() != self._index:
+            return self._elsewhere(self.read, stream, (pos, n, dtype, out))
+        h = self.n_kv_heads
+        if out is None:
+            shape, dtype = (max(n, 0), h, self.head_dim), dtype or _torch.float16
+            k = _torch.empty(shape, dtype=dtype, device=self.device)
+            v = _torch.empty(shape, dtype=dtype, device=self.device)
+        else:
+            k, v = out
+        kr, vr = self._rows(k, max(n, 0), h, "k"), self._rows(v, max(n, 0), h, "v")
+        status = _lib.lf_kv4_read(self._ref, _byref(kr), _byref(vr), n, pos, _raw_stream(self._index))
+        if status:
+            _fail(status, "lf_kv4_read")
+        return k, v
 
     def attend(self, q, pos: int, length: int | None = None, window: int = 0, scale: float = 0.0, out=None,
                stream=None):
         """Causal attention of q [n, n_heads, head_dim], whose rows stand at positions pos .. pos + n - 1, over the
         cached positions 0 .. length - 1 (pos + n unless given); window W > 0 leaves each row the W most recent.
         A row that sees nothing gives zeros.  Returns [n, n_heads, head_dim] in q's dtype."""
-        import torch
-        n, pos = q.shape[0], int(pos)
-        qr = self._rows(q, None, None, "q")
-
-        def call(sp):
-            o = torch.empty(q.shape, dtype=q.dtype, device=self.device) if out is None else out
-            orow = self._rows(o, q.shape[1], n, "out")
-            args = lf_kv4_query(qr, orow, q.shape[1], n, pos, pos + n if length is None else int(length), int(window),
-                                float(scale))
-            ref, need, lib = C.byref(args), C.c_int64(), _lib()
-            _check(lib.lf_kv4_workspace(self._ref, ref, C.byref(need)), "lf_kv4_attend")
+        if stream is not None or _current_device() != self._index:
+            return self._elsewhere(self.attend, stream, (q, pos, length, window, scale, out))
+        shape = q.shape
+        n, heads = shape[0], shape[1]
+        qr = self._rows(q, n, heads, "q")
+        if out is None:
+            out = _torch.empty(shape, dtype=q.dtype, device=self.device)
+        args = lf_kv4_query(qr, self._rows(out, n, heads, "out"), heads, n, pos, pos + n if length is None else length,
+                            window, scale)
+        ref, need = _byref(args), C.c_int64()
+        status = _lib.lf_kv4_workspace(self._ref, ref, _byref(need))
+        if not status:
             # scratch of this call alone: no two streams or captured graphs share it
-            ws = torch.empty(need.value, dtype=torch.uint8, device=self.device) if need.value else None
-            _check(lib.lf_kv4_attend(self._ref, ref, ws.data_ptr() if need.value else None, need.value, sp),
-                   "lf_kv4_attend")
-            return o
-        return self._run(call, stream)
+            size = need.value
+            ws = _torch.empty((size,), dtype=_torch.uint8, device=self.device) if size else None
+            status = _lib.lf_kv4_attend(self._ref, ref, ws.data_ptr() if size else None, size,
+                                        _raw_stream(self._index))
+        if status:
+            _fail(status, "lf_kv4_attend")
+        return out
 
 
-def _check(status: int, where: str) -> None:
-    if status:
-        from . import LFError
-        raise LFError(status, where)
-
-
-_loaded = None
-
-
-def _lib():
-    global _loaded
-    if _loaded is None:
-        from . import lib
-        _loaded = lib()
-    return _loaded
+def _fail(status: int, where: str) -> None:
+    from . import LFError
+    raise LFError(status, where)
