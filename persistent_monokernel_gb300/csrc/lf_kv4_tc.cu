@@ -158,6 +158,112 @@ struct RawRow {
     }
 };
 
+// ---- packed FP32 pairs
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
+    return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The largest of a row's BN scores at TMEM columns ts .. (WHOLE: of all; else of columns lo .. hi - 1).
+template <bool WHOLE>
+__device__ __forceinline__ float row_max(uint32_t ts, int lo, int hi)
+{
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int c = 0; c < BN / 64; ++c) {
+        uint32_t u[2][32];
+        tmem_ld32(ts + (uint32_t)(64 * c), u[0]);
+        tmem_ld32(ts + (uint32_t)(64 * c + 32), u[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+            const float x = __uint_as_float(u[e / 32][e % 32]);
+            const int k = 64 * c + e;
+            if (WHOLE) m[e & 3] = fmaxf(m[e & 3], x);
+            else m[e & 3] = k >= lo && k < hi ? fmaxf(m[e & 3], x) : m[e & 3];
+        }
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// 2^(f s + neg) of a row's BN scores s at TMEM columns ts .., as FP16 pairs over the first 64 of those
+// columns (SPLIT: the remainders over the other 64); zeros outside lo .. hi - 1 unless WHOLE.  Returns their
+// sum, of the FP32 values.
+template <bool WHOLE, bool SPLIT>
+__device__ __forceinline__ float row_probs(uint32_t ts, float f, float neg, int lo, int hi)
+{
+    const uint64_t ff = pack2(f, f), nn = pack2(neg, neg);
+    uint64_t sum[2] = {0ull, 0ull};
+    auto take = [&](const uint32_t (&u)[32], int k0, uint32_t *hw, uint32_t *lw) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            const float2 y = unpack2(fma2(pack2u(u[e], u[e + 1]), ff, nn));
+            float x0 = ex2(y.x), x1 = ex2(y.y);
+            if (!WHOLE) {
+                if (!(k0 + e >= lo && k0 + e < hi)) x0 = 0.f;
+                if (!(k0 + e + 1 >= lo && k0 + e + 1 < hi)) x1 = 0.f;
+            }
+            sum[e / 2 & 1] = add2(sum[e / 2 & 1], pack2(x0, x1));
+            const __half2 h = __floats2half2_rn(x0, x1);
+            hw[e / 2] = *reinterpret_cast<const unsigned *>(&h);
+            if (SPLIT) {
+                const float2 b = __half22float2(h);
+                const __half2 r = __floats2half2_rn(x0 - b.x, x1 - b.y);
+                lw[e / 2] = *reinterpret_cast<const unsigned *>(&r);
+            }
+        }
+    };
+    uint32_t u[2][32], v[2][32], hw[32], lw[32];
+    tmem_ld32(ts, u[0]);
+    tmem_ld32(ts + 32u, u[1]);
+    if (SPLIT) {   // the remainders land on the second half's scores
+        tmem_ld32(ts + 64u, v[0]);
+        tmem_ld32(ts + 96u, v[1]);
+    }
+    tmem_ld_wait();
+    take(u[0], 0, hw, lw);
+    take(u[1], 32, hw + 16, lw + 16);
+    if (!SPLIT) {
+        tmem_ld32(ts + 64u, v[0]);
+        tmem_ld32(ts + 96u, v[1]);
+    }
+    tmem_st32(ts, hw);
+    if (SPLIT) tmem_st32(ts + 64u, lw);
+    if (!SPLIT) tmem_ld_wait();
+    take(v[0], 64, hw, lw);
+    take(v[1], 96, hw + 16, lw + 16);
+    tmem_st32(ts + 32u, hw);
+    if (SPLIT) tmem_st32(ts + 96u, lw);
+    const float2 t = unpack2(add2(sum[0], sum[1]));
+    return t.x + t.y;
+}
+
 template <int HD, bool SPLIT>
 __global__ void __launch_bounds__(TcCfg<HD, SPLIT>::NTHR, 1) attn_tiles(const __grid_constant__ Attn a)
 {
@@ -281,7 +387,8 @@ __global__ void __launch_bounds__(TcCfg<HD, SPLIT>::NTHR, 1) attn_tiles(const __
         const bool live = row < rows;
         const int tok = (r0 + min(row, rows - 1)) / a.G, head = kvh * a.G + (r0 + min(row, rows - 1)) % a.G;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        float f = a.scale * 1.4426950408889634f;            // score factor: scale x log2(e) / the row's power of two
+        // score factor: |scale| x log2(e) / the row's power of two; a negative scale turns q
+        float f = fabsf(a.scale) * 1.4426950408889634f;
         {
             const size_t at = (size_t)tok * a.q.ts + (size_t)head * a.q.hs;
             auto load = [&](int c, float (&x)[16]) {
@@ -302,6 +409,7 @@ __global__ void __launch_bounds__(TcCfg<HD, SPLIT>::NTHR, 1) attn_tiles(const __
                 fac = range_factor(m);
                 f /= fac;
             }
+            if (a.scale < 0.f) fac = -fac;
             uint8_t *qh = smem + C::OFF_Q + (SPLIT ? 0u : (uint32_t)mt * C::ROWB);
 #pragma unroll 1
             for (int c = 0; c < HD / 16; ++c) {
@@ -342,23 +450,10 @@ __global__ void __launch_bounds__(TcCfg<HD, SPLIT>::NTHR, 1) attn_tiles(const __
             const uint32_t ts = tl + (uint32_t)s * BN;
             const int key0 = p0 + i * BN;
             const bool whole = __all_sync(0xffffffffu, key0 >= klo && key0 + BN <= khi);
-            const float sgn = f < 0.f ? -1.f : 1.f;
             // ---- the chunk's maximum
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
-                uint32_t u[32];
-                tmem_ld32(ts + (uint32_t)(32 * c), u);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int key = key0 + 32 * c + e;
-                    const float x = __uint_as_float(u[e]) * sgn;
-                    mx = whole || (key >= klo && key < khi) ? fmaxf(mx, x) : mx;
-                }
-            }
-            mx = mx * fabsf(f) - TC_EXP;                     // -inf stays (f = 0: NaN, taken as 0 below)
-            if (f == 0.f) mx = khi > klo ? -TC_EXP : -INFINITY;
+            const float top = whole ? row_max<true>(ts, 0, BN) : row_max<false>(ts, klo - key0, khi - key0);
+            float mx = fmaf(top, f, -TC_EXP);                // -inf stays
+            if (f == 0.f) mx = top == -INFINITY ? top : -TC_EXP;
             const bool up = mx > ref + SLACK;                // also from -inf
             if (__any_sync(0xffffffffu, up)) {
                 const float alpha = up ? ex2(ref - mx) : 1.f;   // 0 from -inf
@@ -386,58 +481,9 @@ __global__ void __launch_bounds__(TcCfg<HD, SPLIT>::NTHR, 1) attn_tiles(const __
                     tmem_st_wait();
                 }
             }
-            // ---- P, over S: 64 scores to 32 columns of FP16 pairs (SPLIT: the remainders 64 columns on,
-            // so the scores of the second half are taken first)
+            // ---- P, over S
             const float neg = ref == -INFINITY ? 0.f : -ref;
-            uint32_t u2[64];
-            if (SPLIT) {
-                uint32_t u[32];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    tmem_ld32(ts + (uint32_t)(64 + 32 * c), u);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) u2[32 * c + e] = u[e];
-                }
-            }
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                uint32_t hw[32], lw[32];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t u[32];
-                    if (!SPLIT || hf == 0) {
-                        tmem_ld32(ts + (uint32_t)(64 * hf + 32 * c), u);
-                        tmem_ld_wait();
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) u[e] = u2[32 * c + e];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const int key = key0 + 64 * hf + 32 * c + e;
-                        float x0 = ex2(fmaf(__uint_as_float(u[e]), f, neg));
-                        float x1 = ex2(fmaf(__uint_as_float(u[e + 1]), f, neg));
-                        if (!whole) {
-                            if (!(key >= klo && key < khi)) x0 = 0.f;
-                            if (!(key + 1 >= klo && key + 1 < khi)) x1 = 0.f;
-                        }
-                        l += x0 + x1;
-                        if (SPLIT) {
-                            __half h0, m0, h1, m1;
-                            lfk::split_h(x0, h0, m0);
-                            lfk::split_h(x1, h1, m1);
-                            hw[16 * c + e / 2] = lfk::pack_h2(h0, h1);
-                            lw[16 * c + e / 2] = lfk::pack_h2(m0, m1);
-                        } else {
-                            const __half2 h = __floats2half2_rn(x0, x1);
-                            hw[16 * c + e / 2] = *reinterpret_cast<const unsigned *>(&h);
-                        }
-                    }
-                }
-                tmem_st32(ts + (uint32_t)(32 * hf), hw);
-                if (SPLIT) tmem_st32(ts + BN / 2 + (uint32_t)(32 * hf), lw);
-            }
+            l += whole ? row_probs<true, SPLIT>(ts, f, neg, 0, BN) : row_probs<false, SPLIT>(ts, f, neg, klo - key0, khi - key0);
             tmem_st_wait();
             fence_before_sync();
             lfk::mbar_arrive(&b->p_full[s]);
