@@ -122,7 +122,7 @@ struct RowCfg {
     static constexpr int QW = SPLIT ? 4 : 2;           // words per q fragment
     static constexpr int SMEM = NT * KS * 32 * QW * 4 + (2 * NW + 1) * RT * 4 + NW * RT * HD * 4;
 };
-constexpr float P_EXP = 15.f;
+constexpr float P_EXP = 11.f;
 constexpr int SL = 2;                                  // 16-position slabs per softmax step
 constexpr int CH = 16 * SL;
 
@@ -258,7 +258,10 @@ __global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
                     }
 #pragma unroll
                 for (int sh = 4; sh <= 16; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-                const float mn = fmaxf(m[i][e], mx - P_EXP), ref = mn == -INFINITY ? 0.f : mn;
+                float mn = mx - P_EXP;
+                if (mx - mn > 15.f) mn = mx;               // scores so large that their steps are
+                mn = fmaxf(m[i][e], mn);
+                const float ref = mn == -INFINITY ? 0.f : mn;
                 const float alpha = ex2(m[i][e] - ref);    // 0 while nothing was seen
                 m[i][e] = mn;
                 float sum = 0.f;
@@ -392,7 +395,7 @@ constexpr int kTileRows = 33;
 static void plan_tiles(Attn &a, int sms, int rows, int hi)
 {
     constexpr int BN = 128;
-    a.rt = a.q.dtype == F32 ? 128 : 256;
+    a.rt = 128;
     a.tiles = (rows + a.rt - 1) / a.rt;
     a.lo = a.lo / BN * BN;
     const int chunks = std::max(1, (hi - a.lo + BN - 1) / BN);

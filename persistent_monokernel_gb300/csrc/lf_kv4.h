@@ -53,7 +53,7 @@ size_t plan_attn(Attn &a, int sms);
 cudaError_t launch_append(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s);
 cudaError_t launch_read(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s);
 cudaError_t launch_attn(const Attn &a, cudaStream_t s);
-// Tiles of 128 or 256 query rows on tcgen05 (lf_kv4_tc.cu); launch_attn calls it by the plan's rt.
+// Tiles of 128 query rows on tcgen05 (lf_kv4_tc.cu); launch_attn calls it by the plan's rt.
 cudaError_t launch_attn_tiles(const Attn &a, cudaStream_t s);
 // Error record of that kernel (out[0] = 0: none), read after synchronising s, and cleared.
 cudaError_t tiles_status(unsigned out[4], cudaStream_t s);

@@ -64,9 +64,9 @@ def attention(q, k, v, pos, length, window, scale):
         and the conversions of q (BF16: exact or 2^-25 of the row's largest); twice, as the sum is off as well;
       - FP32 sums over the positions, rounded or cut off at every 16 of them: (length / 16 + 16) 2^-23;
     and besides S:
-      - FP16 runs out of exponents: the kernels scale the row's largest probability to 2^11 at least, so that a
-        head or remainder that is subnormal is off by up to 2^-25, 2^-25 / 2^11 = 2^-36 of the largest; each position
-        may be (the sum is at least the largest): length * 2^-36 max|v|;
+      - FP16 runs out of exponents: the kernels scale the row's largest probability to 2^7 at least, so that a
+        head or remainder that is subnormal is off by up to 2^-25, 2^-25 / 2^7 = 2^-32 of the largest; each position
+        may be (the sum is at least the largest): length * 2^-32 max|v|;
       - the output's own rounding, half a step of its type."""
     n, Hq, hd = q.shape
     G = Hq // k.shape[0]
@@ -88,6 +88,6 @@ def attention(q, k, v, pos, length, window, scale):
         d = (hd + 8) * 2.0 ** -23 * abs(scale) * ((qq.abs() @ kk.abs().T) * vis).amax(-1, keepdim=True)
         d = d + 2.0 ** -25 * abs(scale) * qq.abs().amax(-1, keepdim=True) * (kk.abs().sum(-1) * vis).amax(-1, keepdim=True)
         rel = (2.0 ** -20 if wide else 2.0 ** -11 + 2.0 ** -20) + 2 * d + (length / 16 + 16) * 2.0 ** -23
-        bound[:, h] = mag * rel + length * 2.0 ** -36 * vv.abs().amax()
+        bound[:, h] = mag * rel + length * 2.0 ** -32 * vv.abs().amax()
     half = torch.finfo(q.dtype).eps / 2
     return out, bound + (out.abs() + bound) * half + torch.finfo(q.dtype).tiny
