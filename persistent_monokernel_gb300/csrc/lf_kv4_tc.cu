@@ -4,10 +4,11 @@
 // One CTA takes 128 query rows that share a KV head (row r = token r / G, head
 // r % G of the group) and walks its positions in chunks of 128:
 //
-//   dequantise  four warps, one thread per position: the row's codes and scales
-//               (prefetched one chunk ahead into registers) -> FP16, written to
-//               shared memory in the 128-byte-swizzle layout, K as a K-major
-//               operand, V (the same row layout) as an MN-major one
+//   dequantise  four warps for K and four for V, one thread per position: the
+//               row's codes and scales (prefetched one chunk ahead into
+//               registers) -> FP16, written to shared memory in the
+//               128-byte-swizzle layout, K as a K-major operand, V (the same row
+//               layout) as an MN-major one
 //   S = Q K^T   tcgen05.mma, Q from TMEM, FP32 scores in TMEM (two buffers)
 //   P           two threads per query row, 64 positions each: mask, 2^x, running
 //               sum, FP16 into TMEM
@@ -53,7 +54,10 @@ constexpr float TC_EXP = 7.f, TC_TOP = 15.f;     // a new reference puts the row
 constexpr long long kWaitNs = 2000000000LL;      // bound of every wait
 
 constexpr int NSM = 256;                         // softmax threads: two per query row
-constexpr int W_DQ = 8, W_MMA = 12, NTHR = 416;  // warps: 0-7 softmax, 8-11 dequantisation, 12 MMA
+constexpr int W_DQ = 8, W_MMA = 16, NTHR = 640;  // warps: 0-7 softmax, 8-15 dequantisation (K, V), 16 MMA (17-19 idle)
+// Registers per thread after the split; the launch has 96 for each of its five warpgroups
+constexpr int REG_SM = 144, REG_DQ = 72, REG_MMA = 40;
+static_assert(2 * REG_SM + 2 * REG_DQ + REG_MMA <= 5 * 96, "the warpgroups' registers come out of the launch's");
 
 template <int HD, bool SPLIT>
 struct TcCfg {
@@ -74,6 +78,7 @@ struct Bars {
     int abort;
     float x[2][BM];     // exchanged between the two threads of a row
 };
+// (a descriptor's start address has 14 bits of 16 bytes: adding offsets to it never carries out of 256 KB)
 template <int HD, bool SPLIT>
 constexpr uint32_t tc_smem() { return TcCfg<HD, SPLIT>::OFF_BAR + (uint32_t)sizeof(Bars) + 1024u; }
 
@@ -103,6 +108,13 @@ __device__ void settle_phase(uint64_t *bar, unsigned parity)
     while (!lfk::mbar_try_wait(bar, parity))
         if ((long long)(lfk::globaltimer_ns() - t0) > kWaitNs) return;
 }
+// One arrival for a warp whose lanes have each fenced their own writes (256 single arrivals queue up on the
+// barrier's word for longer than a product takes).
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane)
+{
+    __syncwarp();
+    if (lane == 0) lfk::mbar_arrive(bar);
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ uint32_t sw128(int row, int c16) { return (uint32_t)(row * 128 + ((c16 ^ (row & 7)) << 4)); }
 
@@ -118,15 +130,47 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn)
 {
     return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// D[tmem] (+)= A[tmem] . B[smem]
-__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t id, uint32_t accum)
+// D[tmem] (+)= A . B[smem], A in TMEM or (SS) in shared memory.  The descriptors' low words come as a base and a
+// constant offset that is added beside the instruction: with descriptors computed ahead, 32 of them live in
+// registers that the MMA warp does not have, and an MMA every 117 cycles instead of 64.
+template <uint32_t OFF>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t id, uint32_t accum)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(bdesc), "r"(id), "r"(accum)
+        "{\n\t.reg .pred p;\n\t.reg .b32 l;\n\t.reg .b64 q;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "add.u32 l, %2, %6;\n\t"
+        "mov.b64 q, {l, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], q, %4, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(blo), "r"(bhi), "r"(id), "r"(accum), "n"(OFF)
         : "memory");
+}
+template <uint32_t AOFF, uint32_t OFF>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t id, uint32_t accum)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 l;\n\t.reg .b64 q, r;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "add.u32 l, %1, %6;\n\t"
+        "mov.b64 r, {l, %3};\n\t"
+        "add.u32 l, %2, %7;\n\t"
+        "mov.b64 q, {l, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], r, q, %4, p;\n\t}"
+        ::"r"(d), "r"(alo), "r"(blo), "r"(hi), "r"(id), "r"(accum), "n"(AOFF), "n"(OFF)
+        : "memory");
+}
+template <uint32_t N>
+struct Int {
+    static constexpr uint32_t value = N;
+};
+// f(Int<0>), f(Int<1>), .. f(Int<N - 1>)
+template <uint32_t N, class F>
+__device__ __forceinline__ void unroll(F &&f)
+{
+    if constexpr (N > 0) {
+        unroll<N - 1>(f);
+        f(Int<N - 1>{});
+    }
 }
 
 // One position's row: HD / 2 code bytes and HD / 16 scales, held in registers.
@@ -141,25 +185,46 @@ struct RawRow {
         if (HD == 128) s = __ldg(reinterpret_cast<const uint2 *>(scales));
         else s = make_uint2(__ldg(reinterpret_cast<const unsigned *>(scales)), 0u);
     }
-    // row `row` of an operand tile at `base`
-    __device__ __forceinline__ void store(uint8_t *base, int row) const
+    // One row of an operand tile: 16-byte group c of its 64-dim half h to at[c] + h * 16,384 (the shared-memory
+    // addresses of the row's eight swizzled groups) + off.
+    __device__ __forceinline__ void store(const uint32_t (&at)[8], uint32_t off) const
     {
 #pragma unroll
-        for (int j = 0; j < HD / 32; ++j) {
+        for (int j = 0; j < HD / 32; ++j) {            // 32 values: two blocks
+            const unsigned sw = j < 2 ? s.x : s.y;
+            const unsigned sc = e4m3x2_h2(j & 1 ? sw >> 16 : sw);
+            const __half2 s2 = *reinterpret_cast<const __half2 *>(&sc);
+            const __half2 lo = __low2half2(s2), hi = __high2half2(s2);
             const unsigned w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {          // 8 values: 16 bytes of FP16
-                const int blk = 2 * j + u / 2;     // their block of 16
-                const unsigned sc = e4m3_h2_same(((blk < 4 ? s.x : s.y) >> (8 * (blk & 3))) & 255u);
+            for (int u = 0; u < 4; ++u) {              // 8 values: 16 bytes of FP16
                 unsigned h[4];
                 e2m1x8_h2(w[u], h[0], h[1], h[2], h[3]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&h[q]), u < 2 ? lo : hi);
+                    h[q] = *reinterpret_cast<const unsigned *>(&v);
+                }
                 const int c16 = 4 * j + u;
-                *reinterpret_cast<uint4 *>(base + (c16 / 8) * (128 * 128) + sw128(row, c16 % 8)) =
-                    make_uint4(hmul2(h[0], sc), hmul2(h[1], sc), hmul2(h[2], sc), hmul2(h[3], sc));
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at[c16 % 8] + off + (uint32_t)(c16 / 8) * 16384u),
+                             "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                             : "memory");
             }
         }
     }
 };
+
+// One lane of a converged warp, the same at every call.
+__device__ __forceinline__ bool elect_one()
+{
+    unsigned r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // ---- packed FP32 pairs
 __device__ __forceinline__ uint64_t pack2(float a, float b)
@@ -277,15 +342,15 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            lfk::mbar_init(&b->k_full[i], 128);
+            lfk::mbar_init(&b->k_full[i], 4);
             lfk::mbar_init(&b->k_empty[i], 1);
-            lfk::mbar_init(&b->v_full[i], 128);
+            lfk::mbar_init(&b->v_full[i], 4);
             lfk::mbar_init(&b->v_empty[i], 1);
             lfk::mbar_init(&b->s_full[i], 1);
         }
-        lfk::mbar_init(&b->p_full, NSM);
+        lfk::mbar_init(&b->p_full, NSM / 32);
         lfk::mbar_init(&b->pv_done, 1);
-        lfk::mbar_init(&b->q_ready, NSM);
+        lfk::mbar_init(&b->q_ready, NSM / 32);
         lfk::mbar_init(&b->drained, 1);
         b->abort = 0;
         lfk::mbar_fence_init();
@@ -297,81 +362,108 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tmem = b->tmem;
+    // All 512 columns are this CTA's, so the allocation starts at column 0: constant addresses keep the MMA
+    // warp's operands out of the vector registers.  (Anything else would be a broken allocation: nothing runs.)
+    constexpr uint32_t tmem = 0;
+    if (threadIdx.x == 0 && b->tmem != 0u) {
+        b->abort = 1;
+        if (atomicCAS(g_status, 0u, (unsigned)lfk::STATUS_TIMEOUT) == 0u) g_status[1] = 711;
+    }
+    __syncthreads();
+    const bool dead = b->abort != 0;
 
-    if (warp == W_MMA) {
-        if (lane == 0 && nc > 0) {
+    if (warp >= W_MMA) {
+        setmaxnreg_dec<REG_MMA>();
+        if (warp == W_MMA && nc > 0 && !dead) {
+            // The whole warp walks the loop with uniform values; one elected lane issues.
+            const bool one = elect_one();
             const uint32_t sb = lfk::smem_u32(smem);
-            auto issue_s = [&](int i) -> bool {
-                if (!wait_phase(&b->k_full[i & 1], (unsigned)(i >> 1) & 1u, b, 701)) return false;
+            const uint64_t kd = sdesc_kmajor_sw128(sb + C::OFF_K), vd = sdesc_mn_sw128(sb + C::OFF_V, C::ATOM);
+            const uint32_t klo = (uint32_t)kd, vlo = (uint32_t)vd, khi = (uint32_t)(kd >> 32), vhi = (uint32_t)(vd >> 32);
+            const uint32_t qlo = (uint32_t)sdesc_kmajor_sw128(sb + C::OFF_Q);
+            auto issue_s = [&](int i, auto stage) -> bool {
+                constexpr uint32_t S = decltype(stage)::value, D = tmem + S * BN;
+                if (!__all_sync(0xffffffffu, wait_phase(&b->k_full[S], (unsigned)(i >> 1) & 1u, b, 701))) return false;
                 fence_after_sync();
-                const uint32_t kb = sb + C::OFF_K + (uint32_t)(i & 1) * C::ROWB, d = tmem + (uint32_t)(i & 1) * BN;
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t off = (uint32_t)(kk / 4) * C::ATOM + (uint32_t)(kk % 4) * 32u;
-                    const uint64_t bd = sdesc_kmajor_sw128(kb + off);
-                    if (SPLIT) {
-                        mma_f16(d, sdesc_kmajor_sw128(sb + C::OFF_Q + off), bd, idesc(BM, BN, false), kk != 0);
-                        mma_f16(d, sdesc_kmajor_sw128(sb + C::OFF_Q + C::ROWB + off), bd, idesc(BM, BN, false), 1u);
-                    } else {
-                        mma_f16_ta(d, tmem + C::T_Q + (uint32_t)kk * 8u, bd, idesc(BM, BN, false), kk != 0);
-                    }
+                if (one) {
+                    unroll<HD / 16>([&](auto kc) {
+                        constexpr uint32_t kk = decltype(kc)::value, off = (kk / 4 * C::ATOM + kk % 4 * 32u) >> 4;
+                        constexpr uint32_t id = idesc(BM, BN, false);
+                        if constexpr (SPLIT) {
+                            mma_ss<off, off + (S * C::ROWB >> 4)>(D, qlo, klo, khi, id, kk != 0);
+                            mma_ss<off + (C::ROWB >> 4), off + (S * C::ROWB >> 4)>(D, qlo, klo, khi, id, 1u);
+                        } else {
+                            mma_ts<off + (S * C::ROWB >> 4)>(D, tmem + C::T_Q + kk * 8u, klo, khi, id, kk != 0);
+                        }
+                    });
+                    commit(&b->k_empty[S]);
+                    commit(&b->s_full[S]);
                 }
-                commit(&b->k_empty[i & 1]);
-                commit(&b->s_full[i & 1]);
+                __syncwarp();
                 return true;
             };
-            bool ok = wait_phase(&b->q_ready, 0u, b, 700) && issue_s(0) && (nc < 2 || issue_s(1));
-            for (int i = 0; ok && i < nc; ++i) {
-                if (!wait_phase(&b->v_full[i & 1], (unsigned)(i >> 1) & 1u, b, 702)) break;
-                if (!wait_phase(&b->p_full, (unsigned)i & 1u, b, 703)) break;
+            auto step = [&](int i, auto stage) -> bool {
+                constexpr uint32_t S = decltype(stage)::value;
+                if (!__all_sync(0xffffffffu, wait_phase(&b->v_full[S], (unsigned)(i >> 1) & 1u, b, 702) &&
+                                                 wait_phase(&b->p_full, (unsigned)i & 1u, b, 703)))
+                    return false;
                 fence_after_sync();
-                const uint32_t vb = sb + C::OFF_V + (uint32_t)(i & 1) * C::ROWB;
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk) {
-                    const uint64_t vd = sdesc_mn_sw128(vb + (uint32_t)kk * 2048u, C::ATOM);
-                    mma_f16_ta(tmem + C::T_O, tmem + C::T_P + (uint32_t)kk * 8u, vd, idesc(BM, HD, true), (i | kk) != 0);
-                    if (SPLIT)
-                        mma_f16_ta(tmem + C::T_O, tmem + C::T_P + BN / 2 + (uint32_t)kk * 8u, vd, idesc(BM, HD, true), 1u);
+                if (one) {
+                    unroll<BN / 16>([&](auto kc) {
+                        constexpr uint32_t kk = decltype(kc)::value, off = (S * C::ROWB >> 4) + kk * 128u;
+                        constexpr uint32_t id = idesc(BM, HD, true);
+                        mma_ts<off>(tmem + C::T_O, tmem + C::T_P + kk * 8u, vlo, vhi, id, kk != 0 ? 1u : (uint32_t)(i != 0));
+                        if constexpr (SPLIT)
+                            mma_ts<off>(tmem + C::T_O, tmem + C::T_P + BN / 2 + kk * 8u, vlo, vhi, id, 1u);
+                    });
+                    commit(&b->v_empty[S]);
+                    commit(&b->pv_done);
                 }
-                commit(&b->v_empty[i & 1]);
-                commit(&b->pv_done);
-                if (i + 2 < nc) ok = issue_s(i + 2);   // p_full: the scores of chunk i were read
-            }
+                __syncwarp();
+                return i + 2 < nc ? issue_s(i + 2, stage) : true;   // p_full: the scores of chunk i were read
+            };
+            if (__all_sync(0xffffffffu, wait_phase(&b->q_ready, 0u, b, 700)) && issue_s(0, Int<0>{}) &&
+                (nc < 2 || issue_s(1, Int<1>{})))
+                for (int i = 0; i < nc; i += 2) {
+                    if (!step(i, Int<0>{})) break;
+                    if (i + 1 < nc && !step(i + 1, Int<1>{})) break;
+                }
         }
     } else if (warp >= W_DQ) {
-        // ---- dequantisation: thread j takes position j of every chunk
-        const int j = threadIdx.x - W_DQ * 32;
+        // ---- dequantisation: one warpgroup takes K, the other V; thread j position j of every chunk
+        setmaxnreg_dec<REG_DQ>();
+        const int j = threadIdx.x & 127;
+        const bool isv = warp >= W_DQ + 4;
         const size_t row0 = (size_t)kvh * a.c.cap;
-        auto row = [&](int i) { return row0 + (size_t)max(min(p0 + i * BN + j, p1 - 1), lo_t); };   // outside: a seen row, masked
-        RawRow<HD> k, v;
-        auto fetch_k = [&](int i) { k.load(a.c.kc + row(i) * code_bytes(HD), a.c.ks + row(i) * scale_bytes(HD)); };
-        auto fetch_v = [&](int i) { v.load(a.c.vc + row(i) * code_bytes(HD), a.c.vs + row(i) * scale_bytes(HD)); };
-        // K runs one chunk ahead of V: the order the products want them in
-        if (nc > 0) {
-            fetch_k(0);
-            fetch_v(0);
-        }
-        for (int i = 0; i <= nc && nc > 0; ++i) {
-            if (i < nc) {
-                if (!wait_phase(&b->k_empty[i & 1], ((unsigned)(i >> 1) & 1u) ^ 1u, b, 705)) break;
-                k.store(smem + C::OFF_K + (uint32_t)(i & 1) * C::ROWB, j);
-                fence_async_smem();
-                lfk::mbar_arrive(&b->k_full[i & 1]);
-                if (i + 1 < nc) fetch_k(i + 1);
-            }
-            if (i > 0) {
-                const int c = i - 1;
-                if (!wait_phase(&b->v_empty[c & 1], ((unsigned)(c >> 1) & 1u) ^ 1u, b, 706)) break;
-                v.store(smem + C::OFF_V + (uint32_t)(c & 1) * C::ROWB, j);
-                fence_async_smem();
-                lfk::mbar_arrive(&b->v_full[c & 1]);
-                if (i < nc) fetch_v(i);
-            }
+        const uint8_t *codes = (isv ? a.c.vc : a.c.kc) + row0 * code_bytes(HD);
+        const uint8_t *scales = (isv ? a.c.vs : a.c.ks) + row0 * scale_bytes(HD);
+        uint64_t *full = isv ? b->v_full : b->k_full, *empty = isv ? b->v_empty : b->k_empty;
+        uint32_t at[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) at[c] = lfk::smem_u32(smem) + (isv ? C::OFF_V : C::OFF_K) + sw128(j, c);
+        RawRow<HD> raw;
+        auto fetch = [&](int i) {
+            const size_t r = (size_t)max(min(p0 + i * BN + j, p1 - 1), lo_t);   // outside: a seen row, masked
+            raw.load(codes + r * code_bytes(HD), scales + r * scale_bytes(HD));
+        };
+        if (nc > 0) fetch(0);
+        auto step = [&](int i, auto stage) -> bool {
+            constexpr uint32_t S = decltype(stage)::value;
+            if (!wait_phase(&empty[S], ((unsigned)(i >> 1) & 1u) ^ 1u, b, 705)) return false;
+            raw.store(at, S * C::ROWB);
+            fence_async_smem();
+            warp_arrive(&full[S], lane);
+            if (i + 1 < nc) fetch(i + 1);
+            return true;
+        };
+        for (int i = 0; i < nc; i += 2) {
+            if (!step(i, Int<0>{})) break;
+            if (i + 1 < nc && !step(i + 1, Int<1>{})) break;
         }
     } else {
         // ---- softmax and output: thread (r, hf) takes positions 64 hf .. 64 hf + 63 of every chunk for row r,
         // and half of its q and of its output
+        setmaxnreg_inc<REG_SM>();
         const int hf = warp >> 2, r = (warp & 3) * 32 + lane;
         const bool live = r < rows;
         const int tok = (r0 + min(r, rows - 1)) / a.G, head = kvh * a.G + (r0 + min(r, rows - 1)) % a.G;
@@ -442,7 +534,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         }
         if (SPLIT) fence_async_smem();
         else fence_before_sync();
-        lfk::mbar_arrive(&b->q_ready);
+        warp_arrive(&b->q_ready, lane);
         const int klo = key_lo(a.pos, tok, a.win), khi = min(key_hi(a.pos, tok, a.len), p1);
         float ref = -INFINITY, l = 0.f;
         bool run = true;
@@ -507,7 +599,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
             if (SPLIT) tmem_st32(tl + C::T_P + BN / 2 + (uint32_t)(32 * hf), lw);
             tmem_st_wait();
             fence_before_sync();
-            lfk::mbar_arrive(&b->p_full);
+            warp_arrive(&b->p_full, lane);
         }
         // ---- output: O / l, or the partial state of a split
         if (run && nc > 0) {
@@ -549,14 +641,14 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
     fence_before_sync();
     __syncthreads();
     if (warp == W_MMA) {
-        if (lane == 0 && b->abort && nc > 0) {
-            // nothing may still write TMEM: one more commit covers every MMA issued
+        if (b->abort && nc > 0 && elect_one()) {
+            // nothing may still write TMEM: one more commit, by the lane that issued them, covers every MMA
             commit(&b->drained);
             settle_phase(&b->drained, 0u);
         }
         __syncwarp();
         fence_after_sync();
-        tmem_dealloc(tmem, C::T_COLS);
+        tmem_dealloc(b->tmem, C::T_COLS);
     }
 }
 
@@ -570,6 +662,11 @@ static cudaError_t run_tiles(const Attn &a, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !ready[dev]) {
+        // the register split waits for ever unless the launch holds what it hands out
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, attn_tiles<HD, SPLIT>);
+        if (e != cudaSuccess) return e;
+        if ((fa.numRegs + 7) / 8 * 8 * 5 < 2 * REG_SM + 2 * REG_DQ + REG_MMA) return cudaErrorLaunchOutOfResources;
         e = cudaFuncSetAttribute(attn_tiles<HD, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready[dev] = true;
