@@ -10,23 +10,25 @@
 //               128-byte-swizzle layout, K as a K-major operand, V (the same row
 //               layout) as an MN-major one
 //   S = Q K^T   tcgen05.mma, Q from TMEM, FP32 scores in TMEM (two buffers)
-//   P           two threads per query row, 64 positions each: mask, 2^x, running
-//               sum, FP16 into TMEM
+//   P           two groups of four warps take the chunks in turn, one thread per
+//               query row: mask, maximum, 2^x, running sum, FP16 into TMEM
 //   O += P V    tcgen05.mma, P from TMEM, FP32 in TMEM
 //
 // Shared memory's 128 bytes per cycle are the second limit after the tensor
 // cores: a 128 x 128 x 16 product that reads both operands there takes all of
 // them.  With Q and P in TMEM a chunk moves 128 KB (K and V written once and read
-// once) in the 1,024 cycles of its products at peak rate.  The MMA order is
-//   S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...
-// with P beside S, not over it: S(i + 2) needs only that the scores of chunk i
-// were read, so that the tensor cores find the next product queued.
+// once) in the 1,024 cycles of its products at peak rate.  P lies beside
+// S, not over it: S(i + 2) needs only that the scores of chunk i were read, so
+// that the tensor cores find the next product queued.
 //
-// The softmax makes one pass: P is taken relative to the reference of the row so
-// far, and only when a score exceeds it by more than the 2^15 that FP16 holds, or
-// a row sees its first position, is the chunk's maximum exchanged between the
-// row's two threads, the reference moved to 2^TC_EXP below it, O and l rescaled
-// and P taken again.  The quotient O / l does not depend on the reference.
+// A chunk's softmax takes longer than its two products, so two chunks are in
+// flight, and no maximum is taken on the common path.  P is formed relative to the
+// row's reference as last known; 128 values whose sum is at most 2^15 cannot have
+// left FP16's range, so the sum, which is needed anyway, is the check.  At the end
+// of a chunk the groups hand the reference on in chunk order; only where it has
+// moved, the sum was too large, or the row saw its first position, is the maximum
+// taken, the reference put 2^TC_EXP below it, O and l rescaled and P formed
+// again.  The quotient O / l does not depend on the reference.
 //
 // FP32 queries (SPLIT): q and P as an FP16 head and remainder, each product
 // formed twice; Q then lies in shared memory (TMEM is full).
@@ -50,13 +52,14 @@ using namespace lftc;
 __device__ unsigned g_status[8];   // error record of the kernels below (status[4]: unused abort word)
 
 constexpr int BM = 128, BN = 128;
-constexpr float TC_EXP = 7.f, TC_TOP = 15.f;     // a new reference puts the row's largest P at 2^7; none exceeds 2^15
+constexpr float TC_EXP = 7.f;                    // a new reference puts the row's largest P at 2^7 (a sum of at most 2^14)
+constexpr float TC_SUM = 32768.f;                // a chunk's sum that shows every P in range
 constexpr long long kWaitNs = 2000000000LL;      // bound of every wait
 
 constexpr int NSM = 256;                         // softmax threads: two per query row
-constexpr int W_DQ = 8, W_MMA = 16, NTHR = 640;  // warps: 0-7 softmax, 8-15 dequantisation (K, V), 16 MMA (17-19 idle)
+constexpr int W_DQ = 8, W_MMA = 16, NTHR = 640;  // warps: 0-7 softmax, 8-15 dequantisation (K, V), 16 S, 17 P V (18, 19 idle)
 // Registers per thread after the split; the launch has 96 for each of its five warpgroups
-constexpr int REG_SM = 144, REG_DQ = 72, REG_MMA = 40;
+constexpr int REG_SM = 152, REG_DQ = 64, REG_MMA = 40;
 static_assert(2 * REG_SM + 2 * REG_DQ + REG_MMA <= 5 * 96, "the warpgroups' registers come out of the launch's");
 
 template <int HD, bool SPLIT>
@@ -73,10 +76,11 @@ struct TcCfg {
 
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_full, pv_done, q_ready, drained;
+    uint64_t s_full[2], s_free[2], pv_done[2], p_full, q_ready, drained[2];
     uint32_t tmem;
     int abort;
     float x[2][BM];     // exchanged between the two threads of a row
+    float ref[BM];      // the row's reference, handed on from chunk to chunk
 };
 // (a descriptor's start address has 14 bits of 16 bytes: adding offsets to it never carries out of 256 KB)
 template <int HD, bool SPLIT>
@@ -101,6 +105,12 @@ __device__ bool wait_phase(uint64_t *bar, unsigned parity, Bars *b, unsigned whe
             }
         }
     }
+}
+// Both of two barriers; asked together, since an answer takes its time.
+__device__ __forceinline__ bool wait_both(uint64_t *x, unsigned px, uint64_t *y, unsigned py, Bars *b, unsigned where)
+{
+    const bool okx = lfk::mbar_try_wait(x, px), oky = lfk::mbar_try_wait(y, py);
+    return (okx || wait_phase(x, px, b, where)) && (oky || wait_phase(y, py, b, where + 50));
 }
 __device__ void settle_phase(uint64_t *bar, unsigned parity)
 {
@@ -258,7 +268,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return d;
 }
 
-// The two warps that share 32 rows (w and w + 4): OR of a predicate, and a barrier.
+// The two warps that share 32 rows (w and w + 4): OR of a predicate, a barrier, and the hand-over from one
+// group to the other (arrive by the one, sync by the other).
 __device__ __forceinline__ bool pair_or(int warp, bool pred)
 {
     unsigned r;
@@ -273,7 +284,33 @@ __device__ __forceinline__ bool pair_or(int warp, bool pred)
     return r != 0;
 }
 __device__ __forceinline__ void pair_sync(int warp) { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); }
+__device__ __forceinline__ void hand_over(int warp)
+{
+    asm volatile("bar.arrive %0, 64;" ::"r"(5 + (warp & 7)) : "memory");
+}
+__device__ __forceinline__ void take_over(int warp)
+{
+    asm volatile("bar.sync %0, 64;" ::"r"(5 + ((warp ^ 4) & 7)) : "memory");
+}
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 __device__ __forceinline__ void load64(uint32_t ts, uint32_t (&u)[2][32])
 {
     tmem_ld32(ts, u[0]);
@@ -281,15 +318,14 @@ __device__ __forceinline__ void load64(uint32_t ts, uint32_t (&u)[2][32])
     tmem_ld_wait();
 }
 
-// y = f s + neg of 64 scores (-inf outside columns lo .. hi - 1 unless WHOLE): their largest, the sum of 2^y, and
-// 2^y as FP16 pairs hw (SPLIT: and the remainders lw).
+// 2^(f s + neg) of 64 scores (0 outside columns lo .. hi - 1 unless WHOLE) as FP16 pairs hw (SPLIT: and the
+// remainders lw), and their sum.
 template <bool WHOLE, bool SPLIT>
-__device__ __forceinline__ float probs(const uint32_t (&u)[2][32], float f, float neg, int lo, int hi, float &sum,
-                                       uint32_t (&hw)[32], uint32_t (&lw)[32])
+__device__ __forceinline__ float probs(const uint32_t (&u)[2][32], float f, float neg, int lo, int hi, uint32_t (&hw)[32],
+                                       uint32_t (&lw)[32])
 {
     const uint64_t ff = pack2(f, f), nn = pack2(neg, neg);
     uint64_t acc[2] = {0ull, 0ull};
-    float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int e = 0; e < 64; e += 2) {
         float2 y = unpack2(fma2(pack2u(u[e / 32][e % 32], u[e / 32][e % 32 + 1]), ff, nn));
@@ -297,7 +333,6 @@ __device__ __forceinline__ float probs(const uint32_t (&u)[2][32], float f, floa
             if (e < lo || e >= hi) y.x = -INFINITY;
             if (e + 1 < lo || e + 1 >= hi) y.y = -INFINITY;
         }
-        m[e / 2 & 1] = fmaxf(m[e / 2 & 1], fmaxf(y.x, y.y));
         const float x0 = ex2(y.x), x1 = ex2(y.y);
         acc[e / 2 & 1] = add2(acc[e / 2 & 1], pack2(x0, x1));
         const __half2 h = __floats2half2_rn(x0, x1);
@@ -309,13 +344,11 @@ __device__ __forceinline__ float probs(const uint32_t (&u)[2][32], float f, floa
         }
     }
     const float2 t = unpack2(add2(acc[0], acc[1]));
-    sum = t.x + t.y;
-    return fmaxf(m[0], m[1]);
+    return t.x + t.y;
 }
-// The largest of 64 scores, of columns lo .. hi - 1.
-__device__ __forceinline__ float row_max(const uint32_t (&u)[2][32], int lo, int hi)
+// The largest of m and 64 scores of columns lo .. hi - 1.
+__device__ __forceinline__ float row_max(float m, const uint32_t (&u)[2][32], int lo, int hi)
 {
-    float m = -INFINITY;
 #pragma unroll
     for (int e = 0; e < 64; ++e)
         if (e >= lo && e < hi) m = fmaxf(m, __uint_as_float(u[e / 32][e % 32]));
@@ -347,11 +380,12 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
             lfk::mbar_init(&b->v_full[i], 4);
             lfk::mbar_init(&b->v_empty[i], 1);
             lfk::mbar_init(&b->s_full[i], 1);
+            lfk::mbar_init(&b->s_free[i], SPLIT ? 5 : 4);
+            lfk::mbar_init(&b->drained[i], 1);
+            lfk::mbar_init(&b->pv_done[i], 1);
         }
-        lfk::mbar_init(&b->p_full, NSM / 32);
-        lfk::mbar_init(&b->pv_done, 1);
+        lfk::mbar_init(&b->p_full, 4);
         lfk::mbar_init(&b->q_ready, NSM / 32);
-        lfk::mbar_init(&b->drained, 1);
         b->abort = 0;
         lfk::mbar_fence_init();
     }
@@ -374,16 +408,19 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
 
     if (warp >= W_MMA) {
         setmaxnreg_dec<REG_MMA>();
+        // One warp issues the S products, another the P V products: a wait takes as long as a third of a product
+        // even when what it waits for is there.  Each warp walks its loop with uniform values; one elected lane
+        // issues.
+        const bool one = elect_one();
+        const uint32_t sb = lfk::smem_u32(smem);
         if (warp == W_MMA && nc > 0 && !dead) {
-            // The whole warp walks the loop with uniform values; one elected lane issues.
-            const bool one = elect_one();
-            const uint32_t sb = lfk::smem_u32(smem);
-            const uint64_t kd = sdesc_kmajor_sw128(sb + C::OFF_K), vd = sdesc_mn_sw128(sb + C::OFF_V, C::ATOM);
-            const uint32_t klo = (uint32_t)kd, vlo = (uint32_t)vd, khi = (uint32_t)(kd >> 32), vhi = (uint32_t)(vd >> 32);
+            const uint64_t kd = sdesc_kmajor_sw128(sb + C::OFF_K);
+            const uint32_t klo = (uint32_t)kd, khi = (uint32_t)(kd >> 32);
             const uint32_t qlo = (uint32_t)sdesc_kmajor_sw128(sb + C::OFF_Q);
-            auto issue_s = [&](int i, auto stage) -> bool {
+            auto step = [&](int i, auto stage) -> bool {
                 constexpr uint32_t S = decltype(stage)::value, D = tmem + S * BN;
-                if (!__all_sync(0xffffffffu, wait_phase(&b->k_full[S], (unsigned)(i >> 1) & 1u, b, 701))) return false;
+                const unsigned ph = (unsigned)(i >> 1) & 1u;
+                if (!__all_sync(0xffffffffu, wait_both(&b->s_free[S], ph ^ 1u, &b->k_full[S], ph, b, 701))) return false;
                 fence_after_sync();
                 if (one) {
                     unroll<HD / 16>([&](auto kc) {
@@ -402,10 +439,17 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
                 __syncwarp();
                 return true;
             };
+            if (__all_sync(0xffffffffu, wait_phase(&b->q_ready, 0u, b, 700)))
+                for (int i = 0; i < nc; i += 2) {
+                    if (!step(i, Int<0>{})) break;
+                    if (i + 1 < nc && !step(i + 1, Int<1>{})) break;
+                }
+        } else if (warp == W_MMA + 1 && nc > 0 && !dead) {
+            const uint64_t vd = sdesc_mn_sw128(sb + C::OFF_V, C::ATOM);
+            const uint32_t vlo = (uint32_t)vd, vhi = (uint32_t)(vd >> 32);
             auto step = [&](int i, auto stage) -> bool {
                 constexpr uint32_t S = decltype(stage)::value;
-                if (!__all_sync(0xffffffffu, wait_phase(&b->v_full[S], (unsigned)(i >> 1) & 1u, b, 702) &&
-                                                 wait_phase(&b->p_full, (unsigned)i & 1u, b, 703)))
+                if (!__all_sync(0xffffffffu, wait_both(&b->v_full[S], (unsigned)(i >> 1) & 1u, &b->p_full, (unsigned)i & 1u, b, 702)))
                     return false;
                 fence_after_sync();
                 if (one) {
@@ -417,18 +461,24 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
                             mma_ts<off>(tmem + C::T_O, tmem + C::T_P + BN / 2 + kk * 8u, vlo, vhi, id, 1u);
                     });
                     commit(&b->v_empty[S]);
-                    commit(&b->pv_done);
+                    commit(&b->pv_done[S]);
+                    // its scores are free with P (SPLIT): the next S goes behind this product, not before it
+                    if (SPLIT) lfk::mbar_arrive(&b->s_free[S]);
                 }
                 __syncwarp();
-                return i + 2 < nc ? issue_s(i + 2, stage) : true;   // p_full: the scores of chunk i were read
+                return true;
             };
-            if (__all_sync(0xffffffffu, wait_phase(&b->q_ready, 0u, b, 700)) && issue_s(0, Int<0>{}) &&
-                (nc < 2 || issue_s(1, Int<1>{})))
-                for (int i = 0; i < nc; i += 2) {
-                    if (!step(i, Int<0>{})) break;
-                    if (i + 1 < nc && !step(i + 1, Int<1>{})) break;
-                }
+            for (int i = 0; i < nc; i += 2) {
+                if (!step(i, Int<0>{})) break;
+                if (i + 1 < nc && !step(i + 1, Int<1>{})) break;
+            }
         }
+        // after a wait that ran out nothing may still write TMEM: one more commit by each of the lanes that issued
+        if (warp <= W_MMA + 1 && nc > 0 && !dead && one && *reinterpret_cast<volatile int *>(&b->abort)) {
+            commit(&b->drained[warp - W_MMA]);
+            settle_phase(&b->drained[warp - W_MMA], 0u);
+        }
+        __syncwarp();
     } else if (warp >= W_DQ) {
         // ---- dequantisation: one warpgroup takes K, the other V; thread j position j of every chunk
         setmaxnreg_dec<REG_DQ>();
@@ -461,8 +511,8 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
             if (i + 1 < nc && !step(i + 1, Int<1>{})) break;
         }
     } else {
-        // ---- softmax and output: thread (r, hf) takes positions 64 hf .. 64 hf + 63 of every chunk for row r,
-        // and half of its q and of its output
+        // ---- softmax and output: thread (r, hf) takes chunks hf, hf + 2, .. for row r, and half of its q and of
+        // its output
         setmaxnreg_inc<REG_SM>();
         const int hf = warp >> 2, r = (warp & 3) * 32 + lane;
         const bool live = r < rows;
@@ -538,74 +588,125 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         const int klo = key_lo(a.pos, tok, a.win), khi = min(key_hi(a.pos, tok, a.len), p1);
         float ref = -INFINITY, l = 0.f;
         bool run = true;
-        // (after a wait that ran out both warps of a pair leave at the same barrier: the pair_or below)
-        for (int i = 0; i < nc; ++i) {
-            run = __all_sync(0xffffffffu, run && wait_phase(&b->s_full[i & 1], (unsigned)(i >> 1) & 1u, b, 707));
+        for (int i = hf; i < nc; i += 2) {
+            run = __all_sync(0xffffffffu, run && !dead && wait_phase(&b->s_full[hf], (unsigned)(i >> 1) & 1u, b, 707));
             fence_after_sync();
-            const uint32_t ts = tl + (uint32_t)(i & 1) * BN + (uint32_t)(64 * hf);
-            const int key0 = p0 + i * BN + 64 * hf, lo = klo - key0, hi = khi - key0;
-            const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
-            uint32_t u[2][32], hw[32], lw[32];
-            float sum;
-            load64(ts, u);
-            float neg = ref == -INFINITY ? 0.f : -ref;
-            const float top = whole ? probs<true, SPLIT>(u, f, neg, 0, 64, sum, hw, lw)
-                                    : probs<false, SPLIT>(u, f, neg, lo, hi, sum, hw, lw);
-            // P out of range, or the row's first position: a new reference for both of its threads
-            if (pair_or(warp, !run || top > (ref == -INFINITY ? ref : TC_TOP))) {
-                if (pair_or(warp, !run)) {
-                    run = false;
-                    break;
-                }
+            const uint32_t ts = tl + (uint32_t)hf * BN;
+            const int key0 = p0 + i * BN, lo = klo - key0, hi = khi - key0;
+            const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= BN);
+            uint32_t u[2][32], hw[2][32], lw[32];
+            float sum = 0.f, now = -INFINITY;
+            // P of one half of the chunk; put: into its columns
+            auto half = [&](int h, float neg, auto all) {
+                constexpr bool WHOLE = decltype(all)::value != 0;
+                sum += probs<WHOLE, SPLIT>(u, f, neg, lo - 64 * h, hi - 64 * h, hw[h], lw);
+            };
+            auto put = [&](int h) {
+                tmem_st32(tl + C::T_P + (uint32_t)(32 * h), hw[h]);
+                if (SPLIT) tmem_st32(tl + C::T_P + BN / 2 + (uint32_t)(32 * h), lw);
+            };
+            // P's columns are free once the previous chunk's product has read them: FP16 P waits in registers
+            // for that until the chunk's end; head and remainder do not fit there, their first half waits midway.
+            // (One barrier per parity: this warp waited for PV(i - 3) in its chunk before, so that the phase it waits
+            // for now is PV(i - 1)'s and no earlier one.)
+            auto p_free = [&] {
+                if (i == 0) return;
+                run = __all_sync(0xffffffffu, run && wait_phase(&b->pv_done[hf ^ 1], (unsigned)((i - 1) >> 1) & 1u, b, 708));
+                fence_after_sync();
+            };
+            if (i == 1) {                                     // nothing known of the row yet: the first chunk's reference
+                take_over(warp);
+                ref = now = b->ref[r];
+            }
+            if (i > 0 && run) {
+                const float neg = ref == -INFINITY ? 0.f : -ref;
+                load64(ts + 64u, u);
+                if (whole) half(1, neg, Int<1>{});
+                else half(1, neg, Int<0>{});
                 load64(ts, u);
-                const float mx = row_max(u, lo, hi);
-                b->x[hf][r] = mx == -INFINITY ? mx : mx * f;
-                pair_sync(warp);
-                const float m = fmaxf(b->x[0][r], b->x[1][r]);
-                pair_sync(warp);
-                float alpha = 1.f;
-                if (m > ref && (ref == -INFINITY || m - ref > TC_TOP)) {
-                    float nref = m - TC_EXP;
-                    if (!(m - nref <= TC_TOP)) nref = m;      // scores so large that their steps are
-                    alpha = ex2(ref - nref);                  // 0 from -inf
-                    l *= alpha;
-                    ref = nref;
-                    neg = -ref;
+                if (SPLIT) {
+                    p_free();
+                    put(1);
                 }
-                if (i > 0) {
-                    run = __all_sync(0xffffffffu, wait_phase(&b->pv_done, (unsigned)(i - 1) & 1u, b, 708));
-                    fence_after_sync();
+                if (whole) half(0, neg, Int<1>{});
+                else half(0, neg, Int<0>{});
+                if (SPLIT) put(0);
+            }
+            // ---- the reference after the chunk before (the hand-over also runs after a failed wait)
+            if (i > 1) {
+                take_over(warp);
+                now = b->ref[r];
+            }
+            const bool again = now != ref || now == -INFINITY || !(sum <= TC_SUM);
+            if (run && __any_sync(0xffffffffu, again)) {
+                float m = -INFINITY, alpha = 1.f;
+                load64(ts + 64u, u);
+                m = row_max(m, u, lo - 64, hi - 64);
+                load64(ts, u);
+                m = row_max(m, u, lo, hi);
+                m = m == -INFINITY ? m : m * f;
+                const bool up = m > now && (now == -INFINITY || m - now > TC_EXP + 1.f);
+                if (up) {
+                    float n = m - TC_EXP;
+                    if (!(m - n <= 15.f)) n = m;              // scores so large that their steps are
+                    alpha = ex2(now - n);                     // 0 from -inf
+                    now = n;
+                }
+                if (i > 0 && __any_sync(0xffffffffu, up)) {
+                    if (!SPLIT) p_free();                     // and O holds every earlier product
 #pragma unroll 1
-                    for (int c = 0; c < HD / 64; ++c) {
-                        const uint32_t oc = tl + C::T_O + (uint32_t)(HD / 2 * hf + 32 * c);
-                        uint32_t o[32];
-                        tmem_ld32(oc, o);
+                    for (int c = 0; c < HD / 16; ++c) {
+                        const uint32_t oc = tl + C::T_O + (uint32_t)(16 * c);
+                        uint32_t o[16];
+                        tmem_ld16(oc, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st32(oc, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st16(oc, o);
                     }
-                    tmem_st_wait();
                 }
-                (void)probs<false, SPLIT>(u, f, neg, lo, hi, sum, hw, lw);
+                const float neg = now == -INFINITY ? 0.f : -now;
+                sum = 0.f;
+                half(0, neg, Int<0>{});
+                if (SPLIT) put(0);
+                load64(ts + 64u, u);
+                half(1, neg, Int<0>{});
+                if (SPLIT) put(1);
+            }
+            if (i + 1 < nc) {
+                b->ref[r] = now;
+                hand_over(warp);
+            }
+            if (now != ref) {                                 // moved since this thread's last chunk
+                l *= ex2(ref - now);
+                ref = now;
             }
             l += sum;
-            // P's columns are free once the previous chunk's product has read them
-            if (i > 0) {
-                run = __all_sync(0xffffffffu, run && wait_phase(&b->pv_done, (unsigned)(i - 1) & 1u, b, 709));
-                fence_after_sync();
+            if (!SPLIT) {
+                fence_before_sync();
+                warp_arrive(&b->s_free[hf], lane);            // the scores are read: the next product may replace them
+                p_free();
+                if (!run) continue;
+                put(1);
+                put(0);
             }
-            tmem_st32(tl + C::T_P + (uint32_t)(32 * hf), hw);
-            if (SPLIT) tmem_st32(tl + C::T_P + BN / 2 + (uint32_t)(32 * hf), lw);
+            if (!run) continue;
             tmem_st_wait();
             fence_before_sync();
+            if (SPLIT) warp_arrive(&b->s_free[hf], lane);
             warp_arrive(&b->p_full, lane);
         }
         // ---- output: O / l, or the partial state of a split
         if (run && nc > 0) {
-            run = __all_sync(0xffffffffu, wait_phase(&b->pv_done, (unsigned)(nc - 1) & 1u, b, 710));
+            run = __all_sync(0xffffffffu, wait_phase(&b->pv_done[(nc - 1) & 1], (unsigned)((nc - 1) >> 1) & 1u, b, 710));
             fence_after_sync();
         }
+        // the reference of the last chunk is its group's; the other group's sum follows it
+        if (nc > 0 && ((nc - 1) & 1) == hf) b->ref[r] = ref;
+        pair_sync(warp);
+        const float last = nc > 0 ? b->ref[r] : -INFINITY;
+        if (last != ref) l *= ex2(ref - last);
+        ref = last;
         b->x[hf][r] = l;
         if (!pair_or(warp, !run)) {
             l = b->x[0][r] + b->x[1][r];
@@ -641,11 +742,6 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
     fence_before_sync();
     __syncthreads();
     if (warp == W_MMA) {
-        if (b->abort && nc > 0 && elect_one()) {
-            // nothing may still write TMEM: one more commit, by the lane that issued them, covers every MMA
-            commit(&b->drained);
-            settle_phase(&b->drained, 0u);
-        }
         __syncwarp();
         fence_after_sync();
         tmem_dealloc(b->tmem, C::T_COLS);
