@@ -33,6 +33,8 @@ namespace lfq {
 template <class T>
 __global__ void __launch_bounds__(256) append_rows(Cache c, Rows k, Rows v, int n, int pos)
 {
+    dependents_may_launch();
+    wait_for_prerequisites();
     const int bpr = c.hd / 16;
     const Rows &in = blockIdx.y ? v : k;
     uint8_t *codes = blockIdx.y ? c.vc : c.kc, *scales = blockIdx.y ? c.vs : c.ks;
@@ -67,6 +69,8 @@ __global__ void __launch_bounds__(256) append_rows(Cache c, Rows k, Rows v, int 
 template <class T>
 __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n, int pos)
 {
+    dependents_may_launch();
+    wait_for_prerequisites();
     const int bpr = c.hd / 16;
     const Rows &out = blockIdx.y ? v : k;
     const uint8_t *codes = blockIdx.y ? c.vc : c.kc, *scales = blockIdx.y ? c.vs : c.ks;
@@ -107,27 +111,64 @@ __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n,
 // and 2 more for i + 8, the same in both products, so that the scores become
 // the second product's operand by one 8x8 transpose in registers.
 //
-// The softmax is online: per chunk of 16 SL positions the running reference m
-// (the largest score less P_EXP, so that the largest P is 2^P_EXP) and sum l of
-// a row in FP32, exponentials to base 2.  P is rounded to FP16: relative error
+// The softmax is online, FP32, exponentials to base 2.  P is taken relative to a
+// reference of the row, and no maximum is formed on the common path: a lane whose
+// P sum to at most 2^15 has none that FP16 could not hold.  Otherwise, and at a
+// row's first position, the maximum over the chunk is taken, the reference put
+// 2^P_EXP below it and O and l rescaled.  P is rounded to FP16: relative error
 // 2^-11, below that of a half-precision output, down to 2^-(14 + P_EXP) of the
 // row's largest, where FP16 runs out of exponents.  With FP32 queries (SPLIT) q
 // and P are split into an FP16 head and remainder and the products are formed
 // twice, which leaves errors near 2^-22.
+//
+// What bounds it: instructions.  A cached value costs a conversion and a multiply
+// by its scale per pair, and its share of the product; everything else is kept off
+// the loop (addresses advance by constants, no maximum, no rescaling).
+__device__ __forceinline__ void add_scaled(float4 &acc, const float4 &v, float x)
+{
+    acc.x = fmaf(v.x, x, acc.x);
+    acc.y = fmaf(v.y, x, acc.y);
+    acc.z = fmaf(v.z, x, acc.z);
+    acc.w = fmaf(v.w, x, acc.w);
+}
+// Partial softmax states (reference M, sum L, four of the row's outputs) added up, relative to the largest
+// reference so far: O = sum 2^(M_s - M) O_s, L likewise.
+struct Joined {
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void add(float2 ml, float4 v)
+    {
+        const float n = fmaxf(M, ml.x), m = n == -INFINITY ? 0.f : n;
+        const float x = ex2(M - m), y = ex2(ml.x - m);      // 0 from -inf
+        M = n;
+        L = fmaf(ml.y, y, L * x);
+        acc = make_float4(acc.x * x, acc.y * x, acc.z * x, acc.w * x);
+        add_scaled(acc, v, y);
+    }
+    // row = token * G + head of the group
+    __device__ __forceinline__ void store(const Attn &a, int row, int kvh, int d) const
+    {
+        const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);   // a row that saw nothing is 0; NaN stays
+        const int tt = row / a.G, hh = kvh * a.G + row % a.G;
+        store4(a.o, (size_t)tt * a.o.ts + (size_t)hh * a.o.hs + d, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    }
+};
+
 template <int HD, int NT, bool SPLIT>
 struct RowCfg {
     static constexpr int NW = 8;                       // warps
     static constexpr int RT = 8 * NT;                  // query rows
     static constexpr int KS = HD / 16;                 // k-steps of S, m-tiles of O
     static constexpr int QW = SPLIT ? 4 : 2;           // words per q fragment
-    static constexpr int SMEM = NT * KS * 32 * QW * 4 + (2 * NW + 1) * RT * 4 + NW * RT * HD * 4;
+    static constexpr int SMEM = NT * KS * 32 * QW * 4 + (2 * NW + 1) * RT * 4 + NW * RT * HD * 4 +
+                                RT * (HD + PAD) * 4;
 };
-constexpr float P_EXP = 11.f;
+constexpr float P_EXP = 7.f, P_SUM = 32768.f;
 constexpr int SL = 2;                                  // 16-position slabs per softmax step
 constexpr int CH = 16 * SL;
 
 template <int HD, int NT, bool SPLIT>
-__global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
+__global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_constant__ Attn a)
 {
     using C = RowCfg<HD, NT, SPLIT>;
     constexpr int NW = C::NW, RT = C::RT, KS = C::KS;
@@ -136,85 +177,116 @@ __global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
     float *rs = reinterpret_cast<float *>(qf + NT * KS * 32 * C::QW);   // [RT] score factor of a row
     float *wm = rs + RT, *wl = wm + NW * RT;                            // [NW][RT]
     float *wo = wl + NW * RT;                                           // [NW][RT][HD]
+    float *cs = wo + NW * RT * HD;                                      // [RT][HD + PAD] the CTA's state, for its cluster
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int kvh = blockIdx.y, split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
     const int r0 = tile * RT, rows = min(RT, a.n * a.G - r0);
+    dependents_may_launch();
+    wait_for_prerequisites();                            // the rows appended just before, q
 
     // ---- q: row r as an FP16 B operand, scaled by a power of two for BF16 and FP32 (their
-    // range is wider than FP16's), which the row's score factor takes back
-    for (int r = warp; r < RT; r += NW) {
-        float x[HD / 32];
-        const int tt = (r0 + r) / a.G, hh = kvh * a.G + (r0 + r) % a.G;
-        const bool live = r < rows;
-        load_q<HD>(a.q, live, tt, hh, lane, x);
-        float f = 1.f;
-        if (a.q.dtype != F16) f = range_factor(warp_amax<HD / 32>(x));
-        if (lane == 0) rs[r] = a.scale * 1.4426950408889634f / f;
-        // dims HD/32 lane ..: element d of the row belongs to lane t = d / (HD/4), k-step (d % (HD/4)) / 4
-#pragma unroll
-        for (int j = 0; j < HD / 32; j += 2) {
-            const int d = lane * (HD / 32) + j, qt = d / (HD / 4), k = d % (HD / 4) / 4, w = d % 4 / 2;
-            unsigned *dst = qf + (((r / 8) * KS + k) * 32 + (r % 8) * 4 + qt) * C::QW;
-            __half h0, m0, h1, m1;
-            lfk::split_h(x[j] * f, h0, m0);
-            lfk::split_h(x[j + 1] * f, h1, m1);
-            dst[w] = lfk::pack_h2(h0, h1);
-            if (SPLIT) dst[2 + w] = lfk::pack_h2(m0, m1);
-        }
-    }
-    __syncthreads();
-
-    // ---- this lane's rows 2t, 2t+1 of each n-tile: visible keys and score factors
+    // range is wider than FP16's), which the row's score factor takes back; then this lane's rows 2t, 2t + 1 of
+    // each n-tile: visible keys and score factors
     int khi[NT][2], klo[NT][2];
     float f[NT][2];
+    auto prepare_q = [&] {
+        for (int r = warp; r < RT; r += NW) {
+            float x[HD / 32];
+            const int tt = (r0 + r) / a.G, hh = kvh * a.G + (r0 + r) % a.G;
+            const bool live = r < rows;
+            load_q<HD>(a.q, live, tt, hh, lane, x);
+            float f = 1.f;
+            if (a.q.dtype != F16) f = range_factor(warp_amax<HD / 32>(x));
+            if (lane == 0) rs[r] = a.scale * 1.4426950408889634f / f;
+            // dims HD/32 lane ..: element d of the row belongs to lane t = d / (HD/4), k-step (d % (HD/4)) / 4
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 8 * i + 2 * t + e, tt = (r0 + min(r, rows - 1)) / a.G;
-            khi[i][e] = key_hi(a.pos, tt, a.len);
-            klo[i][e] = key_lo(a.pos, tt, a.win);
-            f[i][e] = rs[r];
+            for (int j = 0; j < HD / 32; j += 2) {
+                const int d = lane * (HD / 32) + j, qt = d / (HD / 4), k = d % (HD / 4) / 4, w = d % 4 / 2;
+                unsigned *dst = qf + (((r / 8) * KS + k) * 32 + (r % 8) * 4 + qt) * C::QW;
+                __half h0, m0, h1, m1;
+                lfk::split_h(x[j] * f, h0, m0);
+                lfk::split_h(x[j + 1] * f, h1, m1);
+                dst[w] = lfk::pack_h2(h0, h1);
+                if (SPLIT) dst[2 + w] = lfk::pack_h2(m0, m1);
+            }
         }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * i + 2 * t + e, tt = (r0 + min(r, rows - 1)) / a.G;
+                khi[i][e] = key_hi(a.pos, tt, a.len);
+                klo[i][e] = key_lo(a.pos, tt, a.win);
+                f[i][e] = rs[r];
+            }
+    };
     // positions of this CTA: the split's, cut to what the tile's rows see
     const int t_first = r0 / a.G, t_last = (r0 + rows - 1) / a.G;
     const int lo_t = key_lo(a.pos, t_first, a.win), hi_r = key_hi(a.pos, t_last, a.len);
     const int hi_t = hi_r > lo_t ? hi_r : 0;              // no position at all: an empty range
     const int p0 = max(a.lo + split * a.per, lo_t / CH * CH), p1 = min(a.lo + (split + 1) * a.per, hi_t);
     // inside [all_lo, all_hi) every row sees every position
-    const int all_lo = key_lo(a.pos, t_last, a.win), all_hi = key_hi(a.pos, t_first, a.len);
+    const int all_lo = key_lo(a.pos, t_last, a.win), all_hi = min(key_hi(a.pos, t_first, a.len), p1);
 
-    float m[NT][2], l[NT][2], o[NT][KS][4];
+    float ref[NT][2], l[NT][2], o[NT][KS][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        m[i][0] = m[i][1] = -INFINITY;
+        ref[i][0] = ref[i][1] = -INFINITY;
         l[i][0] = l[i][1] = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) o[i][k][0] = o[i][k][1] = o[i][k][2] = o[i][k][3] = 0.f;
     }
-    const size_t row0 = (size_t)kvh * a.c.cap;
-    const uint8_t *kc = a.c.kc + row0 * code_bytes(HD) + t * (HD / 8);
-    const uint8_t *ks = a.c.ks + row0 * scale_bytes(HD) + t * (HD / 64);
-    const uint8_t *vc = a.c.vc + row0 * code_bytes(HD) + g * (HD / 16);
-    const uint8_t *vs = a.c.vs + row0 * scale_bytes(HD) + g * (HD / 16) / 8;
+    // this lane's bytes of position 0 of the chunk in hand; they advance by whole chunks
     const int sg = 4 * (g >> 1) + (g & 1);                 // slab position of rows g (and + 2: of g + 8)
+    const size_t first = (size_t)kvh * a.c.cap + (size_t)(p0 + warp * CH);
+    const uint8_t *kc = a.c.kc + first * code_bytes(HD) + t * (HD / 8);
+    const uint8_t *ks = a.c.ks + first * scale_bytes(HD) + t * (HD / 64);
+    const uint8_t *vc = a.c.vc + first * code_bytes(HD) + g * (HD / 16);
+    const uint8_t *vs = a.c.vs + first * scale_bytes(HD) + g * (HD / 16) / 8;
 
-    for (int p = p0 + warp * CH; p < p1; p += NW * CH) {
-        KRaw<HD> kr[SL][2];
-        VRaw<HD> vr[SL][4];
+    // K of the next chunk is fetched once the scores have used this one's, V after its product: loads are in
+    // flight all the time and no register holds two chunks
+    KRaw<HD> kr[SL][2];
+    VRaw<HD> vr[SL][4];
+    // rows of the chunk at p that may be read; others become the nearest of those, masked below
+    auto fetch_k = [&](int p) {
+        auto load = [&](auto row) {
 #pragma unroll
-        for (int s = 0; s < SL; ++s) {
+            for (int s = 0; s < SL; ++s)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const size_t r = (size_t)max(min(p + 16 * s + sg + 2 * e, p1 - 1), lo_t);   // outside: a seen row, masked below
-                kr[s][e].load(kc + r * code_bytes(HD), ks + r * scale_bytes(HD));
-            }
+                for (int e = 0; e < 2; ++e) {
+                    const int r = row(16 * s + sg + 2 * e);
+                    kr[s][e].load(kc + r * code_bytes(HD), ks + r * scale_bytes(HD));
+                }
+        };
+        if (p >= lo_t && p + CH <= p1) load([](int r) { return r; });
+        else load([&](int r) { return max(min(r, p1 - 1 - p), lo_t - p); });
+        kc += (size_t)NW * CH * code_bytes(HD);
+        ks += (size_t)NW * CH * scale_bytes(HD);
+    };
+    auto fetch_v = [&](int p) {
+        auto load = [&](auto row) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const size_t r = (size_t)max(min(p + 16 * s + 4 * t + e, p1 - 1), lo_t);
-                vr[s][e].load(vc + r * code_bytes(HD), vs + r * scale_bytes(HD));
-            }
-        }
+            for (int s = 0; s < SL; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = row(16 * s + 4 * t + e);
+                    vr[s][e].load(vc + r * code_bytes(HD), vs + r * scale_bytes(HD));
+                }
+        };
+        if (p >= lo_t && p + CH <= p1) load([](int r) { return r; });
+        else load([&](int r) { return max(min(r, p1 - 1 - p), lo_t - p); });
+        vc += (size_t)NW * CH * code_bytes(HD);
+        vs += (size_t)NW * CH * scale_bytes(HD);
+    };
+    int p = p0 + warp * CH;
+    if (p < p1) {
+        fetch_k(p);
+        fetch_v(p);
+    }
+    prepare_q();
+    for (; p < p1; p += NW * CH) {
         // ---- scores
         float st[SL][NT][4];
 #pragma unroll
@@ -239,60 +311,85 @@ __global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
                     }
                 }
         }
-        // ---- scale, mask, running maximum
-        const bool whole = p >= all_lo && p + CH <= min(all_hi, p1);
+        if (p + NW * CH < p1) fetch_k(p + NW * CH);
+        // ---- P relative to the reference, and the lanes' sums
+        const bool whole = p >= all_lo && p + CH <= all_hi;
+        float pr[SL][NT][4], sum[NT][2];
+        auto probs = [&] {
+            bool bad = false;
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = -INFINITY;
+                for (int e = 0; e < 2; ++e) {
+                    const float neg = ref[i][e] == -INFINITY ? 0.f : -ref[i][e];
+                    sum[i][e] = 0.f;
 #pragma unroll
-                for (int s = 0; s < SL; ++s)
+                    for (int s = 0; s < SL; ++s)
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float &x = st[s][i][2 * u + e];
-                        x *= f[i][e];
-                        const int key = p + 16 * s + sg + 2 * u;
-                        if (!whole && !(key >= klo[i][e] && key < min(khi[i][e], p1))) x = -INFINITY;
-                        mx = fmaxf(mx, x);
-                    }
-#pragma unroll
-                for (int sh = 4; sh <= 16; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-                float mn = mx - P_EXP;
-                if (mx - mn > 15.f) mn = mx;               // scores so large that their steps are
-                mn = fmaxf(m[i][e], mn);
-                const float ref = mn == -INFINITY ? 0.f : mn;
-                const float alpha = ex2(m[i][e] - ref);    // 0 while nothing was seen
-                m[i][e] = mn;
-                float sum = 0.f;
-#pragma unroll
-                for (int s = 0; s < SL; ++s)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float &x = st[s][i][2 * u + e];
-                        x = ex2(x - ref);
-                        sum += x;
-                    }
-                l[i][e] = fmaf(l[i][e], alpha, sum);
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    o[i][k][e] *= alpha;
-                    o[i][k][2 + e] *= alpha;
+                        for (int u = 0; u < 2; ++u) {
+                            float x = ex2(fmaf(st[s][i][2 * u + e], f[i][e], neg));
+                            const int key = p + 16 * s + sg + 2 * u;
+                            if (!whole && !(key >= klo[i][e] && key < min(khi[i][e], p1))) x = 0.f;
+                            pr[s][i][2 * u + e] = x;
+                            sum[i][e] += x;
+                        }
+                    bad = bad || !(sum[i][e] <= P_SUM) || ref[i][e] == -INFINITY;
                 }
-            }
+            return bad;
+        };
+        if (__any_sync(0xffffffffu, probs())) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int s = 0; s < SL; ++s)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int key = p + 16 * s + sg + 2 * u;
+                            if (whole || (key >= klo[i][e] && key < min(khi[i][e], p1)))
+                                mx = fmaxf(mx, st[s][i][2 * u + e] * f[i][e]);
+                        }
+#pragma unroll
+                    for (int sh = 4; sh <= 16; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                    float &r = ref[i][e];
+                    if (mx > r && (r == -INFINITY || mx - r > P_EXP + 1.f)) {
+                        float n = mx - P_EXP;
+                        if (!(mx - n <= 15.f)) n = mx;     // scores so large that their steps are
+                        const float alpha = ex2(r - n);    // 0 from -inf
+                        l[i][e] *= alpha;
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            o[i][k][e] *= alpha;
+                            o[i][k][2 + e] *= alpha;
+                        }
+                        r = n;
+                    }
+                }
+            probs();
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            l[i][0] += sum[i][0];
+            l[i][1] += sum[i][1];
+        }
         // ---- O^T += V^T P^T
 #pragma unroll
         for (int s = 0; s < SL; ++s) {
-            unsigned pb[NT][2], pr[NT][2];
+            unsigned pb[NT][2], pm[NT][2];
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    __half h0, m0, h1, m1;
-                    lfk::split_h(st[s][i][2 * u], h0, m0);
-                    lfk::split_h(st[s][i][2 * u + 1], h1, m1);
-                    pb[i][u] = lfk::movm_t(lfk::pack_h2(h0, h1));
-                    if (SPLIT) pr[i][u] = lfk::movm_t(lfk::pack_h2(m0, m1));
+                    const float x = pr[s][i][2 * u], y = pr[s][i][2 * u + 1];
+                    const __half2 h = __floats2half2_rn(x, y);
+                    pb[i][u] = lfk::movm_t(*reinterpret_cast<const unsigned *>(&h));
+                    if (SPLIT) {
+                        const float2 b = __half22float2(h);
+                        const __half2 r = __floats2half2_rn(x - b.x, y - b.y);
+                        pm[i][u] = lfk::movm_t(*reinterpret_cast<const unsigned *>(&r));
+                    }
                 }
             unsigned va[KS][2], vb[KS][2];                 // positions 4t, 4t+1 and 4t+2, 4t+3
             weave<HD>(vr[s][0], vr[s][1], va);
@@ -302,9 +399,10 @@ __global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     lfk::mma16816(o[i][k], va[k][0], va[k][1], vb[k][0], vb[k][1], pb[i][0], pb[i][1]);
-                    if (SPLIT) lfk::mma16816(o[i][k], va[k][0], va[k][1], vb[k][0], vb[k][1], pr[i][0], pr[i][1]);
+                    if (SPLIT) lfk::mma16816(o[i][k], va[k][0], va[k][1], vb[k][0], vb[k][1], pm[i][0], pm[i][1]);
                 }
         }
+        if (p + NW * CH < p1) fetch_v(p + NW * CH);
     }
 
     // ---- the warps' states, joined: O = sum 2^(m_w - M) O_w over l likewise
@@ -317,7 +415,7 @@ __global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
 #pragma unroll
             for (int sh = 4; sh <= 16; sh <<= 1) s += __shfl_xor_sync(0xffffffffu, s, sh);
             if (g == 0) {
-                wm[warp * RT + r] = m[i][e];
+                wm[warp * RT + r] = ref[i][e];
                 wl[warp * RT + r] = s;
             }
             float *dst = wo + ((size_t)warp * RT + r) * HD + g * (HD / 8);
@@ -328,67 +426,95 @@ __global__ void __launch_bounds__(256) attn_rows(const __grid_constant__ Attn a)
             }
         }
     __syncthreads();
+    // joined state of (row r, dims d ..): the CTA's, then over the splits
+    auto state = [&](int r, int d, float &M, float &L, float4 &acc) {
+        M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * RT + r]);
+        const float m = M == -INFINITY ? 0.f : M;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float x = ex2(wm[w * RT + r] - m);
+            L = fmaf(wl[w * RT + r], x, L);
+            add_scaled(acc, *reinterpret_cast<const float4 *>(wo + ((size_t)w * RT + r) * HD + d), x);
+        }
+    };
+    if (a.splits > 1 && !a.part) {
+        // the splits are one cluster: each CTA leaves its state in its shared memory and joins its share of the rows
+        for (int i = threadIdx.x; i < rows * (HD / 4); i += NW * 32) {
+            const int r = i / (HD / 4), d = i % (HD / 4) * 4;
+            float M, L;
+            float4 acc;
+            state(r, d, M, L, acc);
+            *reinterpret_cast<float4 *>(cs + r * (HD + PAD) + d) = acc;
+            if (d == 0) *reinterpret_cast<float2 *>(cs + r * (HD + PAD) + HD) = make_float2(M, L);
+        }
+        cluster_sync();
+        for (int i = split * NW * 32 + threadIdx.x; i < rows * (HD / 4); i += a.splits * NW * 32) {
+            const int r = i / (HD / 4), d = i % (HD / 4) * 4;
+            Joined j;
+            for (int s = 0; s < a.splits; ++s) {
+                const uint32_t base = cluster_smem(cs + r * (HD + PAD), s);
+                j.add(ld_cluster2(base + HD * 4), ld_cluster4(base + d * 4));
+            }
+            j.store(a, r0 + r, kvh, d);
+        }
+        cluster_sync();   // no CTA leaves while its state may be read
+        return;
+    }
     float *part = a.part ? a.part + ((size_t)(kvh * a.tiles + tile) * a.splits + split) * RT * (HD + PAD) : nullptr;
     for (int i = threadIdx.x; i < rows * (HD / 4); i += NW * 32) {
         const int r = i / (HD / 4), d = i % (HD / 4) * 4;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * RT + r]);
-        const float ref = M == -INFINITY ? 0.f : M;
-        float L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float x = ex2(wm[w * RT + r] - ref);
-            const float4 v = *reinterpret_cast<const float4 *>(wo + ((size_t)w * RT + r) * HD + d);
-            L = fmaf(wl[w * RT + r], x, L);
-            acc.x = fmaf(v.x, x, acc.x);
-            acc.y = fmaf(v.y, x, acc.y);
-            acc.z = fmaf(v.z, x, acc.z);
-            acc.w = fmaf(v.w, x, acc.w);
-        }
+        float M, L;
+        float4 acc;
+        state(r, d, M, L, acc);
         if (part) {
             *reinterpret_cast<float4 *>(part + (size_t)r * (HD + PAD) + d) = acc;
             if (d == 0) *reinterpret_cast<float2 *>(part + (size_t)r * (HD + PAD) + HD) = make_float2(M, L);
         } else {
-            const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);   // a row that saw nothing is 0; NaN stays
-            const int tt = (r0 + r) / a.G, hh = kvh * a.G + (r0 + r) % a.G;
-            store4(a.o, (size_t)tt * a.o.ts + (size_t)hh * a.o.hs + d, acc.x * inv, acc.y * inv, acc.z * inv,
-                   acc.w * inv);
+            Joined j;
+            j.add(make_float2(M, L), acc);
+            j.store(a, r0 + r, kvh, d);
         }
     }
 }
 
-// Joins the splits of a row: HD / 4 threads per query row and KV head.
-__global__ void __launch_bounds__(256) attn_join(const __grid_constant__ Attn a)
+// Joins the splits of a row: `groups` x hd / 4 threads per query row and KV head, each group taking every
+// groups-th split, then the groups through shared memory.
+constexpr int JOIN_THREADS = 256;
+__global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant__ Attn a, int groups)
 {
-    const int hd = a.c.hd, per = 1024 / hd;                 // rows per block
-    const int row = blockIdx.x * per + threadIdx.x / (hd / 4), kvh = blockIdx.y, d = threadIdx.x % (hd / 4) * 4;
-    if (row >= a.n * a.G) return;
-    const float *part = a.part + ((size_t)((size_t)kvh * a.tiles + row / a.rt) * a.splits * a.rt + row % a.rt) * (hd + PAD);
-    const size_t step = (size_t)a.rt * (hd + PAD);
-    float M = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, part[s * step + hd]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < a.splits; ++s) {
-        const float2 ml = *reinterpret_cast<const float2 *>(part + s * step + hd);
-        const float4 u = *reinterpret_cast<const float4 *>(part + s * step + d);
-        const float x = ex2(ml.x - ref);
-        L = fmaf(ml.y, x, L);
-        acc.x = fmaf(u.x, x, acc.x);
-        acc.y = fmaf(u.y, x, acc.y);
-        acc.z = fmaf(u.z, x, acc.z);
-        acc.w = fmaf(u.w, x, acc.w);
+    __shared__ float sh[JOIN_THREADS][6];
+    const int hd = a.c.hd, lanes = hd / 4, per = JOIN_THREADS / (lanes * groups);   // rows per block
+    const int row = blockIdx.x * per + threadIdx.x / (lanes * groups), kvh = blockIdx.y;
+    const int grp = threadIdx.x / lanes % groups, d = threadIdx.x % lanes * 4;
+    wait_for_prerequisites();
+    Joined j;
+    if (row < a.n * a.G) {
+        const size_t step = (size_t)a.rt * (hd + PAD);
+        const float *part = a.part + ((size_t)((size_t)kvh * a.tiles + row / a.rt) * a.splits * a.rt + row % a.rt) * (hd + PAD);
+#pragma unroll 4
+        for (int s = grp; s < a.splits; s += groups)
+            j.add(__ldcg(reinterpret_cast<const float2 *>(part + s * step + hd)),
+                  __ldcg(reinterpret_cast<const float4 *>(part + s * step + d)));
     }
-    const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);
-    const int tt = row / a.G, hh = kvh * a.G + row % a.G;
-    store4(a.o, (size_t)tt * a.o.ts + (size_t)hh * a.o.hs + d, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (groups > 1) {
+        float *x = sh[threadIdx.x];
+        x[0] = j.acc.x, x[1] = j.acc.y, x[2] = j.acc.z, x[3] = j.acc.w, x[4] = j.M, x[5] = j.L;
+        __syncthreads();
+        if (grp) return;
+        for (int g = 1; g < groups; ++g) {
+            const float *y = sh[threadIdx.x + g * lanes];
+            j.add(make_float2(y[4], y[5]), make_float4(y[0], y[1], y[2], y[3]));
+        }
+    }
+    if (row < a.n * a.G) j.store(a, row, kvh, d);
 }
 
 // ---------------------------------------------------------------- launches
 
+constexpr int kClusterChunks = 4;
 // Rows per KV head from which the tiles kernel takes over.
 constexpr int kTileRows = 33;
 
@@ -426,19 +552,22 @@ size_t plan_attn(Attn &a, int sms)
     a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
     if (rows >= kTileRows) {
         plan_tiles(a, sms, rows, hi);
-    } else {
-        a.rt = rows <= 8 ? 8 : 16;
-        a.tiles = (rows + a.rt - 1) / a.rt;
-        const int chunks = std::max(1, (hi - a.lo + CH - 1) / CH);
-        // one CTA per SM, each warp at least one chunk
-        const long long ctas = (long long)a.tiles * a.c.Hkv;
-        int splits = (int)std::max<long long>(1, sms / ctas);
-        splits = std::min(splits, (chunks + 7) / 8);
-        const int per = (chunks + splits - 1) / splits;
-        a.splits = (chunks + per - 1) / per;
-        a.per = per * CH;
+        return a.splits > 1 ? (size_t)a.c.Hkv * a.tiles * a.splits * a.rt * (a.c.hd + PAD) : 0;
     }
-    return a.splits > 1 ? (size_t)a.c.Hkv * a.tiles * a.splits * a.rt * (a.c.hd + PAD) : 0;
+    a.rt = rows <= 8 ? 8 : 16;
+    a.tiles = (rows + a.rt - 1) / a.rt;
+    const int chunks = std::max(1, (hi - a.lo + CH - 1) / CH);
+    // Each warp at least one chunk.  Up to kClusterChunks a warp, the splits of a row tile are one cluster of at
+    // most 8 CTAs, which joins them in its shared memory; beyond that every SM takes part (two CTAs each, one of 16
+    // rows), through the workspace and a second launch.
+    int splits = (chunks + 7) / 8;
+    const bool cluster = chunks <= 8 * 8 * kClusterChunks;
+    if (cluster) splits = std::min(splits, 8);
+    else splits = (int)std::min<long long>(splits, std::max<long long>(1, (a.rt == 8 ? 2 : 1) * sms / ((long long)a.tiles * a.c.Hkv)));
+    const int per = (chunks + splits - 1) / splits;
+    a.splits = (chunks + per - 1) / per;
+    a.per = per * CH;
+    return a.splits > 1 && !cluster ? (size_t)a.c.Hkv * a.tiles * a.splits * a.rt * (a.c.hd + PAD) : 0;
 }
 
 template <template <class> class F, class... A>
@@ -455,20 +584,38 @@ static dim3 block_grid(const Cache &c, int n)
 {
     return dim3((unsigned)(((long long)n * c.Hkv * (c.hd / 16) + 255) / 256), 2);
 }
+// A launch as a programmatic dependent of the previous kernel on the stream (it waits for that kernel's end before
+// any access to global memory), in clusters of `cluster` CTAs along x.
+template <class... P, class... A>
+static cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t s, const A &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 template <class T>
 struct RunAppend {
     static cudaError_t run(Cache c, Rows k, Rows v, int n, int pos, cudaStream_t s)
     {
-        append_rows<T><<<block_grid(c, n), 256, 0, s>>>(c, k, v, n, pos);
-        return cudaGetLastError();
+        return launch(append_rows<T>, block_grid(c, n), 256, 0, 1, s, c, k, v, n, pos);
     }
 };
 template <class T>
 struct RunRead {
     static cudaError_t run(Cache c, Rows k, Rows v, int n, int pos, cudaStream_t s)
     {
-        read_rows<T><<<block_grid(c, n), 256, 0, s>>>(c, k, v, n, pos);
-        return cudaGetLastError();
+        return launch(read_rows<T>, block_grid(c, n), 256, 0, 1, s, c, k, v, n, pos);
     }
 };
 cudaError_t launch_append(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s)
@@ -493,8 +640,8 @@ static cudaError_t run_rows(const Attn &a, cudaStream_t s)
         if (e != cudaSuccess) return e;
         if (dev < 64) ready[dev] = true;
     }
-    attn_rows<HD, NT, SPLIT><<<dim3((unsigned)(a.tiles * a.splits), (unsigned)a.c.Hkv), 256, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch(attn_rows<HD, NT, SPLIT>, dim3((unsigned)(a.tiles * a.splits), (unsigned)a.c.Hkv), 256, smem,
+                  a.part ? 1 : a.splits, s, a);
 }
 
 cudaError_t launch_attn(const Attn &a, cudaStream_t s)
@@ -509,10 +656,12 @@ cudaError_t launch_attn(const Attn &a, cudaStream_t s)
     else
         e = a.rt == 8 ? (split ? run_rows<64, 1, true>(a, s) : run_rows<64, 1, false>(a, s))
                       : (split ? run_rows<64, 2, true>(a, s) : run_rows<64, 2, false>(a, s));
-    if (e == cudaSuccess && a.splits > 1) {
-        const int per = 1024 / a.c.hd;
-        attn_join<<<dim3((unsigned)((a.n * a.G + per - 1) / per), (unsigned)a.c.Hkv), 256, 0, s>>>(a);
-        e = cudaGetLastError();
+    if (e == cudaSuccess && a.splits > 1 && a.part) {
+        // few rows: the splits of a row are spread over a whole block; many: one group each, the traffic counts
+        const int lanes = a.c.hd / 4, rows = a.n * a.G;
+        const int groups = (long long)rows * a.c.Hkv >= 4096 ? 1 : JOIN_THREADS / lanes;
+        const int per = JOIN_THREADS / (lanes * groups);
+        e = launch(attn_join, dim3((unsigned)((rows + per - 1) / per), (unsigned)a.c.Hkv), JOIN_THREADS, 0, 1, s, a, groups);
     }
     return e;
 }

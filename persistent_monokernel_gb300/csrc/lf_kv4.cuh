@@ -57,6 +57,34 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// ---- programmatic dependent launches: the next kernel may start its prologue; wait for the previous one's end
+__device__ __forceinline__ void dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ---- clusters: a barrier, and loads from another CTA's shared memory
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_smem(const void *p, int rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(lfk::smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
+}
+
 // ---- rows by element type: 16 consecutive values (16-byte aligned)
 template <class T>
 __device__ __forceinline__ void load16(const T *p, float (&x)[16]);
@@ -206,15 +234,17 @@ struct KRaw<128> {
     __device__ __forceinline__ void values(unsigned (&v)[8][2]) const
     {
         const unsigned w[4] = {c.x, c.y, c.z, c.w};
-        const unsigned s0 = e4m3_h2_same(s & 255u), s1 = e4m3_h2_same(s >> 8);
+        const unsigned sc2 = e4m3x2_h2(s);
+        const __half2 sh = *reinterpret_cast<const __half2 *>(&sc2);
+        const __half2 s0 = __low2half2(sh), s1 = __high2half2(sh);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             e2m1x8_h2(w[j], v[2 * j][0], v[2 * j][1], v[2 * j + 1][0], v[2 * j + 1][1]);
-            const unsigned sc = j < 2 ? s0 : s1;
+            const __half2 sc = j < 2 ? s0 : s1;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                v[2 * j + u][0] = hmul2(v[2 * j + u][0], sc);
-                v[2 * j + u][1] = hmul2(v[2 * j + u][1], sc);
+            for (int u = 0; u < 4; ++u) {
+                const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&v[2 * j + u / 2][u % 2]), sc);
+                v[2 * j + u / 2][u % 2] = *reinterpret_cast<const unsigned *>(&x);
             }
         }
     }

@@ -37,7 +37,7 @@ struct Attn {
     // plan: row tiles of rt query rows (n * G rows per KV head, row r = token r / G,
     // head r % G), each over `splits` ranges of `per` positions from lo on
     int rt, tiles, splits, per, lo;
-    float *part;            // [Hkv * tiles * splits][rt][hd + PAD]: O, then m and l; splits > 1
+    float *part;            // [Hkv * tiles * splits][rt][hd + PAD]: O, then m and l; null: one split, or one cluster
 };
 
 // Keys that query row t (position pos + t) sees: [key_lo, key_hi).

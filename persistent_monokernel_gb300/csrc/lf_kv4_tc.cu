@@ -399,6 +399,8 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
     // All 512 columns are this CTA's, so the allocation starts at column 0: constant addresses keep the MMA
     // warp's operands out of the vector registers.  (Anything else would be a broken allocation: nothing runs.)
     constexpr uint32_t tmem = 0;
+    dependents_may_launch();
+    wait_for_prerequisites();
     if (threadIdx.x == 0 && b->tmem != 0u) {
         b->abort = 1;
         if (atomicCAS(g_status, 0u, (unsigned)lfk::STATUS_TIMEOUT) == 0u) g_status[1] = 711;
@@ -767,9 +769,17 @@ static cudaError_t run_tiles(const Attn &a, cudaStream_t s)
         if (e != cudaSuccess) return e;
         if (dev < 64) ready[dev] = true;
     }
-    attn_tiles<HD, SPLIT>
-        <<<dim3((unsigned)(a.tiles * a.splits), (unsigned)a.c.Hkv), NTHR, smem, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.tiles * a.splits), (unsigned)a.c.Hkv);
+    cfg.blockDim = dim3(NTHR);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_tiles<HD, SPLIT>, a);
 }
 
 cudaError_t launch_attn_tiles(const Attn &a, cudaStream_t s)
