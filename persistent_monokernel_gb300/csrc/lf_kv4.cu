@@ -245,48 +245,32 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
     const uint8_t *vc = a.c.vc + first * code_bytes(HD) + g * (HD / 16);
     const uint8_t *vs = a.c.vs + first * scale_bytes(HD) + g * (HD / 16) / 8;
 
-    // K of the next chunk is fetched once the scores have used this one's, V after its product: loads are in
-    // flight all the time and no register holds two chunks
-    KRaw<HD> kr[SL][2];
-    VRaw<HD> vr[SL][4];
-    // rows of the chunk at p that may be read; others become the nearest of those, masked below
-    auto fetch_k = [&](int p) {
+    prepare_q();
+    for (int p = p0 + warp * CH; p < p1; p += NW * CH) {
+        KRaw<HD> kr[SL][2];
+        VRaw<HD> vr[SL][4];
+        // row: rows of the chunk that may be read; others become the nearest of those, masked below
         auto load = [&](auto row) {
 #pragma unroll
-            for (int s = 0; s < SL; ++s)
+            for (int s = 0; s < SL; ++s) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = row(16 * s + sg + 2 * e);
                     kr[s][e].load(kc + r * code_bytes(HD), ks + r * scale_bytes(HD));
                 }
-        };
-        if (p >= lo_t && p + CH <= p1) load([](int r) { return r; });
-        else load([&](int r) { return max(min(r, p1 - 1 - p), lo_t - p); });
-        kc += (size_t)NW * CH * code_bytes(HD);
-        ks += (size_t)NW * CH * scale_bytes(HD);
-    };
-    auto fetch_v = [&](int p) {
-        auto load = [&](auto row) {
-#pragma unroll
-            for (int s = 0; s < SL; ++s)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = row(16 * s + 4 * t + e);
                     vr[s][e].load(vc + r * code_bytes(HD), vs + r * scale_bytes(HD));
                 }
+            }
         };
         if (p >= lo_t && p + CH <= p1) load([](int r) { return r; });
         else load([&](int r) { return max(min(r, p1 - 1 - p), lo_t - p); });
+        kc += (size_t)NW * CH * code_bytes(HD);
+        ks += (size_t)NW * CH * scale_bytes(HD);
         vc += (size_t)NW * CH * code_bytes(HD);
         vs += (size_t)NW * CH * scale_bytes(HD);
-    };
-    int p = p0 + warp * CH;
-    if (p < p1) {
-        fetch_k(p);
-        fetch_v(p);
-    }
-    prepare_q();
-    for (; p < p1; p += NW * CH) {
         // ---- scores
         float st[SL][NT][4];
 #pragma unroll
@@ -311,7 +295,6 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
                     }
                 }
         }
-        if (p + NW * CH < p1) fetch_k(p + NW * CH);
         // ---- P relative to the reference, and the lanes' sums
         const bool whole = p >= all_lo && p + CH <= all_hi;
         float pr[SL][NT][4], sum[NT][2];
@@ -402,7 +385,6 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
                     if (SPLIT) lfk::mma16816(o[i][k], va[k][0], va[k][1], vb[k][0], vb[k][1], pm[i][0], pm[i][1]);
                 }
         }
-        if (p + NW * CH < p1) fetch_v(p + NW * CH);
     }
 
     // ---- the warps' states, joined: O = sum 2^(m_w - M) O_w over l likewise
