@@ -27,69 +27,80 @@ namespace lfq {
 
 // ---------------------------------------------------------------- append and read
 
-// One thread per block of 16 values.  Non-finite inputs: an infinity counts as
-// the largest finite value (the block then saturates), a NaN as 0, so that the
-// cache holds finite values only and a masked position can never reach a result.
+// One thread per block of 16 values, one grid row per KV head and K or V (no division finds a thread's row).
+// Non-finite inputs: an infinity counts as the largest finite value (the block then saturates), a NaN as 0, so
+// that the cache holds finite values only and a masked position can never reach a result.
+//
+// x / s decides which code is nearest, and only its side of a half-way value t counts.  With r = 1 / s rounded,
+// q = x r corrected once by its exact remainder x - q s is the quotient rounded to nearest, to about 2^-46 before
+// that rounding; and an FP32 x other than t s is at least mant(t) / mant(t s) >= 1 / 1.875 steps of t away from it
+// in the quotient, more than the half step that would round it to t.  So the codes are those of the exact quotient
+// (the same holds for A / 6 and the scales' half-way values).
 template <class T>
-__global__ void __launch_bounds__(256) append_rows(Cache c, Rows k, Rows v, int n, int pos)
+__global__ void __launch_bounds__(256) append_rows(Cache c, Rows k, Rows v, int n, int pos, int shift)
 {
     dependents_may_launch();
     wait_for_prerequisites();
-    const int bpr = c.hd / 16;
-    const Rows &in = blockIdx.y ? v : k;
-    uint8_t *codes = blockIdx.y ? c.vc : c.kc, *scales = blockIdx.y ? c.vs : c.ks;
-    const long long total = (long long)n * c.Hkv * bpr;
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= total) return;
-    const int b = (int)(i % bpr);
-    const long long r = i / bpr;
-    const int h = (int)(r % c.Hkv);
-    const long long t = r / c.Hkv;
+    const bool isv = blockIdx.y & 1;
+    const int h = blockIdx.y >> 1;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, t = i >> shift;   // 2^shift blocks per row
+    const int b = (int)(i & ((1 << shift) - 1));
+    if (t >= n) return;
+    const Rows &in = isv ? v : k;
     float x[16];
     load16<T>(static_cast<const T *>(in.p) + t * in.ts + h * in.hs + b * 16, x);
-    float amax = 0.f;
+    unsigned top = 0u;                                    // the largest magnitude's bits: NaN above infinity above all
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        x[j] = x[j] != x[j] ? 0.f : fminf(fmaxf(x[j], -3.402823466e38f), 3.402823466e38f);
-        amax = fmaxf(amax, fabsf(x[j]));
+    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+    if (top >= 0x7f800000u) {
+        top = 0u;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            x[j] = x[j] != x[j] ? 0.f : fminf(fmaxf(x[j], -3.402823466e38f), 3.402823466e38f);
+            top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+        }
     }
-    const unsigned s8 = __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f), __NV_SATFINITE, __NV_E4M3);
+    const unsigned s8 = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.0f), __NV_SATFINITE, __NV_E4M3);
     const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3)));
     unsigned w[2] = {0u, 0u};
     if (s > 0.f) {   // a block below E4M3's range (A < 6 * 2^-10) is stored as zeros
+        const float r = __frcp_rn(s);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w[j / 4] |= e2m1x2(__fdiv_rn(x[2 * j], s), __fdiv_rn(x[2 * j + 1], s)) << (8 * (j % 4));
+        for (int j = 0; j < 16; ++j) {
+            const float q = x[j] * r;
+            x[j] = fmaf(fmaf(-q, s, x[j]), r, q);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j / 4] |= e2m1x2(x[2 * j], x[2 * j + 1]) << (8 * (j % 4));
     }
     const size_t row = (size_t)h * c.cap + (size_t)pos + (size_t)t;
-    *reinterpret_cast<uint2 *>(codes + row * code_bytes(c.hd) + b * 8) = make_uint2(w[0], w[1]);
-    scales[row * scale_bytes(c.hd) + b] = (uint8_t)s8;
+    *reinterpret_cast<uint2 *>((isv ? c.vc : c.kc) + row * code_bytes(c.hd) + b * 8) = make_uint2(w[0], w[1]);
+    ((isv ? c.vs : c.ks) + row * scale_bytes(c.hd))[b] = (uint8_t)s8;
 }
 
+// One thread per 16 bytes of the output (8 values, 4 in FP32), so that a warp's stores are contiguous.
 template <class T>
-__global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n, int pos)
+__global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n, int pos, int shift)
 {
+    constexpr int N = 16 / sizeof(T);
     dependents_may_launch();
     wait_for_prerequisites();
-    const int bpr = c.hd / 16;
-    const Rows &out = blockIdx.y ? v : k;
-    const uint8_t *codes = blockIdx.y ? c.vc : c.kc, *scales = blockIdx.y ? c.vs : c.ks;
-    const long long total = (long long)n * c.Hkv * bpr;
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= total) return;
-    const int b = (int)(i % bpr);
-    const long long r = i / bpr;
-    const int h = (int)(r % c.Hkv);
-    const long long t = r / c.Hkv;
+    const bool isv = blockIdx.y & 1;
+    const int h = blockIdx.y >> 1;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, t = i >> shift;   // 2^shift threads per row
+    const int b = (int)(i & ((1 << shift) - 1));
+    if (t >= n) return;
     const size_t row = (size_t)h * c.cap + (size_t)pos + (size_t)t;
-    const uint2 w = *reinterpret_cast<const uint2 *>(codes + row * code_bytes(c.hd) + b * 8);
-    const unsigned s2 = e4m3_h2_same(scales[row * scale_bytes(c.hd) + b]);
-    unsigned hv[8];
-    e2m1x8_h2(w.x, hv[0], hv[1], hv[2], hv[3]);
-    e2m1x8_h2(w.y, hv[4], hv[5], hv[6], hv[7]);
+    const uint8_t *codes = (isv ? c.vc : c.kc) + row * code_bytes(c.hd) + b * (N / 2);
+    const unsigned w = N == 8 ? __ldg(reinterpret_cast<const unsigned *>(codes))
+                              : __ldg(reinterpret_cast<const unsigned short *>(codes));
+    const unsigned s2 = e4m3_h2_same(__ldg((isv ? c.vs : c.ks) + row * scale_bytes(c.hd) + b * N / 16));
+    unsigned hv[4];
+    e2m1x8_h2(w, hv[0], hv[1], hv[2], hv[3]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) hv[j] = hmul2(hv[j], s2);
-    store16<T>(static_cast<T *>(out.p) + t * out.ts + h * out.hs + b * 16, hv);
+    for (int j = 0; j < N / 2; ++j) hv[j] = hmul2(hv[j], s2);
+    const Rows &out = isv ? v : k;
+    store_values(static_cast<T *>(out.p) + t * out.ts + h * out.hs + b * N, hv);
 }
 
 // ---------------------------------------------------------------- attention, few rows
@@ -164,7 +175,7 @@ struct RowCfg {
                                 RT * (HD + PAD) * 4;
 };
 constexpr float P_EXP = 7.f, P_SUM = 32768.f;
-constexpr int SL = 2;                                  // 16-position slabs per softmax step
+constexpr int SL = 2;                                  // slabs of 16 positions per chunk
 constexpr int CH = 16 * SL;
 
 template <int HD, int NT, bool SPLIT>
@@ -225,7 +236,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
     const int t_first = r0 / a.G, t_last = (r0 + rows - 1) / a.G;
     const int lo_t = key_lo(a.pos, t_first, a.win), hi_r = key_hi(a.pos, t_last, a.len);
     const int hi_t = hi_r > lo_t ? hi_r : 0;              // no position at all: an empty range
-    const int p0 = max(a.lo + split * a.per, lo_t / CH * CH), p1 = min(a.lo + (split + 1) * a.per, hi_t);
+    const int p0 = max(a.lo + split * a.per, lo_t), p1 = min(a.lo + (split + 1) * a.per, hi_t);
     // inside [all_lo, all_hi) every row sees every position
     const int all_lo = key_lo(a.pos, t_last, a.win), all_hi = min(key_hi(a.pos, t_first, a.len), p1);
 
@@ -237,7 +248,6 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
 #pragma unroll
         for (int k = 0; k < KS; ++k) o[i][k][0] = o[i][k][1] = o[i][k][2] = o[i][k][3] = 0.f;
     }
-    // this lane's bytes of position 0 of the chunk in hand; they advance by whole chunks
     const int sg = 4 * (g >> 1) + (g & 1);                 // slab position of rows g (and + 2: of g + 8)
     const size_t first = (size_t)kvh * a.c.cap + (size_t)(p0 + warp * CH);
     const uint8_t *kc = a.c.kc + first * code_bytes(HD) + t * (HD / 8);
@@ -246,31 +256,36 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
     const uint8_t *vs = a.c.vs + first * scale_bytes(HD) + g * (HD / 16) / 8;
 
     prepare_q();
-    for (int p = p0 + warp * CH; p < p1; p += NW * CH) {
-        KRaw<HD> kr[SL][2];
-        VRaw<HD> vr[SL][4];
-        // row: rows of the chunk that may be read; others become the nearest of those, masked below
-        auto load = [&](auto row) {
+    // One chunk: SL slabs of 16 positions from p on.  Positions past the end read the last row that counts, and are
+    // masked.
+    struct Raw {
+        KRaw<HD> k[SL][2];
+        VRaw<HD> v[SL][4];
+    };
+    auto load = [&](Raw &w, int p) {
+        auto rows = [&](auto row) {
 #pragma unroll
             for (int s = 0; s < SL; ++s) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = row(16 * s + sg + 2 * e);
-                    kr[s][e].load(kc + r * code_bytes(HD), ks + r * scale_bytes(HD));
+                    w.k[s][e].load(kc + r * code_bytes(HD), ks + r * scale_bytes(HD));
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = row(16 * s + 4 * t + e);
-                    vr[s][e].load(vc + r * code_bytes(HD), vs + r * scale_bytes(HD));
+                    w.v[s][e].load(vc + r * code_bytes(HD), vs + r * scale_bytes(HD));
                 }
             }
         };
-        if (p >= lo_t && p + CH <= p1) load([](int r) { return r; });
-        else load([&](int r) { return max(min(r, p1 - 1 - p), lo_t - p); });
+        if (p + CH <= p1) rows([](int r) { return r; });
+        else rows([&](int r) { return min(r, p1 - 1 - p); });
         kc += (size_t)NW * CH * code_bytes(HD);
         ks += (size_t)NW * CH * scale_bytes(HD);
         vc += (size_t)NW * CH * code_bytes(HD);
         vs += (size_t)NW * CH * scale_bytes(HD);
+    };
+    auto chunk = [&](const Raw &w, int p) {
         // ---- scores
         float st[SL][NT][4];
 #pragma unroll
@@ -278,8 +293,8 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
 #pragma unroll
             for (int i = 0; i < NT; ++i) st[s][i][0] = st[s][i][1] = st[s][i][2] = st[s][i][3] = 0.f;
             unsigned ka[KS][2], kb[KS][2];
-            kr[s][0].values(ka);
-            kr[s][1].values(kb);
+            w.k[s][0].values(ka);
+            w.k[s][1].values(kb);
 #pragma unroll
             for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -375,8 +390,8 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
                     }
                 }
             unsigned va[KS][2], vb[KS][2];                 // positions 4t, 4t+1 and 4t+2, 4t+3
-            weave<HD>(vr[s][0], vr[s][1], va);
-            weave<HD>(vr[s][2], vr[s][3], vb);
+            weave<HD>(w.v[s][0], w.v[s][1], va);
+            weave<HD>(w.v[s][2], w.v[s][3], vb);
 #pragma unroll
             for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -385,6 +400,11 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
                     if (SPLIT) lfk::mma16816(o[i][k], va[k][0], va[k][1], vb[k][0], vb[k][1], pm[i][0], pm[i][1]);
                 }
         }
+    };
+    for (int p = p0 + warp * CH; p < p1; p += NW * CH) {
+        Raw w;
+        load(w, p);
+        chunk(w, p);
     }
 
     // ---- the warps' states, joined: O = sum 2^(m_w - M) O_w over l likewise
@@ -422,48 +442,48 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
             add_scaled(acc, *reinterpret_cast<const float4 *>(wo + ((size_t)w * RT + r) * HD + d), x);
         }
     };
-    if (a.splits > 1 && !a.part) {
-        // the splits are one cluster: each CTA leaves its state in its shared memory and joins its share of the rows
+    auto finish = [&](int r, int d, const Joined &j) {
+        if (!a.part) {
+            j.store(a, r0 + r, kvh, d);
+            return;
+        }
+        float *part = a.part + ((size_t)((size_t)(kvh * a.tiles + tile) * (a.splits / a.cl) + split / a.cl) * RT + r) * (HD + PAD);
+        *reinterpret_cast<float4 *>(part + d) = j.acc;
+        if (d == 0) *reinterpret_cast<float2 *>(part + HD) = make_float2(j.M, j.L);
+    };
+    if (a.cl == 1) {
         for (int i = threadIdx.x; i < rows * (HD / 4); i += NW * 32) {
             const int r = i / (HD / 4), d = i % (HD / 4) * 4;
-            float M, L;
-            float4 acc;
-            state(r, d, M, L, acc);
-            *reinterpret_cast<float4 *>(cs + r * (HD + PAD) + d) = acc;
-            if (d == 0) *reinterpret_cast<float2 *>(cs + r * (HD + PAD) + HD) = make_float2(M, L);
-        }
-        cluster_sync();
-        for (int i = split * NW * 32 + threadIdx.x; i < rows * (HD / 4); i += a.splits * NW * 32) {
-            const int r = i / (HD / 4), d = i % (HD / 4) * 4;
             Joined j;
-            for (int s = 0; s < a.splits; ++s) {
-                const uint32_t base = cluster_smem(cs + r * (HD + PAD), s);
-                j.add(ld_cluster2(base + HD * 4), ld_cluster4(base + d * 4));
-            }
-            j.store(a, r0 + r, kvh, d);
+            state(r, d, j.M, j.L, j.acc);
+            finish(r, d, j);
         }
-        cluster_sync();   // no CTA leaves while its state may be read
         return;
     }
-    float *part = a.part ? a.part + ((size_t)(kvh * a.tiles + tile) * a.splits + split) * RT * (HD + PAD) : nullptr;
+    // a cluster: each CTA leaves its state in its shared memory and joins its share of the rows
     for (int i = threadIdx.x; i < rows * (HD / 4); i += NW * 32) {
         const int r = i / (HD / 4), d = i % (HD / 4) * 4;
         float M, L;
         float4 acc;
         state(r, d, M, L, acc);
-        if (part) {
-            *reinterpret_cast<float4 *>(part + (size_t)r * (HD + PAD) + d) = acc;
-            if (d == 0) *reinterpret_cast<float2 *>(part + (size_t)r * (HD + PAD) + HD) = make_float2(M, L);
-        } else {
-            Joined j;
-            j.add(make_float2(M, L), acc);
-            j.store(a, r0 + r, kvh, d);
-        }
+        *reinterpret_cast<float4 *>(cs + r * (HD + PAD) + d) = acc;
+        if (d == 0) *reinterpret_cast<float2 *>(cs + r * (HD + PAD) + HD) = make_float2(M, L);
     }
+    cluster_sync();
+    for (int i = split % a.cl * NW * 32 + threadIdx.x; i < rows * (HD / 4); i += a.cl * NW * 32) {
+        const int r = i / (HD / 4), d = i % (HD / 4) * 4;
+        Joined j;
+        for (int s = 0; s < a.cl; ++s) {
+            const uint32_t base = cluster_smem(cs + r * (HD + PAD), s);
+            j.add(ld_cluster2(base + HD * 4), ld_cluster4(base + d * 4));
+        }
+        finish(r, d, j);
+    }
+    cluster_sync();   // no CTA leaves while its state may be read
 }
 
-// Joins the splits of a row: `groups` x hd / 4 threads per query row and KV head, each group taking every
-// groups-th split, then the groups through shared memory.
+// Joins the partial states of a row: `groups` x hd / 4 threads per query row and KV head, each group taking every
+// groups-th state, then the groups through shared memory.
 constexpr int JOIN_THREADS = 256;
 __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant__ Attn a, int groups)
 {
@@ -475,9 +495,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant_
     Joined j;
     if (row < a.n * a.G) {
         const size_t step = (size_t)a.rt * (hd + PAD);
-        const float *part = a.part + ((size_t)((size_t)kvh * a.tiles + row / a.rt) * a.splits * a.rt + row % a.rt) * (hd + PAD);
+        const int parts = a.splits / a.cl;
+        const float *part = a.part + ((size_t)((size_t)kvh * a.tiles + row / a.rt) * parts * a.rt + row % a.rt) * (hd + PAD);
 #pragma unroll 4
-        for (int s = grp; s < a.splits; s += groups)
+        for (int s = grp; s < parts; s += groups)
             j.add(__ldcg(reinterpret_cast<const float2 *>(part + s * step + hd)),
                   __ldcg(reinterpret_cast<const float4 *>(part + s * step + d)));
     }
@@ -496,6 +517,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant_
 
 // ---------------------------------------------------------------- launches
 
+// Chunks a warp up to which one cluster of 8 CTAs takes a row tile's whole range.
 constexpr int kClusterChunks = 4;
 // Rows per KV head from which the tiles kernel takes over.
 constexpr int kTileRows = 33;
@@ -532,24 +554,42 @@ size_t plan_attn(Attn &a, int sms)
 {
     const int rows = a.n * a.G, hi = key_hi(a.pos, a.n - 1, a.len);
     a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
+    const size_t state = (size_t)a.c.Hkv * (a.c.hd + PAD);
+    a.cl = 1;
     if (rows >= kTileRows) {
         plan_tiles(a, sms, rows, hi);
-        return a.splits > 1 ? (size_t)a.c.Hkv * a.tiles * a.splits * a.rt * (a.c.hd + PAD) : 0;
+        return a.splits > 1 ? state * a.tiles * a.rt * a.splits : 0;
     }
     a.rt = rows <= 8 ? 8 : 16;
     a.tiles = (rows + a.rt - 1) / a.rt;
     const int chunks = std::max(1, (hi - a.lo + CH - 1) / CH);
-    // Each warp at least one chunk.  Up to kClusterChunks a warp, the splits of a row tile are one cluster of at
-    // most 8 CTAs, which joins them in its shared memory; beyond that every SM takes part (two CTAs each, one of 16
-    // rows), through the workspace and a second launch.
-    int splits = (chunks + 7) / 8;
-    const bool cluster = chunks <= 8 * 8 * kClusterChunks;
-    if (cluster) splits = std::min(splits, 8);
-    else splits = (int)std::min<long long>(splits, std::max<long long>(1, (a.rt == 8 ? 2 : 1) * sms / ((long long)a.tiles * a.c.Hkv)));
-    const int per = (chunks + splits - 1) / splits;
-    a.splits = (chunks + per - 1) / per;
-    a.per = per * CH;
-    return a.splits > 1 && !cluster ? (size_t)a.c.Hkv * a.tiles * a.splits * a.rt * (a.c.hd + PAD) : 0;
+    // Eight warps a CTA, so its range is a whole number of eights of chunks.
+    const int eights = (chunks + 7) / 8;
+    if (eights <= 8 * kClusterChunks) {
+        // short: one cluster of at most 8 CTAs per row tile does it all in one launch
+        const int per = (eights + 7) / 8;
+        a.splits = a.cl = (eights + per - 1) / per;
+        a.per = per * 8 * CH;
+        return 0;
+    }
+    // long: two CTAs per SM (one of 16 rows), joined through the workspace by a second launch.  Of the cluster sizes
+    // that leave no more slots empty than the best, the largest: the join then has the fewest states (131,072
+    // positions: one KV head 14 us with clusters of 8, 25 without; eight heads 41 with 304 slots full, 43 with 256).
+    const int slots = (a.rt == 8 ? 2 : 1) * sms, t = (int)std::min<long long>((long long)a.tiles * a.c.Hkv, 1 << 20);
+    int best = 0, groups = 1;
+    for (int cl = 8; cl >= 1; cl /= 2) {
+        const int g = std::max(1, slots / (t * cl));
+        if (g * cl * t > best + best / 100) {
+            best = g * cl * t;
+            a.cl = cl;
+            groups = g;
+        }
+    }
+    const int per = (eights + groups * a.cl - 1) / (groups * a.cl);
+    groups = (eights + per * a.cl - 1) / (per * a.cl);
+    a.splits = groups * a.cl;
+    a.per = per * 8 * CH;
+    return groups > 1 ? state * a.tiles * a.rt * groups : 0;
 }
 
 template <template <class> class F, class... A>
@@ -562,9 +602,10 @@ static cudaError_t by_dtype(int dtype, A... args)
     }
 }
 
-static dim3 block_grid(const Cache &c, int n)
+// Grid of 2^shift threads for each of n rows, by KV head and K or V.
+static dim3 row_grid(const Cache &c, int n, int shift)
 {
-    return dim3((unsigned)(((long long)n * c.Hkv * (c.hd / 16) + 255) / 256), 2);
+    return dim3((unsigned)((((long long)n << shift) + 255) / 256), (unsigned)(2 * c.Hkv));
 }
 // A launch as a programmatic dependent of the previous kernel on the stream (it waits for that kernel's end before
 // any access to global memory), in clusters of `cluster` CTAs along x.
@@ -590,14 +631,16 @@ template <class T>
 struct RunAppend {
     static cudaError_t run(Cache c, Rows k, Rows v, int n, int pos, cudaStream_t s)
     {
-        return launch(append_rows<T>, block_grid(c, n), 256, 0, 1, s, c, k, v, n, pos);
+        const int shift = c.hd == 128 ? 3 : 2;            // blocks of 16
+        return launch(append_rows<T>, row_grid(c, n, shift), 256, 0, 1, s, c, k, v, n, pos, shift);
     }
 };
 template <class T>
 struct RunRead {
     static cudaError_t run(Cache c, Rows k, Rows v, int n, int pos, cudaStream_t s)
     {
-        return launch(read_rows<T>, block_grid(c, n), 256, 0, 1, s, c, k, v, n, pos);
+        const int shift = (c.hd == 128 ? 4 : 3) + (sizeof(T) == 4 ? 1 : 0);
+        return launch(read_rows<T>, row_grid(c, n, shift), 256, 0, 1, s, c, k, v, n, pos, shift);
     }
 };
 cudaError_t launch_append(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s)
@@ -623,7 +666,7 @@ static cudaError_t run_rows(const Attn &a, cudaStream_t s)
         if (dev < 64) ready[dev] = true;
     }
     return launch(attn_rows<HD, NT, SPLIT>, dim3((unsigned)(a.tiles * a.splits), (unsigned)a.c.Hkv), 256, smem,
-                  a.part ? 1 : a.splits, s, a);
+                  a.cl, s, a);
 }
 
 cudaError_t launch_attn(const Attn &a, cudaStream_t s)
@@ -638,7 +681,7 @@ cudaError_t launch_attn(const Attn &a, cudaStream_t s)
     else
         e = a.rt == 8 ? (split ? run_rows<64, 1, true>(a, s) : run_rows<64, 1, false>(a, s))
                       : (split ? run_rows<64, 2, true>(a, s) : run_rows<64, 2, false>(a, s));
-    if (e == cudaSuccess && a.splits > 1 && a.part) {
+    if (e == cudaSuccess && a.splits > a.cl) {
         // few rows: the splits of a row are spread over a whole block; many: one group each, the traffic counts
         const int lanes = a.c.hd / 4, rows = a.n * a.G;
         const int groups = (long long)rows * a.c.Hkv >= 4096 ? 1 : JOIN_THREADS / lanes;

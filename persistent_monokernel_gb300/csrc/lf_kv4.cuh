@@ -125,41 +125,31 @@ __device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16 *p, fl
         }
     }
 }
-// 16 cached values as FP16 pairs -> T (exact: at most 6 significant bits)
-template <class T>
-__device__ __forceinline__ void store16(T *p, const unsigned (&h)[8]);
-template <>
-__device__ __forceinline__ void store16<__half>(__half *p, const unsigned (&h)[8])
-{
-    reinterpret_cast<uint4 *>(p)[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    reinterpret_cast<uint4 *>(p)[1] = make_uint4(h[4], h[5], h[6], h[7]);
-}
 __device__ __forceinline__ float2 h2_f2(unsigned h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 __device__ __forceinline__ unsigned pack_bf2(float lo, float hi)
 {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const unsigned *>(&b);
 }
-template <>
-__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16 *p, const unsigned (&h)[8])
+// 16 bytes of cached values, FP16 pairs in h, as T (exact: at most 6 significant bits)
+__device__ __forceinline__ void store_values(__half *p, const unsigned (&h)[4])
 {
-    unsigned w[8];
+    *reinterpret_cast<uint4 *>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+}
+__device__ __forceinline__ void store_values(__nv_bfloat16 *p, const unsigned (&h)[4])
+{
+    unsigned w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
         const float2 f = h2_f2(h[j]);
         w[j] = pack_bf2(f.x, f.y);
     }
-    reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <>
-__device__ __forceinline__ void store16<float>(float *p, const unsigned (&h)[8])
+__device__ __forceinline__ void store_values(float *p, const unsigned (&h)[4])
 {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 a = h2_f2(h[2 * j]), b = h2_f2(h[2 * j + 1]);
-        reinterpret_cast<float4 *>(p)[j] = make_float4(a.x, a.y, b.x, b.y);
-    }
+    const float2 a = h2_f2(h[0]), b = h2_f2(h[1]);
+    *reinterpret_cast<float4 *>(p) = make_float4(a.x, a.y, b.x, b.y);
 }
 // Four values at element offset `at` of o (rounded once, to nearest even).
 __device__ __forceinline__ void store4(const Rows &o, size_t at, float a, float b, float c, float d)

@@ -34,10 +34,11 @@ struct Attn {
     int n, pos;             // query rows at positions pos .. pos + n - 1
     int len, win;           // keys 0 .. len - 1; window (0: all)
     float scale;
-    // plan: row tiles of rt query rows (n * G rows per KV head, row r = token r / G,
-    // head r % G), each over `splits` ranges of `per` positions from lo on
-    int rt, tiles, splits, per, lo;
-    float *part;            // [Hkv * tiles * splits][rt][hd + PAD]: O, then m and l; null: one split, or one cluster
+    // plan: row tiles of rt query rows (n * G rows per KV head, row r = token r / G, head r % G), each over
+    // `splits` ranges of `per` positions from lo on; `cl` ranges in a row are one cluster, which joins them into
+    // one of splits / cl partial states
+    int rt, tiles, splits, cl, per, lo;
+    float *part;            // [Hkv * tiles * splits / cl][rt][hd + PAD]: O, then m and l; null: one partial state
 };
 
 // Keys that query row t (position pos + t) sees: [key_lo, key_hi).
