@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(256) append_rows(Cache c, Rows k, Rows v, int 
     ((isv ? c.vs : c.ks) + row * scale_bytes(c.hd))[b] = (uint8_t)s8;
 }
 
-// One thread per 16 bytes of the output (8 values, 4 in FP32), so that a warp's stores are contiguous.
+// A thread takes 16 bytes of the output (8 values, 4 in FP32) of READ_U places 256 apart: a warp's stores are
+// contiguous, and each thread has several loads on their way.
+constexpr int READ_U = 4;
 template <class T>
 __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n, int pos, int shift)
 {
@@ -87,20 +89,33 @@ __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n,
     wait_for_prerequisites();
     const bool isv = blockIdx.y & 1;
     const int h = blockIdx.y >> 1;
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, t = i >> shift;   // 2^shift threads per row
-    const int b = (int)(i & ((1 << shift) - 1));
-    if (t >= n) return;
-    const size_t row = (size_t)h * c.cap + (size_t)pos + (size_t)t;
-    const uint8_t *codes = (isv ? c.vc : c.kc) + row * code_bytes(c.hd) + b * (N / 2);
-    const unsigned w = N == 8 ? __ldg(reinterpret_cast<const unsigned *>(codes))
-                              : __ldg(reinterpret_cast<const unsigned short *>(codes));
-    const unsigned s2 = e4m3_h2_same(__ldg((isv ? c.vs : c.ks) + row * scale_bytes(c.hd) + b * N / 16));
-    unsigned hv[4];
-    e2m1x8_h2(w, hv[0], hv[1], hv[2], hv[3]);
+    const long long i0 = (long long)blockIdx.x * (256 * READ_U) + threadIdx.x;              // 2^shift places per row
+    const int b = (int)(threadIdx.x & ((1 << shift) - 1));                                  // 256 is a multiple of it
+    const size_t row0 = (size_t)h * c.cap + (size_t)pos;
+    const uint8_t *codes = (isv ? c.vc : c.kc) + row0 * code_bytes(c.hd) + b * (N / 2);
+    const uint8_t *scales = (isv ? c.vs : c.ks) + row0 * scale_bytes(c.hd) + b * N / 16;
+    unsigned w[READ_U], s[READ_U];
 #pragma unroll
-    for (int j = 0; j < N / 2; ++j) hv[j] = hmul2(hv[j], s2);
+    for (int u = 0; u < READ_U; ++u) {
+        const long long t = (i0 + u * 256) >> shift;
+        if (t >= n) continue;
+        w[u] = N == 8 ? __ldg(reinterpret_cast<const unsigned *>(codes + t * code_bytes(c.hd)))
+                      : __ldg(reinterpret_cast<const unsigned short *>(codes + t * code_bytes(c.hd)));
+        s[u] = __ldg(scales + t * scale_bytes(c.hd));
+    }
     const Rows &out = isv ? v : k;
-    store_values(static_cast<T *>(out.p) + t * out.ts + h * out.hs + b * N, hv);
+    T *dst = static_cast<T *>(out.p) + h * out.hs + b * N;
+#pragma unroll
+    for (int u = 0; u < READ_U; ++u) {
+        const long long t = (i0 + u * 256) >> shift;
+        if (t >= n) continue;
+        const unsigned s2 = e4m3_h2_same(s[u]);
+        unsigned hv[4];
+        e2m1x8_h2(w[u], hv[0], hv[1], hv[2], hv[3]);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) hv[j] = hmul2(hv[j], s2);
+        store_values(dst + t * out.ts, hv);
+    }
 }
 
 // ---------------------------------------------------------------- attention, few rows
@@ -602,10 +617,10 @@ static cudaError_t by_dtype(int dtype, A... args)
     }
 }
 
-// Grid of 2^shift threads for each of n rows, by KV head and K or V.
-static dim3 row_grid(const Cache &c, int n, int shift)
+// Grid of 2^shift places for each of n rows, `per` a block, by KV head and K or V.
+static dim3 row_grid(const Cache &c, int n, int shift, int per)
 {
-    return dim3((unsigned)((((long long)n << shift) + 255) / 256), (unsigned)(2 * c.Hkv));
+    return dim3((unsigned)((((long long)n << shift) + per - 1) / per), (unsigned)(2 * c.Hkv));
 }
 // A launch as a programmatic dependent of the previous kernel on the stream (it waits for that kernel's end before
 // any access to global memory), in clusters of `cluster` CTAs along x.
@@ -632,7 +647,7 @@ struct RunAppend {
     static cudaError_t run(Cache c, Rows k, Rows v, int n, int pos, cudaStream_t s)
     {
         const int shift = c.hd == 128 ? 3 : 2;            // blocks of 16
-        return launch(append_rows<T>, row_grid(c, n, shift), 256, 0, 1, s, c, k, v, n, pos, shift);
+        return launch(append_rows<T>, row_grid(c, n, shift, 256), 256, 0, 1, s, c, k, v, n, pos, shift);
     }
 };
 template <class T>
@@ -640,7 +655,7 @@ struct RunRead {
     static cudaError_t run(Cache c, Rows k, Rows v, int n, int pos, cudaStream_t s)
     {
         const int shift = (c.hd == 128 ? 4 : 3) + (sizeof(T) == 4 ? 1 : 0);
-        return launch(read_rows<T>, row_grid(c, n, shift), 256, 0, 1, s, c, k, v, n, pos, shift);
+        return launch(read_rows<T>, row_grid(c, n, shift, 256 * READ_U), 256, 0, 1, s, c, k, v, n, pos, shift);
     }
 };
 cudaError_t launch_append(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s)

@@ -8,6 +8,7 @@ current stream of the cache's device or the one passed.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 
 
 class lf_kv4(C.Structure):
@@ -27,19 +28,31 @@ class lf_kv4_query(C.Structure):
 F16, BF16, F32 = 0, 1, 2
 BLOCK = 16          # values that share a scale
 _byref = C.byref
-_torch = _lib = _codes = _raw_stream = _current_device = None
+_torch = _lib = _append = _read = _attend = _codes = _raw_stream = _current_device = None
+# The argument structures as bytes, packed in one call (a ctypes structure takes a microsecond to fill, and a decode
+# step's kernels take a few on the GPU): data, dtype, token_stride, head_stride; then the query's other fields.
+_ROWS = struct.Struct("@Piqq")
+_QUERY = struct.Struct("@PiqqPiqqiiiiif")
 
 
 def _load():
     """torch and the library, once, at the first cache (the package imports without torch)."""
-    global _torch, _lib, _codes, _raw_stream, _current_device
+    global _torch, _lib, _append, _read, _attend, _codes, _raw_stream, _current_device
     import torch
 
     from . import lib
     _lib = lib()
+    assert _ROWS.size == C.sizeof(lf_rows) and _QUERY.size == C.sizeof(lf_kv4_query)
+    # prototypes of their own that take the packed bytes
+    calls = [_lib["lf_kv4_append"], _lib["lf_kv4_read"], _lib["lf_kv4_attend"]]
+    for f in calls[:2]:
+        f.argtypes = [C.c_void_p, C.c_char_p, C.c_char_p, C.c_int32, C.c_int32, C.c_void_p]
+    calls[2].argtypes = [C.c_void_p, C.c_char_p, C.c_void_p, C.c_int64, C.c_void_p]
+    for f in calls:
+        f.restype = C.c_int
+    _append, _read, _attend = calls
     _codes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
-    # the plain functions behind torch.cuda.current_stream and current_device: a decode step's calls
-    # take a few microseconds on the GPU, and a Stream object costs three
+    # the plain functions behind torch.cuda.current_stream and current_device (a Stream object costs three microseconds)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda i: torch.cuda.current_stream(i).cuda_stream)
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -85,14 +98,14 @@ class KV4Cache:
         self._index = k_codes.get_device()
         self._c = lf_kv4(h, 2 * half, s, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                          v_scales.data_ptr())
-        self._ref = _byref(self._c)
+        self._ref, self._addr = _byref(self._c), C.addressof(self._c)
 
     @property
     def nbytes(self) -> int:
         return sum(t.numel() for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales))
 
-    def _rows(self, t, n, heads, what) -> lf_rows:
-        """lf_rows of t [n, heads, head_dim]."""
+    def _rows(self, t, n, heads, what):
+        """The fields of lf_rows for t [n, heads, head_dim]."""
         stride = t.stride()
         code = _codes.get(t.dtype)
         if t.shape != (n, heads, self.head_dim) or t.get_device() != self._index or stride[2] != 1 or code is None:
@@ -100,7 +113,7 @@ class KV4Cache:
                              f"{self.head_dim}] float16, bfloat16 or float32 with a contiguous last dimension on "
                              f"{self.device} is needed")
         # the stride of a dimension of one is never used (and may be anything)
-        return lf_rows(t.data_ptr(), code, stride[0] if n > 1 else 0, stride[1] if heads > 1 else 0)
+        return t.data_ptr(), code, stride[0] if n > 1 else 0, stride[1] if heads > 1 else 0
 
     def _elsewhere(self, call, stream, args):
         """The call again with the cache's device, and the stream if one is passed, current: what it allocates belongs
@@ -117,9 +130,9 @@ class KV4Cache:
         """Quantise k, v [n, n_kv_heads, head_dim] into positions pos .. pos + n - 1."""
         if stream is not None or _current_device() != self._index:
             return self._elsewhere(self.append, stream, (k, v, pos))
-        n = k.shape[0]
-        kr, vr = self._rows(k, n, self.n_kv_heads, "k"), self._rows(v, n, self.n_kv_heads, "v")
-        status = _lib.lf_kv4_append(self._ref, _byref(kr), _byref(vr), n, pos, _raw_stream(self._index))
+        n, h = k.shape[0], self.n_kv_heads
+        status = _append(self._addr, _ROWS.pack(*self._rows(k, n, h, "k")), _ROWS.pack(*self._rows(v, n, h, "v")), n, pos,
+                         _raw_stream(self._index))
         if status:
             _fail(status, "lf_kv4_append")
 
@@ -135,8 +148,8 @@ class KV4Cache:
             v = _torch.empty(shape, dtype=dtype, device=self.device)
         else:
             k, v = out
-        kr, vr = self._rows(k, max(n, 0), h, "k"), self._rows(v, max(n, 0), h, "v")
-        status = _lib.lf_kv4_read(self._ref, _byref(kr), _byref(vr), n, pos, _raw_stream(self._index))
+        status = _read(self._addr, _ROWS.pack(*self._rows(k, max(n, 0), h, "k")),
+                       _ROWS.pack(*self._rows(v, max(n, 0), h, "v")), n, pos, _raw_stream(self._index))
         if status:
             _fail(status, "lf_kv4_read")
         return k, v
@@ -150,22 +163,26 @@ class KV4Cache:
             return self._elsewhere(self.attend, stream, (q, pos, length, window, scale, out))
         shape = q.shape
         n, heads = shape[0], shape[1]
-        qr = self._rows(q, n, heads, "q")
+        rows = self._rows(q, n, heads, "q")
         if out is None:
             out = _torch.empty(shape, dtype=q.dtype, device=self.device)
-        args = lf_kv4_query(qr, self._rows(out, n, heads, "out"), heads, n, pos, pos + n if length is None else length,
-                            window, scale)
-        ref, need = _byref(args), C.c_int64()
-        status = _lib.lf_kv4_workspace(self._ref, ref, _byref(need))
-        if not status:
-            # scratch of this call alone: no two streams or captured graphs share it
-            size = need.value
-            ws = _torch.empty((size,), dtype=_torch.uint8, device=self.device) if size else None
-            status = _lib.lf_kv4_attend(self._ref, ref, ws.data_ptr() if size else None, size,
-                                        _raw_stream(self._index))
+        args = _QUERY.pack(*rows, *self._rows(out, n, heads, "out"), heads, n, pos, pos + n if length is None else length,
+                           window, scale)
+        status = _attend(self._addr, args, None, 0, _raw_stream(self._index))
         if status:
-            _fail(status, "lf_kv4_attend")
+            status = self._attend_with_workspace(args, status)
+            if status:
+                _fail(status, "lf_kv4_attend")
         return out
+
+    def _attend_with_workspace(self, args, status):
+        """The call again with the scratch it needs, if that is what it lacked (long contexts and large blocks)."""
+        query, need = lf_kv4_query.from_buffer_copy(args), C.c_int64()
+        if _lib.lf_kv4_workspace(self._ref, _byref(query), _byref(need)) or not need.value:
+            return status
+        # scratch of this call alone: no two streams or captured graphs share it
+        ws = _torch.empty((need.value,), dtype=_torch.uint8, device=self.device)
+        return _attend(self._addr, args, ws.data_ptr(), need.value, _raw_stream(self._index))
 
 
 def _fail(status: int, where: str) -> None:
