@@ -259,6 +259,17 @@ typedef struct {
  * be encoded). */
 LF_API lf_status lf_create(const lf_config *cfg, const lf_weights *weights, lf_handle **out);
 
+/* lf_create with the KV cache in 4 bits (the format of lf_kv4 below; 3.6 times
+ * less memory than FP16, lf_info.kv_cache_bytes): every layer quantises its K
+ * and V rows, rounded to FP16 first as in the FP16 cache, as they are appended,
+ * the position in hand included, and attends to the quantised cache.  Every
+ * weight format, window, expert setting and prefill of lf_create works; a step
+ * runs as persistent launches of the stages between two attentions, with the
+ * attention between them as launches of its own.  cfg->fault_step is ignored;
+ * lf_set_schedule takes LF_SCHED_FLAGS only and lf_enable_trace 0 only
+ * (NOT_SUPPORTED).  Errors as for lf_create. */
+LF_API lf_status lf_create_kv4(const lf_config *cfg, const lf_weights *weights, lf_handle **out);
+
 /* Release every library-owned allocation.  Synchronizes the device first.
  * Accepts NULL. */
 LF_API void lf_destroy(lf_handle *h);

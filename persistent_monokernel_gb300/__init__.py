@@ -28,7 +28,7 @@ TRACE_STAMPS = 9
 EXPORTS = ("lf_create", "lf_destroy", "lf_prefill", "lf_decode", "lf_generate", "lf_sync", "lf_reset",
            "lf_set_schedule", "lf_get_info", "lf_error_string", "lf_abi_version", "lf_generate_noalloc",
            "lf_enable_trace", "lf_read_trace", "lf_sync_latency", "lf_kv4_append", "lf_kv4_read", "lf_kv4_workspace",
-           "lf_kv4_attend", "lf_kv4_status")
+           "lf_kv4_attend", "lf_kv4_status", "lf_create_kv4")
 
 
 class LFError(RuntimeError):
@@ -81,6 +81,7 @@ def lib() -> C.CDLL:
         L = C.CDLL(LIB_PATH)
         vp = C.c_void_p
         L.lf_create.argtypes = [C.POINTER(lf_config), C.POINTER(lf_weights), C.POINTER(vp)]
+        L.lf_create_kv4.argtypes = L.lf_create.argtypes
         L.lf_destroy.argtypes = [vp]
         L.lf_destroy.restype = None
         L.lf_prefill.argtypes = [vp, vp, C.c_int32, vp]
@@ -110,7 +111,7 @@ def lib() -> C.CDLL:
         L.lf_kv4_status.argtypes = [vp]
         for name in ("lf_kv4_status", "lf_kv4_append", "lf_kv4_read", "lf_kv4_workspace", "lf_kv4_attend"):
             getattr(L, name).restype = C.c_int
-        for name in ("lf_create", "lf_prefill", "lf_decode", "lf_generate", "lf_sync", "lf_reset",
+        for name in ("lf_create", "lf_create_kv4", "lf_prefill", "lf_decode", "lf_generate", "lf_sync", "lf_reset",
                      "lf_set_schedule", "lf_get_info"):
             getattr(L, name).restype = C.c_int
         _lib = L
@@ -149,10 +150,11 @@ class Decoder:
     `model` is any object with the attributes n_layers, d_model, n_heads,
     n_kv_heads, head_dim, ffn_dim, vocab, rope_theta and rms_eps; `weights`
     maps the lf_weights field names to contiguous CUDA float16 tensors.
+    kv4=True keeps the KV cache in 4 bits (lf_create_kv4).
     """
 
     def __init__(self, model, weights: dict, max_seq: int, n_ctas: int = 0, wait_timeout_ns: int = 0,
-                 fault_step: int = -1, layer_window=None, prefill_block: int = 0):
+                 fault_step: int = -1, layer_window=None, prefill_block: int = 0, kv4: bool = False):
         import torch
         self.model = model
         self.max_seq = int(max_seq)
@@ -189,7 +191,8 @@ class Decoder:
                        *[_dptr(weights[n]) if quant else None for n in SCALE_FIELDS],
                        _dptr(weights["w_router"]) if n_exp else None)
         h = C.c_void_p()
-        _check(lib().lf_create(C.byref(cfg), C.byref(w), C.byref(h)), "lf_create")
+        create = "lf_create_kv4" if kv4 else "lf_create"
+        _check(getattr(lib(), create)(C.byref(cfg), C.byref(w), C.byref(h)), create)
         self._h = h
 
     # ---- lifetime

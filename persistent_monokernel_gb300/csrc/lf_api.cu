@@ -12,6 +12,7 @@
 
 #include "../../include/lf.h"
 #include "lf_internal.cuh"
+#include "lf_kv4.h"
 #include "lf_prefill.h"
 
 extern "C" cudaError_t lfk_set_smem(int smem_bytes);
@@ -90,6 +91,16 @@ struct lf_handle {
     lfp_maps pf_maps;              // TMA tensor maps of the prefill GEMM operands
     size_t pf_bytes = 0;
     size_t pf_woff[4] = {}, pf_soff[4] = {};   // [qkv, o, gu, d] element offsets
+    // 4-bit cache (lf_create_kv4): codes and scales of every layer [L][Hkv][max_seq][..], the attention's scratch,
+    // the batched prefill's staging of a block's K and V, the windows on the host.  kc and vc then hold one
+    // position per layer and head (the QKV stage's FP16 rows, [L][Hkv][hd]).
+    bool kv4 = false;
+    uint8_t *q4_kc = nullptr, *q4_ks = nullptr, *q4_vc = nullptr, *q4_vs = nullptr;
+    size_t q4_codes = 0, q4_scales = 0;   // bytes of one layer
+    float *q4_ws = nullptr;
+    size_t q4_floats = 0;
+    __half *q4_stage = nullptr;
+    std::vector<int> h_win;
 };
 
 namespace {
@@ -104,7 +115,8 @@ void free_all(lf_handle *h)
 {
     void *ptrs[] = {h->d_plans, h->wstream, h->kc, h->vc, h->rope, h->qbuf, h->attn, h->xattn, h->hbuf,
                     h->xout, h->apart, h->kvf, h->win, h->wsc, h->counters, h->lm_part, h->tok_buf, h->tok_seq, h->status,
-                    h->stage_in, h->stage_out, h->trace, h->pf_w, h->pf_s, h->pf_ws, h->pf_tok};
+                    h->stage_in, h->stage_out, h->trace, h->pf_w, h->pf_s, h->pf_ws, h->pf_tok,
+                    h->q4_kc, h->q4_ks, h->q4_vc, h->q4_vs, h->q4_ws, h->q4_stage};
     for (void *p : ptrs)
         if (p) cudaFree(p);
 }
@@ -195,6 +207,18 @@ lfp_args prefill_args(const lf_handle *h)
     a.sms = h->sm_count;
     a.attn_stamps = h->trace_steps > 0 ? h->trace : nullptr;   // with tracing on: the prefill attention's stamps
     a.ws = lfp_carve(h->pf_ws, g, h->pf_block, h->sm_count);
+    a.q4 = {h->q4_kc, h->q4_ks, h->q4_vc, h->q4_vs, g.Hkv, g.hd, g.max_seq};
+    a.q4_codes = h->q4_codes;
+    a.q4_scales = h->q4_scales;
+    a.q4_k = a.q4_v = nullptr;
+    a.q4_win = h->h_win.empty() ? nullptr : h->h_win.data();
+    a.q4_ws = h->q4_ws;
+    a.q4_floats = h->q4_floats;
+    if (h->kv4) {
+        a.kc = a.vc = nullptr;
+        a.q4_k = h->q4_stage;
+        a.q4_v = h->q4_stage + (size_t)h->pf_block * g.KV;
+    }
     return a;
 }
 
@@ -262,8 +286,11 @@ lf_status setup_prefill(lf_handle *h, const lf_weights *w)
     if (e == cudaSuccess && fp8) e = dalloc(&h->pf_s, st);
     if (e == cudaSuccess) e = dalloc(&h->pf_ws, ws_bytes);
     if (e == cudaSuccess) e = dalloc(&h->pf_tok, (size_t)g.max_seq);
+    const size_t stage = h->kv4 ? 2 * (size_t)h->pf_block * KV : 0;
+    if (e == cudaSuccess && stage) e = dalloc(&h->q4_stage, stage);
     if (e != cudaSuccess) return from_cuda(e);
-    h->pf_bytes = wt * sizeof(__half) + (fp8 ? st * sizeof(float) : 0) + ws_bytes + (size_t)g.max_seq * sizeof(int);
+    h->pf_bytes = wt * sizeof(__half) + (fp8 ? st * sizeof(float) : 0) + ws_bytes + (size_t)g.max_seq * sizeof(int) +
+                  stage * sizeof(__half);
     // A [units, cols] matrix (gate or up rows) into the interleaved gate/up
     // layout: its rows of units 128b .. 128b+127 go to rows 256b + half*128 ..
     // (elem bytes per value: 2 for the FP16 weights, 4 for the FP8 row scales).
@@ -400,30 +427,84 @@ lfk::Params base_params(lf_handle *h)
     return p;
 }
 
+// Step i of a call as a call of its own.
+lfk::Params one_step(const lf_handle *h, const lfk::Params &p, int i)
+{
+    lfk::Params q = p;
+    q.n_steps = 1;
+    q.pos0 = p.pos0 + i;
+    q.epoch0 = p.epoch0 + (unsigned)i;
+    q.tok_base = p.tok_base + (unsigned)i;
+    q.fault_step = -1;
+    q.trace = nullptr;
+    if (p.mode == lfk::MODE_PREFILL) {
+        q.has_pending = (p.has_pending && i == 0) ? 1 : 0;
+        q.prompt = p.prompt + (i - (p.has_pending ? 1 : 0));
+        if (q.has_pending) q.prompt = p.prompt;
+    } else {
+        q.out_tokens = p.out_tokens + i;
+        q.debug_logits = p.debug_logits ? p.debug_logits + (size_t)i * h->g.V : nullptr;
+        q.force_tokens = p.force_tokens ? p.force_tokens + i : nullptr;
+    }
+    return q;
+}
+
+// 4-bit cache, layer l at position pos: quantise the pass's K and V rows into the cache and attend to it, from and
+// to the persistent kernel's tagged buffers.
+lf_status kv4_attention(lf_handle *h, int l, int pos, unsigned epoch, cudaStream_t s)
+{
+    const lfk::Geo &g = h->g;
+    lfq::Attn a = {};
+    a.c = {h->q4_kc + (size_t)l * h->q4_codes, h->q4_ks + (size_t)l * h->q4_scales, h->q4_vc + (size_t)l * h->q4_codes,
+           h->q4_vs + (size_t)l * h->q4_scales, g.Hkv, g.hd, g.max_seq};
+    float *kv = h->kvf + (size_t)l * 2 * g.KV;
+    cudaError_t e = lfq::launch_append(a.c, {kv, lfq::TAG32, g.KV, g.hd, 0, nullptr},
+                                       {kv + g.KV, lfq::TAG32, g.KV, g.hd, 0, nullptr}, 1, pos, s);
+    a.q = {h->qbuf + (size_t)l * g.Q, lfq::F32, g.Q, g.hd, 0, nullptr};
+    a.o = {h->attn + (size_t)l * g.Q, lfq::TAG32, g.Q, g.hd, (int)((epoch & 1u) ^ 1u), nullptr};
+    a.Hq = g.Hq;
+    a.G = g.group;
+    a.n = 1;
+    a.pos = pos;
+    a.len = pos + 1;
+    a.win = h->h_win.empty() ? 0 : h->h_win[l];
+    a.scale = 1.0f / std::sqrt((float)g.hd);
+    a.part = lfq::plan_attn(a, h->sm_count, h->q4_floats) ? h->q4_ws : nullptr;
+    if (e == cudaSuccess) e = lfq::launch_attn(a, s);
+    return from_cuda(e);
+}
+
+// 4-bit cache: per step, persistent launches of the stages between two attentions, and the attentions.
+lf_status run_steps_kv4(lf_handle *h, const lfk::Params &p, cudaStream_t stream)
+{
+    for (int i = 0; i < p.n_steps; ++i) {
+        lfk::Params q = one_step(h, p, i);
+        q.only_stage = lfk::STAGE_SEGMENT;
+        // the FP16 K and V rows of this position, whatever it is, go to kc / vc [L][Hkv][hd]
+        q.g.max_seq = 1;
+        const uintptr_t back = (uintptr_t)q.pos0 * h->g.hd * sizeof(__half);
+        q.kc = reinterpret_cast<__half *>(reinterpret_cast<uintptr_t>(h->kc) - back);
+        q.vc = reinterpret_cast<__half *>(reinterpret_cast<uintptr_t>(h->vc) - back);
+        for (int l = -1; l < h->g.L; ++l) {
+            q.only_layer = l;
+            lf_status st = launch(h, q, stream);
+            if (st == LF_OK && l + 1 < h->g.L) st = kv4_attention(h, l + 1, q.pos0, q.epoch0, stream);
+            if (st != LF_OK) return st;
+        }
+    }
+    return LF_OK;
+}
+
 // Runs the steps of one prefill or decode call under the current schedule.
 lf_status run_steps(lf_handle *h, lfk::Params p, cudaStream_t stream)
 {
+    if (h->kv4) return run_steps_kv4(h, p, stream);
     if (p.sched != lfk::SCHED_MULTI) return launch(h, p, stream);
     // multi-kernel ablation: one launch per (step, layer, stage) + one for the LM head
     const int L = h->g.L;
     const int n = p.n_steps;
     for (int i = 0; i < n; ++i) {
-        lfk::Params q = p;
-        q.n_steps = 1;
-        q.pos0 = p.pos0 + i;
-        q.epoch0 = p.epoch0 + (unsigned)i;
-        q.tok_base = p.tok_base + (unsigned)i;
-        q.fault_step = -1;
-        q.trace = nullptr;
-        if (p.mode == lfk::MODE_PREFILL) {
-            q.has_pending = (p.has_pending && i == 0) ? 1 : 0;
-            q.prompt = p.prompt + (i - (p.has_pending ? 1 : 0));
-            if (q.has_pending) q.prompt = p.prompt;
-        } else {
-            q.out_tokens = p.out_tokens + i;
-            q.debug_logits = p.debug_logits ? p.debug_logits + (size_t)i * h->g.V : nullptr;
-            q.force_tokens = p.force_tokens ? p.force_tokens + i : nullptr;
-        }
+        lfk::Params q = one_step(h, p, i);
         for (int l = 0; l < L; ++l) {
             for (int s = 0; s < 5; ++s) {
                 q.only_layer = l;
@@ -464,7 +545,7 @@ const char *lf_error_string(lf_status s)
     return "unknown lf_status";
 }
 
-lf_status lf_create(const lf_config *cfg, const lf_weights *w, lf_handle **out)
+static lf_status create(const lf_config *cfg, const lf_weights *w, lf_handle **out, bool kv4)
 {
     if (!cfg || !w || !out) return LF_ERR_INVALID_ARG;
     *out = nullptr;
@@ -492,6 +573,7 @@ lf_status lf_create(const lf_config *cfg, const lf_weights *w, lf_handle **out)
     lf_handle *h = new (std::nothrow) lf_handle();
     if (!h) return LF_ERR_OUT_OF_MEMORY;
     h->cfg = *cfg;
+    h->kv4 = kv4;
     h->cfg.layer_window = nullptr;   // the caller's array is copied to the device below
     h->attn_min_len = attn_min_len_from_env();
     lfk::Geo &g = h->g;
@@ -587,7 +669,7 @@ lf_status lf_create(const lf_config *cfg, const lf_weights *w, lf_handle **out)
     }
 
     // ---- allocations
-    const size_t kv_elems = (size_t)g.L * g.Hkv * (size_t)g.max_seq * g.hd;
+    const size_t kv_elems = (size_t)g.L * g.Hkv * (kv4 ? (size_t)1 : (size_t)g.max_seq) * g.hd;
     const size_t sig_words = (size_t)g.L * lfk::sig_layout(g).per_layer * lfk::SIG_STRIDE;
     const size_t n_attn_done = (size_t)g.L * g.Hkv;
     const size_t n_words = sig_words + (n_attn_done + 3) * lfk::CNT_STRIDE;
@@ -626,6 +708,37 @@ lf_status lf_create(const lf_config *cfg, const lf_weights *w, lf_handle **out)
             delete h;
             return from_cuda(e);
         }
+    }
+    if (kv4) {
+        // the cache starts as zeros; the attention's scratch covers every call of one row and of a whole block
+        const size_t rows = (size_t)g.Hkv * g.max_seq;
+        h->q4_codes = rows * lfq::code_bytes(g.hd);
+        h->q4_scales = rows * lfq::scale_bytes(g.hd);
+        lfq::Attn a = {};
+        a.c = {nullptr, nullptr, nullptr, nullptr, g.Hkv, g.hd, g.max_seq};
+        a.q.dtype = lfq::F32;
+        a.Hq = g.Hq;
+        a.G = g.group;
+        a.n = std::min(1024, g.max_seq);
+        a.pos = g.max_seq - a.n;
+        a.len = g.max_seq;
+        h->q4_floats = lfq::min_workspace(a.c, h->sm_count);
+        if (cfg->prefill_block != 0) h->q4_floats = std::max(h->q4_floats, lfq::plan_attn(a, h->sm_count));
+        e = dalloc(&h->q4_kc, h->q4_codes * g.L);
+        if (e == cudaSuccess) e = dalloc(&h->q4_vc, h->q4_codes * g.L);
+        if (e == cudaSuccess) e = dalloc(&h->q4_ks, h->q4_scales * g.L);
+        if (e == cudaSuccess) e = dalloc(&h->q4_vs, h->q4_scales * g.L);
+        if (e == cudaSuccess) e = dalloc(&h->q4_ws, h->q4_floats);
+        if (e == cudaSuccess) e = cudaMemset(h->q4_kc, 0, h->q4_codes * g.L);
+        if (e == cudaSuccess) e = cudaMemset(h->q4_vc, 0, h->q4_codes * g.L);
+        if (e == cudaSuccess) e = cudaMemset(h->q4_ks, 0, h->q4_scales * g.L);
+        if (e == cudaSuccess) e = cudaMemset(h->q4_vs, 0, h->q4_scales * g.L);
+        if (e != cudaSuccess) {
+            free_all(h);
+            delete h;
+            return from_cuda(e);
+        }
+        if (cfg->layer_window) h->h_win.assign(cfg->layer_window, cfg->layer_window + g.L);
     }
     bool windowed = false;
     if (cfg->layer_window)
@@ -708,6 +821,10 @@ lf_status lf_create(const lf_config *cfg, const lf_weights *w, lf_handle **out)
     *out = h;
     return LF_OK;
 }
+
+lf_status lf_create(const lf_config *cfg, const lf_weights *weights, lf_handle **out) { return create(cfg, weights, out, false); }
+
+lf_status lf_create_kv4(const lf_config *cfg, const lf_weights *weights, lf_handle **out) { return create(cfg, weights, out, true); }
 
 void lf_destroy(lf_handle *h)
 {
@@ -803,6 +920,12 @@ lf_status lf_sync(lf_handle *h)
     if (e != cudaSuccess) return from_cuda(e);
     if (st[0] == (unsigned)lfk::STATUS_TIMEOUT) h->latched = LF_ERR_TIMEOUT;
     else if (st[0] != 0u) h->latched = LF_ERR_INVALID_ARG;
+    if (h->kv4 && h->latched == LF_OK) {
+        unsigned rec[4] = {0, 0, 0, 0};
+        e = lfq::tiles_status(rec, h->last_stream);
+        if (e != cudaSuccess) return from_cuda(e);
+        if (rec[0]) h->latched = LF_ERR_TIMEOUT;
+    }
     return h->latched;
 }
 
@@ -829,6 +952,8 @@ lf_status lf_set_schedule(lf_handle *h, int32_t schedule)
         return LF_ERR_INVALID_ARG;
     // the expert choice lives in shared memory for the rest of the launch
     if (schedule == LF_SCHED_MULTI_KERNEL && h->g.E > 0) return LF_ERR_NOT_SUPPORTED;
+    // the 4-bit cache's attention is a launch of its own
+    if (schedule != LF_SCHED_FLAGS && h->kv4) return LF_ERR_NOT_SUPPORTED;
     h->sched = schedule;
     return LF_OK;
 }
@@ -845,7 +970,8 @@ lf_status lf_get_info(const lf_handle *h, lf_info *out)
     out->has_pending = h->has_pending;
     out->schedule = h->sched;
     out->weight_stream_bytes = (int64_t)h->wstream_bytes;
-    out->kv_cache_bytes = (int64_t)(2ull * h->g.L * h->g.Hkv * (size_t)h->g.max_seq * h->g.hd * 2ull);
+    out->kv_cache_bytes = h->kv4 ? (int64_t)(2ull * h->g.L * (h->q4_codes + h->q4_scales))
+                                 : (int64_t)(2ull * h->g.L * h->g.Hkv * (size_t)h->g.max_seq * h->g.hd * 2ull);
     out->prefill_block = h->pf_block;
     out->prefill_bytes = (int64_t)h->pf_bytes;
     return LF_OK;
@@ -885,6 +1011,7 @@ extern "C" {
 lf_status lf_enable_trace(lf_handle *h, int32_t max_steps)
 {
     if (!h || max_steps < 0) return LF_ERR_INVALID_ARG;
+    if (h->kv4 && max_steps > 0) return LF_ERR_NOT_SUPPORTED;
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return from_cuda(e);
     if (h->trace) cudaFree(h->trace);

@@ -103,11 +103,16 @@ struct Ctx {
 };
 
 // Stage ids for the multi-kernel schedule's stage filter.
-enum { SID_QKV = 0, SID_ATTN = 1, SID_O = 2, SID_GU = 3, SID_D = 4, SID_LM = 5 };
+enum { SID_QKV = 0, SID_ATTN = 1, SID_O = 2, SID_GU = 3, SID_D = 4, SID_LM = 5, SID_SEGMENT = STAGE_SEGMENT };
 
 __device__ __forceinline__ bool stage_active(const Params &p, int layer, int sid)
 {
     if (p.only_stage < 0) return true;
+    // the segment between two attentions that run as launches of their own (4-bit cache): O, gate/up and down of
+    // layer only_layer, then QKV of the next one, or the LM head
+    if (p.only_stage == SID_SEGMENT)
+        return sid == SID_LM ? p.only_layer == p.g.L - 1
+                             : sid == SID_QKV ? layer == p.only_layer + 1 : sid != SID_ATTN && layer == p.only_layer;
     return p.only_stage == sid && (sid == SID_LM || p.only_layer == layer);
 }
 

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(256) append_rows(Cache c, Rows k, Rows v, int 
     if (t >= n) return;
     const Rows &in = isv ? v : k;
     float x[16];
-    load16<T>(static_cast<const T *>(in.p) + t * in.ts + h * in.hs + b * 16, x);
+    load_block<T>(in, t, h, b, x);
     unsigned top = 0u;                                    // the largest magnitude's bits: NaN above infinity above all
 #pragma unroll
     for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
@@ -537,7 +537,7 @@ constexpr int kClusterChunks = 4;
 // Rows per KV head from which the tiles kernel takes over.
 constexpr int kTileRows = 33;
 
-static void plan_tiles(Attn &a, int sms, int rows, int hi)
+static void plan_tiles(Attn &a, int sms, int rows, int hi, size_t limit)
 {
     constexpr int BN = 128;
     a.rt = 128;
@@ -552,6 +552,7 @@ static void plan_tiles(Attn &a, int sms, int rows, int hi)
     a.splits = 1;
     for (int s = 1; s <= chunks && s <= 64; ++s) {
         const int per = (chunks + s - 1) / s, n = (chunks + per - 1) / per;
+        if (n > 1 && (double)ctas * n * a.rt * (a.c.hd + PAD) > (double)limit) break;
         const double waves = (double)((ctas * n + sms - 1) / sms);
         const double join = n > 1 ? 2.0 + 2.0 * rows * a.c.Hkv * n * (a.c.hd + PAD) * 4.0 / 6.5e12 / 1.2e-6 : 0.0;
         const double cost = waves * (per + 2.0) + join;
@@ -565,14 +566,16 @@ static void plan_tiles(Attn &a, int sms, int rows, int hi)
     a.per = per * BN;
 }
 
-size_t plan_attn(Attn &a, int sms)
+size_t min_workspace(const Cache &c, int sms) { return (size_t)2 * sms * 16 * (c.hd + PAD); }
+
+size_t plan_attn(Attn &a, int sms, size_t limit)
 {
     const int rows = a.n * a.G, hi = key_hi(a.pos, a.n - 1, a.len);
     a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
     const size_t state = (size_t)a.c.Hkv * (a.c.hd + PAD);
     a.cl = 1;
     if (rows >= kTileRows) {
-        plan_tiles(a, sms, rows, hi);
+        plan_tiles(a, sms, rows, hi, limit);
         return a.splits > 1 ? state * a.tiles * a.rt * a.splits : 0;
     }
     a.rt = rows <= 8 ? 8 : 16;
@@ -660,6 +663,8 @@ struct RunRead {
 };
 cudaError_t launch_append(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s)
 {
+    if (k.dtype == TAG32) return RunAppend<Tagged>::run(c, k, v, n, pos, s);
+    if (k.dtype == SWZ16) return RunAppend<Swizzled>::run(c, k, v, n, pos, s);
     return by_dtype<RunAppend>(k.dtype, c, k, v, n, pos, s);
 }
 cudaError_t launch_read(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s)
@@ -760,7 +765,7 @@ Cache cache_of(const lf_kv4 *c)
     return {static_cast<uint8_t *>(c->k_codes), static_cast<uint8_t *>(c->k_scales), static_cast<uint8_t *>(c->v_codes),
             static_cast<uint8_t *>(c->v_scales), c->n_kv_heads, c->head_dim, c->max_seq};
 }
-Rows rows_of(const lf_rows *r) { return {r->data, r->dtype, r->token_stride, r->head_stride}; }
+Rows rows_of(const lf_rows *r) { return {r->data, r->dtype, r->token_stride, r->head_stride, 0, nullptr}; }
 
 lf_status check_copy(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int n, int pos, bool written)
 {

@@ -131,6 +131,37 @@ __device__ __forceinline__ unsigned pack_bf2(float lo, float hi)
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const unsigned *>(&b);
 }
+// Block b of row (t, h) of `in`, by element type (Tagged, Swizzled: the decoder's own buffers).
+struct Tagged {};
+struct Swizzled {};
+template <class T>
+__device__ __forceinline__ void load_block(const Rows &in, long long t, int h, int b, float (&x)[16])
+{
+    load16<T>(static_cast<const T *>(in.p) + t * in.ts + h * in.hs + b * 16, x);
+}
+template <>
+__device__ __forceinline__ void load_block<Tagged>(const Rows &in, long long t, int h, int b, float (&x)[16])
+{
+    load16<float>(static_cast<const float *>(in.p) + t * in.ts + h * in.hs + b * 16, x);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = __half2float(__float2half_rn(x[j]));
+}
+template <>
+__device__ __forceinline__ void load_block<Swizzled>(const Rows &in, long long t, int h, int b, float (&x)[16])
+{
+    const __half *row = static_cast<const __half *>(in.p) + t * in.ts + h * in.hs;
+    const int sw = (int)((in.aux + t) & 7);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(row + ((2 * b + j) ^ sw) * 8);
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[u]));
+            x[8 * j + 2 * u] = f.x, x[8 * j + 2 * u + 1] = f.y;
+        }
+    }
+}
 // 16 bytes of cached values, FP16 pairs in h, as T (exact: at most 6 significant bits)
 __device__ __forceinline__ void store_values(__half *p, const unsigned (&h)[4])
 {
@@ -156,7 +187,7 @@ __device__ __forceinline__ void store4(const Rows &o, size_t at, float a, float 
 {
     if (o.dtype == F32) {
         *reinterpret_cast<float4 *>(static_cast<float *>(o.p) + at) = make_float4(a, b, c, d);
-    } else {
+    } else if (o.dtype == F16 || o.dtype == BF16) {
         unsigned x, y;
         if (o.dtype == F16) {
             const __half2 u = __floats2half2_rn(a, b), v = __floats2half2_rn(c, d);
@@ -167,6 +198,21 @@ __device__ __forceinline__ void store4(const Rows &o, size_t at, float a, float 
             y = pack_bf2(c, d);
         }
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o.p) + at) = make_uint2(x, y);
+    } else if (o.dtype == TAG32) {
+        const unsigned tag = (unsigned)o.aux;
+        *reinterpret_cast<uint4 *>(static_cast<unsigned *>(o.p) + at) =
+            make_uint4((__float_as_uint(a) & ~1u) | tag, (__float_as_uint(b) & ~1u) | tag, (__float_as_uint(c) & ~1u) | tag,
+                       (__float_as_uint(d) & ~1u) | tag);
+    } else {   // SPLIT16
+        __half h[4], m[4];
+        lfk::split_h(a, h[0], m[0]);
+        lfk::split_h(b, h[1], m[1]);
+        lfk::split_h(c, h[2], m[2]);
+        lfk::split_h(d, h[3], m[3]);
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o.p) + at) =
+            make_uint2(lfk::pack_h2(h[0], h[1]), lfk::pack_h2(h[2], h[3]));
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o.p2) + at) =
+            make_uint2(lfk::pack_h2(m[0], m[1]), lfk::pack_h2(m[2], m[3]));
     }
 }
 // One row of q, HD / 32 consecutive values per lane (zeros for a row that is not there).

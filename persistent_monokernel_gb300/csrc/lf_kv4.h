@@ -2,13 +2,19 @@
 // launches used by the C entry points and by the decoder's own 4-bit path.
 #pragma once
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace lfq {
 
 constexpr int PAD = 4;      // words of a partial row behind O: m, l, and two that keep rows 16-byte aligned
 
-enum DType { F16 = 0, BF16 = 1, F32 = 2 };
+// Element types of the public calls, then those of the decoder's own buffers:
+//   TAG32    FP32 with a tag in the lowest mantissa bit; read: FP16 values (the tag is rounded away); written: the
+//            value with Rows::aux there
+//   SWZ16    read: FP16 rows whose 16-byte groups are XOR-ed with the position (Rows::aux: position of token 0) mod 8
+//   SPLIT16  written: an FP16 head to p and remainder to p2
+enum DType { F16 = 0, BF16 = 1, F32 = 2, TAG32 = 3, SWZ16 = 4, SPLIT16 = 5 };
 
 // Bytes of one row of head_dim values: codes (two per byte) and scales (one per 16).
 __host__ __device__ constexpr int code_bytes(int hd) { return hd / 2; }
@@ -25,6 +31,8 @@ struct Rows {
     void *p;
     int dtype;
     long long ts, hs;
+    int aux;
+    void *p2;
 };
 
 struct Attn {
@@ -48,8 +56,10 @@ __host__ __device__ inline int key_lo(int pos, int t, int win)
     return (win > 0 && pos + t + 1 > win) ? pos + t + 1 - win : 0;
 }
 
-// Fills a's plan for `sms` SMs (a.q.dtype is set) and returns the workspace floats it needs.
-size_t plan_attn(Attn &a, int sms);
+// Fills a's plan for `sms` SMs (a.q.dtype is set) and returns the workspace floats it needs, at most `limit`
+// (which is at least min_workspace).
+size_t plan_attn(Attn &a, int sms, size_t limit = SIZE_MAX);
+size_t min_workspace(const Cache &c, int sms);
 
 cudaError_t launch_append(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s);
 cudaError_t launch_read(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s);

@@ -607,7 +607,7 @@ extern "C" int lfp_make_maps(const lfp_args *a, lfp_maps *m)
         r |= lfg_tensor_map(&m->wqkv[i], a->wqkv, L * NQKV, d, 128 << i);
         r |= lfg_tensor_map(&m->wo[i], a->wo, L * d, Q, 128 << i);
     }
-    if (g.hd == 128) {
+    if (g.hd == 128 && a->kc) {
         const unsigned long long rows = L * (unsigned long long)g.Hkv * (unsigned long long)g.max_seq;
         r |= lfa_cache_map(&m->kc, a->kc, rows);
         r |= lfa_cache_map(&m->vc, a->vc, rows);
@@ -629,6 +629,39 @@ extern "C" int lfp_make_maps(const lfp_args *a, lfp_maps *m)
     }
     return r ? 1 : 0;
 }
+
+namespace lfp {
+
+// 4-bit cache: the block's staged K and V rows quantised into layer l's cache, then the attention of its queries
+// over it, the output as the FP16 head and remainder that the next product takes.
+static cudaError_t attn_q4(const lfp_args *a, int l, int T, int pos0, cudaStream_t s)
+{
+    const Geo &g = a->g;
+    lfq::Cache c = a->q4;
+    c.kc += (size_t)l * a->q4_codes;
+    c.vc += (size_t)l * a->q4_codes;
+    c.ks += (size_t)l * a->q4_scales;
+    c.vs += (size_t)l * a->q4_scales;
+    const long long hs = (long long)a->block * g.hd;
+    cudaError_t e = lfq::launch_append(c, {a->q4_k, lfq::SWZ16, g.hd, hs, pos0, nullptr}, {a->q4_v, lfq::SWZ16, g.hd, hs, pos0, nullptr},
+                                       T, pos0, s);
+    if (e != cudaSuccess) return e;
+    lfq::Attn q = {};
+    q.c = c;
+    q.q = {a->ws.Qr, lfq::F32, g.Q, g.hd, 0, nullptr};
+    q.o = {a->ws.Ah, lfq::SPLIT16, g.Q, g.hd, 0, a->ws.Al};
+    q.Hq = g.Hq;
+    q.G = g.group;
+    q.n = T;
+    q.pos = pos0;
+    q.len = pos0 + T;
+    q.win = a->q4_win ? a->q4_win[l] : 0;
+    q.scale = 1.0f / sqrtf((float)g.hd);
+    q.part = lfq::plan_attn(q, a->sms, a->q4_floats) ? a->q4_ws : nullptr;
+    return lfq::launch_attn(q, s);
+}
+
+}  // namespace lfp
 
 extern "C" int lfp_run(const lfp_args *a, const lfp_maps *m, cudaStream_t s)
 {
@@ -678,9 +711,19 @@ extern "C" int lfp_run(const lfp_args *a, const lfp_maps *m, cudaStream_t s)
             q.Qr = w.Qr;
             q.kc = a->kc;
             q.vc = a->vc;
+            if (a->q4.kc) {
+                // position pos0 + r of head h goes to row r of the block's staging [Hkv][block][hd]
+                q.layer = 0;
+                q.g.max_seq = a->block;
+                const uintptr_t back = (uintptr_t)pos0 * g.hd * sizeof(__half);
+                q.kc = reinterpret_cast<__half *>(reinterpret_cast<uintptr_t>(a->q4_k) - back);
+                q.vc = reinterpret_cast<__half *>(reinterpret_cast<uintptr_t>(a->q4_v) - back);
+            }
             const int bq = plan(q, T, true);
             if (lfg_launch(lfg::EPI_QKV, bq, &m->xh, &m->xl, &m->wqkv[bq / 256], &q, 1, 1, s) != cudaSuccess) return 1;
-            if (g.hd == 128) {
+            if (a->q4.kc) {
+                if (attn_q4(a, l, T, pos0, s) != cudaSuccess) return 1;
+            } else if (g.hd == 128) {
                 if (lfa_launch(&m->kc, &m->vc, w.Qr, T, pos0, l, g, a->win, w.Ah, w.Al, a->status,
                                l == 1 && t0 == 0 ? a->attn_stamps : nullptr, s) != cudaSuccess)
                     return 1;

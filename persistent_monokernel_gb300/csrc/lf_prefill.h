@@ -8,6 +8,7 @@
 #include <cuda.h>
 
 #include "lf_internal.cuh"
+#include "lf_kv4.h"
 
 // Device scratch of one block of T <= block positions (all row-major).
 struct lfp_workspace {
@@ -62,6 +63,14 @@ struct lfp_args {
     // block ([grid][8]; profiling aid, null = off)
     unsigned long long *attn_stamps;
     lfp_workspace ws;
+    // 4-bit cache (q4.kc not null; kc and vc are null): layer 0's cache, a layer's bytes, the block's K and V
+    // [Hkv][block][hd] before they are quantised (group-swizzled by position), windows on the host (or null), scratch
+    lfq::Cache q4;
+    size_t q4_codes, q4_scales;
+    __half *q4_k, *q4_v;
+    const int *q4_win;
+    float *q4_ws;
+    size_t q4_floats;
 };
 
 // TMA tensor maps of the GEMM operands (built once per handle: the workspace
