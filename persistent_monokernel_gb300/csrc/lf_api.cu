@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -420,8 +421,8 @@ lfk::Params base_params(lf_handle *h)
     p.lm_rows_max = h->lm_rows_max;
     p.attn_min_len = h->attn_min_len;
     p.sched = h->sched;
-    p.only_layer = -1;
-    p.only_stage = -1;
+    p.sub_lo = 0;
+    p.sub_hi = INT_MAX;
     p.trace = h->trace;
     p.trace_steps = h->trace_steps;
     return p;
@@ -479,14 +480,15 @@ lf_status run_steps_kv4(lf_handle *h, const lfk::Params &p, cudaStream_t stream)
 {
     for (int i = 0; i < p.n_steps; ++i) {
         lfk::Params q = one_step(h, p, i);
-        q.only_stage = lfk::STAGE_SEGMENT;
         // the FP16 K and V rows of this position, whatever it is, go to kc / vc [L][Hkv][hd]
         q.g.max_seq = 1;
         const uintptr_t back = (uintptr_t)q.pos0 * h->g.hd * sizeof(__half);
         q.kc = reinterpret_cast<__half *>(reinterpret_cast<uintptr_t>(h->kc) - back);
         q.vc = reinterpret_cast<__half *>(reinterpret_cast<uintptr_t>(h->vc) - back);
         for (int l = -1; l < h->g.L; ++l) {
-            q.only_layer = l;
+            // O, gate/up and down of layer l, then QKV of the next one or the LM head
+            q.sub_lo = l < 0 ? 0 : 5 * l + 2;
+            q.sub_hi = 5 * (l + 1) + 1;
             lf_status st = launch(h, q, stream);
             if (st == LF_OK && l + 1 < h->g.L) st = kv4_attention(h, l + 1, q.pos0, q.epoch0, stream);
             if (st != LF_OK) return st;
@@ -507,15 +509,15 @@ lf_status run_steps(lf_handle *h, lfk::Params p, cudaStream_t stream)
         lfk::Params q = one_step(h, p, i);
         for (int l = 0; l < L; ++l) {
             for (int s = 0; s < 5; ++s) {
-                q.only_layer = l;
-                q.only_stage = s;
+                q.sub_lo = 5 * l + s;
+                q.sub_hi = q.sub_lo + 1;
                 lf_status st = launch(h, q, stream);
                 if (st != LF_OK) return st;
             }
         }
         if (p.mode == lfk::MODE_DECODE) {
-            q.only_layer = 0;
-            q.only_stage = 5;
+            q.sub_lo = 5 * L;
+            q.sub_hi = 5 * L + 1;
             lf_status st = launch(h, q, stream);
             if (st != LF_OK) return st;
         }

@@ -32,7 +32,6 @@ constexpr int PART_STRIDE = TILE_ROWS + 1;  // per warp: 32 row sums + the sum o
 constexpr int MAX_SLICES = 64;        // 256-element slices of one activation vector (length <= 16384)
 
 enum Stage { ST_QKV = 0, ST_O = 1, ST_GU = 2, ST_D = 3, ST_LM = 4, N_GEMV = 5 };
-constexpr int STAGE_SEGMENT = 100;   // Params::only_stage
 enum Mode { MODE_PREFILL = 0, MODE_DECODE = 1 };
 enum Sched { SCHED_FLAGS = 0, SCHED_GRID = 1, SCHED_MULTI = 2 };
 enum StatusCode { STATUS_OK = 0, STATUS_BAD_TOKEN = 1, STATUS_TIMEOUT = 6 };
@@ -249,9 +248,10 @@ struct Params {
     int lm_rows_max;
     int attn_min_len;
     int sched;
-    // multi-kernel schedule: run only stage `only_stage` of layer `only_layer` of step 0; STAGE_SEGMENT: the stages
-    // between the attentions of layers only_layer and only_layer + 1
-    int only_layer, only_stage;
+    // sub-stages of a step that the launch runs, [sub_lo, sub_hi): stage s of layer l is 5 l + s (QKV, attention, O,
+    // gate/up, down), the LM head 5 L.  0 and INT_MAX: all of them; the multi-kernel schedule runs one per launch,
+    // a 4-bit cache those between two attentions.
+    int sub_lo, sub_hi;
     // optional %globaltimer trace: [step][slot][cta][4] (slot = 5 * layer + stage, LM = 5 * L)
     unsigned long long *trace;
     int trace_steps;

@@ -102,19 +102,9 @@ struct Ctx {
     int tid, warp, lane;
 };
 
-// Stage ids for the multi-kernel schedule's stage filter.
-enum { SID_QKV = 0, SID_ATTN = 1, SID_O = 2, SID_GU = 3, SID_D = 4, SID_LM = 5, SID_SEGMENT = STAGE_SEGMENT };
-
-__device__ __forceinline__ bool stage_active(const Params &p, int layer, int sid)
-{
-    if (p.only_stage < 0) return true;
-    // the segment between two attentions that run as launches of their own (4-bit cache): O, gate/up and down of
-    // layer only_layer, then QKV of the next one, or the LM head
-    if (p.only_stage == SID_SEGMENT)
-        return sid == SID_LM ? p.only_layer == p.g.L - 1
-                             : sid == SID_QKV ? layer == p.only_layer + 1 : sid != SID_ATTN && layer == p.only_layer;
-    return p.only_stage == sid && (sid == SID_LM || p.only_layer == layer);
-}
+// Stages of a layer, in the order of the sub-stages (sub-stage k: stage k % 5 of layer k / 5; the last one is the
+// LM head).
+enum { SID_QKV = 0, SID_ATTN = 1, SID_O = 2, SID_GU = 3, SID_D = 4, SID_LM = 5 };
 
 __device__ __forceinline__ void trace_mark(const Ctx &c, int step, int slot, int stamp)
 {
@@ -1244,14 +1234,14 @@ __device__ void reducer(const Ctx &c)
 {
     const Params &p = *c.p;
     const Geo &g = p.g;
-    const int n_sub = 5 * g.L + (p.mode == MODE_DECODE ? 1 : 0);
+    const int n_sub = min(5 * g.L + (p.mode == MODE_DECODE ? 1 : 0), p.sub_hi);
     PipeState ps;
     for (int step = 0; step < p.n_steps; ++step) {
-        for (int k = 0; k < n_sub; ++k) {
+        for (int k = p.sub_lo; k < n_sub; ++k) {
             const bool lm = k == 5 * g.L;
             const int l = lm ? g.L - 1 : k / 5;
             const int sid = lm ? SID_LM : k % 5;
-            if (!stage_active(p, l, sid) || sid == SID_ATTN) continue;
+            if (sid == SID_ATTN) continue;
             if (reduce_stage<MOE>(c, ps, stage_of(sid), l, step, false)) return;
         }
     }
@@ -1822,7 +1812,7 @@ __device__ void consumer(const Ctx &c)
     PipeState ps;
     const bool ab = false;
     const bool decode = p.mode == MODE_DECODE;
-    const int n_sub = 5 * g.L + (decode ? 1 : 0);
+    const int n_sub = min(5 * g.L + (decode ? 1 : 0), p.sub_hi);
     // A GEMV stage has no consumer barrier, so a warp without chunks in it
     // may run ahead to the next point where the consumer warps meet (a named
     // barrier, which cannot time out).  A warp whose GEMV stage gives up (the
@@ -1831,11 +1821,10 @@ __device__ void consumer(const Ctx &c)
     // warp leaves there, or reaches the end if none is left.
     bool failed = false;
     for (int step = 0; step < p.n_steps; ++step) {
-        for (int k = 0; k < n_sub; ++k) {
+        for (int k = p.sub_lo; k < n_sub; ++k) {
             const bool lm = k == 5 * g.L;
             const int l = lm ? g.L - 1 : k / 5;
             const int sid = lm ? SID_LM : k % 5;
-            if (!stage_active(p, l, sid)) continue;
             if (failed) {
                 unsigned idx;
                 const bool meets = sid == SID_ATTN || lm || (MOE && sid == SID_GU) ||
@@ -2059,17 +2048,16 @@ __device__ void producer(const Ctx &c, const RepackSrc *w)
         pr.pol_kv = kv_read > (128ll << 20) ? policy_evict_first() : policy_evict_normal();
     }
     bool ok = true;
-    const int n_sub = 5 * g.L + (p.mode == MODE_DECODE ? 1 : 0);
+    const int n_sub = min(5 * g.L + (p.mode == MODE_DECODE ? 1 : 0), p.sub_hi);
     unsigned routes = 0;   // expert choices consumed (mixture of experts)
     for (int step = 0; step < p.n_steps && ok; ++step) {
         step_now = step;
         const unsigned e = p.epoch0 + (unsigned)step;
         const int pos = p.pos0 + step;
-        for (int k = 0; k < n_sub && ok; ++k) {
+        for (int k = p.sub_lo; k < n_sub && ok; ++k) {
             const bool lm = k == 5 * g.L;
             const int l = lm ? 0 : k / 5;
             const int sid = lm ? SID_LM : k % 5;
-            if (!stage_active(p, l, sid)) continue;
             trace_mark_producer(c, step, k, TR_P0);
             if (sid != SID_ATTN) {
                 const int st = sid == SID_QKV ? ST_QKV : sid == SID_O ? ST_O : sid == SID_GU ? ST_GU

@@ -23,6 +23,7 @@
 // no queued copy or kernel still uses the array when the call returns.
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstring>
 
@@ -258,8 +259,8 @@ extern "C" LF_API lf_status lf_generate_noalloc(const lf_config *cfg, const lf_w
     p.lm_rows_max = lm_rows_max;
     p.attn_min_len = kAttnMinLen;
     p.sched = lfk::SCHED_FLAGS;
-    p.only_layer = -1;
-    p.only_stage = -1;
+    p.sub_lo = 0;
+    p.sub_hi = INT_MAX;
 
     // ---- prefill: forward passes of prompt[0 .. n_prompt-2]
     if (n_prompt > 1) {
