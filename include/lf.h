@@ -411,7 +411,7 @@ LF_API lf_status lf_generate_noalloc(const lf_config *cfg, const lf_weights *w, 
 typedef struct {
     int32_t n_kv_heads;      /* 1 .. 1024 */
     int32_t head_dim;        /* 64 or 128 */
-    int32_t max_seq;         /* capacity in positions */
+    int32_t max_seq;         /* capacity in positions, 1 .. 2^30 */
     /* device buffers, each 16-byte aligned and position-major per KV head:
      * codes uint8 [n_kv_heads, max_seq, head_dim / 2], element 2i in the low
      * nibble of byte i; scales uint8 (E4M3) [n_kv_heads, max_seq, head_dim / 16] */
@@ -432,7 +432,8 @@ typedef struct {
 /* Quantise rows k and v [n][n_kv_heads][head_dim] (one dtype) into positions
  * pos .. pos + n - 1; other positions keep their bytes.  n = 0 does nothing.
  * Errors: INVALID_ARG (NULL, alignment, negative sizes, differing dtypes),
- * NOT_SUPPORTED (head_dim, n_kv_heads, dtype), CAPACITY (pos + n > max_seq), CUDA. */
+ * NOT_SUPPORTED (head_dim, n_kv_heads, max_seq, dtype), CAPACITY (pos + n >
+ * max_seq), CUDA. */
 LF_API lf_status lf_kv4_append(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int32_t n, int32_t pos,
                                void *stream);
 
@@ -470,9 +471,9 @@ LF_API lf_status lf_kv4_workspace(const lf_kv4 *c, const lf_kv4_query *q, int64_
  * and holds nothing between calls; calls that may run at the same time need
  * one each.  Errors: INVALID_ARG (NULL, alignment, negative sizes, a scale
  * that is not finite, differing dtypes, out = q, a workspace that is too
- * small), NOT_SUPPORTED (head_dim, n_kv_heads, dtype, n_heads no multiple of
- * n_kv_heads, n * n_heads / n_kv_heads above 2^28), CAPACITY (length >
- * max_seq), CUDA. */
+ * small), NOT_SUPPORTED (head_dim, n_kv_heads, max_seq, dtype, n_heads no
+ * multiple of n_kv_heads, pos + n above 2^30, n * n_heads / n_kv_heads above
+ * 2^28), CAPACITY (length > max_seq), CUDA. */
 LF_API lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *workspace, int64_t workspace_bytes,
                                void *stream);
 

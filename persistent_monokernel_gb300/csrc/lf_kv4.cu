@@ -14,7 +14,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <climits>
 #include <cmath>
 
 #include "../../include/lf.h"
@@ -720,6 +719,7 @@ namespace {
 using namespace lfq;
 
 constexpr int kMaxKvHeads = 1024;
+constexpr int kMaxPositions = 1 << 30;   // positions rounded up to whole splits stay in 32 bits
 
 lf_status status_of(cudaError_t e)
 {
@@ -734,7 +734,7 @@ lf_status check_cache(const lf_kv4 *c)
 {
     if (!c || c->n_kv_heads < 1 || c->max_seq < 1) return LF_ERR_INVALID_ARG;
     if (c->head_dim != 64 && c->head_dim != 128) return LF_ERR_NOT_SUPPORTED;
-    if (c->n_kv_heads > kMaxKvHeads) return LF_ERR_NOT_SUPPORTED;
+    if (c->n_kv_heads > kMaxKvHeads || c->max_seq > kMaxPositions) return LF_ERR_NOT_SUPPORTED;
     if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
         return LF_ERR_INVALID_ARG;
     return LF_OK;
@@ -806,8 +806,7 @@ lf_status make_attn(const lf_kv4 *c, const lf_kv4_query *q, Attn *a, size_t *flo
     if (q->length > c->max_seq) return LF_ERR_CAPACITY;
     if (q->n_heads % c->n_kv_heads) return LF_ERR_NOT_SUPPORTED;
     const int G = q->n_heads / c->n_kv_heads;
-    // rows per KV head and positions stay in 31 bits with room to spare
-    if ((long long)q->n * G > (1ll << 28) || (long long)q->pos + q->n > INT_MAX - 1024) return LF_ERR_NOT_SUPPORTED;
+    if ((long long)q->n * G > (1ll << 28) || (long long)q->pos + q->n > kMaxPositions) return LF_ERR_NOT_SUPPORTED;
     a->c = cache_of(c);
     a->Hq = q->n_heads;
     a->G = G;

@@ -27,6 +27,7 @@ class lf_kv4_query(C.Structure):
 
 F16, BF16, F32 = 0, 1, 2
 BLOCK = 16          # values that share a scale
+_INT = 2 ** 31
 _byref = C.byref
 _torch = _lib = _append = _read = _attend = _codes = _raw_stream = _current_device = None
 # The argument structures as bytes, packed in one call (a ctypes structure takes a microsecond to fill, and a decode
@@ -99,6 +100,7 @@ class KV4Cache:
         self._c = lf_kv4(h, 2 * half, s, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                          v_scales.data_ptr())
         self._ref, self._addr = _byref(self._c), C.addressof(self._c)
+        self._scratch = None, 0     # shape of the last query that needed scratch, and how much
 
     @property
     def nbytes(self) -> int:
@@ -131,6 +133,8 @@ class KV4Cache:
         if stream is not None or _current_device() != self._index:
             return self._elsewhere(self.append, stream, (k, v, pos))
         n, h = k.shape[0], self.n_kv_heads
+        if not -_INT < pos < _INT:
+            raise ValueError(f"pos {pos}: 32 bits are needed")
         status = _append(self._addr, _ROWS.pack(*self._rows(k, n, h, "k")), _ROWS.pack(*self._rows(v, n, h, "v")), n, pos,
                          _raw_stream(self._index))
         if status:
@@ -142,6 +146,8 @@ class KV4Cache:
         if stream is not None or _current_device() != self._index:
             return self._elsewhere(self.read, stream, (pos, n, dtype, out))
         h = self.n_kv_heads
+        if not (-_INT < pos < _INT and -_INT < n < _INT):
+            raise ValueError(f"pos {pos}, n {n}: 32 bits are needed")
         if out is None:
             shape, dtype = (max(n, 0), h, self.head_dim), dtype or _torch.float16
             k = _torch.empty(shape, dtype=dtype, device=self.device)
@@ -166,23 +172,38 @@ class KV4Cache:
         rows = self._rows(q, n, heads, "q")
         if out is None:
             out = _torch.empty(shape, dtype=q.dtype, device=self.device)
-        args = _QUERY.pack(*rows, *self._rows(out, n, heads, "out"), heads, n, pos, pos + n if length is None else length,
-                           window, scale)
-        status = _attend(self._addr, args, None, 0, _raw_stream(self._index))
+        try:
+            args = _QUERY.pack(*rows, *self._rows(out, n, heads, "out"), heads, n, pos, pos + n if length is None else length,
+                               window, scale)
+        except struct.error as err:
+            raise ValueError(f"pos {pos}, length {length}, window {window}, scale {scale}: {err}") from None
+        # Scratch (long contexts and large blocks need some) belongs to this call alone: no two streams or captured
+        # graphs share it.  Its size is asked for when a call like the last one turns out not to have enough.
+        key, size = self._scratch
+        if key != (n, heads):
+            size = 0
+        ws = _torch.empty((size,), dtype=_torch.uint8, device=self.device).data_ptr() if size else None
+        status = _attend(self._addr, args, ws, size, _raw_stream(self._index))
         if status:
-            status = self._attend_with_workspace(args, status)
+            status = self._attend_with_workspace(args, status, (n, heads))
             if status:
                 _fail(status, "lf_kv4_attend")
         return out
 
-    def _attend_with_workspace(self, args, status):
-        """The call again with the scratch it needs, if that is what it lacked (long contexts and large blocks)."""
+    def _attend_with_workspace(self, args, status, key):
+        """The call again with the scratch it needs, if that is what it lacked."""
         query, need = lf_kv4_query.from_buffer_copy(args), C.c_int64()
         if _lib.lf_kv4_workspace(self._ref, _byref(query), _byref(need)) or not need.value:
             return status
-        # scratch of this call alone: no two streams or captured graphs share it
+        self._scratch = key, need.value
         ws = _torch.empty((need.value,), dtype=_torch.uint8, device=self.device)
         return _attend(self._addr, args, ws.data_ptr(), need.value, _raw_stream(self._index))
+
+    def sync(self) -> int:
+        """Synchronise the current stream of the cache's device: 0, or LF_ERR_TIMEOUT (6) if a device-side wait of an
+        attend call ran out since the last sync (lf_kv4_status)."""
+        with _torch.cuda.device(self.device):
+            return int(_lib.lf_kv4_status(_raw_stream(self._index)))
 
 
 def _fail(status: int, where: str) -> None:

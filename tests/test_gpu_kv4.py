@@ -323,3 +323,75 @@ def test_two_streams_at_once(pm):
             got += [(i, cache.attend(q, 3800, stream=s)) for i, q in enumerate(qs)]
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[i]) for i, o in got)
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    """Kernels that no call has loaded yet, recorded at once."""
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+    code = """
+import torch, persistent_monokernel_gb300 as pm
+cache = pm.KV4Cache(2, 128, 6000)
+k = torch.randn(5000, 2, 128, device="cuda").half()
+q, b = torch.randn(1, 8, 128, device="cuda").half(), torch.randn(100, 8, 128, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    cache.append(k, k, 0)
+    outs = cache.attend(q, 4999), cache.attend(b, 4900), cache.read(7, 9)[0]
+g.replay()
+torch.cuda.synchronize()
+assert cache.sync() == 0
+want = cache.attend(q, 4999), cache.attend(b, 4900), cache.read(7, 9)[0]
+assert all(torch.equal(x, y) and y.abs().sum() > 0 for x, y in zip(outs, want))
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT, timeout=300)
+
+
+def test_refusals_in_python(pm):
+    cache = pm.KV4Cache(2, 64, 32)
+    x = torch.randn(4, 2, 64, device="cuda").half()
+    q = torch.randn(4, 8, 64, device="cuda").half()
+    for bad in (x.cpu(), x[:, :1], x[:, :, :32], x.double(), x.transpose(1, 2).contiguous().transpose(1, 2), x[:3]):
+        with pytest.raises(ValueError):
+            cache.append(x, bad, 0)
+    odd = torch.empty(4 * 2 * 64 + 1, dtype=torch.float16, device="cuda")[1:].view(4, 2, 64)
+    for call in (lambda: cache.append(x, odd, 0), lambda: cache.append(x, x, 30), lambda: cache.append(x, x, -1),
+                 lambda: cache.append(x, x.float(), 0), lambda: cache.read(30, 4), lambda: cache.read(0, -1),
+                 lambda: cache.read(0, 4, out=(x, x[:1].expand(4, 2, 64))), lambda: cache.attend(q, 30),
+                 lambda: cache.attend(q, 0, length=33), lambda: cache.attend(q, -1), lambda: cache.attend(q, 0, window=-1),
+                 lambda: cache.attend(q, 0, scale=math.inf), lambda: cache.attend(q[:, :3], 0),
+                 lambda: cache.attend(q, 0, out=q)):
+        with pytest.raises(pm.LFError):
+            call()
+    for call in (lambda: cache.append(x, x, 2 ** 32), lambda: cache.read(2 ** 32, 1), lambda: cache.attend(q, 2 ** 32),
+                 lambda: cache.read(0, 4, torch.float64), lambda: cache.attend(q, 0, out=q[:3]),
+                 lambda: cache.attend(q, 0, out=q.float().half()[..., :32])):
+        with pytest.raises((ValueError, pm.LFError)):
+            call()
+    assert cache.sync() == 0
+    assert (cache.k_codes == 0).all() and (cache.v_scales == 0).all()
+
+
+def test_on_a_stream_that_is_not_the_current_one(pm):
+    """Inputs made, appended, attended to and read on a side stream, while the current one is busy."""
+    s = torch.cuda.Stream()
+    cache, _ = filled(pm, 5, 128, 9000, 2)
+    qkv = torch.randn(1, 30, 128, generator=gen(1), device="cuda").half()
+    q, k, v = qkv.split((20, 5, 5), 1)
+    cache.append(k, v, 8990)
+    want, row = cache.attend(q, 8990), cache.read(8990, 1)[0]
+    busy = torch.randn(6000, 6000, device="cuda")
+    for p in (cache.k_codes, cache.v_codes):
+        p[:, 8990] = 0
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        busy = busy @ busy
+        busy /= busy.abs().max()
+    cache.append(k, v, 8990, stream=s)
+    out = cache.attend(q, 8990, stream=s)
+    got = cache.read(8990, 1, stream=s)[0]
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(got, row)

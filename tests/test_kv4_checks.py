@@ -29,7 +29,7 @@ def rows(pm, **over):
 
 
 CACHES = [(dict(n_kv_heads=0), INVALID), (dict(max_seq=0), INVALID), (dict(head_dim=96), UNSUPPORTED),
-          (dict(head_dim=256), UNSUPPORTED), (dict(n_kv_heads=1025), UNSUPPORTED), (dict(k_codes=0), INVALID),
+          (dict(head_dim=256), UNSUPPORTED), (dict(n_kv_heads=1025), UNSUPPORTED), (dict(max_seq=2 ** 30 + 1), UNSUPPORTED), (dict(k_codes=0), INVALID),
           (dict(v_scales=P + 8), INVALID), (dict(v_codes=P + 4), INVALID), (dict(k_scales=None), INVALID)]
 
 
@@ -82,7 +82,7 @@ def test_k_and_v_of_one_dtype(pm):
 QUERIES = [(dict(n_heads=0), INVALID), (dict(n_heads=3), UNSUPPORTED), (dict(n=-1), INVALID), (dict(pos=-1), INVALID),
            (dict(length=-1), INVALID), (dict(length=65), CAPACITY), (dict(window=-1), INVALID),
            (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
-           (dict(n=1 << 28, n_heads=4), UNSUPPORTED), (dict(pos=2 ** 31 - 5), UNSUPPORTED), (dict(n=0), OK)]
+           (dict(n=1 << 28, n_heads=4), UNSUPPORTED), (dict(pos=2 ** 31 - 5), UNSUPPORTED), (dict(pos=2 ** 30 - 1), UNSUPPORTED), (dict(n=0), OK)]
 
 
 @pytest.mark.parametrize("over,status", QUERIES)
@@ -127,3 +127,14 @@ def test_host_tensors_are_refused(pm):
         pm.KV4Cache.wrap(*z)
     with pytest.raises(ValueError):
         pm.KV4Cache.wrap(z[0][0], *z[1:])
+
+
+def test_a_decoder_on_the_4_bit_cache_checks_its_arguments_like_lf_create(pm):
+    L, h = pm.lib(), C.c_void_p()
+    w = pm.lf_weights(*([0x1000] * 12))
+    good = dict(n_layers=2, d_model=256, n_heads=4, n_kv_heads=4, head_dim=64, ffn_dim=1024, vocab=4096, max_seq=64,
+                rope_theta=10000.0, rms_eps=1e-5, fault_step=-1)
+    for change, status in ((dict(head_dim=96), UNSUPPORTED), (dict(max_seq=0), INVALID), (dict(prefill_block=-2), INVALID)):
+        cfg = pm.lf_config(**{**good, **change})
+        assert L.lf_create_kv4(C.byref(cfg), C.byref(w), C.byref(h)) == status
+    assert L.lf_create_kv4(None, C.byref(w), C.byref(h)) == INVALID
