@@ -98,8 +98,7 @@ struct lf_handle {
     bool kv4 = false;
     uint8_t *q4_kc = nullptr, *q4_ks = nullptr, *q4_vc = nullptr, *q4_vs = nullptr;
     size_t q4_codes = 0, q4_scales = 0;   // bytes of one layer
-    float *q4_ws = nullptr;
-    size_t q4_floats = 0;
+    uint8_t *q4_ws = nullptr;
     __half *q4_stage = nullptr;
     std::vector<int> h_win;
 };
@@ -214,7 +213,6 @@ lfp_args prefill_args(const lf_handle *h)
     a.q4_k = a.q4_v = nullptr;
     a.q4_win = h->h_win.empty() ? nullptr : h->h_win.data();
     a.q4_ws = h->q4_ws;
-    a.q4_floats = h->q4_floats;
     if (h->kv4) {
         a.kc = a.vc = nullptr;
         a.q4_k = h->q4_stage;
@@ -470,7 +468,8 @@ lf_status kv4_attention(lf_handle *h, int l, int pos, unsigned epoch, cudaStream
     a.len = pos + 1;
     a.win = h->h_win.empty() ? 0 : h->h_win[l];
     a.scale = 1.0f / std::sqrt((float)g.hd);
-    a.part = lfq::plan_attn(a, h->sm_count, h->q4_floats) ? h->q4_ws : nullptr;
+    const size_t need = lfq::plan_attn(a, h->sm_count);
+    lfq::set_workspace(a, need ? h->q4_ws : nullptr);
     if (e == cudaSuccess) e = lfq::launch_attn(a, s);
     return from_cuda(e);
 }
@@ -716,21 +715,14 @@ static lf_status create(const lf_config *cfg, const lf_weights *w, lf_handle **o
         const size_t rows = (size_t)g.Hkv * g.max_seq;
         h->q4_codes = rows * lfq::code_bytes(g.hd);
         h->q4_scales = rows * lfq::scale_bytes(g.hd);
-        lfq::Attn a = {};
-        a.c = {nullptr, nullptr, nullptr, nullptr, g.Hkv, g.hd, g.max_seq};
-        a.q.dtype = lfq::F32;
-        a.Hq = g.Hq;
-        a.G = g.group;
-        a.n = std::min(1024, g.max_seq);
-        a.pos = g.max_seq - a.n;
-        a.len = g.max_seq;
-        h->q4_floats = lfq::min_workspace(a.c, h->sm_count);
-        if (cfg->prefill_block != 0) h->q4_floats = std::max(h->q4_floats, lfq::plan_attn(a, h->sm_count));
+        const lfq::Cache c = {nullptr, nullptr, nullptr, nullptr, g.Hkv, g.hd, g.max_seq};
+        const int rows_most = cfg->prefill_block == 0 ? 1 : cfg->prefill_block > 0 ? std::min(cfg->prefill_block, g.max_seq)
+                                                                                  : std::min(1024, g.max_seq);
         e = dalloc(&h->q4_kc, h->q4_codes * g.L);
         if (e == cudaSuccess) e = dalloc(&h->q4_vc, h->q4_codes * g.L);
         if (e == cudaSuccess) e = dalloc(&h->q4_ks, h->q4_scales * g.L);
         if (e == cudaSuccess) e = dalloc(&h->q4_vs, h->q4_scales * g.L);
-        if (e == cudaSuccess) e = dalloc(&h->q4_ws, h->q4_floats);
+        if (e == cudaSuccess) e = dalloc(&h->q4_ws, lfq::max_workspace(c, g.Hq, rows_most, h->sm_count));
         if (e == cudaSuccess) e = cudaMemset(h->q4_kc, 0, h->q4_codes * g.L);
         if (e == cudaSuccess) e = cudaMemset(h->q4_vc, 0, h->q4_codes * g.L);
         if (e == cudaSuccess) e = cudaMemset(h->q4_ks, 0, h->q4_scales * g.L);

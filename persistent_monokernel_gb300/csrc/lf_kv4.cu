@@ -507,14 +507,20 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant_
     const int grp = threadIdx.x / lanes % groups, d = threadIdx.x % lanes * 4;
     wait_for_prerequisites();
     Joined j;
+    int parts = 0;
     if (row < a.n * a.G) {
-        const size_t step = (size_t)a.rt * (hd + PAD);
-        const int parts = a.splits / a.cl;
-        const float *part = a.part + ((size_t)((size_t)kvh * a.tiles + row / a.rt) * parts * a.rt + row % a.rt) * (hd + PAD);
+        // state s of the row's tile: number at(s) of all
+        const size_t tile = (size_t)kvh * a.tiles + row / a.rt, step = (size_t)a.rt * (hd + PAD);
+        const int2 pc = a.pieces ? __ldcg(a.pieces + tile) : make_int2(0, a.splits / a.cl);
+        parts = pc.y;
+        const float *part = a.part + (size_t)(row % a.rt) * (hd + PAD);
 #pragma unroll 4
-        for (int s = grp; s < parts; s += groups)
-            j.add(__ldcg(reinterpret_cast<const float2 *>(part + s * step + hd)),
-                  __ldcg(reinterpret_cast<const float4 *>(part + s * step + d)));
+        for (int s = grp; s < parts; s += groups) {
+            // a CTA's second place holds the tile that it begins and leaves, its first the one it goes on with
+            const size_t at = a.pieces ? 2 * (size_t)(pc.x + s) + (s == 0 ? 1 : 0) : tile * parts + s;
+            j.add(__ldcg(reinterpret_cast<const float2 *>(part + at * step + hd)),
+                  __ldcg(reinterpret_cast<const float4 *>(part + at * step + d)));
+        }
     }
     if (groups > 1) {
         float *x = sh[threadIdx.x];
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant_
             j.add(make_float2(y[4], y[5]), make_float4(y[0], y[1], y[2], y[3]));
         }
     }
-    if (row < a.n * a.G) j.store(a, row, kvh, d);
+    if (parts) j.store(a, row, kvh, d);   // (a tile of one piece has its output)
 }
 
 // ---------------------------------------------------------------- launches
@@ -536,47 +542,105 @@ constexpr int kClusterChunks = 4;
 // Rows per KV head from which the tiles kernel takes over.
 constexpr int kTileRows = 33;
 
-static void plan_tiles(Attn &a, int sms, int rows, int hi, size_t limit)
+// Workspace of the tiles kernel: two states per CTA, and where each tile's are.
+static size_t tiles_workspace(const Cache &c, size_t ctas, size_t tiles)
 {
-    constexpr int BN = 128;
-    a.rt = 128;
-    a.tiles = (rows + a.rt - 1) / a.rt;
-    a.lo = a.lo / BN * BN;
-    const int chunks = std::max(1, (hi - a.lo + BN - 1) / BN);
-    // One CTA per SM at a time.  In units of a chunk's time (about 1.2 us): each wave costs its CTAs' chunks
-    // and about two for their start and end; splits cost the partial states written and read at about 6.5 TB/s
-    // and the join's launch.
-    const long long ctas = (long long)a.tiles * a.c.Hkv;
-    double best = 1e30;
-    a.splits = 1;
-    for (int s = 1; s <= chunks && s <= 64; ++s) {
-        const int per = (chunks + s - 1) / s, n = (chunks + per - 1) / per;
-        if (n > 1 && (double)ctas * n * a.rt * (a.c.hd + PAD) > (double)limit) break;
-        const double waves = (double)((ctas * n + sms - 1) / sms);
-        const double join = n > 1 ? 2.0 + 2.0 * rows * a.c.Hkv * n * (a.c.hd + PAD) * 4.0 / 6.5e12 / 1.2e-6 : 0.0;
-        const double cost = waves * (per + 2.0) + join;
-        if (cost < best * 0.98) {
-            best = cost;
-            a.splits = n;
-        }
-    }
-    const int per = (chunks + a.splits - 1) / a.splits;
-    a.splits = (chunks + per - 1) / per;
-    a.per = per * BN;
+    return (2 * ctas * 128 * (c.hd + PAD)) * sizeof(float) + tiles * sizeof(int2);
 }
 
-size_t min_workspace(const Cache &c, int sms) { return (size_t)2 * sms * 16 * (c.hd + PAD); }
+// What a tile, or a piece of one, costs beside its chunks, in chunks (about 1 us each, 1.5 in FP32): q, the first
+// chunk's latency, the output.
+static int piece_cost(const Attn &a) { return a.q.dtype == F32 ? 4 : 5; }
 
-size_t plan_attn(Attn &a, int sms, size_t limit)
+int share_tiles(const Attn &a, int ctas, Shares &sh)
+{
+    const int all = a.tiles * a.c.Hkv, extra = piece_cost(a);
+    if (ctas == 0) {
+        for (int c = 0; c <= all; ++c) sh.at[c] = {c, 0, 0};
+        return all;
+    }
+    int first;
+    long long left = 0;   // the cost of what is not dealt out yet
+    for (int t = 0; t < a.tiles; ++t) left += tile_chunks(a, t, first) + extra;
+    left *= a.c.Hkv;
+    Share at = {0, 0, 0};
+    for (int c = 0; c < ctas; ++c) {
+        sh.at[c] = at;
+        // an even part of it, and the piece that the cut at its end makes
+        const long long budget = (left + ctas - c - 1) / (ctas - c) + extra;
+        long long spent = 0;
+        while (at.tile < all) {
+            const int have = tile_chunks(a, at.tile % a.tiles, first) - at.skip;
+            const int room = (int)std::min<long long>(budget - spent - extra, have);
+            if (have <= room + 1 || (spent == 0 && have <= 3) || c == ctas - 1) {   // the rest of the tile
+                spent += have + extra;
+                left -= have + extra;
+                at = {at.tile + 1, 0, 0};
+            } else if (room < 2 && spent > 0) {              // too little left to begin another tile
+                break;
+            } else {
+                const int take = std::max(room, 2);          // have is more
+                left -= take;
+                at = {at.tile, at.skip + take, at.piece + 1};
+                break;
+            }
+        }
+        if (at.tile >= all) {
+            sh.at[c + 1] = at;
+            return c + 1;
+        }
+    }
+    return ctas;   // not reached: the last CTA takes what is left
+}
+
+static size_t plan_tiles(Attn &a, int sms, int rows)
+{
+    a.rt = 128;
+    a.tiles = (rows + 127) / 128;
+    sms = std::min(sms, MAX_CTAS);
+    long long total = 0;
+    int most = 1, first;
+    for (int t = 0; t < a.tiles; ++t) {
+        const int c = tile_chunks(a, t, first);
+        total += c;
+        most = std::max(most, c);
+    }
+    total *= a.c.Hkv;
+    // One CTA per SM.  Either every tile has a CTA of its own, or all SMs share the work evenly, cutting tiles, and
+    // a launch joins the pieces (about five and a half chunks, with the pieces written and read).
+    const long long t = (long long)a.tiles * a.c.Hkv, ctas = std::min<long long>(sms, std::max<long long>(1, total / 2));
+    const double extra = piece_cost(a), shared = (double)(total + (t + ctas) * extra) / (double)ctas + 5.5;
+    if (t <= sms && most + extra <= shared) {
+        a.splits = (int)t;
+        a.per = 0;
+        return 0;
+    }
+    Shares sh;
+    a.per = (int)ctas;
+    a.splits = share_tiles(a, a.per, sh);
+    return tiles_workspace(a.c, (size_t)a.splits, (size_t)t);
+}
+
+size_t max_workspace(const Cache &c, int Hq, int n, int sms)
+{
+    const size_t rows = (size_t)n * (Hq / c.Hkv);
+    return std::max((size_t)2 * sms * 16 * (c.hd + PAD) * sizeof(float),
+                    rows < (size_t)kTileRows ? (size_t)0 : tiles_workspace(c, (size_t)sms, (rows + 127) / 128 * c.Hkv));
+}
+
+void set_workspace(Attn &a, void *ws)
+{
+    a.part = static_cast<float *>(ws);
+    a.pieces = ws && a.rt == 128 ? reinterpret_cast<int2 *>(a.part + (size_t)2 * a.splits * 128 * (a.c.hd + PAD)) : nullptr;
+}
+
+size_t plan_attn(Attn &a, int sms)
 {
     const int rows = a.n * a.G, hi = key_hi(a.pos, a.n - 1, a.len);
     a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
-    const size_t state = (size_t)a.c.Hkv * (a.c.hd + PAD);
+    const size_t state = (size_t)a.c.Hkv * (a.c.hd + PAD) * sizeof(float);
     a.cl = 1;
-    if (rows >= kTileRows) {
-        plan_tiles(a, sms, rows, hi, limit);
-        return a.splits > 1 ? state * a.tiles * a.rt * a.splits : 0;
-    }
+    if (rows >= kTileRows) return plan_tiles(a, sms, rows);
     a.rt = rows <= 8 ? 8 : 16;
     a.tiles = (rows + a.rt - 1) / a.rt;
     const int chunks = std::max(1, (hi - a.lo + CH - 1) / CH);
@@ -700,7 +764,7 @@ cudaError_t launch_attn(const Attn &a, cudaStream_t s)
     else
         e = a.rt == 8 ? (split ? run_rows<64, 1, true>(a, s) : run_rows<64, 1, false>(a, s))
                       : (split ? run_rows<64, 2, true>(a, s) : run_rows<64, 2, false>(a, s));
-    if (e == cudaSuccess && a.splits > a.cl) {
+    if (e == cudaSuccess && a.part) {
         // few rows: the splits of a row are spread over a whole block; many: one group each, the traffic counts
         const int lanes = a.c.hd / 4, rows = a.n * a.G;
         const int groups = (long long)rows * a.c.Hkv >= 4096 ? 1 : JOIN_THREADS / lanes;
@@ -797,7 +861,7 @@ lf_status sm_count(int *out)
     return LF_OK;
 }
 
-lf_status make_attn(const lf_kv4 *c, const lf_kv4_query *q, Attn *a, size_t *floats)
+lf_status make_attn(const lf_kv4 *c, const lf_kv4_query *q, Attn *a, size_t *bytes)
 {
     lf_status st = check_cache(c);
     if (st != LF_OK) return st;
@@ -817,12 +881,12 @@ lf_status make_attn(const lf_kv4 *c, const lf_kv4_query *q, Attn *a, size_t *flo
     if (q->q.dtype != LF_F16 && q->q.dtype != LF_BF16 && q->q.dtype != LF_F32) return LF_ERR_NOT_SUPPORTED;
     a->q = rows_of(&q->q);
     a->scale = q->scale != 0.f ? q->scale : 1.0f / std::sqrt((float)c->head_dim);
-    a->part = nullptr;
-    *floats = 0;
+    set_workspace(*a, nullptr);
+    *bytes = 0;
     if (q->n == 0) return LF_OK;
     int sms = 0;
     st = sm_count(&sms);
-    if (st == LF_OK) *floats = plan_attn(*a, sms);
+    if (st == LF_OK) *bytes = plan_attn(*a, sms);
     return st;
 }
 
@@ -847,26 +911,26 @@ lf_status lf_kv4_read(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int32
 lf_status lf_kv4_workspace(const lf_kv4 *c, const lf_kv4_query *q, int64_t *bytes)
 {
     if (!bytes) return LF_ERR_INVALID_ARG;
-    Attn a;
-    size_t floats = 0;
-    const lf_status st = make_attn(c, q, &a, &floats);
-    if (st == LF_OK) *bytes = (int64_t)(floats * sizeof(float));
+    Attn a = {};
+    size_t need = 0;
+    const lf_status st = make_attn(c, q, &a, &need);
+    if (st == LF_OK) *bytes = (int64_t)need;
     return st;
 }
 
 lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *workspace, int64_t workspace_bytes, void *stream)
 {
-    Attn a;
-    size_t floats = 0;
-    lf_status st = make_attn(c, q, &a, &floats);
+    Attn a = {};
+    size_t need = 0;
+    lf_status st = make_attn(c, q, &a, &need);
     if (st != LF_OK || a.n == 0) return st;
     st = check_rows(&q->q, a.n, a.Hq, c->head_dim, false);
     if (st == LF_OK) st = check_rows(&q->out, a.n, a.Hq, c->head_dim, true);
     if (st != LF_OK) return st;
     if (q->q.dtype != q->out.dtype || q->q.data == q->out.data) return LF_ERR_INVALID_ARG;
-    if (floats && (!aligned16(workspace) || workspace_bytes < (int64_t)(floats * sizeof(float)))) return LF_ERR_INVALID_ARG;
+    if (need && (!aligned16(workspace) || workspace_bytes < (int64_t)need)) return LF_ERR_INVALID_ARG;
     a.o = rows_of(&q->out);
-    a.part = floats ? static_cast<float *>(workspace) : nullptr;
+    set_workspace(a, need ? workspace : nullptr);
     return status_of(launch_attn(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -42,11 +42,16 @@ struct Attn {
     int n, pos;             // query rows at positions pos .. pos + n - 1
     int len, win;           // keys 0 .. len - 1; window (0: all)
     float scale;
-    // plan: row tiles of rt query rows (n * G rows per KV head, row r = token r / G, head r % G), each over
-    // `splits` ranges of `per` positions from lo on; `cl` ranges in a row are one cluster, which joins them into
-    // one of splits / cl partial states
+    // plan: row tiles of rt query rows (n * G rows per KV head, row r = token r / G, head r % G).
+    // rt 8 or 16: each over `splits` ranges of `per` positions from lo on; `cl` ranges in a row are one cluster,
+    // which joins them into one of splits / cl partial states.
+    // rt 128: `splits` CTAs share all chunks of all tiles (share_tiles of `per` CTAs; 0: one tile each).
     int rt, tiles, splits, cl, per, lo;
-    float *part;            // [Hkv * tiles * splits / cl][rt][hd + PAD]: O, then m and l; null: one partial state
+    // partial states [..][rt][hd + PAD]: O, then m and l (null: none).  rt 8 or 16: [Hkv * tiles * splits / cl];
+    // rt 128: two per CTA, for the tile it goes on with and the tile it leaves unfinished, and where a tile's are:
+    // pieces[Hkv * tiles] = (first CTA, number of pieces or 0).
+    float *part;
+    int2 *pieces;
 };
 
 // Keys that query row t (position pos + t) sees: [key_lo, key_hi).
@@ -56,10 +61,31 @@ __host__ __device__ inline int key_lo(int pos, int t, int win)
     return (win > 0 && pos + t + 1 > win) ? pos + t + 1 - win : 0;
 }
 
-// Fills a's plan for `sms` SMs (a.q.dtype is set) and returns the workspace floats it needs, at most `limit`
-// (which is at least min_workspace).
-size_t plan_attn(Attn &a, int sms, size_t limit = SIZE_MAX);
-size_t min_workspace(const Cache &c, int sms);
+// Chunks of 128 positions that some row of tile `tile` (of 128 rows) sees: their count, at least 1, and the first.
+__host__ __device__ inline int tile_chunks(const Attn &a, int tile, int &first)
+{
+    const int r0 = tile * 128, last = r0 + 127 < a.n * a.G ? r0 + 127 : a.n * a.G - 1;
+    const int lo = key_lo(a.pos, r0 / a.G, a.win), hi = key_hi(a.pos, last / a.G, a.len);
+    first = lo / 128;
+    return hi > lo ? (hi + 127) / 128 - first : 1;
+}
+// Where CTA c of the tiles kernel begins: tile (KV head * tiles + tile), chunks and pieces of it that are earlier CTAs'.
+struct Share {
+    int tile, skip, piece;
+};
+constexpr int MAX_CTAS = 256;
+struct Shares {
+    Share at[MAX_CTAS + 1];
+};
+// Deals the chunks of all tiles out to at most `ctas` CTAs and returns how many have any (0: one tile each).
+int share_tiles(const Attn &a, int ctas, Shares &sh);
+
+// Fills a's plan for `sms` SMs (a.q.dtype is set) and returns the workspace bytes it needs, at most
+// max_workspace for blocks of up to n rows.
+size_t plan_attn(Attn &a, int sms);
+size_t max_workspace(const Cache &c, int Hq, int n, int sms);
+// Points a at its workspace (null where the plan needs none).
+void set_workspace(Attn &a, void *ws);
 
 cudaError_t launch_append(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s);
 cudaError_t launch_read(const Cache &c, const Rows &k, const Rows &v, int n, int pos, cudaStream_t s);

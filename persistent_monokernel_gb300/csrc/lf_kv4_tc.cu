@@ -356,22 +356,43 @@ __device__ __forceinline__ float row_max(float m, const uint32_t (&u)[2][32], in
 }
 
 template <int HD, bool SPLIT>
-__global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ Attn a)
+__global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ Attn a, const __grid_constant__ Shares sh)
 {
     using C = TcCfg<HD, SPLIT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) & ~uintptr_t(1023));
     Bars *b = reinterpret_cast<Bars *>(smem + C::OFF_BAR);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x % a.splits, tile = a.tiles - 1 - blockIdx.x / a.splits;   // the longest rows first
-    const int kvh = blockIdx.y;
-    const int r0 = tile * BM, rows = min(BM, a.n * a.G - r0);
-    const int t_first = r0 / a.G, t_last = (r0 + rows - 1) / a.G;
-    // positions of this CTA: the split's, cut to what the tile's rows see
-    const int lo_t = key_lo(a.pos, t_first, a.win), hi_r = key_hi(a.pos, t_last, a.len);
-    const int hi_t = hi_r > lo_t ? hi_r : 0;              // no position at all: an empty range
-    const int p0 = max(a.lo + split * a.per, lo_t / BN * BN), p1 = min(a.lo + (split + 1) * a.per, hi_t);
-    const int nc = p1 > p0 ? (p1 - p0 + BN - 1) / BN : 0;
+    // this CTA's share of the tiles, tile by tile
+    const Share begin = sh.at[blockIdx.x], end = sh.at[blockIdx.x + 1];
+    struct Walk {
+        int tile, skip, piece;
+    };
+    struct Seg {
+        int gt, kvh, r0, rows, lo, p0, p1, nc, piece;
+        bool first, last;       // the tile's first chunks, its last ones
+    };
+    auto next = [&](Walk &w, Seg &s) -> bool {
+        if (w.tile > end.tile || (w.tile == end.tile && w.skip >= end.skip)) return false;
+        s.gt = w.tile;
+        s.kvh = w.tile / a.tiles;
+        const int tile = w.tile % a.tiles;
+        s.r0 = tile * BM;
+        s.rows = min(BM, a.n * a.G - s.r0);
+        const int t_first = s.r0 / a.G, t_last = (s.r0 + s.rows - 1) / a.G;
+        const int hi = key_hi(a.pos, t_last, a.len);
+        int c0;
+        const int all = tile_chunks(a, tile, c0), stop = w.tile == end.tile ? end.skip : all;
+        s.lo = key_lo(a.pos, t_first, a.win);
+        s.p0 = max((c0 + w.skip) * BN, s.lo / BN * BN);
+        s.p1 = hi > s.lo ? min((c0 + stop) * BN, hi) : 0;     // no position at all: an empty range
+        s.nc = s.p1 > s.p0 ? (s.p1 - s.p0 + BN - 1) / BN : 0;
+        s.first = w.skip == 0;
+        s.last = stop == all;
+        s.piece = w.piece;
+        w = {w.tile + 1, 0, 0};
+        return true;
+    };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -415,13 +436,16 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         // issues.
         const bool one = elect_one();
         const uint32_t sb = lfk::smem_u32(smem);
-        if (warp == W_MMA && nc > 0 && !dead) {
+        Walk walk = {begin.tile, begin.skip, begin.piece};
+        Seg g;
+        unsigned use0 = 0, use1 = 0;                      // chunks so far in each stage: a barrier's phases
+        if (warp == W_MMA && !dead) {
             const uint64_t kd = sdesc_kmajor_sw128(sb + C::OFF_K);
             const uint32_t klo = (uint32_t)kd, khi = (uint32_t)(kd >> 32);
             const uint32_t qlo = (uint32_t)sdesc_kmajor_sw128(sb + C::OFF_Q);
             auto step = [&](int i, auto stage) -> bool {
                 constexpr uint32_t S = decltype(stage)::value, D = tmem + S * BN;
-                const unsigned ph = (unsigned)(i >> 1) & 1u;
+                const unsigned ph = ((S ? use1 : use0) + (unsigned)(i >> 1)) & 1u;
                 if (!__all_sync(0xffffffffu, wait_both(&b->s_free[S], ph ^ 1u, &b->k_full[S], ph, b, 701))) return false;
                 fence_after_sync();
                 if (one) {
@@ -441,17 +465,20 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
                 __syncwarp();
                 return true;
             };
-            if (__all_sync(0xffffffffu, wait_phase(&b->q_ready, 0u, b, 700)))
-                for (int i = 0; i < nc; i += 2) {
-                    if (!step(i, Int<0>{})) break;
-                    if (i + 1 < nc && !step(i + 1, Int<1>{})) break;
-                }
-        } else if (warp == W_MMA + 1 && nc > 0 && !dead) {
+            bool ok = true;
+            for (unsigned n = 0; ok && next(walk, g); ++n) {
+                ok = __all_sync(0xffffffffu, wait_phase(&b->q_ready, n & 1u, b, 700));
+                for (int i = 0; ok && i < g.nc; i += 2) ok = step(i, Int<0>{}) && (i + 1 >= g.nc || step(i + 1, Int<1>{}));
+                use0 += (unsigned)(g.nc + 1) / 2;
+                use1 += (unsigned)g.nc / 2;
+            }
+        } else if (warp == W_MMA + 1 && !dead) {
             const uint64_t vd = sdesc_mn_sw128(sb + C::OFF_V, C::ATOM);
             const uint32_t vlo = (uint32_t)vd, vhi = (uint32_t)(vd >> 32);
             auto step = [&](int i, auto stage) -> bool {
                 constexpr uint32_t S = decltype(stage)::value;
-                if (!__all_sync(0xffffffffu, wait_both(&b->v_full[S], (unsigned)(i >> 1) & 1u, &b->p_full, (unsigned)i & 1u, b, 702)))
+                if (!__all_sync(0xffffffffu, wait_both(&b->v_full[S], ((S ? use1 : use0) + (unsigned)(i >> 1)) & 1u, &b->p_full,
+                                                       (use0 + use1 + (unsigned)i) & 1u, b, 702)))
                     return false;
                 fence_after_sync();
                 if (one) {
@@ -470,13 +497,15 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
                 __syncwarp();
                 return true;
             };
-            for (int i = 0; i < nc; i += 2) {
-                if (!step(i, Int<0>{})) break;
-                if (i + 1 < nc && !step(i + 1, Int<1>{})) break;
+            bool ok = true;
+            while (ok && next(walk, g)) {
+                for (int i = 0; ok && i < g.nc; i += 2) ok = step(i, Int<0>{}) && (i + 1 >= g.nc || step(i + 1, Int<1>{}));
+                use0 += (unsigned)(g.nc + 1) / 2;
+                use1 += (unsigned)g.nc / 2;
             }
         }
         // after a wait that ran out nothing may still write TMEM: one more commit by each of the lanes that issued
-        if (warp <= W_MMA + 1 && nc > 0 && !dead && one && *reinterpret_cast<volatile int *>(&b->abort)) {
+        if (warp <= W_MMA + 1 && !dead && one && *reinterpret_cast<volatile int *>(&b->abort)) {
             commit(&b->drained[warp - W_MMA]);
             settle_phase(&b->drained[warp - W_MMA], 0u);
         }
@@ -486,39 +515,50 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         setmaxnreg_dec<REG_DQ>();
         const int j = threadIdx.x & 127;
         const bool isv = warp >= W_DQ + 4;
-        const size_t row0 = (size_t)kvh * a.c.cap;
-        const uint8_t *codes = (isv ? a.c.vc : a.c.kc) + row0 * code_bytes(HD);
-        const uint8_t *scales = (isv ? a.c.vs : a.c.ks) + row0 * scale_bytes(HD);
         uint64_t *full = isv ? b->v_full : b->k_full, *empty = isv ? b->v_empty : b->k_empty;
         uint32_t at[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) at[c] = lfk::smem_u32(smem) + (isv ? C::OFF_V : C::OFF_K) + sw128(j, c);
         RawRow<HD> raw;
-        auto fetch = [&](int i) {
-            const size_t r = (size_t)max(min(p0 + i * BN + j, p1 - 1), lo_t);   // outside: a seen row, masked
-            raw.load(codes + r * code_bytes(HD), scales + r * scale_bytes(HD));
-        };
-        if (nc > 0) fetch(0);
-        auto step = [&](int i, auto stage) -> bool {
-            constexpr uint32_t S = decltype(stage)::value;
-            if (!wait_phase(&empty[S], ((unsigned)(i >> 1) & 1u) ^ 1u, b, 705)) return false;
-            raw.store(at, S * C::ROWB);
-            fence_async_smem();
-            warp_arrive(&full[S], lane);
-            if (i + 1 < nc) fetch(i + 1);
-            return true;
-        };
-        for (int i = 0; i < nc; i += 2) {
-            if (!step(i, Int<0>{})) break;
-            if (i + 1 < nc && !step(i + 1, Int<1>{})) break;
+        Walk walk = {begin.tile, begin.skip, begin.piece};
+        Seg g;
+        unsigned use0 = 0, use1 = 0;
+        bool ok = !dead;
+        while (ok && next(walk, g)) {
+            const size_t row0 = (size_t)g.kvh * a.c.cap;
+            const uint8_t *codes = (isv ? a.c.vc : a.c.kc) + row0 * code_bytes(HD);
+            const uint8_t *scales = (isv ? a.c.vs : a.c.ks) + row0 * scale_bytes(HD);
+            auto fetch = [&](int i) {
+                const size_t r = (size_t)max(min(g.p0 + i * BN + j, g.p1 - 1), g.lo);   // outside: a seen row, masked
+                raw.load(codes + r * code_bytes(HD), scales + r * scale_bytes(HD));
+            };
+            auto step = [&](int i, auto stage) -> bool {
+                constexpr uint32_t S = decltype(stage)::value;
+                if (!wait_phase(&empty[S], (((S ? use1 : use0) + (unsigned)(i >> 1)) & 1u) ^ 1u, b, 705)) return false;
+                raw.store(at, S * C::ROWB);
+                fence_async_smem();
+                warp_arrive(&full[S], lane);
+                if (i + 1 < g.nc) fetch(i + 1);
+                return true;
+            };
+            if (g.nc > 0) fetch(0);
+            for (int i = 0; ok && i < g.nc; i += 2) ok = step(i, Int<0>{}) && (i + 1 >= g.nc || step(i + 1, Int<1>{}));
+            use0 += (unsigned)(g.nc + 1) / 2;
+            use1 += (unsigned)g.nc / 2;
         }
     } else {
         // ---- softmax and output: thread (r, hf) takes chunks hf, hf + 2, .. for row r, and half of its q and of
         // its output
         setmaxnreg_inc<REG_SM>();
         const int hf = warp >> 2, r = (warp & 3) * 32 + lane;
-        const bool live = r < rows;
-        const int tok = (r0 + min(r, rows - 1)) / a.G, head = kvh * a.G + (r0 + min(r, rows - 1)) % a.G;
+        Walk walk = {begin.tile, begin.skip, begin.piece};
+        Seg g;
+        unsigned use0 = 0, use1 = 0;
+        bool run = true;
+        while (next(walk, g)) {
+        const int nc = g.nc, p0 = g.p0;
+        const bool live = r < g.rows;
+        const int tok = (g.r0 + min(r, g.rows - 1)) / a.G, head = g.kvh * a.G + (g.r0 + min(r, g.rows - 1)) % a.G;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         // score factor: |scale| x log2(e) / the row's power of two; a negative scale turns q
         float f = fabsf(a.scale) * 1.4426950408889634f;
@@ -587,11 +627,11 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         if (SPLIT) fence_async_smem();
         else fence_before_sync();
         warp_arrive(&b->q_ready, lane);
-        const int klo = key_lo(a.pos, tok, a.win), khi = min(key_hi(a.pos, tok, a.len), p1);
+        const int klo = key_lo(a.pos, tok, a.win), khi = min(key_hi(a.pos, tok, a.len), g.p1);
         float ref = -INFINITY, l = 0.f;
-        bool run = true;
+        const unsigned mine = hf ? use1 : use0, other = hf ? use0 : use1;
         for (int i = hf; i < nc; i += 2) {
-            run = __all_sync(0xffffffffu, run && !dead && wait_phase(&b->s_full[hf], (unsigned)(i >> 1) & 1u, b, 707));
+            run = __all_sync(0xffffffffu, run && !dead && wait_phase(&b->s_full[hf], (mine + (unsigned)(i >> 1)) & 1u, b, 707));
             fence_after_sync();
             const uint32_t ts = tl + (uint32_t)hf * BN;
             const int key0 = p0 + i * BN, lo = klo - key0, hi = khi - key0;
@@ -613,7 +653,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
             // for now is PV(i - 1)'s and no earlier one.)
             auto p_free = [&] {
                 if (i == 0) return;
-                run = __all_sync(0xffffffffu, run && wait_phase(&b->pv_done[hf ^ 1], (unsigned)((i - 1) >> 1) & 1u, b, 708));
+                run = __all_sync(0xffffffffu, run && wait_phase(&b->pv_done[hf ^ 1], (other + (unsigned)((i - 1) >> 1)) & 1u, b, 708));
                 fence_after_sync();
             };
             if (i == 1) {                                     // nothing known of the row yet: the first chunk's reference
@@ -700,7 +740,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         }
         // ---- output: O / l, or the partial state of a split
         if (run && nc > 0) {
-            run = __all_sync(0xffffffffu, wait_phase(&b->pv_done[(nc - 1) & 1], (unsigned)((nc - 1) >> 1) & 1u, b, 710));
+            run = __all_sync(0xffffffffu, wait_phase(&b->pv_done[(nc - 1) & 1], (((nc - 1) & 1 ? use1 : use0) + (unsigned)((nc - 1) >> 1)) & 1u, b, 710));
             fence_after_sync();
         }
         // the reference of the last chunk is its group's; the other group's sum follows it
@@ -712,8 +752,12 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         b->x[hf][r] = l;
         if (!pair_or(warp, !run)) {
             l = b->x[0][r] + b->x[1][r];
-            float *part = a.part ? a.part + ((size_t)((size_t)(kvh * a.tiles + tile) * a.splits + split) * a.rt + r) * (HD + PAD)
-                                 : nullptr;
+            // a whole tile: its output; a piece of one: a partial state (and the last piece says where they are)
+            const bool whole_tile = g.first && g.last;
+            float *part = whole_tile ? nullptr
+                                     : a.part + ((size_t)(2 * blockIdx.x + (g.first ? 1 : 0)) * BM + r) * (HD + PAD);
+            if (a.pieces && g.last && threadIdx.x == 0)
+                a.pieces[g.gt] = whole_tile ? make_int2(0, 0) : make_int2((int)blockIdx.x - g.piece, g.piece + 1);
             const float inv = part ? 1.f : (l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l));   // a row that saw nothing is 0
             const size_t at = (size_t)tok * a.o.ts + (size_t)head * a.o.hs;
 #pragma unroll 1
@@ -740,6 +784,12 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
             }
             if (part && live && hf == 0) *reinterpret_cast<float2 *>(part + HD) = make_float2(ref, l);
         }
+        // the next tile's first product overwrites O, which both threads of a row have read by now
+        fence_before_sync();
+        pair_sync(warp);
+        use0 += (unsigned)(nc + 1) / 2;
+        use1 += (unsigned)nc / 2;
+        }
     }
     fence_before_sync();
     __syncthreads();
@@ -751,7 +801,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
 }
 
 template <int HD, bool SPLIT>
-static cudaError_t run_tiles(const Attn &a, cudaStream_t s)
+static cudaError_t run_tiles(const Attn &a, const Shares &sh, cudaStream_t s)
 {
     constexpr int smem = (int)tc_smem<HD, SPLIT>();
     static_assert(smem <= 232448, "shared memory of the tiles kernel");
@@ -770,7 +820,7 @@ static cudaError_t run_tiles(const Attn &a, cudaStream_t s)
         if (dev < 64) ready[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.tiles * a.splits), (unsigned)a.c.Hkv);
+    cfg.gridDim = dim3((unsigned)a.splits);
     cfg.blockDim = dim3(NTHR);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
@@ -779,14 +829,17 @@ static cudaError_t run_tiles(const Attn &a, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tiles<HD, SPLIT>, a);
+    return cudaLaunchKernelEx(&cfg, attn_tiles<HD, SPLIT>, a, sh);
 }
 
 cudaError_t launch_attn_tiles(const Attn &a, cudaStream_t s)
 {
+    if (a.splits < 1 || a.splits > MAX_CTAS) return cudaErrorInvalidConfiguration;
+    Shares sh;
+    if (share_tiles(a, a.per, sh) != a.splits) return cudaErrorInvalidConfiguration;
     const bool split = a.q.dtype == F32;
-    if (a.c.hd == 128) return split ? run_tiles<128, true>(a, s) : run_tiles<128, false>(a, s);
-    return split ? run_tiles<64, true>(a, s) : run_tiles<64, false>(a, s);
+    if (a.c.hd == 128) return split ? run_tiles<128, true>(a, sh, s) : run_tiles<128, false>(a, sh, s);
+    return split ? run_tiles<64, true>(a, sh, s) : run_tiles<64, false>(a, sh, s);
 }
 
 cudaError_t tiles_status(unsigned out[4], cudaStream_t s)

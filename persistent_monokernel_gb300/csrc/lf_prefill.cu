@@ -657,7 +657,8 @@ static cudaError_t attn_q4(const lfp_args *a, int l, int T, int pos0, cudaStream
     q.len = pos0 + T;
     q.win = a->q4_win ? a->q4_win[l] : 0;
     q.scale = 1.0f / sqrtf((float)g.hd);
-    q.part = lfq::plan_attn(q, a->sms, a->q4_floats) ? a->q4_ws : nullptr;
+    const size_t need = lfq::plan_attn(q, a->sms);
+    lfq::set_workspace(q, need ? a->q4_ws : nullptr);
     return lfq::launch_attn(q, s);
 }
 

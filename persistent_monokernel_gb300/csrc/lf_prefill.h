@@ -69,8 +69,7 @@ struct lfp_args {
     size_t q4_codes, q4_scales;
     __half *q4_k, *q4_v;
     const int *q4_win;
-    float *q4_ws;
-    size_t q4_floats;
+    void *q4_ws;
 };
 
 // TMA tensor maps of the GEMM operands (built once per handle: the workspace
