@@ -174,7 +174,7 @@ struct Joined {
     __device__ __forceinline__ void store(const Attn &a, int row, int kvh, int d) const
     {
         const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);   // a row that saw nothing is 0; NaN stays
-        const int tt = row / a.G, hh = kvh * a.G + row % a.G;
+        const int tt = row_token(a, row), hh = row_head(a, kvh, row, tt);
         store4(a.o, (size_t)tt * a.o.ts + (size_t)hh * a.o.hs + d, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     }
 };
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
     auto prepare_q = [&] {
         for (int r = warp; r < RT; r += NW) {
             float x[HD / 32];
-            const int tt = (r0 + r) / a.G, hh = kvh * a.G + (r0 + r) % a.G;
+            const int tt = row_token(a, r0 + r), hh = row_head(a, kvh, r0 + r, tt);
             const bool live = r < rows;
             load_q<HD>(a.q, live, tt, hh, lane, x);
             float f = 1.f;
@@ -240,14 +240,14 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 8 * i + 2 * t + e, tt = (r0 + min(r, rows - 1)) / a.G;
+                const int r = 8 * i + 2 * t + e, tt = row_token(a, r0 + min(r, rows - 1));
                 khi[i][e] = key_hi(a.pos, tt, a.len);
                 klo[i][e] = key_lo(a.pos, tt, a.win);
                 f[i][e] = rs[r];
             }
     };
     // positions of this CTA: the split's, cut to what the tile's rows see
-    const int t_first = r0 / a.G, t_last = (r0 + rows - 1) / a.G;
+    const int t_first = row_token(a, r0), t_last = row_token(a, r0 + rows - 1);
     const int lo_t = key_lo(a.pos, t_first, a.win), hi_r = key_hi(a.pos, t_last, a.len);
     const int hi_t = hi_r > lo_t ? hi_r : 0;              // no position at all: an empty range
     const int p0 = max(a.lo + split * a.per, lo_t), p1 = min(a.lo + (split + 1) * a.per, hi_t);
@@ -548,17 +548,13 @@ static size_t tiles_workspace(const Cache &c, size_t ctas, size_t tiles)
     return (2 * ctas * 128 * (c.hd + PAD)) * sizeof(float) + tiles * sizeof(int2);
 }
 
-// What a tile, or a piece of one, costs beside its chunks, in chunks (about 1 us each, 1.5 in FP32): q, the first
-// chunk's latency, the output.
-static int piece_cost(const Attn &a) { return a.q.dtype == F32 ? 4 : 5; }
+// What a tile, or a piece of one, costs beside its chunks, in chunks (1,570 cycles each, 3,060 in FP32, beside about
+// 20,000 a piece, from the CTAs' own clocks): q, the way to the first P and from the last one, the output.
+static int piece_cost(const Attn &a) { return a.q.dtype == F32 ? 7 : 12; }
 
 int share_tiles(const Attn &a, int ctas, Shares &sh)
 {
     const int all = a.tiles * a.c.Hkv, extra = piece_cost(a);
-    if (ctas == 0) {
-        for (int c = 0; c <= all; ++c) sh.at[c] = {c, 0, 0};
-        return all;
-    }
     int first;
     long long left = 0;   // the cost of what is not dealt out yet
     for (int t = 0; t < a.tiles; ++t) left += tile_chunks(a, t, first) + extra;
@@ -606,11 +602,13 @@ static size_t plan_tiles(Attn &a, int sms, int rows)
         most = std::max(most, c);
     }
     total *= a.c.Hkv;
-    // One CTA per SM.  Either every tile has a CTA of its own, or all SMs share the work evenly, cutting tiles, and
-    // a launch joins the pieces (about five and a half chunks, with the pieces written and read).
+    // One CTA per SM at a time.  Either every tile has a CTA of its own, the longest first (the last one to start ends
+    // about half a tile after the others), or all SMs share the work evenly, cutting tiles (by whole pieces, hence a
+    // tenth more), and a launch joins the pieces (about eight chunks' time, with the pieces written and read).
     const long long t = (long long)a.tiles * a.c.Hkv, ctas = std::min<long long>(sms, std::max<long long>(1, total / 2));
-    const double extra = piece_cost(a), shared = (double)(total + (t + ctas) * extra) / (double)ctas + 5.5;
-    if (t <= sms && most + extra <= shared) {
+    const double extra = piece_cost(a), shared = 1.1 * (double)(total + (t + ctas) * extra) / (double)ctas + 8.0;
+    const double each = t <= sms ? most + extra : (double)(total + t * extra) / (double)sms + (most + extra) / 2.0;
+    if (each <= shared && t < (1ll << 30)) {
         a.splits = (int)t;
         a.per = 0;
         return 0;
@@ -636,6 +634,9 @@ void set_workspace(Attn &a, void *ws)
 
 size_t plan_attn(Attn &a, int sms)
 {
+    a.gsh = -1;
+    for (int s = 0; s < 30; ++s)
+        if (a.G == 1 << s) a.gsh = s;
     const int rows = a.n * a.G, hi = key_hi(a.pos, a.n - 1, a.len);
     a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
     const size_t state = (size_t)a.c.Hkv * (a.c.hd + PAD) * sizeof(float);

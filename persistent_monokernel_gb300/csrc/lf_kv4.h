@@ -39,13 +39,14 @@ struct Attn {
     Cache c;
     Rows q, o;
     int Hq, G;              // query heads; per KV head
+    int gsh;                // log2 G, or -1 (set by the plan)
     int n, pos;             // query rows at positions pos .. pos + n - 1
     int len, win;           // keys 0 .. len - 1; window (0: all)
     float scale;
     // plan: row tiles of rt query rows (n * G rows per KV head, row r = token r / G, head r % G).
     // rt 8 or 16: each over `splits` ranges of `per` positions from lo on; `cl` ranges in a row are one cluster,
     // which joins them into one of splits / cl partial states.
-    // rt 128: `splits` CTAs share all chunks of all tiles (share_tiles of `per` CTAs; 0: one tile each).
+    // rt 128: `splits` CTAs share all chunks of all tiles (share_tiles of `per` CTAs), or (per 0) take a tile each.
     int rt, tiles, splits, cl, per, lo;
     // partial states [..][rt][hd + PAD]: O, then m and l (null: none).  rt 8 or 16: [Hkv * tiles * splits / cl];
     // rt 128: two per CTA, for the tile it goes on with and the tile it leaves unfinished, and where a tile's are:
@@ -61,11 +62,16 @@ __host__ __device__ inline int key_lo(int pos, int t, int win)
     return (win > 0 && pos + t + 1 > win) ? pos + t + 1 - win : 0;
 }
 
+// Token of row x (of a KV head's n * G rows); a division costs 30 instructions, and G is mostly a power of two.
+__host__ __device__ inline int row_token(const Attn &a, int x) { return a.gsh >= 0 ? x >> a.gsh : x / a.G; }
+// Query head of row x of token t.
+__host__ __device__ inline int row_head(const Attn &a, int kvh, int x, int t) { return kvh * a.G + x - t * a.G; }
+
 // Chunks of 128 positions that some row of tile `tile` (of 128 rows) sees: their count, at least 1, and the first.
 __host__ __device__ inline int tile_chunks(const Attn &a, int tile, int &first)
 {
     const int r0 = tile * 128, last = r0 + 127 < a.n * a.G ? r0 + 127 : a.n * a.G - 1;
-    const int lo = key_lo(a.pos, r0 / a.G, a.win), hi = key_hi(a.pos, last / a.G, a.len);
+    const int lo = key_lo(a.pos, row_token(a, r0), a.win), hi = key_hi(a.pos, row_token(a, last), a.len);
     first = lo / 128;
     return hi > lo ? (hi + 127) / 128 - first : 1;
 }
@@ -77,7 +83,7 @@ constexpr int MAX_CTAS = 256;
 struct Shares {
     Share at[MAX_CTAS + 1];
 };
-// Deals the chunks of all tiles out to at most `ctas` CTAs and returns how many have any (0: one tile each).
+// Deals the chunks of all tiles out to at most `ctas` CTAs and returns how many have any.
 int share_tiles(const Attn &a, int ctas, Shares &sh);
 
 // Fills a's plan for `sms` SMs (a.q.dtype is set) and returns the workspace bytes it needs, at most

@@ -67,8 +67,8 @@ struct TcCfg {
     static constexpr uint32_t ATOM = 128 * 128;             // 128 rows x 64 FP16
     static constexpr uint32_t ROWB = (HD / 64) * ATOM;      // a 128-row operand
     static constexpr uint32_t OFF_K = 0, OFF_V = 2 * ROWB;  // two stages each
-    static constexpr uint32_t OFF_Q = 4 * ROWB;             // SPLIT: head, remainder
-    static constexpr uint32_t OFF_BAR = OFF_Q + (SPLIT ? 2 * ROWB : 0);
+    static constexpr uint32_t OFF_Q = 4 * ROWB;             // staging of q on its way to TMEM (SPLIT: q itself,
+    static constexpr uint32_t OFF_BAR = OFF_Q + 2 * ROWB;   // head and remainder), then of the output, FP32
     // TMEM columns: scores (two buffers), O, P (head, remainder), Q
     static constexpr uint32_t T_O = 2 * BN, T_P = T_O + HD, T_Q = T_P + BN / 2 * (SPLIT ? 2 : 1), T_COLS = 512;
     static_assert(T_Q + (SPLIT ? 0 : HD / 2) <= T_COLS, "TMEM columns");
@@ -81,20 +81,24 @@ struct Bars {
     int abort;
     float x[2][BM];     // exchanged between the two threads of a row
     float ref[BM];      // the row's reference, handed on from chunk to chunk
+    long long qrow[BM], orow[BM];   // the rows' element offsets in q and in the output
+    float fac[BM];      // the power of two that q was multiplied with
 };
 // (a descriptor's start address has 14 bits of 16 bytes: adding offsets to it never carries out of 256 KB)
 template <int HD, bool SPLIT>
 constexpr uint32_t tc_smem() { return TcCfg<HD, SPLIT>::OFF_BAR + (uint32_t)sizeof(Bars) + 1024u; }
 
+// (The timer is read from the 64th poll on: reading it before costs a wait several times its own length.)
 __device__ bool wait_phase(uint64_t *bar, unsigned parity, Bars *b, unsigned where)
 {
-    if (lfk::mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = lfk::globaltimer_ns();
-    for (unsigned it = 0;; ++it) {
+    unsigned long long t0 = 0;
+    for (unsigned it = 1;; ++it) {
         if (lfk::mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 63u) {
+        if ((it & 63u) == 0u) {
             if (*reinterpret_cast<volatile int *>(&b->abort)) return false;
-            if ((long long)(lfk::globaltimer_ns() - t0) > kWaitNs) {
+            const unsigned long long now = lfk::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if ((long long)(now - t0) > kWaitNs) {
                 *reinterpret_cast<volatile int *>(&b->abort) = 1;
                 if (atomicCAS(g_status, 0u, (unsigned)lfk::STATUS_TIMEOUT) == 0u) {
                     g_status[1] = where;
@@ -284,6 +288,7 @@ __device__ __forceinline__ bool pair_or(int warp, bool pred)
     return r != 0;
 }
 __device__ __forceinline__ void pair_sync(int warp) { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); }
+__device__ __forceinline__ void all_rows_sync() { asm volatile("bar.sync 13, 256;" ::: "memory"); }   // the softmax warps
 __device__ __forceinline__ void hand_over(int warp)
 {
     asm volatile("bar.arrive %0, 64;" ::"r"(5 + (warp & 7)) : "memory");
@@ -364,10 +369,18 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
     Bars *b = reinterpret_cast<Bars *>(smem + C::OFF_BAR);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // this CTA's share of the tiles, tile by tile
-    const Share begin = sh.at[blockIdx.x], end = sh.at[blockIdx.x + 1];
+    Share begin, end;
+    if (a.per == 0) {                                     // one tile, the longest (latest) ones first
+        begin = {(int)(blockIdx.x % a.c.Hkv) * a.tiles + a.tiles - 1 - (int)(blockIdx.x / a.c.Hkv), 0, 0};
+        end = {begin.tile + 1, 0, 0};
+    } else {
+        begin = sh.at[blockIdx.x];
+        end = sh.at[blockIdx.x + 1];
+    }
     struct Walk {
-        int tile, skip, piece;
+        int tile, skip, piece, kvh, t;   // t: the tile within KV head kvh
     };
+    const Walk start = {begin.tile, begin.skip, begin.piece, begin.tile / a.tiles, begin.tile % a.tiles};
     struct Seg {
         int gt, kvh, r0, rows, lo, p0, p1, nc, piece;
         bool first, last;       // the tile's first chunks, its last ones
@@ -375,11 +388,11 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
     auto next = [&](Walk &w, Seg &s) -> bool {
         if (w.tile > end.tile || (w.tile == end.tile && w.skip >= end.skip)) return false;
         s.gt = w.tile;
-        s.kvh = w.tile / a.tiles;
-        const int tile = w.tile % a.tiles;
+        s.kvh = w.kvh;
+        const int tile = w.t;
         s.r0 = tile * BM;
         s.rows = min(BM, a.n * a.G - s.r0);
-        const int t_first = s.r0 / a.G, t_last = (s.r0 + s.rows - 1) / a.G;
+        const int t_first = row_token(a, s.r0), t_last = row_token(a, s.r0 + s.rows - 1);
         const int hi = key_hi(a.pos, t_last, a.len);
         int c0;
         const int all = tile_chunks(a, tile, c0), stop = w.tile == end.tile ? end.skip : all;
@@ -390,7 +403,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         s.first = w.skip == 0;
         s.last = stop == all;
         s.piece = w.piece;
-        w = {w.tile + 1, 0, 0};
+        w = tile + 1 < a.tiles ? Walk{w.tile + 1, 0, 0, w.kvh, tile + 1} : Walk{w.tile + 1, 0, 0, w.kvh + 1, 0};
         return true;
     };
 
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         // issues.
         const bool one = elect_one();
         const uint32_t sb = lfk::smem_u32(smem);
-        Walk walk = {begin.tile, begin.skip, begin.piece};
+        Walk walk = start;
         Seg g;
         unsigned use0 = 0, use1 = 0;                      // chunks so far in each stage: a barrier's phases
         if (warp == W_MMA && !dead) {
@@ -520,7 +533,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
 #pragma unroll
         for (int c = 0; c < 8; ++c) at[c] = lfk::smem_u32(smem) + (isv ? C::OFF_V : C::OFF_K) + sw128(j, c);
         RawRow<HD> raw;
-        Walk walk = {begin.tile, begin.skip, begin.piece};
+        Walk walk = start;
         Seg g;
         unsigned use0 = 0, use1 = 0;
         bool ok = !dead;
@@ -551,81 +564,106 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         // its output
         setmaxnreg_inc<REG_SM>();
         const int hf = warp >> 2, r = (warp & 3) * 32 + lane;
-        Walk walk = {begin.tile, begin.skip, begin.piece};
+        Walk walk = start;
         Seg g;
         unsigned use0 = 0, use1 = 0;
         bool run = true;
         while (next(walk, g)) {
         const int nc = g.nc, p0 = g.p0;
         const bool live = r < g.rows;
-        const int tok = (g.r0 + min(r, g.rows - 1)) / a.G, head = g.kvh * a.G + (g.r0 + min(r, g.rows - 1)) % a.G;
+        const int tok = row_token(a, g.r0 + min(r, g.rows - 1)), head = row_head(a, g.kvh, g.r0 + min(r, g.rows - 1), tok);
+        if (hf == 0) b->qrow[r] = (long long)tok * a.q.ts + (long long)head * a.q.hs;
+        else b->orow[r] = (long long)tok * a.o.ts + (long long)head * a.o.hs;
+        all_rows_sync();                                  // the rows' places
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        // score factor: |scale| x log2(e) / the row's power of two; a negative scale turns q
-        float f = fabsf(a.scale) * 1.4426950408889634f;
+        // ---- q: a row's lanes side by side, so that the loads are whole lines; a power of two brings BF16 and FP32
+        // rows into FP16's range, a negative scale turns them
         {
-            // 64 dims per thread (head_dim 64: the first thread of the row alone)
-            const size_t at = (size_t)tok * a.q.ts + (size_t)head * a.q.hs + 64 * hf;
-            const bool has = 64 * hf < HD;
-            auto load = [&](int c, float (&x)[16]) {
-                if (a.q.dtype == F16) load16<__half>(static_cast<const __half *>(a.q.p) + at + c * 16, x);
-                else if (a.q.dtype == BF16) load16<__nv_bfloat16>(static_cast<const __nv_bfloat16 *>(a.q.p) + at + c * 16, x);
-                else load16<float>(static_cast<const float *>(a.q.p) + at + c * 16, x);
-            };
-            float fac = 1.f;
-            if (a.q.dtype != F16) {
-                float m = 0.f;
-                if (has) {
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float x[16];
-                        load(c, x);
+            constexpr int V = SPLIT ? 4 : 8, L = HD / V, P = 128 * L / NSM;   // values per lane, lanes per row, passes
+            uint4 raw[P];
+            const int c = threadIdx.x % L;
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) m = fmaxf(m, fabsf(x[u]));
-                    }
-                }
-                b->x[hf][r] = m;
-                pair_sync(warp);
-                fac = range_factor(fmaxf(b->x[0][r], b->x[1][r]));
-                f /= fac;
-                pair_sync(warp);
+            for (int i = 0; i < P; ++i) {
+                const int row = i * (NSM / L) + threadIdx.x / L;
+                raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (row < g.rows)
+                    raw[i] = *reinterpret_cast<const uint4 *>(static_cast<const char *>(a.q.p) + (b->qrow[row] + c * V) * (16 / V));
             }
-            if (a.scale < 0.f) fac = -fac;
-            if (!live) fac = 0.f;
-            uint32_t hw[32];
-            if (has) {
+            uint8_t *qs = smem + C::OFF_Q;
+            auto place = [&](int i) { return i * (NSM / L) + (int)threadIdx.x / L; };
+            if (!SPLIT && a.q.dtype == F16 && a.scale > 0.f) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float x[16];
-                    load(c, x);
-                    uint32_t lw[8];
+                for (int i = 0; i < P; ++i) {
+                    *reinterpret_cast<uint4 *>(qs + place(i) * (HD * 2) + ((c ^ (place(i) & 7)) << 4)) = raw[i];
+                    if (c == 0) b->fac[place(i)] = 1.f;
+                }
+            } else {
+                float fac[P];
+                if (a.q.dtype == F16) {
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        __half h0, m0, h1, m1;
-                        lfk::split_h(live ? x[2 * u] * fac : 0.f, h0, m0);
-                        lfk::split_h(live ? x[2 * u + 1] * fac : 0.f, h1, m1);
-                        hw[8 * c + u] = lfk::pack_h2(h0, h1);
-                        lw[u] = lfk::pack_h2(m0, m1);
-                    }
-                    if (SPLIT) {
-                        uint8_t *qh = smem + C::OFF_Q + (uint32_t)hf * C::ATOM;
+                    for (int i = 0; i < P; ++i) fac[i] = 1.f;
+                } else {
+                    // the largest magnitude's bits (FP32's; BF16's lie in their upper half)
+                    unsigned m[P];
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const uint32_t o = sw128(r, 2 * c + u);
-                            const uint32_t *h = hw + 8 * c + 4 * u, *m = lw + 4 * u;
-                            *reinterpret_cast<uint4 *>(qh + o) = make_uint4(h[0], h[1], h[2], h[3]);
-                            *reinterpret_cast<uint4 *>(qh + C::ROWB + o) = make_uint4(m[0], m[1], m[2], m[3]);
+                    for (int i = 0; i < P; ++i) {
+                        const unsigned w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                        m[i] = 0u;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            m[i] = max(m[i], w[u] & (SPLIT ? 0x7fffffffu : 0x7fff0000u));
+                            if (!SPLIT) m[i] = max(m[i], (w[u] << 16) & 0x7fff0000u);
                         }
                     }
+#pragma unroll
+                    for (int o = L / 2; o; o >>= 1)
+#pragma unroll
+                        for (int i = 0; i < P; ++i) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+                    for (int i = 0; i < P; ++i) fac[i] = range_factor(__uint_as_float(m[i]));
                 }
-                __syncwarp();
-                if (!SPLIT) {
-                    tmem_st32(tl + C::T_Q + (uint32_t)(32 * hf), hw);
-                    tmem_st_wait();
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    if (c == 0) b->fac[place(i)] = fac[i];
+                    const float fc = a.scale < 0.f ? -fac[i] : fac[i];
+                    const unsigned w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                    if constexpr (SPLIT) {                    // to its place in the K-major operand
+                        __half h[4], m[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) lfk::split_h(__uint_as_float(w[u]) * fc, h[u], m[u]);
+                        const int d = c * V;
+                        uint8_t *at = qs + (d / 64) * C::ATOM + sw128(place(i), d % 64 / 8) + d % 8 * 2;
+                        *reinterpret_cast<uint2 *>(at) = make_uint2(lfk::pack_h2(h[0], h[1]), lfk::pack_h2(h[2], h[3]));
+                        *reinterpret_cast<uint2 *>(at + C::ROWB) = make_uint2(lfk::pack_h2(m[0], m[1]), lfk::pack_h2(m[2], m[3]));
+                    } else {
+                        uint32_t hw[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const float2 y = a.q.dtype == F16 ? h2_f2(w[u])
+                                                              : make_float2(__uint_as_float(w[u] << 16), __uint_as_float(w[u] & 0xffff0000u));
+                            const __half2 v = __floats2half2_rn(y.x * fc, y.y * fc);
+                            hw[u] = *reinterpret_cast<const unsigned *>(&v);
+                        }
+                        *reinterpret_cast<uint4 *>(qs + place(i) * (HD * 2) + ((c ^ (place(i) & 7)) << 4)) =
+                            make_uint4(hw[0], hw[1], hw[2], hw[3]);
+                    }
                 }
             }
         }
         if (SPLIT) fence_async_smem();
-        else fence_before_sync();
+        all_rows_sync();
+        const float f = fabsf(a.scale) * 1.4426950408889634f / b->fac[r];   // score factor
+        if (!SPLIT && 64 * hf < HD) {
+            uint32_t hw[32];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(smem + C::OFF_Q + r * (HD * 2) + (((8 * hf + c) ^ (r & 7)) << 4));
+                hw[4 * c] = v.x, hw[4 * c + 1] = v.y, hw[4 * c + 2] = v.z, hw[4 * c + 3] = v.w;
+            }
+            tmem_st32(tl + C::T_Q + (uint32_t)(32 * hf), hw);
+            tmem_st_wait();
+        }
+        if (!SPLIT) fence_before_sync();
         warp_arrive(&b->q_ready, lane);
         const int klo = key_lo(a.pos, tok, a.win), khi = min(key_hi(a.pos, tok, a.len), g.p1);
         float ref = -INFINITY, l = 0.f;
@@ -750,43 +788,75 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         if (last != ref) l *= ex2(ref - last);
         ref = last;
         b->x[hf][r] = l;
-        if (!pair_or(warp, !run)) {
-            l = b->x[0][r] + b->x[1][r];
-            // a whole tile: its output; a piece of one: a partial state (and the last piece says where they are)
-            const bool whole_tile = g.first && g.last;
-            float *part = whole_tile ? nullptr
-                                     : a.part + ((size_t)(2 * blockIdx.x + (g.first ? 1 : 0)) * BM + r) * (HD + PAD);
-            if (a.pieces && g.last && threadIdx.x == 0)
-                a.pieces[g.gt] = whole_tile ? make_int2(0, 0) : make_int2((int)blockIdx.x - g.piece, g.piece + 1);
+        const bool good = !pair_or(warp, !run);
+        l = b->x[0][r] + b->x[1][r];
+        // a whole tile: its output; a piece of one: a partial state (and the last piece says where they are)
+        const bool whole_tile = g.first && g.last;
+        float *part = whole_tile ? nullptr : a.part + (size_t)(2 * blockIdx.x + (g.first ? 1 : 0)) * BM * (HD + PAD);
+        if (a.pieces && g.last && threadIdx.x == 0)
+            a.pieces[g.gt] = whole_tile ? make_int2(0, 0) : make_int2((int)blockIdx.x - g.piece, g.piece + 1);
+        // through shared memory (q's staging, read by now), so that the stores are whole lines
+        if (good) {
             const float inv = part ? 1.f : (l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l));   // a row that saw nothing is 0
-            const size_t at = (size_t)tok * a.o.ts + (size_t)head * a.o.hs;
 #pragma unroll 1
             for (int c = 0; c < HD / 64; ++c) {
-                const int d = HD / 2 * hf + 32 * c;
                 uint32_t o[32];
                 if (nc > 0) {
-                    tmem_ld32(tl + C::T_O + (uint32_t)d, o);
+                    tmem_ld32(tl + C::T_O + (uint32_t)(HD / 2 * hf + 32 * c), o);
                     tmem_ld_wait();
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0u;
                 }
-                if (live) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float x = __uint_as_float(o[e]) * inv, y = __uint_as_float(o[e + 1]) * inv,
-                                    z = __uint_as_float(o[e + 2]) * inv, v = __uint_as_float(o[e + 3]) * inv;
-                        if (part) *reinterpret_cast<float4 *>(part + d + e) = make_float4(x, y, z, v);
-                        else store4(a.o, at + d + e, x, y, z, v);
-                    }
+                for (int e = 0; e < 32; e += 4) {
+                    const int c16 = (HD / 2 * hf + 32 * c + e) / 4;
+                    *reinterpret_cast<float4 *>(smem + C::OFF_Q + r * (HD * 4) + ((c16 ^ (r & 7)) << 4)) =
+                        make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                    __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
                 }
-                __syncwarp();
             }
-            if (part && live && hf == 0) *reinterpret_cast<float2 *>(part + HD) = make_float2(ref, l);
+            if (part && live && hf == 0) *reinterpret_cast<float2 *>(part + (size_t)r * (HD + PAD) + HD) = make_float2(ref, l);
         }
-        // the next tile's first product overwrites O, which both threads of a row have read by now
-        fence_before_sync();
-        pair_sync(warp);
+        fence_before_sync();                              // O is read: the next tile's first product overwrites it
+        all_rows_sync();
+        {
+            // V values per lane: 16 bytes in the staging's FP32, or in a 16-bit output
+            auto copy = [&](auto lanes, auto put) {
+                constexpr int L = decltype(lanes)::value, V = HD / L;
+                const int c = threadIdx.x % L;
+#pragma unroll 2
+                for (int row = threadIdx.x / L; row < g.rows; row += NSM / L) {
+                    float4 v[V / 4];
+#pragma unroll
+                    for (int u = 0; u < V / 4; ++u)
+                        v[u] = *reinterpret_cast<const float4 *>(smem + C::OFF_Q + row * (HD * 4) + (((c * (V / 4) + u) ^ (row & 7)) << 4));
+                    put(row, c * V, v);
+                }
+            };
+            if (part)
+                copy(Int<HD / 4>{}, [&](int row, int d, const float4 *v) {
+                    *reinterpret_cast<float4 *>(part + (size_t)row * (HD + PAD) + d) = v[0];
+                });
+            else if (a.o.dtype == F16 || a.o.dtype == BF16)
+                copy(Int<HD / 8>{}, [&](int row, int d, const float4 *v) {
+                    uint4 w;
+                    if (a.o.dtype == F16) {
+                        const __half2 x[4] = {__floats2half2_rn(v[0].x, v[0].y), __floats2half2_rn(v[0].z, v[0].w),
+                                              __floats2half2_rn(v[1].x, v[1].y), __floats2half2_rn(v[1].z, v[1].w)};
+                        w = *reinterpret_cast<const uint4 *>(x);
+                    } else {
+                        w = make_uint4(pack_bf2(v[0].x, v[0].y), pack_bf2(v[0].z, v[0].w), pack_bf2(v[1].x, v[1].y),
+                                       pack_bf2(v[1].z, v[1].w));
+                    }
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o.p) + b->orow[row] + d) = w;
+                });
+            else
+                copy(Int<HD / 4>{}, [&](int row, int d, const float4 *v) {
+                    store4(a.o, (size_t)b->orow[row] + d, v[0].x, v[0].y, v[0].z, v[0].w);
+                });
+        }
+        all_rows_sync();                                  // the staging is free for the next tile's q
         use0 += (unsigned)(nc + 1) / 2;
         use1 += (unsigned)nc / 2;
         }
@@ -834,9 +904,8 @@ static cudaError_t run_tiles(const Attn &a, const Shares &sh, cudaStream_t s)
 
 cudaError_t launch_attn_tiles(const Attn &a, cudaStream_t s)
 {
-    if (a.splits < 1 || a.splits > MAX_CTAS) return cudaErrorInvalidConfiguration;
     Shares sh;
-    if (share_tiles(a, a.per, sh) != a.splits) return cudaErrorInvalidConfiguration;
+    if (a.per > 0 && (a.per > MAX_CTAS || share_tiles(a, a.per, sh) != a.splits)) return cudaErrorInvalidConfiguration;
     const bool split = a.q.dtype == F32;
     if (a.c.hd == 128) return split ? run_tiles<128, true>(a, sh, s) : run_tiles<128, false>(a, sh, s);
     return split ? run_tiles<64, true>(a, sh, s) : run_tiles<64, false>(a, sh, s);
