@@ -98,9 +98,9 @@ __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n,
     for (int u = 0; u < READ_U; ++u) {
         const long long t = (i0 + u * 256) >> shift;
         if (t >= n) continue;
-        w[u] = N == 8 ? __ldg(reinterpret_cast<const unsigned *>(codes + t * code_bytes(c.hd)))
-                      : __ldg(reinterpret_cast<const unsigned short *>(codes + t * code_bytes(c.hd)));
-        s[u] = __ldg(scales + t * scale_bytes(c.hd));
+        w[u] = N == 8 ? ld(reinterpret_cast<const unsigned *>(codes + t * code_bytes(c.hd)))
+                      : ld(reinterpret_cast<const unsigned short *>(codes + t * code_bytes(c.hd)));
+        s[u] = ld(scales + t * scale_bytes(c.hd));
     }
     const Rows &out = isv ? v : k;
     T *dst = static_cast<T *>(out.p) + h * out.hs + b * N;
@@ -511,15 +511,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant_
     if (row < a.n * a.G) {
         // state s of the row's tile: number at(s) of all
         const size_t tile = (size_t)kvh * a.tiles + row / a.rt, step = (size_t)a.rt * (hd + PAD);
-        const int2 pc = a.pieces ? __ldcg(a.pieces + tile) : make_int2(0, a.splits / a.cl);
+        const int2 pc = a.pieces ? ld(a.pieces + tile) : make_int2(0, a.splits / a.cl);
         parts = pc.y;
         const float *part = a.part + (size_t)(row % a.rt) * (hd + PAD);
 #pragma unroll 4
         for (int s = grp; s < parts; s += groups) {
             // a CTA's second place holds the tile that it begins and leaves, its first the one it goes on with
             const size_t at = a.pieces ? 2 * (size_t)(pc.x + s) + (s == 0 ? 1 : 0) : tile * parts + s;
-            j.add(__ldcg(reinterpret_cast<const float2 *>(part + at * step + hd)),
-                  __ldcg(reinterpret_cast<const float4 *>(part + at * step + d)));
+            j.add(ld(reinterpret_cast<const float2 *>(part + at * step + hd)),
+                  ld(reinterpret_cast<const float4 *>(part + at * step + d)));
         }
     }
     if (groups > 1) {

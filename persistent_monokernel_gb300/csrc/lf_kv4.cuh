@@ -60,6 +60,11 @@ __device__ __forceinline__ float ex2(float x)
 // ---- programmatic dependent launches: the next kernel may start its prologue; wait for the previous one's end
 __device__ __forceinline__ void dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A load of what a kernel before this one wrote.  A plain one: the read-only path's is for data that nothing writes
+// while the kernel runs, and a dependent launch runs beside its predecessors until it has waited for them; the
+// compiler may move such a load ahead of the wait.
+template <class T>
+__device__ __forceinline__ T ld(const T *p) { return *p; }
 
 // ---- clusters: a barrier, and loads from another CTA's shared memory
 __device__ __forceinline__ void cluster_sync()
@@ -93,7 +98,7 @@ __device__ __forceinline__ void load16<float>(const float *p, float (&x)[16])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p) + j);
+        const float4 v = ld(reinterpret_cast<const float4 *>(p) + j);
         x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
     }
 }
@@ -102,7 +107,7 @@ __device__ __forceinline__ void load16<__half>(const __half *p, float (&x)[16])
 {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + j);
+        const uint4 v = ld(reinterpret_cast<const uint4 *>(p) + j);
         const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -116,7 +121,7 @@ __device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16 *p, fl
 {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + j);
+        const uint4 v = ld(reinterpret_cast<const uint4 *>(p) + j);
         const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -264,8 +269,8 @@ struct KRaw<128> {
     unsigned s;
     __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales)
     {
-        c = __ldg(reinterpret_cast<const uint4 *>(codes));
-        s = __ldg(reinterpret_cast<const unsigned short *>(scales));
+        c = ld(reinterpret_cast<const uint4 *>(codes));
+        s = ld(reinterpret_cast<const unsigned short *>(scales));
     }
     __device__ __forceinline__ void values(unsigned (&v)[8][2]) const
     {
@@ -291,8 +296,8 @@ struct KRaw<64> {
     unsigned s;
     __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales)
     {
-        c = __ldg(reinterpret_cast<const uint2 *>(codes));
-        s = __ldg(scales);
+        c = ld(reinterpret_cast<const uint2 *>(codes));
+        s = ld(scales);
     }
     __device__ __forceinline__ void values(unsigned (&v)[4][2]) const
     {
@@ -315,8 +320,8 @@ struct VRaw<128> {
     unsigned s;
     __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales)
     {
-        c = __ldg(reinterpret_cast<const uint2 *>(codes));
-        s = __ldg(scales);
+        c = ld(reinterpret_cast<const uint2 *>(codes));
+        s = ld(scales);
     }
     __device__ __forceinline__ unsigned word(int j) const { return j ? c.y : c.x; }
 };
@@ -326,8 +331,8 @@ struct VRaw<64> {
     unsigned s;
     __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales)
     {
-        c = __ldg(reinterpret_cast<const unsigned *>(codes));
-        s = __ldg(scales);
+        c = ld(reinterpret_cast<const unsigned *>(codes));
+        s = ld(scales);
     }
     __device__ __forceinline__ unsigned word(int) const { return c; }
 };

@@ -195,9 +195,9 @@ struct RawRow {
     __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales)
     {
 #pragma unroll
-        for (int j = 0; j < HD / 32; ++j) c[j] = __ldg(reinterpret_cast<const uint4 *>(codes) + j);
-        if (HD == 128) s = __ldg(reinterpret_cast<const uint2 *>(scales));
-        else s = make_uint2(__ldg(reinterpret_cast<const unsigned *>(scales)), 0u);
+        for (int j = 0; j < HD / 32; ++j) c[j] = ld(reinterpret_cast<const uint4 *>(codes) + j);
+        if (HD == 128) s = ld(reinterpret_cast<const uint2 *>(scales));
+        else s = make_uint2(ld(reinterpret_cast<const unsigned *>(scales)), 0u);
     }
     // One row of an operand tile: 16-byte group c of its 64-dim half h to at[c] + h * 16,384 (the shared-memory
     // addresses of the row's eight swizzled groups) + off.
