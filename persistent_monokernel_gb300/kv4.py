@@ -182,8 +182,9 @@ class KV4Cache:
         key, size = self._scratch
         if key != (n, heads):
             size = 0
-        ws = _torch.empty((size,), dtype=_torch.uint8, device=self.device).data_ptr() if size else None
-        status = _attend(self._addr, args, ws, size, _raw_stream(self._index))
+        # (Held until the launch: another thread on this stream may be given what is let go before it.)
+        ws = _torch.empty((size,), dtype=_torch.uint8, device=self.device) if size else None
+        status = _attend(self._addr, args, ws.data_ptr() if size else None, size, _raw_stream(self._index))
         if status:
             status = self._attend_with_workspace(args, status, (n, heads))
             if status:

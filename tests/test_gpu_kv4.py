@@ -325,6 +325,26 @@ def test_two_streams_at_once(pm):
     assert all(torch.equal(o, want[i]) for i, o in got)
 
 
+@pytest.mark.parametrize("n", [1, 140])
+def test_scratch_is_held_until_the_launch(pm, monkeypatch, n):
+    """What another thread on the stream may be given while a call is on its way to the launch is not its scratch."""
+    from persistent_monokernel_gb300 import kv4
+    cache, _ = filled(pm, 8, 128, 40000, 3)
+    q = torch.randn(n, 8 if n == 1 else 32, 128, generator=gen(n), device="cuda").half()
+    want = cache.attend(q, 39000)
+    launch, seen = kv4._attend, []
+
+    def between(addr, args, ws, size, stream):
+        seen.append(size)
+        other = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert all(abs(t.data_ptr() - ws) >= size for t in other)
+        return launch(addr, args, ws, size, stream)
+
+    monkeypatch.setattr(kv4, "_attend", between)
+    assert torch.equal(cache.attend(q, 39000), want)
+    assert seen and seen[0] > 0
+
+
 def test_the_first_calls_of_a_process_may_be_captured():
     """Kernels that no call has loaded yet, recorded at once."""
     import subprocess
