@@ -438,8 +438,8 @@ LF_API lf_status lf_kv4_append(const lf_kv4 *c, const lf_rows *k, const lf_rows 
                                void *stream);
 
 /* The values of positions pos .. pos + n - 1 into k and v
- * [n][n_kv_heads][head_dim] (one dtype; exact in all three).  Errors as for
- * lf_kv4_append. */
+ * [n][n_kv_heads][head_dim] (one dtype; exact in all three; they must not
+ * overlap).  Errors as for lf_kv4_append, and INVALID_ARG for k = v. */
 LF_API lf_status lf_kv4_read(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int32_t n, int32_t pos,
                              void *stream);
 
@@ -473,7 +473,7 @@ LF_API lf_status lf_kv4_workspace(const lf_kv4 *c, const lf_kv4_query *q, int64_
  * that is not finite, differing dtypes, out = q, a workspace that is too
  * small), NOT_SUPPORTED (head_dim, n_kv_heads, max_seq, dtype, n_heads no
  * multiple of n_kv_heads, pos + n above 2^30, n * n_heads / n_kv_heads above
- * 2^28), CAPACITY (length > max_seq), CUDA. */
+ * 2^28, n * n_heads above 2^32), CAPACITY (length > max_seq), CUDA. */
 LF_API lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *workspace, int64_t workspace_bytes,
                                void *stream);
 

@@ -785,6 +785,7 @@ using namespace lfq;
 
 constexpr int kMaxKvHeads = 1024;
 constexpr int kMaxPositions = 1 << 30;   // positions rounded up to whole splits stay in 32 bits
+constexpr long long kMaxRows = 1ll << 32;   // rows of all heads (8 GB per dim in FP16): their tiles do too
 
 lf_status status_of(cudaError_t e)
 {
@@ -841,7 +842,7 @@ lf_status check_copy(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int n,
     if (n == 0) return LF_OK;
     st = check_rows(k, n, c->n_kv_heads, c->head_dim, written);
     if (st == LF_OK) st = check_rows(v, n, c->n_kv_heads, c->head_dim, written);
-    if (st == LF_OK && k->dtype != v->dtype) st = LF_ERR_INVALID_ARG;
+    if (st == LF_OK && (k->dtype != v->dtype || (written && k->data == v->data))) st = LF_ERR_INVALID_ARG;
     return st;
 }
 
@@ -871,7 +872,8 @@ lf_status make_attn(const lf_kv4 *c, const lf_kv4_query *q, Attn *a, size_t *byt
     if (q->length > c->max_seq) return LF_ERR_CAPACITY;
     if (q->n_heads % c->n_kv_heads) return LF_ERR_NOT_SUPPORTED;
     const int G = q->n_heads / c->n_kv_heads;
-    if ((long long)q->n * G > (1ll << 28) || (long long)q->pos + q->n > kMaxPositions) return LF_ERR_NOT_SUPPORTED;
+    if ((long long)q->n * G > (1ll << 28) || (long long)q->n * q->n_heads > kMaxRows || (long long)q->pos + q->n > kMaxPositions)
+        return LF_ERR_NOT_SUPPORTED;
     a->c = cache_of(c);
     a->Hq = q->n_heads;
     a->G = G;

@@ -88,6 +88,8 @@ class KV4Cache:
         if k_codes.dim() != 3:
             raise ValueError("codes are [n_kv_heads, max_seq, head_dim / 2]")
         h, s, half = k_codes.shape
+        if max(h, s) >= _INT:
+            raise ValueError(f"{h} heads, {s} positions: 32 bits are needed")
         for t, width in ((k_codes, half), (k_scales, half // 8), (v_codes, half), (v_scales, half // 8)):
             if not (t.is_cuda and t.dtype == _torch.uint8 and t.is_contiguous() and t.device == k_codes.device
                     and tuple(t.shape) == (h, s, width)):
@@ -132,9 +134,9 @@ class KV4Cache:
         """Quantise k, v [n, n_kv_heads, head_dim] into positions pos .. pos + n - 1."""
         if stream is not None or _current_device() != self._index:
             return self._elsewhere(self.append, stream, (k, v, pos))
-        n, h = k.shape[0], self.n_kv_heads
-        if not -_INT < pos < _INT:
-            raise ValueError(f"pos {pos}: 32 bits are needed")
+        n, h = len(k), self.n_kv_heads
+        if not (-_INT < pos < _INT and n < _INT):
+            raise ValueError(f"pos {pos}, {n} rows: 32 bits are needed")
         status = _append(self._addr, _ROWS.pack(*self._rows(k, n, h, "k")), _ROWS.pack(*self._rows(v, n, h, "v")), n, pos,
                          _raw_stream(self._index))
         if status:
@@ -167,8 +169,7 @@ class KV4Cache:
         A row that sees nothing gives zeros.  Returns [n, n_heads, head_dim] in q's dtype."""
         if stream is not None or _current_device() != self._index:
             return self._elsewhere(self.attend, stream, (q, pos, length, window, scale, out))
-        shape = q.shape
-        n, heads = shape[0], shape[1]
+        n, heads, _ = shape = q.shape
         rows = self._rows(q, n, heads, "q")
         if out is None:
             out = _torch.empty(shape, dtype=q.dtype, device=self.device)

@@ -150,6 +150,39 @@ def test_attend_blocks(pm, dtype, hq, hkv, hd, n, pos):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hq,hkv,hd,n,pos,window", [
+    (32, 8, 128, 700, 0, 0), (32, 8, 64, 1100, 130, 0), (15, 5, 64, 1400, 9, 0), (24, 8, 128, 900, 1, 200),   # more tiles than SMs
+    (40, 1, 128, 1, 3000, 0), (33, 1, 64, 1, 20000, 0), (34, 1, 64, 1, 127, 0), (80, 2, 128, 1, 9000, 5000),  # one token
+    (9, 1, 64, 60, 7000, 0), (12, 4, 128, 90, 6000, 0), (35, 5, 64, 77, 2500, 1111)])                         # odd groups, cut tiles
+def test_attend_many_tiles_and_wide_groups(pm, dtype, hq, hkv, hd, n, pos, window):
+    cache, (k, v) = filled(pm, hkv, hd, pos + n, pos + hd)
+    q = torch.randn(n, hq, hd, generator=gen(n), device="cuda").to(dtype)
+    check(cache.attend(q, pos, window=window), *ref.attention(q, k, v, pos, pos + n, window, 0))
+
+
+def test_attend_after_calls_of_the_same_shape_elsewhere(pm):
+    """The same rows at short, long and short contexts again: scratch is asked for by shape, the need depends on more."""
+    cache, (k, v) = filled(pm, 2, 64, 30000, 8)
+    for n in (1, 20, 200):
+        q = torch.randn(n, 8, 64, generator=gen(n), device="cuda").half()
+        for pos, window in ((5, 0), (29000, 0), (64, 0), (29500, 300), (12000, 0), (0, 0)):
+            check(cache.attend(q, pos, window=window), *ref.attention(q, k, v, pos, pos + n, window, 0))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,bad", [(3, 1), (150, 40)])
+def test_a_row_that_is_not_finite_stays_by_itself(pm, dtype, n, bad):
+    """q has to be finite; a padded row that is not may spoil its own output only."""
+    cache, (k, v) = filled(pm, 2, 128, 3000, 8)
+    q = torch.randn(n, 4, 128, generator=gen(n), device="cuda").to(dtype)
+    want, bound = ref.attention(q, k, v, 2700, 2700 + n, 0, 0)
+    rest = [i for i in range(n) if i != bad]
+    for value in (math.nan, math.inf, -math.inf):
+        q[bad, :, ::3] = value
+        check(cache.attend(q, 2700)[rest], want[rest], bound[rest])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n,pos,length,window", [
     (1, 900, 901, 1), (1, 900, 901, 17), (1, 900, 901, 900), (1, 900, 901, 901), (1, 900, 901, 5000),
     (7, 900, 907, 3), (7, 900, 907, 64), (150, 700, 850, 40), (300, 0, 300, 33), (260, 3000, 3260, 1000),

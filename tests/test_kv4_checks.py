@@ -99,6 +99,20 @@ def test_queries(pm, over, status):
         assert need.value == 0
 
 
+def test_k_and_v_are_read_to_different_places(pm):
+    L, c, r = pm.lib(), cache(pm), rows(pm)
+    assert L.lf_kv4_read(C.byref(c), C.byref(r), C.byref(r), 1, 0, None) == INVALID
+
+
+def test_rows_of_all_heads_are_counted_in_64_bits(pm):
+    L, c, need = pm.lib(), cache(pm, n_kv_heads=1024), C.c_int64(-1)
+    r = rows(pm, token_stride=0, head_stride=0)
+    for n, heads in (((1 << 22) + 1, 1024), (1 << 28, 1024), (1 << 18, 16385 * 1024)):
+        q = pm.lf_kv4_query(r, rows(pm, data=2 * P), heads, n, 0, 1, 0, 0.0)
+        assert L.lf_kv4_workspace(C.byref(c), C.byref(q), C.byref(need)) == UNSUPPORTED
+        assert L.lf_kv4_attend(C.byref(c), C.byref(q), 3 * P, 1 << 40, None) == UNSUPPORTED
+
+
 def test_structures_match_the_header(pm):
     import test_abi_layout as lay
     mine = ("lf_kv4", "lf_rows", "lf_kv4_query")
