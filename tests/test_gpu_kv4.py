@@ -358,24 +358,67 @@ def test_two_streams_at_once(pm):
     assert all(torch.equal(o, want[i]) for i, o in got)
 
 
-@pytest.mark.parametrize("n", [1, 140])
-def test_scratch_is_held_until_the_launch(pm, monkeypatch, n):
-    """What another thread on the stream may be given while a call is on its way to the launch is not its scratch."""
-    from persistent_monokernel_gb300 import kv4
+def test_threads_on_one_stream(pm):
+    """Calls that need scratch from several threads: what one lets go of before its launch would be another's."""
+    from concurrent.futures import ThreadPoolExecutor
     cache, _ = filled(pm, 8, 128, 40000, 3)
-    q = torch.randn(n, 8 if n == 1 else 32, 128, generator=gen(n), device="cuda").half()
-    want = cache.attend(q, 39000)
-    launch, seen = kv4._attend, []
+    qs = [torch.randn(n, h, 128, generator=gen(n), device="cuda").half() for n, h in ((1, 8), (140, 32), (1, 16), (3, 8))]
+    want = [cache.attend(q, 39000) for q in qs]
 
-    def between(addr, args, ws, size, stream):
-        seen.append(size)
-        other = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
-        assert all(abs(t.data_ptr() - ws) >= size for t in other)
-        return launch(addr, args, ws, size, stream)
+    def work(i):
+        return all([torch.equal(cache.attend(qs[i], 39000), want[i]) for _ in range(100)])
 
-    monkeypatch.setattr(kv4, "_attend", between)
-    assert torch.equal(cache.attend(q, 39000), want)
-    assert seen and seen[0] > 0
+    with ThreadPoolExecutor(4) as ex:
+        assert all(ex.map(work, range(4)))
+
+
+def test_what_is_no_tensor_or_no_number(pm):
+    cache = pm.KV4Cache(2, 64, 32)
+    x, q = (torch.randn(4, h, 64, device="cuda").half() for h in (2, 8))
+    for call in (lambda: cache.append(None, x, 0), lambda: cache.append(x, [1], 0), lambda: cache.attend(3, 0),
+                 lambda: cache.append(x[0], x, 0), lambda: cache.attend(q[0, 0], 0), lambda: cache.attend(q, 0, out=x),
+                 lambda: cache.read(0, 4, out=(x, None)), lambda: cache.read(0, 4, out=(x,)), lambda: cache.attend(q.to_sparse(), 0),
+                 lambda: cache.attend(q.double(), 0)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: cache.append(x, x, None), lambda: cache.append(x, x, 0.5), lambda: cache.attend(q, None),
+                 lambda: cache.attend(q, 0, window=None), lambda: cache.attend(q, 0, scale="1"), lambda: cache.read("0", 1),
+                 lambda: cache.attend(q, 0, length=1.0)):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: cache.attend(q, 0, out=q.float()), lambda: cache.read(0, 2 ** 31 - 1), lambda: cache.read(2 ** 31 - 1, 2 ** 31 - 1), lambda: cache.attend(q, 2 ** 31 - 1),
+                 lambda: cache.append(x.expand(4, 2, 64)[:1].expand(33, 2, 64), x[:1].expand(33, 2, 64), 0)):
+        with pytest.raises(pm.LFError):
+            call()
+    assert (cache.k_codes == 0).all()
+    # positions as NumPy and torch integers, results in tensors that the caller keeps
+    i = torch.tensor(3)
+    cache.append(x, x, i)
+    k, v = cache.read(i, 4)
+    assert cache.read(3, 4, out=(k, v))[1] is v and torch.equal(k, v)
+    out = torch.empty_like(q)
+    assert cache.attend(q, i, out=out) is out and torch.equal(out, cache.attend(q, 3))
+
+
+def test_calls_keep_no_memory(pm):
+    """References and scratch go with the call, refused ones too."""
+    import gc
+    import sys
+    cache = filled(pm, 8, 128, 40000, 3)[0]
+    q = torch.randn(1, 8, 128, device="cuda").half()
+    out, row = torch.empty_like(q), torch.empty_like(q)
+    cache.attend(q, 39000)
+    gc.collect()                                          # of earlier tests
+    before, refs = torch.cuda.memory_allocated(), [sys.getrefcount(t) for t in (q, out, row)]
+    for _ in range(20):
+        cache.attend(q, 39000)
+        cache.attend(q, 39000, out=out)
+        cache.read(39000, 1), cache.read(0, 1, out=(out, row)), cache.append(q, q, 39999)
+        for call in (lambda: cache.attend(q, 39000, window=-1), lambda: cache.attend(q, 39000, out=q), lambda: cache.read(0, 2, out=(out, row)),
+                     lambda: cache.attend(q, 39000, out=out[0]), lambda: cache.append(q, q, 40000), lambda: cache.attend(q, 2 ** 40, out=out)):
+            with pytest.raises((pm.LFError, ValueError)):
+                call()
+    assert torch.cuda.memory_allocated() == before and [sys.getrefcount(t) for t in (q, out, row)] == refs
 
 
 def test_the_first_calls_of_a_process_may_be_captured():
