@@ -47,30 +47,24 @@ __global__ void __launch_bounds__(256) append_rows(Cache c, Rows k, Rows v, int 
     if (t >= n) return;
     const Rows &in = isv ? v : k;
     float x[16];
-    load_block<T>(in, t, h, b, x);
-    unsigned top = 0u;                                    // the largest magnitude's bits: NaN above infinity above all
-#pragma unroll
-    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+    unsigned top = load_block<T>(in, t, h, b, x);
     if (top >= 0x7f800000u) {
-        top = 0u;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            x[j] = x[j] != x[j] ? 0.f : fminf(fmaxf(x[j], -3.402823466e38f), 3.402823466e38f);
-            top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-        }
+        for (int j = 0; j < 16; ++j) x[j] = x[j] != x[j] ? 0.f : fminf(fmaxf(x[j], -3.402823466e38f), 3.402823466e38f);
+        top = top_of(x);
     }
     const unsigned s8 = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.0f), __NV_SATFINITE, __NV_E4M3);
     const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3)));
     unsigned w[2] = {0u, 0u};
     if (s > 0.f) {   // a block below E4M3's range (A < 6 * 2^-10) is stored as zeros
         const float r = __frcp_rn(s);
+        const uint64_t rr = pack2(r, r), ss = pack2(-s, -s);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float q = x[j] * r;
-            x[j] = fmaf(fmaf(-q, s, x[j]), r, q);
+        for (int j = 0; j < 8; ++j) {
+            const uint64_t v = pack2(x[2 * j], x[2 * j + 1]), q = mul2(v, rr);
+            const float2 y = unpack2(fma2(fma2(q, ss, v), rr, q));   // -q s + x = q (-s) + x
+            w[j / 4] |= e2m1x2(y.x, y.y) << (8 * (j % 4));
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j / 4] |= e2m1x2(x[2 * j], x[2 * j + 1]) << (8 * (j % 4));
     }
     const size_t row = (size_t)h * c.cap + (size_t)pos + (size_t)t;
     *reinterpret_cast<uint2 *>((isv ? c.vc : c.kc) + row * code_bytes(c.hd) + b * 8) = make_uint2(w[0], w[1]);

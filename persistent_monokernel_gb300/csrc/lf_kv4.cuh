@@ -90,45 +90,99 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t a)
     return v;
 }
 
-// ---- rows by element type: 16 consecutive values (16-byte aligned)
+// ---- packed FP32 pairs
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
+    return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// ---- rows by element type: 16 consecutive values (16-byte aligned), and the bits of the largest magnitude as FP32
+// (NaN's above infinity's above all; 16-bit types find it two values at a time)
 template <class T>
-__device__ __forceinline__ void load16(const T *p, float (&x)[16]);
+__device__ __forceinline__ unsigned load16(const T *p, float (&x)[16]);
+__device__ __forceinline__ unsigned top_of(const float (&x)[16])
+{
+    unsigned top = 0u;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+    return top;
+}
+__device__ __forceinline__ unsigned top_of(const uint4 &a, const uint4 &b)
+{
+    const unsigned m = 0x7fff7fffu;
+    const unsigned t = __vmaxu2(__vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m)),
+                                __vmaxu2(__vmaxu2(b.x & m, b.y & m), __vmaxu2(b.z & m, b.w & m)));
+    return max(t & 0xffffu, t >> 16);
+}
+__device__ __forceinline__ unsigned halves(const uint4 &a, const uint4 &b, float (&x)[16])
+{
+    const unsigned w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[u]));
+        x[2 * u] = f.x, x[2 * u + 1] = f.y;
+    }
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top_of(a, b))));
+}
 template <>
-__device__ __forceinline__ void load16<float>(const float *p, float (&x)[16])
+__device__ __forceinline__ unsigned load16<float>(const float *p, float (&x)[16])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float4 v = ld(reinterpret_cast<const float4 *>(p) + j);
         x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
     }
+    return top_of(x);
 }
 template <>
-__device__ __forceinline__ void load16<__half>(const __half *p, float (&x)[16])
+__device__ __forceinline__ unsigned load16<__half>(const __half *p, float (&x)[16])
 {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint4 v = ld(reinterpret_cast<const uint4 *>(p) + j);
-        const unsigned w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[u]));
-            x[8 * j + 2 * u] = f.x, x[8 * j + 2 * u + 1] = f.y;
-        }
-    }
+    const uint4 *v = reinterpret_cast<const uint4 *>(p);
+    return halves(ld(v), ld(v + 1), x);
 }
 template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[16])
+__device__ __forceinline__ unsigned load16<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[16])
 {
+    const uint4 a = ld(reinterpret_cast<const uint4 *>(p)), b = ld(reinterpret_cast<const uint4 *>(p) + 1);
+    const unsigned w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint4 v = ld(reinterpret_cast<const uint4 *>(p) + j);
-        const unsigned w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            x[8 * j + 2 * u] = __uint_as_float(w[u] << 16);
-            x[8 * j + 2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
-        }
+    for (int u = 0; u < 8; ++u) {
+        x[2 * u] = __uint_as_float(w[u] << 16);
+        x[2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
     }
+    return top_of(a, b) << 16;
 }
 __device__ __forceinline__ float2 h2_f2(unsigned h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 __device__ __forceinline__ unsigned pack_bf2(float lo, float hi)
@@ -140,32 +194,25 @@ __device__ __forceinline__ unsigned pack_bf2(float lo, float hi)
 struct Tagged {};
 struct Swizzled {};
 template <class T>
-__device__ __forceinline__ void load_block(const Rows &in, long long t, int h, int b, float (&x)[16])
+__device__ __forceinline__ unsigned load_block(const Rows &in, long long t, int h, int b, float (&x)[16])
 {
-    load16<T>(static_cast<const T *>(in.p) + t * in.ts + h * in.hs + b * 16, x);
+    return load16<T>(static_cast<const T *>(in.p) + t * in.ts + h * in.hs + b * 16, x);
 }
 template <>
-__device__ __forceinline__ void load_block<Tagged>(const Rows &in, long long t, int h, int b, float (&x)[16])
+__device__ __forceinline__ unsigned load_block<Tagged>(const Rows &in, long long t, int h, int b, float (&x)[16])
 {
     load16<float>(static_cast<const float *>(in.p) + t * in.ts + h * in.hs + b * 16, x);
 #pragma unroll
     for (int j = 0; j < 16; ++j) x[j] = __half2float(__float2half_rn(x[j]));
+    return top_of(x);
 }
 template <>
-__device__ __forceinline__ void load_block<Swizzled>(const Rows &in, long long t, int h, int b, float (&x)[16])
+__device__ __forceinline__ unsigned load_block<Swizzled>(const Rows &in, long long t, int h, int b, float (&x)[16])
 {
     const __half *row = static_cast<const __half *>(in.p) + t * in.ts + h * in.hs;
     const int sw = (int)((in.aux + t) & 7);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(row + ((2 * b + j) ^ sw) * 8);
-        const unsigned w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[u]));
-            x[8 * j + 2 * u] = f.x, x[8 * j + 2 * u + 1] = f.y;
-        }
-    }
+    return halves(ld(reinterpret_cast<const uint4 *>(row + ((2 * b) ^ sw) * 8)),
+                  ld(reinterpret_cast<const uint4 *>(row + ((2 * b + 1) ^ sw) * 8)), x);
 }
 // 16 bytes of cached values, FP16 pairs in h, as T (exact: at most 6 significant bits)
 __device__ __forceinline__ void store_values(__half *p, const unsigned (&h)[4])
