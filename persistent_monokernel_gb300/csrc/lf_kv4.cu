@@ -35,6 +35,11 @@ namespace lfq {
 // that rounding; and an FP32 x other than t s is at least mant(t) / mant(t s) >= 1 / 1.875 steps of t away from it
 // in the quotient, more than the half step that would round it to t.  So the codes are those of the exact quotient
 // (the same holds for A / 6 and the scales' half-way values).
+//
+// Bound by memory, the arithmetic close behind: 32,767 positions of 5 heads x 128 take 18.8 us from FP16 (5.7 TB/s)
+// and 29.3 from FP32 (6.5 TB/s), a copy's rate being 6.7; one position takes 1.3 us.  Products two to an
+// instruction: 21.8 us without.  One block a thread: the loads in flight come from many threads of few registers (two
+// blocks of raw bytes a thread: 18.1 us, but 2.0 instead of 1.6 at 777 positions).
 template <class T>
 __global__ void __launch_bounds__(256) append_rows(Cache c, Rows k, Rows v, int n, int pos, int shift)
 {
@@ -72,7 +77,8 @@ __global__ void __launch_bounds__(256) append_rows(Cache c, Rows k, Rows v, int 
 }
 
 // A thread takes 16 bytes of the output (8 values, 4 in FP32) of READ_U places 256 apart: a warp's stores are
-// contiguous, and each thread has several loads on their way.
+// contiguous, and each thread has several loads on their way.  Bound by the stores: 32,767 positions of 5 heads x 128
+// take 15.6 us in FP16 (6.9 TB/s; 20.9 with a division per place), one position 1.1 us.
 constexpr int READ_U = 4;
 template <class T>
 __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n, int pos, int shift)
@@ -140,9 +146,16 @@ __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n,
 // and P are split into an FP16 head and remainder and the products are formed
 // twice, which leaves errors near 2^-22.
 //
-// What bounds it: instructions.  A cached value costs a conversion and a multiply
-// by its scale per pair, and its share of the product; everything else is kept off
-// the loop (addresses advance by constants, no maximum, no rescaling).
+// What bounds it: instructions and memory together, and in short contexts latency.
+// A cached value costs a conversion and a multiply by its scale per pair, half an
+// instruction to bring its byte to the converter, and its share of the product;
+// everything else is kept off the loop (addresses advance by constants, no maximum,
+// no rescaling).  One token over 131,072 positions of 8 KV heads x 128: 41 us, 3.7 TB/s
+// of 6.7, 49 % of the issue slots (65 us with a maximum per chunk, 48 before clusters
+// joined); over 512 positions of 5 heads: 5.2 us.  FP16 values through shared memory
+// would write and read four times the cache's bytes there.  The next chunk's loads
+// one phase ahead: 39.6 us at 131,072, but 47 instead of 45.6 with FP32 queries and
+// 5.6 at 512, as the registers run out.
 __device__ __forceinline__ void add_scaled(float4 &acc, const float4 &v, float x)
 {
     acc.x = fmaf(v.x, x, acc.x);
@@ -491,7 +504,8 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
 }
 
 // Joins the partial states of a row: `groups` x hd / 4 threads per query row and KV head, each group taking every
-// groups-th state, then the groups through shared memory.
+// groups-th state, then the groups through shared memory.  Bound by the launch and
+// one round of loads: 3 of the 41 us of one token over 131,072 positions.
 constexpr int JOIN_THREADS = 256;
 __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant__ Attn a, int groups)
 {
