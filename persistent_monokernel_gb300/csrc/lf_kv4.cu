@@ -513,6 +513,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant_
     const int hd = a.c.hd, lanes = hd / 4, per = JOIN_THREADS / (lanes * groups);   // rows per block
     const int row = blockIdx.x * per + threadIdx.x / (lanes * groups), kvh = blockIdx.y;
     const int grp = threadIdx.x / lanes % groups, d = threadIdx.x % lanes * 4;
+    dependents_may_launch();
     wait_for_prerequisites();
     Joined j;
     int parts = 0;
