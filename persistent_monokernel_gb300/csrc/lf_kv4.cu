@@ -546,10 +546,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant_
 
 // ---------------------------------------------------------------- launches
 
-// Chunks a warp up to which one cluster of 8 CTAs takes a row tile's whole range.
+// Chunks a warp up to which one cluster of 8 CTAs takes a row tile's whole range, in one launch (one token at 8,000
+// positions, 20/5 heads x 128: 9.5 us, in two launches 9.1; at 16,000 14.3 and 11.2).
 constexpr int kClusterChunks = 4;
-// Rows per KV head from which the tiles kernel takes over.
-constexpr int kTileRows = 33;
 
 // Workspace of the tiles kernel: two states per CTA, and where each tile's are.
 static size_t tiles_workspace(const Cache &c, size_t ctas, size_t tiles)
@@ -598,9 +597,11 @@ int share_tiles(const Attn &a, int ctas, Shares &sh)
     return ctas;   // not reached: the last CTA takes what is left
 }
 
-static size_t plan_tiles(Attn &a, int sms, int rows)
+// The tiles kernel's time in microseconds, and its plan but for the shares.
+static double plan_tiles(Attn &a, int sms, int rows)
 {
     a.rt = 128;
+    a.cl = 1;
     a.tiles = (rows + 127) / 128;
     sms = std::min(sms, MAX_CTAS);
     long long total = 0;
@@ -617,22 +618,62 @@ static size_t plan_tiles(Attn &a, int sms, int rows)
     const long long t = (long long)a.tiles * a.c.Hkv, ctas = std::min<long long>(sms, std::max<long long>(1, total / 2));
     const double extra = piece_cost(a), shared = 1.1 * (double)(total + (t + ctas) * extra) / (double)ctas + 8.0;
     const double each = t <= sms ? most + extra : (double)(total + t * extra) / (double)sms + (most + extra) / 2.0;
-    if (each <= shared && t < (1ll << 30)) {
-        a.splits = (int)t;
-        a.per = 0;
-        return 0;
+    const bool own = each <= shared && t < (1ll << 30);
+    a.splits = own ? (int)t : 0;
+    a.per = own ? 0 : (int)ctas;
+    const double chunk = (a.q.dtype == F32 ? 1.6 : 0.8) * (a.c.hd == 128 ? 1.0 : 0.8);
+    return chunk * (own ? each : shared);
+}
+
+// The rows kernel's time in microseconds, its plan and workspace.
+static double plan_rows(Attn &a, int sms, int rows, size_t &bytes)
+{
+    a.rt = rows <= 8 ? 8 : 16;
+    a.tiles = (rows + a.rt - 1) / a.rt;
+    a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
+    a.cl = 1;
+    bytes = 0;
+    const int chunks = std::max(1, (key_hi(a.pos, a.n - 1, a.len) - a.lo + CH - 1) / CH);
+    const int slots = (a.rt == 8 ? 2 : 1) * sms;           // CTAs that run at a time
+    const long long t = (long long)a.tiles * a.c.Hkv;
+    // Eight warps a CTA, so its range is a whole number of eights of chunks.
+    const int eights = (chunks + 7) / 8;
+    int each;
+    if (eights <= 8 * kClusterChunks) {
+        // short: one cluster of at most 8 CTAs per row tile does it all in one launch
+        each = (eights + 7) / 8;
+        a.splits = a.cl = (eights + each - 1) / each;
+    } else {
+        // long: the SMs filled and joined through the workspace by a second launch.  Of the cluster sizes
+        // that leave no more slots empty than the best, the largest: the join then has the fewest states (131,072
+        // positions: one KV head 14 us with clusters of 8, 25 without; eight heads 41 with 304 slots full, 43 with 256).
+        const int most = (int)std::min<long long>(t, 1 << 20);
+        int best = 0, groups = 1;
+        for (int cl = 8; cl >= 1; cl /= 2) {
+            const int g = std::max(1, slots / (most * cl));
+            if (g * cl * most > best + best / 100) {
+                best = g * cl * most;
+                a.cl = cl;
+                groups = g;
+            }
+        }
+        each = (eights + groups * a.cl - 1) / (groups * a.cl);
+        groups = (eights + each * a.cl - 1) / (each * a.cl);
+        a.splits = groups * a.cl;
+        if (groups > 1) bytes = (size_t)t * a.rt * groups * (a.c.hd + PAD) * sizeof(float);
     }
-    Shares sh;
-    a.per = (int)ctas;
-    a.splits = share_tiles(a, a.per, sh);
-    return tiles_workspace(a.c, (size_t)a.splits, (size_t)t);
+    a.per = each * 8 * CH;
+    const bool f32 = a.q.dtype == F32, wide = a.c.hd == 128;
+    const double begin = (wide ? 6.1 : 5.0) + (f32 ? 0.7 : 0.0) + (a.cl > 1 ? (wide ? 1.9 : 1.5) : 0.0);
+    const double chunk = (wide ? 1.8 : 1.45) * (f32 ? 1.2 : 1.0);
+    return (double)((t * a.splits + slots - 1) / slots) * (begin + chunk * (each - 1)) + (bytes ? 2.5 : 0.0);
 }
 
 size_t max_workspace(const Cache &c, int Hq, int n, int sms)
 {
     const size_t rows = (size_t)n * (Hq / c.Hkv);
     return std::max((size_t)2 * sms * 16 * (c.hd + PAD) * sizeof(float),
-                    rows < (size_t)kTileRows ? (size_t)0 : tiles_workspace(c, (size_t)sms, (rows + 127) / 128 * c.Hkv));
+                    rows <= 8 ? (size_t)0 : tiles_workspace(c, (size_t)sms, (rows + 127) / 128 * c.Hkv));
 }
 
 void set_workspace(Attn &a, void *ws)
@@ -646,41 +687,20 @@ size_t plan_attn(Attn &a, int sms)
     a.gsh = -1;
     for (int s = 0; s < 30; ++s)
         if (a.G == 1 << s) a.gsh = s;
-    const int rows = a.n * a.G, hi = key_hi(a.pos, a.n - 1, a.len);
-    a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
-    const size_t state = (size_t)a.c.Hkv * (a.c.hd + PAD) * sizeof(float);
-    a.cl = 1;
-    if (rows >= kTileRows) return plan_tiles(a, sms, rows);
-    a.rt = rows <= 8 ? 8 : 16;
-    a.tiles = (rows + a.rt - 1) / a.rt;
-    const int chunks = std::max(1, (hi - a.lo + CH - 1) / CH);
-    // Eight warps a CTA, so its range is a whole number of eights of chunks.
-    const int eights = (chunks + 7) / 8;
-    if (eights <= 8 * kClusterChunks) {
-        // short: one cluster of at most 8 CTAs per row tile does it all in one launch
-        const int per = (eights + 7) / 8;
-        a.splits = a.cl = (eights + per - 1) / per;
-        a.per = per * 8 * CH;
-        return 0;
-    }
-    // long: two CTAs per SM (one of 16 rows), joined through the workspace by a second launch.  Of the cluster sizes
-    // that leave no more slots empty than the best, the largest: the join then has the fewest states (131,072
-    // positions: one KV head 14 us with clusters of 8, 25 without; eight heads 41 with 304 slots full, 43 with 256).
-    const int slots = (a.rt == 8 ? 2 : 1) * sms, t = (int)std::min<long long>((long long)a.tiles * a.c.Hkv, 1 << 20);
-    int best = 0, groups = 1;
-    for (int cl = 8; cl >= 1; cl /= 2) {
-        const int g = std::max(1, slots / (t * cl));
-        if (g * cl * t > best + best / 100) {
-            best = g * cl * t;
-            a.cl = cl;
-            groups = g;
-        }
-    }
-    const int per = (eights + groups * a.cl - 1) / (groups * a.cl);
-    groups = (eights + per * a.cl - 1) / (per * a.cl);
-    a.splits = groups * a.cl;
-    a.per = per * 8 * CH;
-    return groups > 1 ? state * a.tiles * a.rt * groups : 0;
+    const int rows = a.n * a.G;
+    size_t bytes;
+    const double by_rows = plan_rows(a, sms, rows, bytes);
+    if (rows <= 8) return bytes;
+    // More rows than one n-tile: the faster kernel by the models above.  (20/5 heads x 128, FP16, rows kernel against
+    // tiles kernel: 64 rows at 1,024 8.6 and 16.5 us, at 4,096 11.7 and 15.9, at 8,192 28.0 and 17.8; 256 rows at 0
+    // 6.4 and 9.4, at 256 15.2 and 12.2; 1,024 rows at 0 17.3 and 11.5.)
+    Attn b = a;
+    if (by_rows <= plan_tiles(b, sms, rows)) return bytes;
+    a = b;
+    if (a.per == 0) return 0;
+    Shares sh;
+    a.splits = share_tiles(a, a.per, sh);
+    return tiles_workspace(a.c, (size_t)a.splits, (size_t)a.tiles * a.c.Hkv);
 }
 
 template <template <class> class F, class... A>

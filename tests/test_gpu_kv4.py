@@ -142,7 +142,7 @@ def test_attend_few_rows(pm, dtype, hq, hkv, hd, n, pos):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("hq,hkv,hd", [(16, 4, 64), (20, 5, 128), (8, 1, 128), (24, 2, 128)])
-@pytest.mark.parametrize("n,pos", [(33, 0), (64, 64), (129, 0), (200, 1000), (511, 1), (130, 4000)])
+@pytest.mark.parametrize("n,pos", [(33, 0), (64, 64), (129, 0), (200, 1000), (511, 1), (130, 4000), (1024, 3)])
 def test_attend_blocks(pm, dtype, hq, hkv, hd, n, pos):
     cache, (k, v) = filled(pm, hkv, hd, pos + n + 5, pos + hd)
     q = torch.randn(n, hq, hd, generator=gen(n), device="cuda").to(dtype)
@@ -162,18 +162,18 @@ def test_attend_many_tiles_and_wide_groups(pm, dtype, hq, hkv, hd, n, pos, windo
 
 def test_attend_after_calls_of_the_same_shape_elsewhere(pm):
     """The same rows at short, long and short contexts again: scratch is asked for by shape, the need depends on more."""
-    cache, (k, v) = filled(pm, 2, 64, 30000, 8)
-    for n in (1, 20, 200):
+    cache, (k, v) = filled(pm, 2, 64, 31000, 8)
+    for n in (1, 20, 200, 1000):
         q = torch.randn(n, 8, 64, generator=gen(n), device="cuda").half()
         for pos, window in ((5, 0), (29000, 0), (64, 0), (29500, 300), (12000, 0), (0, 0)):
             check(cache.attend(q, pos, window=window), *ref.attention(q, k, v, pos, pos + n, window, 0))
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("n,bad", [(3, 1), (150, 40)])
+@pytest.mark.parametrize("n,bad", [(3, 1), (150, 40), (2000, 777)])
 def test_a_row_that_is_not_finite_stays_by_itself(pm, dtype, n, bad):
     """q has to be finite; a padded row that is not may spoil its own output only."""
-    cache, (k, v) = filled(pm, 2, 128, 3000, 8)
+    cache, (k, v) = filled(pm, 2, 128, 2850 + n, 8)
     q = torch.randn(n, 4, 128, generator=gen(n), device="cuda").to(dtype)
     want, bound = ref.attention(q, k, v, 2700, 2700 + n, 0, 0)
     rest = [i for i in range(n) if i != bad]
@@ -186,7 +186,8 @@ def test_a_row_that_is_not_finite_stays_by_itself(pm, dtype, n, bad):
 @pytest.mark.parametrize("n,pos,length,window", [
     (1, 900, 901, 1), (1, 900, 901, 17), (1, 900, 901, 900), (1, 900, 901, 901), (1, 900, 901, 5000),
     (7, 900, 907, 3), (7, 900, 907, 64), (150, 700, 850, 40), (300, 0, 300, 33), (260, 3000, 3260, 1000),
-    (200, 100, 150, 0), (200, 100, 50, 0), (4, 10, 3, 0)])
+    (200, 100, 150, 0), (200, 100, 50, 0), (4, 10, 3, 0), (1300, 700, 2000, 40), (1500, 0, 1500, 33), (1400, 3000, 4400, 1000),
+    (1300, 100, 1200, 0), (1300, 100, 50, 0), (1300, 100, 700, 90)])
 def test_attend_windows_and_lengths(pm, dtype, n, pos, length, window):
     cache, (k, v) = filled(pm, 2, 128, max(length, pos + n), 5)
     q = torch.randn(n, 8, 128, generator=gen(n), device="cuda").to(dtype)
@@ -197,7 +198,7 @@ def test_attend_windows_and_lengths(pm, dtype, n, pos, length, window):
 @pytest.mark.parametrize("hd", [64, 128])
 def test_rows_that_see_nothing_are_zero(pm, dtype, hd):
     cache, (k, v) = filled(pm, 2, hd, 400, 1)
-    for n in (1, 6, 300):
+    for n in (1, 6, 300, 1600):
         q = torch.randn(n, 8, hd, generator=gen(n), device="cuda").to(dtype)
         # an empty cache; a window past the last position for some rows, for all of them
         assert (cache.attend(q, 0, length=0) == 0).all()
@@ -209,10 +210,10 @@ def test_rows_that_see_nothing_are_zero(pm, dtype, hd):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("n", [1, 4, 150])
+@pytest.mark.parametrize("n", [1, 4, 150, 2000])
 def test_positions_that_no_row_sees_do_not_count(pm, dtype, n):
     """Scales that stand for NaN (never written by append) before the window and behind the last position."""
-    cache, (k, v) = filled(pm, 2, 64, 700, 9)
+    cache, (k, v) = filled(pm, 2, 64, 550 + n, 9)
     pos, window = 333, 100
     q = torch.randn(n, 4, 64, generator=gen(n), device="cuda").to(dtype)
     want = ref.attention(q, k, v, pos, pos + n, window, 0)
@@ -226,26 +227,26 @@ def test_positions_that_no_row_sees_do_not_count(pm, dtype, n):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("n", [1, 6, 140])
+@pytest.mark.parametrize("n", [1, 6, 140, 1300])
 @pytest.mark.parametrize("size,scale", [(30.0, 0.0), (1.0, 2.5), (1.0, -0.3), (1e-6, 1e5), (1000.0, 1e-3), (0.0, 0.0)])
 def test_attend_scales_and_sizes_of_q(pm, dtype, n, size, scale):
-    cache, (k, v) = filled(pm, 2, 128, 600, 2)
+    cache, (k, v) = filled(pm, 2, 128, 460 + n, 2)
     q = (torch.randn(n, 8, 128, generator=gen(n), device="cuda") * size).to(dtype)
     check(cache.attend(q, 400, scale=scale), *ref.attention(q, k, v, 400, 400 + n, 0, scale))
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("n", [1, 140])
+@pytest.mark.parametrize("n", [1, 140, 2500])
 def test_q_beyond_the_range_of_fp16(pm, dtype, n):
-    cache, (k, v) = filled(pm, 2, 64, 600, 2)
+    cache, (k, v) = filled(pm, 2, 64, 460 + n, 2)
     for size in (1e8, 1e-12, 1e30):
         q = (torch.randn(n, 4, 64, generator=gen(n), device="cuda") * size).to(dtype)
         check(cache.attend(q, 400, scale=1 / size / 8), *ref.attention(q, k, v, 400, 400 + n, 0, 1 / size / 8))
 
 
-@pytest.mark.parametrize("n", [1, 5, 140])
+@pytest.mark.parametrize("n", [1, 5, 140, 1300])
 def test_attend_layouts(pm, n):
-    cache, _ = filled(pm, 2, 128, 700, 4)
+    cache, _ = filled(pm, 2, 128, 560 + n, 4)
     qkv = torch.randn(n, 12, 128, generator=gen(n), device="cuda").half()
     q = qkv[:, :8]
     want = cache.attend(q.contiguous(), 500)
