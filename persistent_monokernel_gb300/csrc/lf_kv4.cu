@@ -546,10 +546,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant_
 
 // ---------------------------------------------------------------- launches
 
-// Chunks a warp up to which one cluster of 8 CTAs takes a row tile's whole range, in one launch (one token at 8,000
-// positions, 20/5 heads x 128: 9.5 us, in two launches 9.1; at 16,000 14.3 and 11.2).
-constexpr int kClusterChunks = 4;
-
 // Workspace of the tiles kernel: two states per CTA, and where each tile's are.
 static size_t tiles_workspace(const Cache &c, size_t ctas, size_t tiles)
 {
@@ -625,48 +621,55 @@ static double plan_tiles(Attn &a, int sms, int rows)
     return chunk * (own ? each : shared);
 }
 
-// The rows kernel's time in microseconds, its plan and workspace.
+// CTAs of the rows kernel that run at a time in clusters of cl (a cluster stays within a group of SMs, so that larger
+// ones leave some empty): two per SM, one of 16 rows, as the runtime's occupancy query gives them for a GB300's 152.
+static int slots_of(int rt, int cl, int sms)
+{
+    static const int two[9] = {0, 304, 304, 291, 296, 290, 276, 266, 288}, one[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};
+    const int n = (rt == 8 ? two : one)[cl] * sms / 152;
+    return std::max(n, cl);
+}
+
+// The rows kernel's time in microseconds, its plan and workspace.  The range of a row tile, in eights of chunks (one
+// chunk for each of a CTA's warps), is dealt out to one cluster, which does it all in one launch, or to as many clusters as
+// run at a time, joined by a second launch (2.7 us on the GPU, and its launch by the host).  Either way the time is that
+// of the rounds of CTAs, each a beginning and so many chunks a warp; the figures are measured ones for few CTAs (more
+// chunks cost more under load, for every choice alike).  One token, 20/5 heads x 128: one launch 6.8 us at 4,096
+// and 9.5 at 8,000, two 8.4 and 9.1; at 16,000 14.3 and 11.2.  192 rows at 1,024: clusters of five, which need three
+// rounds, 23.8 us, of two 11.1.  One head at 131,072, clusters of eight 13 us, without 25.
 static double plan_rows(Attn &a, int sms, int rows, size_t &bytes)
 {
     a.rt = rows <= 8 ? 8 : 16;
     a.tiles = (rows + a.rt - 1) / a.rt;
     a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
-    a.cl = 1;
-    bytes = 0;
-    const int chunks = std::max(1, (key_hi(a.pos, a.n - 1, a.len) - a.lo + CH - 1) / CH);
-    const int slots = (a.rt == 8 ? 2 : 1) * sms;           // CTAs that run at a time
+    const int eights = (std::max(1, key_hi(a.pos, a.n - 1, a.len) - a.lo) + 8 * CH - 1) / (8 * CH);
     const long long t = (long long)a.tiles * a.c.Hkv;
-    // Eight warps a CTA, so its range is a whole number of eights of chunks.
-    const int eights = (chunks + 7) / 8;
-    int each;
-    if (eights <= 8 * kClusterChunks) {
-        // short: one cluster of at most 8 CTAs per row tile does it all in one launch
-        each = (eights + 7) / 8;
-        a.splits = a.cl = (eights + each - 1) / each;
-    } else {
-        // long: the SMs filled and joined through the workspace by a second launch.  Of the cluster sizes
-        // that leave no more slots empty than the best, the largest: the join then has the fewest states (131,072
-        // positions: one KV head 14 us with clusters of 8, 25 without; eight heads 41 with 304 slots full, 43 with 256).
-        const int most = (int)std::min<long long>(t, 1 << 20);
-        int best = 0, groups = 1;
-        for (int cl = 8; cl >= 1; cl /= 2) {
-            const int g = std::max(1, slots / (most * cl));
-            if (g * cl * most > best + best / 100) {
-                best = g * cl * most;
+    const bool f32 = a.q.dtype == F32, wide = a.c.hd == 128, two = a.rt == 16;
+    const double begin = (two ? (wide ? 6.0 : 5.0) : (wide ? 4.0 : 3.4)) + (f32 ? 0.5 : 0.0), cluster = wide ? 1.8 : 1.4;
+    const double chunk = (two ? (wide ? 1.8 : 1.45) : (wide ? 1.45 : 1.15)) * (f32 ? 1.15 : 1.0);
+    double best = 1e30;
+    for (int c = std::min(8, eights); c >= 1; --c) {
+        for (int many = 0; many < (eights > 8 ? 2 : 1); ++many) {
+            int groups = many ? (int)(slots_of(a.rt, c, sms) / (t * c)) : 1, cl = c;
+            if (many && groups < 2) continue;
+            const int each = (eights + groups * cl - 1) / (groups * cl);
+            if (!many) cl = (eights + each - 1) / each;
+            groups = (eights + each * cl - 1) / (each * cl);
+            const int slots = slots_of(a.rt, cl, sms);
+            const long long rounds = (t * groups * cl + slots - 1) / slots;
+            const double time = (double)rounds * (begin + (cl > 1 ? cluster : 0.0) + chunk * (each - 1)) +
+                                (groups > 1 ? 4.5 + 0.035 * groups : 0.0);
+            if (time < best) {
+                best = time;
                 a.cl = cl;
-                groups = g;
+                a.splits = groups * cl;
+                a.per = each * 8 * CH;
             }
         }
-        each = (eights + groups * a.cl - 1) / (groups * a.cl);
-        groups = (eights + each * a.cl - 1) / (each * a.cl);
-        a.splits = groups * a.cl;
-        if (groups > 1) bytes = (size_t)t * a.rt * groups * (a.c.hd + PAD) * sizeof(float);
     }
-    a.per = each * 8 * CH;
-    const bool f32 = a.q.dtype == F32, wide = a.c.hd == 128;
-    const double begin = (wide ? 6.1 : 5.0) + (f32 ? 0.7 : 0.0) + (a.cl > 1 ? (wide ? 1.9 : 1.5) : 0.0);
-    const double chunk = (wide ? 1.8 : 1.45) * (f32 ? 1.2 : 1.0);
-    return (double)((t * a.splits + slots - 1) / slots) * (begin + chunk * (each - 1)) + (bytes ? 2.5 : 0.0);
+    const int groups = a.splits / a.cl;
+    bytes = groups > 1 ? (size_t)t * a.rt * groups * (a.c.hd + PAD) * sizeof(float) : 0;
+    return best;
 }
 
 size_t max_workspace(const Cache &c, int Hq, int n, int sms)
