@@ -150,12 +150,12 @@ __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n,
 // A cached value costs a conversion and a multiply by its scale per pair, half an
 // instruction to bring its byte to the converter, and its share of the product;
 // everything else is kept off the loop (addresses advance by constants, no maximum,
-// no rescaling).  One token over 131,072 positions of 8 KV heads x 128: 41 us, 3.7 TB/s
+// no rescaling).  One token over 131,072 positions of 8 KV heads x 128: 39.6 us, 3.8 TB/s
 // of 6.7, 49 % of the issue slots (65 us with a maximum per chunk, 48 before clusters
 // joined); over 512 positions of 5 heads: 5.2 us.  FP16 values through shared memory
 // would write and read four times the cache's bytes there.  The next chunk's loads
-// one phase ahead: 39.6 us at 131,072, but 47 instead of 45.6 with FP32 queries and
-// 5.6 at 512, as the registers run out.
+// one phase ahead gained 4 % at 131,072, but lost 3 % with FP32 queries and 8 % at 512,
+// as the registers run out.
 __device__ __forceinline__ void add_scaled(float4 &acc, const float4 &v, float x)
 {
     acc.x = fmaf(v.x, x, acc.x);
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_c
 
 // Joins the partial states of a row: `groups` x hd / 4 threads per query row and KV head, each group taking every
 // groups-th state, then the groups through shared memory.  Bound by the launch and
-// one round of loads: 3 of the 41 us of one token over 131,072 positions.
+// one round of loads: 3 of the 40 us of one token over 131,072 positions.
 constexpr int JOIN_THREADS = 256;
 __global__ void __launch_bounds__(JOIN_THREADS) attn_join(const __grid_constant__ Attn a, int groups)
 {
