@@ -150,12 +150,12 @@ __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n,
 // A cached value costs a conversion and a multiply by its scale per pair, half an
 // instruction to bring its byte to the converter, and its share of the product;
 // everything else is kept off the loop (addresses advance by constants, no maximum,
-// no rescaling).  One token over 131,072 positions of 8 KV heads x 128: 39.6 us, 3.8 TB/s
+// no rescaling).  One token over 131,072 positions of 8 KV heads x 128: 39.8 us, 3.8 TB/s
 // of 6.7, 49 % of the issue slots (65 us with a maximum per chunk, 48 before clusters
-// joined); over 512 positions of 5 heads: 5.2 us.  FP16 values through shared memory
+// joined); over 512 positions of 5 heads: 4.5 us.  FP16 values through shared memory
 // would write and read four times the cache's bytes there.  The next chunk's loads
-// one phase ahead gained 4 % at 131,072, but lost 3 % with FP32 queries and 8 % at 512,
-// as the registers run out.
+// one phase ahead gained 4 % at 131,072, but lost 3 % with FP32 queries and 8 % at 512
+// (two slabs), as the registers run out; a third CTA per SM costs 75 % (spills).
 __device__ __forceinline__ void add_scaled(float4 &acc, const float4 &v, float x)
 {
     acc.x = fmaf(v.x, x, acc.x);
@@ -196,14 +196,13 @@ struct RowCfg {
                                 RT * (HD + PAD) * 4;
 };
 constexpr float P_EXP = 7.f, P_SUM = 32768.f;
-constexpr int SL = 2;                                  // slabs of 16 positions per chunk
-constexpr int CH = 16 * SL;
 
-template <int HD, int NT, bool SPLIT>
+// SL: slabs of 16 positions per chunk.
+template <int HD, int NT, bool SPLIT, int SL>
 __global__ void __launch_bounds__(256, NT == 1 ? 2 : 1) attn_rows(const __grid_constant__ Attn a)
 {
     using C = RowCfg<HD, NT, SPLIT>;
-    constexpr int NW = C::NW, RT = C::RT, KS = C::KS;
+    constexpr int NW = C::NW, RT = C::RT, KS = C::KS, CH = 16 * SL;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     unsigned *qf = reinterpret_cast<unsigned *>(smem_raw);              // [NT][KS][32][QW]
     float *rs = reinterpret_cast<float *>(qf + NT * KS * 32 * C::QW);   // [RT] score factor of a row
@@ -621,11 +620,14 @@ static double plan_tiles(Attn &a, int sms, int rows)
     return chunk * (own ? each : shared);
 }
 
-// CTAs of the rows kernel that run at a time in clusters of cl (a cluster stays within a group of SMs, so that larger
-// ones leave some empty): two per SM, one of 16 rows, as the runtime's occupancy query gives them for a GB300's 152.
+// CTAs of the rows kernel that run at a time in clusters of cl: two per SM, one of 16 rows.  A cluster stays within a
+// group of SMs, so that larger ones leave some empty: 304, 304, 291, 296, 290, 276, 266, 288 and 152, 152, 138, 144,
+// 140, 138, 105, 120 of a GB300's 152 by the runtime's occupancy query.  Behind another kernel that still holds
+// SMs the last of them may find no place (45 of 46 clusters of 6: 8 us more): one cluster of 4 or 8, a
+// seventh of the other sizes is not counted on.
 static int slots_of(int rt, int cl, int sms)
 {
-    static const int two[9] = {0, 304, 304, 291, 296, 290, 276, 266, 288}, one[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};
+    static const int two[9] = {0, 304, 304, 249, 292, 245, 234, 224, 280}, one[9] = {0, 152, 152, 117, 140, 120, 114, 91, 112};
     const int n = (rt == 8 ? two : one)[cl] * sms / 152;
     return std::max(n, cl);
 }
@@ -634,36 +636,43 @@ static int slots_of(int rt, int cl, int sms)
 // chunk for each of a CTA's warps), is dealt out to one cluster, which does it all in one launch, or to as many clusters as
 // run at a time, joined by a second launch (2.7 us on the GPU, and its launch by the host).  Either way the time is that
 // of the rounds of CTAs, each a beginning and so many chunks a warp; the figures are measured ones for few CTAs (more
-// chunks cost more under load, for every choice alike).  One token, 20/5 heads x 128: one launch 6.8 us at 4,096
-// and 9.5 at 8,000, two 8.4 and 9.1; at 16,000 14.3 and 11.2.  192 rows at 1,024: clusters of five, which need three
-// rounds, 23.8 us, of two 11.1.  One head at 131,072, clusters of eight 13 us, without 25.
+// chunks cost more under load, for every choice alike).  A chunk of one slab begins sooner, two slabs
+// cost less each.  One token, 20/5 heads x 128, FP16: over 512 positions 4.8 us with clusters of four and one slab, 5.5
+// with two and two, 5.7 with neither; over 4,096 7.1 in one launch, 8.4 in two; over 16,000 14.3 and 11.2.  32/8 heads
+// over 131,072: two slabs 39.8, one 43.1.  192 rows at 1,024: clusters of five, which need three rounds, 23.8, of
+// two 11.1.  One head at 131,072: clusters of eight 13, without 25.
 static double plan_rows(Attn &a, int sms, int rows, size_t &bytes)
 {
     a.rt = rows <= 8 ? 8 : 16;
     a.tiles = (rows + a.rt - 1) / a.rt;
-    a.lo = key_lo(a.pos, 0, a.win) / CH * CH;
-    const int eights = (std::max(1, key_hi(a.pos, a.n - 1, a.len) - a.lo) + 8 * CH - 1) / (8 * CH);
+    a.lo = key_lo(a.pos, 0, a.win);
+    const int range = std::max(1, key_hi(a.pos, a.n - 1, a.len) - a.lo);
     const long long t = (long long)a.tiles * a.c.Hkv;
     const bool f32 = a.q.dtype == F32, wide = a.c.hd == 128, two = a.rt == 16;
-    const double begin = (two ? (wide ? 6.0 : 5.0) : (wide ? 4.0 : 3.4)) + (f32 ? 0.5 : 0.0), cluster = wide ? 1.8 : 1.4;
-    const double chunk = (two ? (wide ? 1.8 : 1.45) : (wide ? 1.45 : 1.15)) * (f32 ? 1.15 : 1.0);
+    const double slab = (two ? (wide ? 0.83 : 0.62) : (wide ? 0.67 : 0.53)) * (f32 ? 1.22 : 1.0);
+    const double first = (two ? (wide ? 5.7 : 4.45) : (wide ? 3.65 : 3.15)) + (f32 ? (two ? 0.6 : 0.2) : 0.0);
     double best = 1e30;
-    for (int c = std::min(8, eights); c >= 1; --c) {
-        for (int many = 0; many < (eights > 8 ? 2 : 1); ++many) {
-            int groups = many ? (int)(slots_of(a.rt, c, sms) / (t * c)) : 1, cl = c;
-            if (many && groups < 2) continue;
-            const int each = (eights + groups * cl - 1) / (groups * cl);
-            if (!many) cl = (eights + each - 1) / each;
-            groups = (eights + each * cl - 1) / (each * cl);
-            const int slots = slots_of(a.rt, cl, sms);
-            const long long rounds = (t * groups * cl + slots - 1) / slots;
-            const double time = (double)rounds * (begin + (cl > 1 ? cluster : 0.0) + chunk * (each - 1)) +
-                                (groups > 1 ? 4.5 + 0.035 * groups : 0.0);
-            if (time < best) {
-                best = time;
-                a.cl = cl;
-                a.splits = groups * cl;
-                a.per = each * 8 * CH;
+    for (int sl = 1; sl <= 2; ++sl) {
+        const int eights = (range - 1) / (128 * sl) + 1;
+        const double begin = first + (sl - 1) * 1.1 * slab, chunk = sl == 1 ? slab : 1.72 * slab;
+        for (int c = std::min(8, eights); c >= 1; --c) {
+            for (int many = 0; many < (eights > 8 ? 2 : 1); ++many) {
+                int groups = many ? (int)(slots_of(a.rt, c, sms) / (t * c)) : 1, cl = c;
+                if (many && groups < 2) continue;
+                const int each = (eights - 1) / (groups * cl) + 1;
+                if (!many) cl = (eights - 1) / each + 1;
+                groups = (eights - 1) / (each * cl) + 1;
+                const int slots = slots_of(a.rt, cl, sms);
+                const long long rounds = (t * groups * cl + slots - 1) / slots;
+                const double join = cl > 1 ? (two ? 1.0 + 0.12 * cl : 0.95 + 0.05 * cl) : 0.0;
+                const double time = (double)rounds * (begin + join + chunk * (each - 1)) + (groups > 1 ? 3.5 + 0.035 * groups : 0.0);
+                if (time < best) {
+                    best = time;
+                    a.sl = sl;
+                    a.cl = cl;
+                    a.splits = groups * cl;
+                    a.per = each * 128 * sl;
+                }
             }
         }
     }
@@ -695,8 +704,8 @@ size_t plan_attn(Attn &a, int sms)
     const double by_rows = plan_rows(a, sms, rows, bytes);
     if (rows <= 8) return bytes;
     // More rows than one n-tile: the faster kernel by the models above.  (20/5 heads x 128, FP16, rows kernel against
-    // tiles kernel: 64 rows at 1,024 8.6 and 16.5 us, at 4,096 11.7 and 15.9, at 8,192 28.0 and 17.8; 256 rows at 0
-    // 6.4 and 9.4, at 256 15.2 and 12.2; 1,024 rows at 0 17.3 and 11.5.)
+    // tiles kernel: 64 rows at 1,024 8.4 and 16.5 us, at 4,096 11.7 and 15.9, at 16,384 39 and 19.9; 256 rows at 0
+    // 5.6 and 9.4, at 1,024 12.3 and 16.9, at 4,096 44 and 20.5; 1,024 rows at 0 17.3 and 11.5.)
     Attn b = a;
     if (by_rows <= plan_tiles(b, sms, rows)) return bytes;
     a = b;
@@ -768,7 +777,7 @@ cudaError_t launch_read(const Cache &c, const Rows &k, const Rows &v, int n, int
     return by_dtype<RunRead>(k.dtype, c, k, v, n, pos, s);
 }
 
-template <int HD, int NT, bool SPLIT>
+template <int HD, int NT, bool SPLIT, int SL>
 static cudaError_t run_rows(const Attn &a, cudaStream_t s)
 {
     constexpr int smem = RowCfg<HD, NT, SPLIT>::SMEM;
@@ -777,26 +786,30 @@ static cudaError_t run_rows(const Attn &a, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !ready[dev]) {
-        e = cudaFuncSetAttribute(attn_rows<HD, NT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(attn_rows<HD, NT, SPLIT, SL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready[dev] = true;
     }
-    return launch(attn_rows<HD, NT, SPLIT>, dim3((unsigned)(a.tiles * a.splits), (unsigned)a.c.Hkv), 256, smem,
+    return launch(attn_rows<HD, NT, SPLIT, SL>, dim3((unsigned)(a.tiles * a.splits), (unsigned)a.c.Hkv), 256, smem,
                   a.cl, s, a);
+}
+
+template <int HD, int NT>
+static cudaError_t run_rows(const Attn &a, cudaStream_t s)
+{
+    if (a.q.dtype == F32) return a.sl == 1 ? run_rows<HD, NT, true, 1>(a, s) : run_rows<HD, NT, true, 2>(a, s);
+    return a.sl == 1 ? run_rows<HD, NT, false, 1>(a, s) : run_rows<HD, NT, false, 2>(a, s);
 }
 
 cudaError_t launch_attn(const Attn &a, cudaStream_t s)
 {
-    const bool split = a.q.dtype == F32;
     cudaError_t e;
     if (a.rt > 16)
         e = launch_attn_tiles(a, s);
     else if (a.c.hd == 128)
-        e = a.rt == 8 ? (split ? run_rows<128, 1, true>(a, s) : run_rows<128, 1, false>(a, s))
-                      : (split ? run_rows<128, 2, true>(a, s) : run_rows<128, 2, false>(a, s));
+        e = a.rt == 8 ? run_rows<128, 1>(a, s) : run_rows<128, 2>(a, s);
     else
-        e = a.rt == 8 ? (split ? run_rows<64, 1, true>(a, s) : run_rows<64, 1, false>(a, s))
-                      : (split ? run_rows<64, 2, true>(a, s) : run_rows<64, 2, false>(a, s));
+        e = a.rt == 8 ? run_rows<64, 1>(a, s) : run_rows<64, 2>(a, s);
     if (e == cudaSuccess && a.part) {
         // few rows: the splits of a row are spread over a whole block; many: one group each, the traffic counts
         const int lanes = a.c.hd / 4, rows = a.n * a.G;

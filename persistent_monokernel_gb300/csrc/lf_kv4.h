@@ -48,6 +48,7 @@ struct Attn {
     // which joins them into one of splits / cl partial states.
     // rt 128: `splits` CTAs share all chunks of all tiles (share_tiles of `per` CTAs), or (per 0) take a tile each.
     int rt, tiles, splits, cl, per, lo;
+    int sl;                 // rt 8 or 16: slabs of 16 positions that a warp takes at a time, 1 or 2
     // partial states [..][rt][hd + PAD]: O, then m and l (null: none).  rt 8 or 16: [Hkv * tiles * splits / cl];
     // rt 128: two per CTA, for the tile it goes on with and the tile it leaves unfinished, and where a tile's are:
     // pieces[Hkv * tiles] = (first CTA, number of pieces or 0).
