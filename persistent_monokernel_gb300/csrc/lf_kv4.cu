@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n,
 // instruction to bring its byte to the converter, and its share of the product;
 // everything else is kept off the loop (addresses advance by constants, no maximum,
 // no rescaling).  One token over 131,072 positions of 8 KV heads x 128: 39.8 us, 3.8 TB/s
-// of 6.7, 49 % of the issue slots (65 us with a maximum per chunk, 48 before clusters
+// of 6.7, 52 % of the issue slots (65 us with a maximum per chunk, 48 before clusters
 // joined); over 512 positions of 5 heads: 4.5 us.  FP16 values through shared memory
 // would write and read four times the cache's bytes there.  The next chunk's loads
 // one phase ahead gained 4 % at 131,072, but lost 3 % with FP32 queries and 8 % at 512
