@@ -203,7 +203,7 @@ __device__ __forceinline__ unsigned load_block<Tagged>(const Rows &in, long long
 {
     load16<float>(static_cast<const float *>(in.p) + t * in.ts + h * in.hs + b * 16, x);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = __half2float(__float2half_rn(x[j]));
+    for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(__float_as_uint(x[j]) & ~1u);   // an infinity with a tag is a NaN
     return top_of(x);
 }
 template <>

@@ -10,7 +10,7 @@ namespace lfq {
 constexpr int PAD = 4;      // words of a partial row behind O: m, l, and two that keep rows 16-byte aligned
 
 // Element types of the public calls, then those of the decoder's own buffers:
-//   TAG32    FP32 with a tag in the lowest mantissa bit; read: FP16 values (the tag is rounded away); written: the
+//   TAG32    FP32 with a tag in the lowest mantissa bit; read: FP16 values (whose own bit there is 0); written: the
 //            value with Rows::aux there
 //   SWZ16    read: FP16 rows whose 16-byte groups are XOR-ed with the position (Rows::aux: position of token 0) mod 8
 //   SPLIT16  written: an FP16 head to p and remainder to p2
