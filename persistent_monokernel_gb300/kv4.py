@@ -51,6 +51,9 @@ class KV4Cache:
     Tensors passed to the calls are CUDA tensors [n, heads, head_dim] on the cache's device with a contiguous last
     dimension, 16-byte aligned rows and any other strides (a slice of a fused projection, or a transposed
     [heads, n, head_dim] tensor); what the library refuses raises LFError.
+
+    A call with stream=s queues its work on s and returns.  Its tensors and the cache may be let go of at once; what it
+    returns belongs to s, as with any torch operation under torch.cuda.stream(s).
     """
 
     def __init__(self, n_kv_heads: int, head_dim: int, max_seq: int, device="cuda"):
@@ -92,14 +95,18 @@ class KV4Cache:
 
     def _elsewhere(self, call, stream, args):
         """The call again with the cache's device, and the stream if one is passed, current: what it allocates belongs
-        to that stream."""
+        to that stream.  What the call reads and writes is marked as in use there, so that memory that the caller lets
+        go of before the stream is done is not given to another."""
         if stream is None:
             with _torch.cuda.device(self.device):
                 return call(*args)
         if stream.device != self.device:
             raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
         with _torch.cuda.stream(stream):
-            return call(*args)
+            got = call(*args)
+        for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales, *_tensors(args)):
+            t.record_stream(stream)
+        return got
 
     def append(self, k, v, pos: int, stream=None) -> None:
         """Quantise k, v [n, n_kv_heads, head_dim] into positions pos .. pos + n - 1."""
@@ -133,6 +140,15 @@ class KV4Cache:
         attend call ran out since the last sync (lf_kv4_status)."""
         with _torch.cuda.device(self.device):
             return int(_lib.lf_kv4_status(_torch.cuda.current_stream().cuda_stream))
+
+
+def _tensors(args):
+    """The tensors among a call's arguments, those of a pair (read's out) too."""
+    for a in args:
+        if isinstance(a, _torch.Tensor):
+            yield a
+        elif isinstance(a, (tuple, list)):
+            yield from _tensors(a)
 
 
 def _fail(status: int, where: str) -> None:

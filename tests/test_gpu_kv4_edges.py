@@ -23,3 +23,58 @@ def test_v_rows_that_overflow_fp16_saturate_at_every_step(pm, block, n_prompt):
         _, lg = run(dec, cfg, prompt, force)
     want = forward(cfg, w, torch.cat((prompt, force[:-1])).long().cuda())[n_prompt - 1:]
     compare_logits(lg.cpu(), want.cpu())
+
+
+def _busy(stream, seconds=0.03):
+    """Work that keeps the stream for about that long."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(seconds * 1.9e9))
+
+
+def _reuse(shape, dtype):
+    """What the allocator gives the current stream next for this shape, overwritten."""
+    return [torch.full(shape, 7.0, dtype=dtype, device="cuda") for _ in range(8)]
+
+
+@pytest.mark.parametrize("n", [1, 300])
+def test_temporaries_passed_to_another_stream(pm, n):
+    """Inputs and outputs that the caller lets go of while the stream has yet to come to them."""
+    g = torch.Generator("cuda").manual_seed(n)
+    k, v, q = (torch.randn(n, h, 128, generator=g, device="cuda").half() for h in (2, 2, 8))
+    want = pm.KV4Cache(2, 128, 400)
+    want.append(k, v, 5)
+    out, rows = want.attend(q, 5), want.read(5, n)
+    cache, s = pm.KV4Cache(2, 128, 400), torch.cuda.Stream()
+    for _ in range(3):
+        a, b, c, o, r = k.clone(), v.clone(), q.clone(), torch.empty_like(q), (torch.empty_like(k), torch.empty_like(v))
+        s.wait_stream(torch.cuda.current_stream())
+        _busy(s)
+        cache.append(a, b, 5, stream=s)
+        got = cache.attend(c, 5, stream=s)
+        cache.attend(c, 5, out=o, stream=s)
+        cache.read(5, n, out=r, stream=s)
+        taken = {t.data_ptr() for t in (a, b, c, o, *r)}
+        del a, b, c, o, r
+        fresh = [t for x in (k, q) for t in _reuse(x.shape, x.dtype)]
+        assert not taken & {t.data_ptr() for t in fresh}
+        torch.cuda.synchronize()
+        assert torch.equal(got, out) and all((t == 7).all() for t in fresh)
+        assert torch.equal(cache.k_codes, want.k_codes) and torch.equal(cache.v_scales, want.v_scales)
+        assert all(torch.equal(x, y) for x, y in zip(cache.read(5, n), rows))
+
+
+def test_a_cache_let_go_of_while_another_stream_has_yet_to_read_it(pm):
+    g = torch.Generator("cuda").manual_seed(1)
+    k, q = (torch.randn(300, h, 128, generator=g, device="cuda").half() for h in (2, 8))
+    cache, s = pm.KV4Cache(2, 128, 400), torch.cuda.Stream()
+    cache.append(k, k, 0)
+    want = cache.attend(q, 0)
+    s.wait_stream(torch.cuda.current_stream())
+    _busy(s)
+    got = cache.attend(q, 0, stream=s)
+    places, shapes = {t.data_ptr() for t in (cache.k_codes, cache.v_scales)}, (cache.k_codes.shape, cache.v_scales.shape)
+    del cache
+    fresh = [t for shape in shapes for t in _reuse(shape, torch.uint8)]
+    assert not places & {t.data_ptr() for t in fresh}
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
