@@ -31,16 +31,32 @@ decltype(&lf_kv4_attend) g_attend;
 decltype(&lf_kv4_workspace) g_workspace;
 PyObject *g_fail;   // raises the library's error: fail(status, entry point)
 
-// A cache as the library has it, its device, and the scratch that the last query that needed some did.
+struct Refused : std::runtime_error {
+    using std::runtime_error::runtime_error;
+};
+
+// A cache as the library has it, its tensors (k_codes, k_scales, v_codes, v_scales) and device, and the scratch that
+// the last query that needed some did.
 struct Cache {
     lf_kv4 c;
+    at::Tensor parts[4];
     c10::DeviceIndex device;
     int n = -1, heads = -1;
     int64_t scratch = 0;
-};
 
-struct Refused : std::runtime_error {
-    using std::runtime_error::runtime_error;
+    // The tensors' addresses as they are now: resize_ or set_ may have moved them, or left something else.
+    void locate()
+    {
+        void **const at[4] = {&c.k_codes, &c.k_scales, &c.v_codes, &c.v_scales};
+        for (int i = 0; i < 4; ++i) {
+            const at::Tensor &t = parts[i];
+            const auto size = t.sizes();
+            if (size.size() != 3 || size[0] != c.n_kv_heads || size[1] != c.max_seq || size[2] != c.head_dim / (i % 2 ? 16 : 2) ||
+                !t.is_contiguous() || t.scalar_type() != at::kByte || t.get_device() != device)
+                throw Refused("a tensor of the cache is no longer what the cache was made with");
+            *at[i] = t.mutable_data_ptr();
+        }
+    }
 };
 
 struct NoGil {   // an allocation may wait for another thread
@@ -118,6 +134,7 @@ PyObject *call(PyObject *const *args, Py_ssize_t n_args, Py_ssize_t want, const 
     HANDLE_TH_ERRORS
     try {
         if (c10::cuda::current_device() != c->device) Py_RETURN_NOTIMPLEMENTED;
+        c->locate();
         lf_status st = LF_OK;
         PyObject *out = f(*c, st);
         if (st == LF_OK || !out) return out;
@@ -232,17 +249,24 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n_args)
 
 void drop(PyObject *o) { delete cache_of(o); }
 
-// cache(n_kv_heads, head_dim, max_seq, device, k_codes, k_scales, v_codes, v_scales): addresses as integers
+// cache(n_kv_heads, head_dim, max_seq, device, k_codes, k_scales, v_codes, v_scales)
 PyObject *cache(PyObject *, PyObject *args)
 {
     int h, hd, s, device;
-    unsigned long long p[4];
-    if (!PyArg_ParseTuple(args, "iiiiKKKK", &h, &hd, &s, &device, &p[0], &p[1], &p[2], &p[3])) return nullptr;
+    PyObject *p[4];
+    if (!PyArg_ParseTuple(args, "iiiiOOOO", &h, &hd, &s, &device, &p[0], &p[1], &p[2], &p[3])) return nullptr;
     Cache *c = new (std::nothrow) Cache;
     if (!c) return PyErr_NoMemory();
-    c->c = {h, hd, s, reinterpret_cast<void *>(p[0]), reinterpret_cast<void *>(p[1]), reinterpret_cast<void *>(p[2]),
-            reinterpret_cast<void *>(p[3])};
+    c->c = {h, hd, s, nullptr, nullptr, nullptr, nullptr};
     c->device = (c10::DeviceIndex)device;
+    for (int i = 0; i < 4; ++i) {
+        if (!THPVariable_Check(p[i])) {
+            delete c;
+            PyErr_SetString(PyExc_ValueError, "a cache is four tensors");
+            return nullptr;
+        }
+        c->parts[i] = THPVariable_Unpack(p[i]);
+    }
     PyObject *o = PyCapsule_New(c, "lf_kv4", drop);
     if (!o) delete c;
     return o;

@@ -1,7 +1,7 @@
 """A KV cache of one layer held in 4 bits (lf_kv4_append / _read / _attend of include/lf.h).
 
 Rows of K and V are stored as E2M1 codes with one E4M3 scale per 16 values, 4.5
-bits per value.  The class owns the four byte tensors; _lft.so marshals its
+bits per value.  The class holds the four byte tensors; _lft.so marshals its
 calls, and quantising, reading back and the attention run in the CUDA library,
 on the current stream of the cache's device or the one passed.
 """
@@ -65,7 +65,8 @@ class KV4Cache:
     @classmethod
     def wrap(cls, k_codes, k_scales, v_codes, v_scales) -> "KV4Cache":
         """A cache over four existing uint8 tensors: codes [n_kv_heads, max_seq, head_dim / 2] and scales
-        [n_kv_heads, max_seq, head_dim / 16], contiguous, on one CUDA device."""
+        [n_kv_heads, max_seq, head_dim / 16], contiguous, on one CUDA device.  They stay the cache's own: another
+        four are another cache."""
         self = cls.__new__(cls)
         self._set(k_codes, k_scales, v_codes, v_scales)
         return self
@@ -83,15 +84,17 @@ class KV4Cache:
                     and tuple(t.shape) == (h, s, width)):
                 raise ValueError("codes [n_kv_heads, max_seq, head_dim / 2] and scales [n_kv_heads, max_seq, "
                                  "head_dim / 16] must be contiguous CUDA torch.uint8 tensors on one device")
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self._parts = (k_codes, k_scales, v_codes, v_scales)
         self.n_kv_heads, self.max_seq, self.head_dim = h, s, 2 * half
         self.device = k_codes.device
-        self._handle = _calls.cache(h, 2 * half, s, k_codes.get_device(), k_codes.data_ptr(), k_scales.data_ptr(),
-                                    v_codes.data_ptr(), v_scales.data_ptr())
+        self._handle = _calls.cache(h, 2 * half, s, k_codes.get_device(), *self._parts)
+
+    # the tensors are read where they lie at each call; others cannot take their place
+    k_codes, k_scales, v_codes, v_scales = (property(lambda self, i=i: self._parts[i]) for i in range(4))
 
     @property
     def nbytes(self) -> int:
-        return sum(t.numel() for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales))
+        return sum(t.numel() for t in self._parts)
 
     def _elsewhere(self, call, stream, args):
         """The call again with the cache's device, and the stream if one is passed, current: what it allocates belongs
@@ -104,7 +107,7 @@ class KV4Cache:
             raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
         with _torch.cuda.stream(stream):
             got = call(*args)
-        for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales, *_tensors(args)):
+        for t in (*self._parts, *_tensors(args)):
             t.record_stream(stream)
         return got
 

@@ -78,3 +78,30 @@ def test_a_cache_let_go_of_while_another_stream_has_yet_to_read_it(pm):
     assert not places & {t.data_ptr() for t in fresh}
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_the_caches_tensors_are_read_where_they_are(pm):
+    """Another memory under a tensor of the cache is used, another size refused, another tensor in its place too."""
+    g = torch.Generator("cuda").manual_seed(2)
+    k, q = (torch.randn(30, h, 64, generator=g, device="cuda").half() for h in (2, 4))
+    cache, other = pm.KV4Cache(2, 64, 40), pm.KV4Cache(2, 64, 40)
+    cache.append(k, -k, 3)
+    want = cache.attend(q, 3)
+    names = ("k_codes", "k_scales", "v_codes", "v_scales")
+    for name in names:
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(other, name))
+        moved = getattr(cache, name).clone()
+        getattr(cache, name).fill_(0x11)                  # (what a stale address would read)
+        getattr(cache, name).set_(moved)
+    assert torch.equal(cache.attend(q, 3), want)
+    cache.append(-k, k, 3)
+    other.append(-k, k, 3)
+    assert all(torch.equal(getattr(cache, n)[:, 3:33], getattr(other, n)[:, 3:33]) for n in names)
+    for name, change in (("v_scales", lambda t: t.resize_(2, 80, 4)), ("k_codes", lambda t: t.set_(t[:, :20]))):
+        cache = pm.KV4Cache(2, 64, 40)
+        change(getattr(cache, name))
+        for call in (lambda: cache.append(k, k, 3), lambda: cache.read(3, 2), lambda: cache.attend(q, 3),
+                     lambda: cache.attend(q, 3, stream=torch.cuda.Stream())):
+            with pytest.raises(ValueError, match="no longer"):
+                call()
