@@ -215,8 +215,10 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n_args)
         } else if (!int32(args[3], q.length, "length")) {
             return nullptr;
         }
-        q.scale = (float)PyFloat_AsDouble(args[5]);
-        if (PyErr_Occurred()) return nullptr;
+        const double scale = PyFloat_AsDouble(args[5]);
+        if (scale == -1.0 && PyErr_Occurred()) return nullptr;
+        q.scale = (float)scale;
+        if (q.scale == 0.f && scale != 0.0) throw Refused("scale vanishes in 32 bits, and 0 selects 1 / sqrt(head_dim)");
         q.q = rows_of(args[1], c, q.n, q.n_heads, "q");
         PyObject *out = args[6];
         void *const stream = stream_of(c);

@@ -105,3 +105,18 @@ def test_the_caches_tensors_are_read_where_they_are(pm):
                      lambda: cache.attend(q, 3, stream=torch.cuda.Stream())):
             with pytest.raises(ValueError, match="no longer"):
                 call()
+
+
+def test_a_scale_that_32_bits_cannot_hold(pm):
+    """One that vanishes in FP32 would be taken for 0, which selects 1 / sqrt(head_dim)."""
+    cache = pm.KV4Cache(2, 64, 40)
+    q = torch.randn(3, 4, 64, device="cuda").half()
+    cache.append(q[:, :2], q[:, 2:], 0)
+    for scale in (1e-60, -1e-60, 2.0 ** -150, 1e39):
+        with pytest.raises((ValueError, pm.LFError)):
+            cache.attend(q, 0, scale=scale)
+    # the smallest that it can hold leaves every score at 0: the mean of what a row sees
+    v = cache.read(0, 3, torch.float32)[1]
+    mean = (v.cumsum(0) / torch.arange(1, 4, device="cuda")[:, None, None]).repeat_interleave(2, 1)
+    assert torch.allclose(cache.attend(q, 0, scale=2.0 ** -149).float(), mean, rtol=2.0 ** -10, atol=2.0 ** -20)
+    assert torch.equal(cache.attend(q, 0, scale=0.0), cache.attend(q, 0, scale=0.125))
