@@ -47,6 +47,7 @@ extern "C" {
 #define LF_ABI_VERSION 6
 #define LF_MAX_TOP_K 64          /* largest top_k that lf_decode accepts (besides 0) */
 #define LF_PREFILL_AUTO (-1)     /* lf_config.prefill_block: batched prefill, block size chosen by the library */
+#define LF_FAULT_PREFILL (-2)    /* lf_config.fault_step: the test hook of lf_create_kv4 */
 
 typedef enum {
     LF_OK = 0,
@@ -265,9 +266,11 @@ LF_API lf_status lf_create(const lf_config *cfg, const lf_weights *weights, lf_h
  * the position in hand included, and attends to the quantised cache.  Every
  * weight format, window, expert setting and prefill of lf_create works; a step
  * runs as persistent launches of the stages between two attentions, with the
- * attention between them as launches of its own.  cfg->fault_step is ignored;
- * lf_set_schedule takes LF_SCHED_FLAGS only and lf_enable_trace 0 only
- * (NOT_SUPPORTED).  Errors as for lf_create. */
+ * attention between them as launches of its own.  cfg->fault_step is ignored,
+ * but for LF_FAULT_PREFILL (test hook): in the batched prefill the attention of
+ * many rows waits for a hand-over that never comes.  lf_set_schedule takes
+ * LF_SCHED_FLAGS only and lf_enable_trace 0 only (NOT_SUPPORTED).  Errors as
+ * for lf_create. */
 LF_API lf_status lf_create_kv4(const lf_config *cfg, const lf_weights *weights, lf_handle **out);
 
 /* Release every library-owned allocation.  Synchronizes the device first.

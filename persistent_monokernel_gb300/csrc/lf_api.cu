@@ -213,6 +213,7 @@ lfp_args prefill_args(const lf_handle *h)
     a.q4_k = a.q4_v = nullptr;
     a.q4_win = h->h_win.empty() ? nullptr : h->h_win.data();
     a.q4_ws = h->q4_ws;
+    a.q4_fault = h->cfg.fault_step == LF_FAULT_PREFILL;
     if (h->kv4) {
         a.kc = a.vc = nullptr;
         a.q4_k = h->q4_stage;

@@ -54,6 +54,7 @@ struct Attn {
     // pieces[Hkv * tiles] = (first CTA, number of pieces or 0).
     float *part;
     int2 *pieces;
+    int fault;              // test hook: the tiles kernel's products wait for a P that is never complete
 };
 
 // Keys that query row t (position pos + t) sees: [key_lo, key_hi).

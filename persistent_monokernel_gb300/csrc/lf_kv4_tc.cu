@@ -42,7 +42,8 @@
 // with even shares).  511 queries from 0, FP32: 21 us.
 //
 // Every wait is bounded by %globaltimer; on expiry the CTA records a timeout
-// in the status word, settles its MMAs, frees TMEM and returns.
+// in the status word, settles its MMAs, frees TMEM and returns; its outputs are not
+// valid then.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
             lfk::mbar_init(&b->drained[i], 1);
             lfk::mbar_init(&b->pv_done[i], 1);
         }
-        lfk::mbar_init(&b->p_full, 4);
+        lfk::mbar_init(&b->p_full, a.fault ? 5 : 4);      // the test hook: a fifth arrival that never comes
         lfk::mbar_init(&b->q_ready, NSM / 32);
         b->abort = 0;
         lfk::mbar_fence_init();
@@ -493,12 +494,6 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
                 use1 += (unsigned)g.nc / 2;
             }
         }
-        // after a wait that ran out nothing may still write TMEM: one more commit by each of the lanes that issued
-        if (warp <= W_MMA + 1 && !dead && one && *reinterpret_cast<volatile int *>(&b->abort)) {
-            commit(&b->drained[warp - W_MMA]);
-            settle_phase(&b->drained[warp - W_MMA], 0u);
-        }
-        __syncwarp();
     } else if (warp >= W_DQ) {
         // ---- dequantisation: one warpgroup takes K, the other V; thread j position j of every chunk
         setmaxnreg_dec<REG_DQ>();
@@ -512,8 +507,10 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         Walk walk = start;
         Seg g;
         unsigned use0 = 0, use1 = 0;
+        // A lane whose wait ran out stays with its warp to the end, doing nothing: the others' barriers count on it
+        // (0.4 % faster at 1,024 queries over 32,768 positions than a vote on who goes on).
         bool ok = !dead;
-        while (ok && next(walk, g)) {
+        while (next(walk, g)) {
             const size_t row0 = (size_t)g.kvh * a.c.cap;
             const uint8_t *codes = (isv ? a.c.vc : a.c.kc) + row0 * code_bytes(HD);
             const uint8_t *scales = (isv ? a.c.vs : a.c.ks) + row0 * scale_bytes(HD);
@@ -521,17 +518,21 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
                 const size_t r = (size_t)max(min(g.p0 + i * BN + j, g.p1 - 1), g.lo);   // outside: a seen row, masked
                 raw.load(codes + r * code_bytes(HD), scales + r * scale_bytes(HD));
             };
-            auto step = [&](int i, auto stage) -> bool {
+            auto step = [&](int i, auto stage) {
                 constexpr uint32_t S = decltype(stage)::value;
-                if (!wait_phase(&empty[S], (((S ? use1 : use0) + (unsigned)(i >> 1)) & 1u) ^ 1u, b, 705)) return false;
-                raw.store(at, S * C::ROWB);
-                fence_async_smem();
+                ok = ok && wait_phase(&empty[S], (((S ? use1 : use0) + (unsigned)(i >> 1)) & 1u) ^ 1u, b, 705);
+                if (ok) {
+                    raw.store(at, S * C::ROWB);
+                    fence_async_smem();
+                }
                 warp_arrive(&full[S], lane);
                 if (i + 1 < g.nc) fetch(i + 1);
-                return true;
             };
             if (g.nc > 0) fetch(0);
-            for (int i = 0; ok && i < g.nc; i += 2) ok = step(i, Int<0>{}) && (i + 1 >= g.nc || step(i + 1, Int<1>{}));
+            for (int i = 0; i < g.nc; i += 2) {
+                step(i, Int<0>{});
+                if (i + 1 < g.nc) step(i + 1, Int<1>{});
+            }
             use0 += (unsigned)(g.nc + 1) / 2;
             use1 += (unsigned)g.nc / 2;
         }
@@ -836,9 +837,22 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         use0 += (unsigned)(nc + 1) / 2;
         use1 += (unsigned)nc / 2;
         }
+        tmem_st_wait();                                   // P that no product waited for
     }
     fence_before_sync();
     __syncthreads();
+    // After a wait that ran out, products may be under way that nothing waited for.  Every role has ended, so none
+    // follows: one more commit by each of the lanes that issued, and TMEM goes when they are done.
+    if (b->abort) {
+        if (warp == W_MMA || warp == W_MMA + 1) {
+            if (elect_one()) {
+                commit(&b->drained[warp - W_MMA]);
+                settle_phase(&b->drained[warp - W_MMA], 0u);
+            }
+            __syncwarp();
+        }
+        __syncthreads();
+    }
     if (warp == W_MMA) {
         __syncwarp();
         fence_after_sync();

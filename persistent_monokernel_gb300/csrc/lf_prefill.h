@@ -70,6 +70,7 @@ struct lfp_args {
     __half *q4_k, *q4_v;
     const int *q4_win;
     void *q4_ws;
+    int q4_fault;               // test hook (lfq::Attn::fault)
 };
 
 // TMA tensor maps of the GEMM operands (built once per handle: the workspace

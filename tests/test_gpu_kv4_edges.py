@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from parity import compare_logits
-from synthetic import make_prompt, make_weights
+from synthetic import ModelConfig, make_prompt, make_weights
 from test_gpu_kv4_decoder import GQA, forward, pm, run  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -120,3 +120,22 @@ def test_a_scale_that_32_bits_cannot_hold(pm):
     mean = (v.cumsum(0) / torch.arange(1, 4, device="cuda")[:, None, None]).repeat_interleave(2, 1)
     assert torch.allclose(cache.attend(q, 0, scale=2.0 ** -149).float(), mean, rtol=2.0 ** -10, atol=2.0 ** -20)
     assert torch.equal(cache.attend(q, 0, scale=0.0), cache.attend(q, 0, scale=0.125))
+
+
+WIDE8 = ModelConfig("wide8", 2, 512, 8, 1, 64, 512, 777)
+
+
+@pytest.mark.parametrize("cfg,n", [(GQA, 600), (WIDE8, 333), (GQA, 1500)])
+def test_a_wait_of_the_batched_prefills_attention_that_runs_out(pm, cfg, n):
+    """A hand-over that never comes (test hook): the kernels end by themselves, the handle says so, and the same
+    kernels are right in the next handle."""
+    w, prompt, force = make_weights(cfg, 5, device="cuda"), make_prompt(cfg.vocab, n, 6), make_prompt(cfg.vocab, 4, 7)
+    with pm.Decoder(cfg, w, n + 4, prefill_block=n, kv4=True, fault_step=pm.FAULT_PREFILL) as dec:
+        dec.prefill(prompt.cuda())
+        assert dec.sync() == 6
+        with pytest.raises(pm.LFError, match="STATE"):
+            dec.decode(1)
+    with pm.Decoder(cfg, w, n + 4, prefill_block=n, kv4=True) as dec:
+        _, lg = run(dec, cfg, prompt, force)
+    want = forward(cfg, w, torch.cat((prompt, force[:-1])).long().cuda())[n - 1:]
+    compare_logits(lg.cpu(), want.cpu())
