@@ -481,8 +481,8 @@ LF_API lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *wor
                                void *stream);
 
 /* Synchronise `stream` and return LF_OK, or LF_ERR_TIMEOUT if a device-side
- * wait of an lf_kv4_attend call on the current device ran out since the last
- * lf_kv4_status (its outputs are then not valid). */
+ * wait of an lf_kv4_attend call on the current device ran out (each is bounded
+ * by 2 s) since the last lf_kv4_status (its outputs are then not valid). */
 LF_API lf_status lf_kv4_status(void *stream);
 
 /* Static string naming a status code. */

@@ -213,6 +213,7 @@ lfp_args prefill_args(const lf_handle *h)
     a.q4_k = a.q4_v = nullptr;
     a.q4_win = h->h_win.empty() ? nullptr : h->h_win.data();
     a.q4_ws = h->q4_ws;
+    a.q4_wait_ns = h->cfg.wait_timeout_ns > 0 ? h->cfg.wait_timeout_ns : kDefaultTimeoutNs;
     a.q4_fault = h->cfg.fault_step == LF_FAULT_PREFILL;
     if (h->kv4) {
         a.kc = a.vc = nullptr;
@@ -469,6 +470,7 @@ lf_status kv4_attention(lf_handle *h, int l, int pos, unsigned epoch, cudaStream
     a.len = pos + 1;
     a.win = h->h_win.empty() ? 0 : h->h_win[l];
     a.scale = 1.0f / std::sqrt((float)g.hd);
+    a.wait_ns = h->cfg.wait_timeout_ns > 0 ? h->cfg.wait_timeout_ns : kDefaultTimeoutNs;
     const size_t need = lfq::plan_attn(a, h->sm_count);
     lfq::set_workspace(a, need ? h->q4_ws : nullptr);
     if (e == cudaSuccess) e = lfq::launch_attn(a, s);

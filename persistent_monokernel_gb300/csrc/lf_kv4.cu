@@ -929,6 +929,7 @@ lf_status make_attn(const lf_kv4 *c, const lf_kv4_query *q, Attn *a, size_t *byt
     if (q->q.dtype != LF_F16 && q->q.dtype != LF_BF16 && q->q.dtype != LF_F32) return LF_ERR_NOT_SUPPORTED;
     a->q = rows_of(&q->q);
     a->scale = q->scale != 0.f ? q->scale : 1.0f / std::sqrt((float)c->head_dim);
+    a->wait_ns = WAIT_NS;
     set_workspace(*a, nullptr);
     *bytes = 0;
     if (q->n == 0) return LF_OK;

@@ -7,6 +7,7 @@
 
 namespace lfq {
 
+constexpr long long WAIT_NS = 2000000000LL;   // bound of a wait where the caller has named none
 constexpr int PAD = 4;      // words of a partial row behind O: m, l, and two that keep rows 16-byte aligned
 
 // Element types of the public calls, then those of the decoder's own buffers:
@@ -54,6 +55,7 @@ struct Attn {
     // pieces[Hkv * tiles] = (first CTA, number of pieces or 0).
     float *part;
     int2 *pieces;
+    long long wait_ns;      // bound of every wait of the tiles kernel
     int fault;              // test hook: the tiles kernel's products wait for a P that is never complete
 };
 

@@ -63,7 +63,6 @@ __device__ unsigned g_status[8];   // error record of the kernels below (status[
 constexpr int BM = 128, BN = 128;
 constexpr float TC_EXP = 7.f;                    // a new reference puts the row's largest P at 2^7 (a sum of at most 2^14)
 constexpr float TC_SUM = 32768.f;                // a chunk's sum that shows every P in range
-constexpr long long kWaitNs = 2000000000LL;      // bound of every wait
 
 constexpr int NSM = 256;                         // softmax threads: two per query row
 constexpr int W_DQ = 8, W_MMA = 16, NTHR = 640;  // warps: 0-7 softmax, 8-15 dequantisation (K, V), 16 S, 17 P V (18, 19 idle)
@@ -88,6 +87,7 @@ struct Bars {
     uint64_t s_full[2], s_free[2], pv_done[2], p_full, q_ready, drained[2];
     uint32_t tmem;
     int abort;
+    long long wait_ns;  // bound of every wait
     float x[2][BM];     // exchanged between the two threads of a row
     float ref[BM];      // the row's reference, handed on from chunk to chunk
     long long qrow[BM], orow[BM];   // the rows' element offsets in q and in the output
@@ -107,7 +107,7 @@ __device__ bool wait_phase(uint64_t *bar, unsigned parity, Bars *b, unsigned whe
             if (*reinterpret_cast<volatile int *>(&b->abort)) return false;
             const unsigned long long now = lfk::globaltimer_ns();
             if (t0 == 0) t0 = now;
-            if ((long long)(now - t0) > kWaitNs) {
+            if ((long long)(now - t0) > b->wait_ns) {
                 *reinterpret_cast<volatile int *>(&b->abort) = 1;
                 if (atomicCAS(g_status, 0u, (unsigned)lfk::STATUS_TIMEOUT) == 0u) {
                     g_status[1] = where;
@@ -129,7 +129,7 @@ __device__ void settle_phase(uint64_t *bar, unsigned parity)
 {
     const unsigned long long t0 = lfk::globaltimer_ns();
     while (!lfk::mbar_try_wait(bar, parity))
-        if ((long long)(lfk::globaltimer_ns() - t0) > kWaitNs) return;
+        if ((long long)(lfk::globaltimer_ns() - t0) > WAIT_NS) return;
 }
 // One arrival for a warp whose lanes have each fenced their own writes (256 single arrivals queue up on the
 // barrier's word for longer than a product takes).
@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         lfk::mbar_init(&b->p_full, a.fault ? 5 : 4);      // the test hook: a fifth arrival that never comes
         lfk::mbar_init(&b->q_ready, NSM / 32);
         b->abort = 0;
+        b->wait_ns = a.wait_ns;
         lfk::mbar_fence_init();
     }
     if (warp == W_MMA) {

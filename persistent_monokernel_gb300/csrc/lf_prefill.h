@@ -70,6 +70,7 @@ struct lfp_args {
     __half *q4_k, *q4_v;
     const int *q4_win;
     void *q4_ws;
+    long long q4_wait_ns;       // lfq::Attn::wait_ns
     int q4_fault;               // test hook (lfq::Attn::fault)
 };
 

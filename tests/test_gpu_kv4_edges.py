@@ -1,4 +1,6 @@
 """The 4-bit KV cache on the GPU where values, memory and waits come to their ends."""
+import time
+
 import pytest
 import torch
 
@@ -139,3 +141,14 @@ def test_a_wait_of_the_batched_prefills_attention_that_runs_out(pm, cfg, n):
         _, lg = run(dec, cfg, prompt, force)
     want = forward(cfg, w, torch.cat((prompt, force[:-1])).long().cuda())[n - 1:]
     compare_logits(lg.cpu(), want.cpu())
+
+
+def test_the_wait_limit_of_a_handle_bounds_its_prefills_attention(pm):
+    """wait_timeout_ns = 20 ms over three layers; the default would take 2 s for each."""
+    cfg, n = GQA, 600
+    w, prompt = make_weights(cfg, 5, device="cuda"), make_prompt(cfg.vocab, n, 6).cuda()
+    with pm.Decoder(cfg, w, n + 4, prefill_block=n, kv4=True, fault_step=pm.FAULT_PREFILL, wait_timeout_ns=20_000_000) as dec:
+        start = time.monotonic()
+        dec.prefill(prompt)
+        assert dec.sync() == 6
+        assert 0.02 < time.monotonic() - start < 2.0
