@@ -470,6 +470,7 @@ lf_status kv4_attention(lf_handle *h, int l, int pos, unsigned epoch, cudaStream
     a.len = pos + 1;
     a.win = h->h_win.empty() ? 0 : h->h_win[l];
     a.scale = 1.0f / std::sqrt((float)g.hd);
+    a.status = h->status;
     a.wait_ns = h->cfg.wait_timeout_ns > 0 ? h->cfg.wait_timeout_ns : kDefaultTimeoutNs;
     const size_t need = lfq::plan_attn(a, h->sm_count);
     lfq::set_workspace(a, need ? h->q4_ws : nullptr);
@@ -917,12 +918,6 @@ lf_status lf_sync(lf_handle *h)
     if (e != cudaSuccess) return from_cuda(e);
     if (st[0] == (unsigned)lfk::STATUS_TIMEOUT) h->latched = LF_ERR_TIMEOUT;
     else if (st[0] != 0u) h->latched = LF_ERR_INVALID_ARG;
-    if (h->kv4 && h->latched == LF_OK) {
-        unsigned rec[4] = {0, 0, 0, 0};
-        e = lfq::tiles_status(rec, h->last_stream);
-        if (e != cudaSuccess) return from_cuda(e);
-        if (rec[0]) h->latched = LF_ERR_TIMEOUT;
-    }
     return h->latched;
 }
 

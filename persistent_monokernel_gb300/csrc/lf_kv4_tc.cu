@@ -58,7 +58,7 @@ namespace lfq {
 
 using namespace lftc;
 
-__device__ unsigned g_status[8];   // error record of the kernels below (status[4]: unused abort word)
+__device__ unsigned g_status[4];   // error record of launches that name none
 
 constexpr int BM = 128, BN = 128;
 constexpr float TC_EXP = 7.f;                    // a new reference puts the row's largest P at 2^7 (a sum of at most 2^14)
@@ -88,6 +88,7 @@ struct Bars {
     uint32_t tmem;
     int abort;
     long long wait_ns;  // bound of every wait
+    unsigned *status;   // error record (null: g_status)
     float x[2][BM];     // exchanged between the two threads of a row
     float ref[BM];      // the row's reference, handed on from chunk to chunk
     long long qrow[BM], orow[BM];   // the rows' element offsets in q and in the output
@@ -97,6 +98,18 @@ struct Bars {
 template <int HD, bool SPLIT>
 constexpr uint32_t tc_smem() { return TcCfg<HD, SPLIT>::OFF_BAR + (uint32_t)sizeof(Bars) + 1024u; }
 
+// Sets error record `status`, or the device's; a record of a handle has an abort word, for its later launches.
+// (Out of line: in every wait it costs the loops 1.8 % at 1,024 queries over 32,768 positions.)
+__device__ __noinline__ void record(unsigned *status, unsigned where)
+{
+    unsigned *r = status ? status : g_status;
+    if (atomicCAS(r, 0u, (unsigned)lfk::STATUS_TIMEOUT) == 0u) {
+        r[1] = where;
+        r[2] = blockIdx.x;
+        r[3] = blockIdx.y;
+    }
+    if (status) atomicExch(status + 4, 1u);
+}
 // (The timer is read from the 64th poll on: reading it before costs a wait several times its own length.)
 __device__ bool wait_phase(uint64_t *bar, unsigned parity, Bars *b, unsigned where)
 {
@@ -109,11 +122,7 @@ __device__ bool wait_phase(uint64_t *bar, unsigned parity, Bars *b, unsigned whe
             if (t0 == 0) t0 = now;
             if ((long long)(now - t0) > b->wait_ns) {
                 *reinterpret_cast<volatile int *>(&b->abort) = 1;
-                if (atomicCAS(g_status, 0u, (unsigned)lfk::STATUS_TIMEOUT) == 0u) {
-                    g_status[1] = where;
-                    g_status[2] = blockIdx.x;
-                    g_status[3] = blockIdx.y;
-                }
+                record(b->status, where);
                 return false;
             }
         }
@@ -399,6 +408,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
         lfk::mbar_init(&b->q_ready, NSM / 32);
         b->abort = 0;
         b->wait_ns = a.wait_ns;
+        b->status = a.status;
         lfk::mbar_fence_init();
     }
     if (warp == W_MMA) {
@@ -415,7 +425,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_tiles(const __grid_constant__ At
     wait_for_prerequisites();
     if (threadIdx.x == 0 && b->tmem != 0u) {
         b->abort = 1;
-        if (atomicCAS(g_status, 0u, (unsigned)lfk::STATUS_TIMEOUT) == 0u) g_status[1] = 711;
+        record(a.status, 711);
     }
     __syncthreads();
     const bool dead = b->abort != 0;
@@ -908,7 +918,7 @@ cudaError_t tiles_status(unsigned out[4], cudaStream_t s)
     cudaError_t e = cudaGetSymbolAddress(&p, g_status);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e == cudaSuccess) e = cudaMemcpy(out, p, 4 * sizeof(unsigned), cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && out[0]) e = cudaMemset(p, 0, 8 * sizeof(unsigned));
+    if (e == cudaSuccess && out[0]) e = cudaMemset(p, 0, 4 * sizeof(unsigned));
     return e;
 }
 

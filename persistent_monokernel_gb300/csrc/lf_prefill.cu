@@ -657,6 +657,7 @@ static cudaError_t attn_q4(const lfp_args *a, int l, int T, int pos0, cudaStream
     q.len = pos0 + T;
     q.win = a->q4_win ? a->q4_win[l] : 0;
     q.scale = 1.0f / sqrtf((float)g.hd);
+    q.status = a->status;
     q.wait_ns = a->q4_wait_ns;
     q.fault = a->q4_fault;
     const size_t need = lfq::plan_attn(q, a->sms);

@@ -152,3 +152,27 @@ def test_the_wait_limit_of_a_handle_bounds_its_prefills_attention(pm):
         dec.prefill(prompt)
         assert dec.sync() == 6
         assert 0.02 < time.monotonic() - start < 2.0
+
+
+def test_a_handles_error_is_its_own(pm):
+    """A wait that ran out in one handle neither latches in another, nor is lost to whoever asks first, nor outlives
+    lf_reset."""
+    cfg, n = GQA, 600
+    w, prompt, force = make_weights(cfg, 5, device="cuda"), make_prompt(cfg.vocab, n, 6), make_prompt(cfg.vocab, 4, 7)
+    cache = pm.KV4Cache(2, 64, 32)
+    with pm.Decoder(cfg, w, n + 4, prefill_block=n, kv4=True, fault_step=pm.FAULT_PREFILL, wait_timeout_ns=20_000_000) as a, \
+            pm.Decoder(cfg, w, n + 4, prefill_block=n, kv4=True) as b:
+        a.prefill(prompt.cuda())
+        torch.cuda.synchronize()
+        assert cache.sync() == 0
+        _, lg = run(b, cfg, prompt, force)                # b.sync() is 0
+        assert a.sync() == 6
+        b.reset()
+        _, again = run(b, cfg, prompt, force)
+        assert a.sync() == 6 and torch.equal(lg, again)
+        a.reset()
+        assert a.sync() == 0
+        # one that nobody asked for before the reset
+        a.prefill(prompt.cuda())
+        a.reset()
+        assert a.sync() == 0 and cache.sync() == 0
