@@ -985,10 +985,10 @@ lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *workspace,
 
 lf_status lf_kv4_status(void *stream)
 {
-    unsigned rec[4];
-    const cudaError_t e = tiles_status(rec, static_cast<cudaStream_t>(stream));
+    bool expired = false;
+    const cudaError_t e = tiles_status(expired, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return status_of(e);
-    return rec[0] ? LF_ERR_TIMEOUT : LF_OK;
+    return expired ? LF_ERR_TIMEOUT : LF_OK;
 }
 
 }  // extern "C"

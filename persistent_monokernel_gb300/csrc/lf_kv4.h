@@ -55,7 +55,7 @@ struct Attn {
     // pieces[Hkv * tiles] = (first CTA, number of pieces or 0).
     float *part;
     int2 *pieces;
-    unsigned *status;       // [8]: error record [0..3] and abort word [4] of a handle; null: the device's record
+    unsigned *status;       // [8]: error record [0..3] and abort word [4] of a handle; null: counted for the device
     long long wait_ns;      // bound of every wait of the tiles kernel
     int fault;              // test hook: the tiles kernel's products wait for a P that is never complete
 };
@@ -103,7 +103,7 @@ cudaError_t launch_read(const Cache &c, const Rows &k, const Rows &v, int n, int
 cudaError_t launch_attn(const Attn &a, cudaStream_t s);
 // Tiles of 128 query rows on tcgen05 (lf_kv4_tc.cu); launch_attn calls it by the plan's rt.
 cudaError_t launch_attn_tiles(const Attn &a, cudaStream_t s);
-// The device's error record (out[0] = 0: none), read after synchronising s, and cleared.
-cudaError_t tiles_status(unsigned out[4], cudaStream_t s);
+// Synchronises s; expired: whether a wait that is counted for the device ran out since this last said so.
+cudaError_t tiles_status(bool &expired, cudaStream_t s);
 
 }  // namespace lfq

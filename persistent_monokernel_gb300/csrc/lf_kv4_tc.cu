@@ -58,7 +58,9 @@ namespace lfq {
 
 using namespace lftc;
 
-__device__ unsigned g_status[4];   // error record of launches that name none
+// Waits that ran out in launches that name no record, and how many of them tiles_status has told of.  The first is
+// only ever added to: none is lost to a status that is asked for meanwhile.
+__device__ unsigned g_expired[2];
 
 constexpr int BM = 128, BN = 128;
 constexpr float TC_EXP = 7.f;                    // a new reference puts the row's largest P at 2^7 (a sum of at most 2^14)
@@ -88,7 +90,7 @@ struct Bars {
     uint32_t tmem;
     int abort;
     long long wait_ns;  // bound of every wait
-    unsigned *status;   // error record (null: g_status)
+    unsigned *status;   // error record (null: g_expired)
     float x[2][BM];     // exchanged between the two threads of a row
     float ref[BM];      // the row's reference, handed on from chunk to chunk
     long long qrow[BM], orow[BM];   // the rows' element offsets in q and in the output
@@ -98,17 +100,20 @@ struct Bars {
 template <int HD, bool SPLIT>
 constexpr uint32_t tc_smem() { return TcCfg<HD, SPLIT>::OFF_BAR + (uint32_t)sizeof(Bars) + 1024u; }
 
-// Sets error record `status`, or the device's; a record of a handle has an abort word, for its later launches.
+// Sets error record `status` and its abort word, which a handle's later launches look at, or counts.
 // (Out of line: in every wait it costs the loops 1.8 % at 1,024 queries over 32,768 positions.)
 __device__ __noinline__ void record(unsigned *status, unsigned where)
 {
-    unsigned *r = status ? status : g_status;
-    if (atomicCAS(r, 0u, (unsigned)lfk::STATUS_TIMEOUT) == 0u) {
-        r[1] = where;
-        r[2] = blockIdx.x;
-        r[3] = blockIdx.y;
+    if (!status) {
+        atomicAdd(g_expired, 1u);
+        return;
     }
-    if (status) atomicExch(status + 4, 1u);
+    if (atomicCAS(status, 0u, (unsigned)lfk::STATUS_TIMEOUT) == 0u) {
+        status[1] = where;
+        status[2] = blockIdx.x;
+        status[3] = blockIdx.y;
+    }
+    atomicExch(status + 4, 1u);
 }
 // (The timer is read from the 64th poll on: reading it before costs a wait several times its own length.)
 __device__ bool wait_phase(uint64_t *bar, unsigned parity, Bars *b, unsigned where)
@@ -912,13 +917,18 @@ cudaError_t launch_attn_tiles(const Attn &a, cudaStream_t s)
     return split ? run_tiles<64, true>(a, sh, s) : run_tiles<64, false>(a, sh, s);
 }
 
-cudaError_t tiles_status(unsigned out[4], cudaStream_t s)
+cudaError_t tiles_status(bool &expired, cudaStream_t s)
 {
     void *p = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&p, g_status);
+    unsigned w[2] = {0, 0};
+    cudaError_t e = cudaGetSymbolAddress(&p, g_expired);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(w, p, sizeof(w), cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess) e = cudaMemcpy(out, p, 4 * sizeof(unsigned), cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && out[0]) e = cudaMemset(p, 0, 4 * sizeof(unsigned));
+    expired = w[0] != w[1];
+    if (e == cudaSuccess && expired) {
+        e = cudaMemcpyAsync(static_cast<unsigned *>(p) + 1, w, sizeof(w[0]), cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
     return e;
 }
 

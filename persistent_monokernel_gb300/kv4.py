@@ -8,6 +8,7 @@ on the current stream of the cache's device or the one passed.
 from __future__ import annotations
 
 import ctypes as C
+import threading
 
 
 class lf_kv4(C.Structure):
@@ -27,7 +28,9 @@ class lf_kv4_query(C.Structure):
 F16, BF16, F32 = 0, 1, 2
 BLOCK = 16          # values that share a scale
 _INT = 2 ** 31
+_TIMEOUT = 6        # LF_ERR_TIMEOUT
 _torch = _lib = _calls = _codes = None
+_told, _told_lock = {}, threading.Lock()   # device: how often lf_kv4_status has told of a wait that ran out
 
 
 def _load():
@@ -87,6 +90,7 @@ class KV4Cache:
         self._parts = (k_codes, k_scales, v_codes, v_scales)
         self.n_kv_heads, self.max_seq, self.head_dim = h, s, 2 * half
         self.device = k_codes.device
+        self._heard = _told.get(self.device, 0)
         self._handle = _calls.cache(h, 2 * half, s, k_codes.get_device(), *self._parts)
 
     # the tensors are read where they lie at each call; others cannot take their place
@@ -140,9 +144,18 @@ class KV4Cache:
 
     def sync(self) -> int:
         """Synchronise the current stream of the cache's device: 0, or LF_ERR_TIMEOUT (6) if a device-side wait of an
-        attend call ran out since the last sync (lf_kv4_status)."""
+        attend call on that device, of this cache or another, ran out since this cache's last sync (lf_kv4_status,
+        which tells once: every cache of the process is told)."""
         with _torch.cuda.device(self.device):
-            return int(_lib.lf_kv4_status(_torch.cuda.current_stream().cuda_stream))
+            status = int(_lib.lf_kv4_status(_torch.cuda.current_stream().cuda_stream))
+        with _told_lock:
+            told = _told.get(self.device, 0)
+            if status == _TIMEOUT:
+                told = _told[self.device] = told + 1
+            elif status == 0 and told != self._heard:
+                status = _TIMEOUT
+            self._heard = told
+        return status
 
 
 def _tensors(args):

@@ -1,4 +1,6 @@
 """The 4-bit KV cache on the GPU where values, memory and waits come to their ends."""
+import os
+import subprocess
 import time
 
 import pytest
@@ -176,3 +178,15 @@ def test_a_handles_error_is_its_own(pm):
         a.prefill(prompt.cuda())
         a.reset()
         assert a.sync() == 0 and cache.sync() == 0
+
+
+def test_waits_that_run_out_outside_a_handle(pm, tmp_path):
+    """kv4_expiry.cu, in a process of its own: every type and head size, tiles of their own and shared ones."""
+    from persistent_monokernel_gb300 import build
+    here, exe = os.path.dirname(os.path.abspath(__file__)), str(tmp_path / "kv4_expiry")
+    objs = [os.path.join(build.BUILD, f) for f in ("lf_kv4.o", "lf_kv4_tc.o")]
+    if not all(os.path.exists(o) for o in objs):
+        build.build(force=True)
+    subprocess.run([build.nvcc(), *build.ARCH, "-O1", "-std=c++17", os.path.join(here, "kv4_expiry.cu"), *objs, "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
