@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -99,6 +100,8 @@ lf_rows rows_of(PyObject *o, const Cache &c, int64_t n, int64_t heads, const cha
           << "] float16, bfloat16 or float32 with a contiguous last dimension on cuda:" << (int)c.device << " is needed";
         throw Refused(s.str());
     }
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        throw Refused(std::string(what) + " requires a gradient, and these calls form none: detach it, or call under torch.no_grad()");
     // the stride of a dimension of one is never used (and may be anything)
     return {const_cast<void *>(t.const_data_ptr()), code, n > 1 ? t.stride(0) : 0, heads > 1 ? t.stride(1) : 0};
 }

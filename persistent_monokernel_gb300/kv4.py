@@ -53,7 +53,8 @@ class KV4Cache:
 
     Tensors passed to the calls are CUDA tensors [n, heads, head_dim] on the cache's device with a contiguous last
     dimension, 16-byte aligned rows and any other strides (a slice of a fused projection, or a transposed
-    [heads, n, head_dim] tensor); what the library refuses raises LFError.
+    [heads, n, head_dim] tensor); what the library refuses raises LFError.  The calls form no gradients: where autograd
+    is on, a tensor that requires one raises ValueError.
 
     A call with stream=s queues its work on s and returns.  Its tensors and the cache may be let go of at once; what it
     returns belongs to s, as with any torch operation under torch.cuda.stream(s).

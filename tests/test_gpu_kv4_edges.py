@@ -190,3 +190,23 @@ def test_waits_that_run_out_outside_a_handle(pm, tmp_path):
     subprocess.run([build.nvcc(), *build.ARCH, "-O1", "-std=c++17", os.path.join(here, "kv4_expiry.cu"), *objs, "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_no_gradient_is_dropped_in_silence(pm):
+    cache = pm.KV4Cache(2, 64, 40)
+    q, k, out = (torch.randn(5, h, 64, device="cuda").half() for h in (4, 2, 4))
+    cache.append(k, k, 0)
+    want = cache.attend(q, 0)
+    rows = cache.read(0, 5)
+    leaf, kl = q.clone().requires_grad_(), k.clone().requires_grad_()
+    for call in (lambda: cache.attend(leaf, 0), lambda: cache.attend(leaf * 2, 0), lambda: cache.attend(q, 0, out=leaf),
+                 lambda: cache.append(kl, k, 0), lambda: cache.append(k, kl, 0), lambda: cache.read(0, 5, out=(kl, k)),
+                 lambda: cache.attend(leaf, 0, stream=torch.cuda.Stream())):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    assert torch.equal(cache.attend(leaf.detach(), 0), want)
+    for off in (torch.no_grad(), torch.inference_mode()):
+        with off:
+            cache.append(kl, kl, 0)
+            assert torch.equal(cache.attend(leaf, 0, out=out), want)
+            assert all(torch.equal(a, b) for a, b in zip(cache.read(0, 5), rows))
