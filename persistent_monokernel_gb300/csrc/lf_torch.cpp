@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <climits>
 #include <optional>
@@ -302,4 +303,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lft", nullptr, -1, methods, nullp
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__lft() { return PyModule_Create(&module); }
+// made_for: the release of torch and the version of Python (sys.hexversion >> 16) that this module fits
+PyMODINIT_FUNC PyInit__lft()
+{
+    PyObject *m = PyModule_Create(&module);
+    PyObject *made = m ? Py_BuildValue("(si)", TORCH_VERSION, (int)(PY_VERSION_HEX >> 16)) : nullptr;
+    if (!made || PyModule_AddObjectRef(m, "made_for", made) < 0) Py_CLEAR(m);
+    Py_XDECREF(made);
+    return m;
+}

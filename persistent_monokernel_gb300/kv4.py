@@ -8,6 +8,8 @@ on the current stream of the cache's device or the one passed.
 from __future__ import annotations
 
 import ctypes as C
+import re
+import sys
 import threading
 
 
@@ -28,6 +30,7 @@ class lf_kv4_query(C.Structure):
 F16, BF16, F32 = 0, 1, 2
 BLOCK = 16          # values that share a scale
 _INT = 2 ** 31
+_BUILD = "build it with `python -m persistent_monokernel_gb300.build`"
 _TIMEOUT = 6        # LF_ERR_TIMEOUT
 _torch = _lib = _calls = _codes = None
 _told, _told_lock = {}, threading.Lock()   # device: how often lf_kv4_status has told of a wait that ran out
@@ -40,7 +43,14 @@ def _load():
 
     from . import lib
     _lib = lib()
-    from . import _lft
+    try:
+        from . import _lft
+    except ImportError as e:
+        raise ImportError(f"_lft.so cannot be loaded ({e}): {_BUILD}") from e
+    have = (".".join(re.findall(r"\d+", torch.__version__)[:3]), sys.hexversion >> 16)
+    if _lft.made_for != have:
+        raise ImportError(f"_lft.so was built for torch {_lft.made_for[0]} and Python {_lft.made_for[1]:#x}, not for "
+                          f"{have[0]} and {have[1]:#x}: {_BUILD}")
     _lft.bind(*(C.cast(getattr(_lib, "lf_kv4_" + f), C.c_void_p).value for f in ("append", "read", "attend", "workspace")),
               _fail)
     _calls = _lft
