@@ -6,8 +6,10 @@ import time
 import pytest
 import torch
 
+import kv4_ref as ref
 from parity import compare_logits
 from synthetic import ModelConfig, make_prompt, make_weights
+from test_gpu_kv4 import check
 from test_gpu_kv4_decoder import GQA, forward, pm, run  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -210,3 +212,23 @@ def test_no_gradient_is_dropped_in_silence(pm):
             cache.append(kl, kl, 0)
             assert torch.equal(cache.attend(leaf, 0, out=out), want)
             assert all(torch.equal(a, b) for a, b in zip(cache.read(0, 5), rows))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_row_offsets_of_one_head_past_31_bits(pm, dtype):
+    """One head of 33.6 million positions: its last rows' codes lie past 2^31 bytes from the head's first."""
+    hd, cap, n, heads = 128, (1 << 25) + 4096, 300, 8
+    cache = pm.KV4Cache(1, hd, cap)
+    assert (cap - n) * (hd // 2) > 1 << 31
+    g = torch.Generator("cuda").manual_seed(5)
+    k, v = (torch.randn(n, 1, hd, generator=g, device="cuda").to(dtype) for _ in range(2))
+    cache.append(k, v, cap - n)
+    want = [ref.values(*ref.quantise(t)) for t in (k, v)]
+    assert all(torch.equal(a.double(), b) for a, b in zip(cache.read(cap - n, n, dtype), want))
+    kk, vv = (t.transpose(0, 1) for t in want)
+    for rows in (1, 5, 150):
+        q = torch.randn(rows, heads, hd, generator=g, device="cuda").to(dtype)
+        # the window covers just what was written: the reference's position 0 is the cache's cap - n
+        w = n - rows + 1
+        check(cache.attend(q, cap - rows, window=w), *ref.attention(q, kk, vv, n - rows, n, w, 0))
+    assert cache.sync() == 0
