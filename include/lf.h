@@ -484,7 +484,8 @@ LF_API lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *wor
  * wait of an lf_kv4_attend call on the current device ran out (each is bounded
  * by 2 s) since the last lf_kv4_status that said so (its outputs are then not
  * valid).  One record per device: whoever asks first is told.  A decoder handle
- * has its own (lf_sync). */
+ * has its own (lf_sync).  Errors: NOT_SUPPORTED (the stream is being captured),
+ * CUDA. */
 LF_API lf_status lf_kv4_status(void *stream);
 
 /* Static string naming a status code. */

@@ -985,8 +985,12 @@ lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *workspace,
 
 lf_status lf_kv4_status(void *stream)
 {
+    // a synchronisation would end the capture with an error
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cs);
+    if (e == cudaSuccess && cs != cudaStreamCaptureStatusNone) return LF_ERR_NOT_SUPPORTED;
     bool expired = false;
-    const cudaError_t e = tiles_status(expired, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = tiles_status(expired, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return status_of(e);
     return expired ? LF_ERR_TIMEOUT : LF_OK;
 }

@@ -232,3 +232,17 @@ def test_row_offsets_of_one_head_past_31_bits(pm, dtype):
         w = n - rows + 1
         check(cache.attend(q, cap - rows, window=w), *ref.attention(q, kk, vv, n - rows, n, w, 0))
     assert cache.sync() == 0
+
+
+def test_sync_inside_a_capture_is_refused_and_the_capture_goes_on(pm):
+    cache = pm.KV4Cache(2, 64, 40)
+    q = torch.randn(3, 4, 64, device="cuda").half()
+    cache.append(q[:, :2], q[:, 2:], 0)
+    want = cache.attend(q, 0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = cache.attend(q, 0)
+        assert cache.sync() == 7                          # LF_ERR_NOT_SUPPORTED
+        cache.append(q[:, :2], q[:, 2:], 0)
+    graph.replay()
+    assert cache.sync() == 0 and torch.equal(out, want)
