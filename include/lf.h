@@ -405,7 +405,10 @@ LF_API lf_status lf_generate_noalloc(const lf_config *cfg, const lf_weights *w, 
  * to even; it stands for the values s * code, which are exact in FP16 and BF16.
  * A is at most 6 * 448 = 2,688 (more saturates); blocks with A < 6 * 2^-10
  * become zeros (below 6 * 2^-6 the scale's own steps grow coarse).  Infinities
- * saturate and NaN is stored as 0: what lf_kv4_append writes is always finite. */
+ * saturate and NaN is stored as 0: what lf_kv4_append writes is always finite.
+ * Scale bytes that stand for NaN (0x7f, 0xff; in memory that was never written)
+ * are read as NaN; in the attention they spoil the rows that see their position,
+ * and no others. */
 
 #define LF_F16 0
 #define LF_BF16 1

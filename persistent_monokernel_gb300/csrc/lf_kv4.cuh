@@ -43,6 +43,16 @@ __device__ __forceinline__ unsigned e4m3x2_h2(unsigned b)
 }
 // One E4M3 byte in both halves of a pair.
 __device__ __forceinline__ unsigned e4m3_h2_same(unsigned b) { return e4m3x2_h2(b | (b << 8)); }
+// Two scale bytes of V for the attention, where the one that stands for NaN counts as 448 (the minimum's other
+// operand): a NaN would meet the zero probability of rows that do not see its position, and make those NaN as well.  (A
+// position that was never written holds whatever the memory held, and padded rows behind a block's end see it.  A NaN
+// of K stays in the scores of its position, which such rows leave out.)
+__device__ __forceinline__ unsigned scales_h2(unsigned b)
+{
+    unsigned d;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(e4m3x2_h2(b)), "r"(0x5f005f00u));
+    return d;
+}
 __device__ __forceinline__ unsigned hmul2(unsigned a, unsigned b)
 {
     unsigned d;
@@ -387,7 +397,7 @@ struct VRaw<64> {
 template <int HD>
 __device__ __forceinline__ void weave(const VRaw<HD> &a, const VRaw<HD> &b, unsigned (&v)[HD / 16][2])
 {
-    const unsigned sc = e4m3x2_h2(a.s | (b.s << 8));
+    const unsigned sc = scales_h2(a.s | (b.s << 8));
 #pragma unroll
     for (int j = 0; j < HD / 64; ++j) {
         const unsigned x = a.word(j), y = b.word(j), m = 0x0f0f0f0fu;

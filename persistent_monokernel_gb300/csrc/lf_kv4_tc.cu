@@ -229,7 +229,7 @@ struct RawRow {
 #pragma unroll
         for (int j = 0; j < HD / 32; ++j) {            // 32 values: two blocks
             const unsigned sw = j < 2 ? s.x : s.y;
-            const unsigned sc = e4m3x2_h2(j & 1 ? sw >> 16 : sw);
+            const unsigned sc = scales_h2(j & 1 ? sw >> 16 : sw);
             const __half2 s2 = *reinterpret_cast<const __half2 *>(&sc);
             const __half2 lo = __low2half2(s2), hi = __high2half2(s2);
             const unsigned w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};

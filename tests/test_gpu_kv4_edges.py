@@ -9,7 +9,7 @@ import torch
 import kv4_ref as ref
 from parity import compare_logits
 from synthetic import ModelConfig, make_prompt, make_weights
-from test_gpu_kv4 import check
+from test_gpu_kv4 import check, filled, gen
 from test_gpu_kv4_decoder import GQA, forward, pm, run  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -246,3 +246,20 @@ def test_sync_inside_a_capture_is_refused_and_the_capture_goes_on(pm):
         cache.append(q[:, :2], q[:, 2:], 0)
     graph.replay()
     assert cache.sync() == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n,good", [(2, 1), (8, 3), (40, 17), (700, 333)])
+def test_positions_never_written_do_not_reach_rows_that_do_not_see_them(pm, dtype, hd, n, good):
+    """A block padded behind its first rows: the padded rows see positions that hold whatever the memory held, among
+    it scales that stand for NaN."""
+    pos = 600
+    cache, (k, v) = filled(pm, 2, hd, pos + n + 3, hd + n)
+    q = torch.randn(n, 16, hd, generator=gen(n), device="cuda").to(dtype)
+    want, bound = ref.attention(q[:good], k, v, pos, pos + good, 0, 0)
+    for byte in (0x7f, 0xff):
+        for s in (cache.k_scales, cache.v_scales):
+            s[:, pos + good:] = byte
+        check(cache.attend(q, pos)[:good], want, bound)
+        check(cache.attend(q[:good], pos), want, bound)
