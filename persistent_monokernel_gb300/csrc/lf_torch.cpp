@@ -233,6 +233,7 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n_args)
         const int64_t had = like ? c.scratch : 0;
         int64_t need = 0;
         at::Tensor made;
+        const lf_kv4 cache = c.c;                         // (c is another thread's to change meanwhile)
         {
             NoGil free;
             if (out == Py_None) {
@@ -242,10 +243,10 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n_args)
             }
             at::Tensor ws;
             if (had) ws = empty({had}, at::kByte, c.device);
-            st = g_attend(&c.c, &q, had ? ws.mutable_data_ptr() : nullptr, had, stream);
-            if (st == LF_ERR_INVALID_ARG && g_workspace(&c.c, &q, &need) == LF_OK && need > had) {
+            st = g_attend(&cache, &q, had ? ws.mutable_data_ptr() : nullptr, had, stream);
+            if (st == LF_ERR_INVALID_ARG && g_workspace(&cache, &q, &need) == LF_OK && need > had) {
                 ws = empty({need}, at::kByte, c.device);
-                st = g_attend(&c.c, &q, ws.mutable_data_ptr(), need, stream);
+                st = g_attend(&cache, &q, ws.mutable_data_ptr(), need, stream);
             }
         }
         if (need > had) c.n = q.n, c.heads = q.n_heads, c.scratch = need;

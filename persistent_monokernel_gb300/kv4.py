@@ -146,7 +146,8 @@ class KV4Cache:
                stream=None):
         """Causal attention of q [n, n_heads, head_dim], whose rows stand at positions pos .. pos + n - 1, over the
         cached positions 0 .. length - 1 (pos + n unless given); window W > 0 leaves each row the W most recent; scale
-        0 selects 1 / sqrt(head_dim).  A row that sees nothing gives zeros.  Returns [n, n_heads, head_dim] in q's dtype."""
+        0 selects 1 / sqrt(head_dim).  A row that sees nothing gives zeros.  Returns [n, n_heads, head_dim] in q's dtype:
+        a new tensor, or `out`, which must not overlap q."""
         if stream is None:
             got = _calls.attend(self._handle, q, pos, length, window, scale, out)
             if got is not NotImplemented:
