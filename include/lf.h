@@ -455,9 +455,12 @@ LF_API lf_status lf_kv4_read(const lf_kv4 *c, const lf_rows *k, const lf_rows *v
  * j > pos + t - window:
  *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K[j]) V[j],
  * a row that sees no position gives zeros.  Positions that no row sees are not
- * read.  Scores, softmax and sums are FP32; with q in FP16 or BF16 the
- * probabilities are rounded to FP16 before they meet V, with q in FP32 the
- * products carry FP32-level operands.  q must be finite. */
+ * read.  Scores, softmax and sums are FP32.  With q in FP16 or BF16 the
+ * probabilities are rounded to FP16 before they meet V, and a BF16 row is brought
+ * into FP16's range by a power of two (exact down to 2^-17 of its largest value).
+ * With q in FP32, q and the probabilities enter the products as an FP16 head and
+ * remainder: about 22 bits, small values to 2^-25 of the row's largest.
+ * q must be finite. */
 typedef struct {
     lf_rows q, out;          /* [n][n_heads][head_dim], one dtype; out must not overlap q */
     int32_t n_heads;         /* a multiple of n_kv_heads */

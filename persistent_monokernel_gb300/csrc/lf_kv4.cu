@@ -37,7 +37,7 @@ namespace lfq {
 // (the same holds for A / 6 and the scales' half-way values).
 //
 // Bound by memory, the arithmetic close behind: 32,767 positions of 5 heads x 128 take 18.8 us from FP16 (5.7 TB/s)
-// and 29.3 from FP32 (6.5 TB/s), a copy's rate being 6.7; one position takes 1.3 us.  Products two to an
+// and 29 from FP32 (6.5 TB/s), a copy's rate being 6.7; one position takes 1.3 us.  Products two to an
 // instruction: 21.8 us without.  One block a thread: the loads in flight come from many threads of few registers (two
 // blocks of raw bytes a thread: 18.1 us, but 2.0 instead of 1.6 at 777 positions).
 template <class T>
@@ -146,16 +146,20 @@ __global__ void __launch_bounds__(256) read_rows(Cache c, Rows k, Rows v, int n,
 // and P are split into an FP16 head and remainder and the products are formed
 // twice, which leaves errors near 2^-22.
 //
-// What bounds it: instructions and memory together, and in short contexts latency.
+// What bounds it: the wait for loads, and in short contexts latency.  A warp loads a
+// chunk and then works on it, with nothing of its own on the way meanwhile; 16 warps
+// an SM do not cover that (waiting for a load is the largest stall, 2.6 warps per
+// issue, while neither the issue slots, at 52 %, nor memory is at its limit).
 // A cached value costs a conversion and a multiply by its scale per pair, half an
 // instruction to bring its byte to the converter, and its share of the product;
 // everything else is kept off the loop (addresses advance by constants, no maximum,
-// no rescaling).  One token over 131,072 positions of 8 KV heads x 128: 39.8 us, 3.8 TB/s
-// of 6.7, 52 % of the issue slots (65 us with a maximum per chunk, 48 before clusters
-// joined); over 512 positions of 5 heads: 4.5 us.  FP16 values through shared memory
-// would write and read four times the cache's bytes there.  The next chunk's loads
-// one phase ahead gained 4 % at 131,072, but lost 3 % with FP32 queries and 8 % at 512
-// (two slabs), as the registers run out; a third CTA per SM costs 75 % (spills).
+// no rescaling).  One token over 131,072 positions of 8 KV heads x 128: 39.4 us, 3.8 TB/s
+// of 6.7 (65 us with a maximum per chunk, 48 before clusters joined); over 512
+// positions of 5 heads: 4.5 us.  FP16 values through shared memory
+// would write and read four times the cache's bytes there; its raw bytes, loaded ahead
+// of their use, would cost no registers and were not tried.  The next chunk's loads
+// one phase ahead in registers gained 4 % at 131,072, but lost 3 % with FP32 queries and 8 % at 512
+// (two slabs), as they run out; a third CTA per SM costs 75 % (spills).
 __device__ __forceinline__ void add_scaled(float4 &acc, const float4 &v, float x)
 {
     acc.x = fmaf(v.x, x, acc.x);
@@ -551,7 +555,7 @@ static size_t tiles_workspace(const Cache &c, size_t ctas, size_t tiles)
     return (2 * ctas * 128 * (c.hd + PAD)) * sizeof(float) + tiles * sizeof(int2);
 }
 
-// What a tile, or a piece of one, costs beside its chunks, in chunks (1,570 cycles each, 3,060 in FP32, beside about
+// What a tile, or a piece of one, costs beside its chunks, in chunks (about 1,600 cycles each, 3,000 in FP32, beside
 // 20,000 a piece, from the CTAs' own clocks): q, the way to the first P and from the last one, the output.
 static int piece_cost(const Attn &a) { return a.q.dtype == F32 ? 7 : 12; }
 

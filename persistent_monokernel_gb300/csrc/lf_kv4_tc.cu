@@ -33,13 +33,13 @@
 // FP32 queries (SPLIT): q and P as an FP16 head and remainder, each product
 // formed twice; Q then lies in shared memory (TMEM is full).
 //
-// What bounds it: the hand-overs between softmax, issue and tensor cores (1,570
-// cycles a chunk of 128 x 128, 3,060 with FP32 queries; the products take 1,024 and
+// What bounds it: the hand-overs between softmax, issue and tensor cores (about 1,600
+// cycles a chunk of 128 x 128, 3,000 with FP32 queries; the products take 1,024 and
 // 2,048), and about 20,000 cycles to begin and end a tile.  1,024 queries over 32,768
-// positions, 20/5 heads x 128, FP16: 247 us, 1.37 PFLOP/s or 71 % of the
+// positions, 20/5 heads x 128, FP16: 255 us, 1.33 PFLOP/s or 69 % of the
 // measured rate (692 us with a maximum per chunk and packed conversions only, 372
 // with one chunk in flight, 320 with two issuing warps and no maximum, 253
-// with even shares).  511 queries from 0, FP32: 21 us.
+// with even shares, before scales were cut).  511 queries from 0, FP32: 20 us.
 //
 // Every wait is bounded by %globaltimer; on expiry the CTA records a timeout
 // in the status word, settles its MMAs, frees TMEM and returns; its outputs are not
@@ -229,7 +229,7 @@ struct RawRow {
 #pragma unroll
         for (int j = 0; j < HD / 32; ++j) {            // 32 values: two blocks
             const unsigned sw = j < 2 ? s.x : s.y;
-            const unsigned sc = scales_h2(j & 1 ? sw >> 16 : sw);
+            const unsigned sc = scales_h2(j & 1 ? sw >> 16 : sw);   // (K's too: one instruction for 32 values)
             const __half2 s2 = *reinterpret_cast<const __half2 *>(&sc);
             const __half2 lo = __low2half2(s2), hi = __high2half2(s2);
             const unsigned w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
