@@ -66,8 +66,9 @@ class KV4Cache:
     [heads, n, head_dim] tensor); what the library refuses raises LFError.  The calls form no gradients: where autograd
     is on, a tensor that requires one raises ValueError.
 
-    A call with stream=s queues its work on s and returns.  Its tensors and the cache may be let go of at once; what it
-    returns belongs to s, as with any torch operation under torch.cuda.stream(s).
+    A call with stream=s queues its work on s and returns.  Its tensors and the cache may be let go of at once (on an
+    ExternalStream, whose life torch does not know, once the work is done); what it returns belongs to s, as with any
+    torch operation under torch.cuda.stream(s).
     """
 
     def __init__(self, n_kv_heads: int, head_dim: int, max_seq: int, device="cuda"):
@@ -122,8 +123,9 @@ class KV4Cache:
             raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
         with _torch.cuda.stream(stream):
             got = call(*args)
-        for t in (*self._parts, *_tensors(args)):
-            t.record_stream(stream)
+        if not isinstance(stream, _torch.cuda.ExternalStream):   # (which may be gone when the memory is let go of)
+            for t in (*self._parts, *_tensors(args)):
+                t.record_stream(stream)
         return got
 
     def append(self, k, v, pos: int, stream=None) -> None:

@@ -263,3 +263,28 @@ def test_positions_never_written_do_not_reach_rows_that_do_not_see_them(pm, dtyp
             s[:, pos + good:] = byte
         check(cache.attend(q, pos)[:good], want, bound)
         check(cache.attend(q[:good], pos), want, bound)
+
+
+def test_a_stream_of_another_library_may_end_before_the_tensors(pm):
+    """Nothing of the allocator's holds on to an ExternalStream when the memory is let go of."""
+    import ctypes
+    rt, handle = torch.cuda.cudart(), ctypes.c_void_p()
+    assert int(rt.cudaStreamCreate(ctypes.addressof(handle))) == 0
+    cache = pm.KV4Cache(2, 128, 400)
+    k, q = (torch.randn(300, h, 128, generator=gen(h), device="cuda").half() for h in (2, 8))
+    torch.cuda.synchronize()
+    s = torch.cuda.ExternalStream(handle.value)
+    cache.append(k, k, 0, stream=s)
+    out = torch.empty_like(q)
+    cache.attend(q, 0, out=out, stream=s)
+    s.synchronize()
+    want = cache.attend(q, 0)
+    assert torch.equal(out, want)
+    # (what the allocator made for the call itself, on s, goes back before s does)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    assert int(rt.cudaStreamDestroy(handle.value)) == 0
+    del cache, k, q, out
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    assert torch.ones(1 << 20, device="cuda").sum() == 1 << 20
