@@ -494,6 +494,111 @@ LF_API lf_status lf_kv4_attend(const lf_kv4 *c, const lf_kv4_query *q, void *wor
  * CUDA. */
 LF_API lf_status lf_kv4_status(void *stream);
 
+/* ---- KV cache in pages
+ *
+ * Operators on the K and V of one layer for many sequences at once, in FP16 or
+ * BF16.  The positions of all sequences lie in pages of `page` positions of one
+ * pool; a sequence owns any pages in any order, listed in its row of a block
+ * table: its position p is slot tables[row][p / page] * page + p % page.  Like
+ * those of the 4-bit cache the calls need no handle; their kernels run on
+ * `stream` of the current device, every buffer is the caller's, and all of them
+ * can be captured into a graph.  A decode step is lf_paged_plan (once for all
+ * layers), then lf_paged_append and lf_paged_attend per layer. */
+
+typedef struct {
+    int32_t n_pages;         /* of the pool; n_pages * page < 2^31 */
+    int32_t n_kv_heads;      /* 1 .. 1024 */
+    int32_t page;            /* positions per page, a multiple of 16 */
+    int32_t head_dim;        /* 64 or 128 */
+    int32_t dtype;           /* LF_F16 or LF_BF16 */
+    /* device buffers, 16-byte aligned: element (page, head, position, i) at k +
+     * page * page_stride + head * head_stride + position * pos_stride + i
+     * (strides in elements, multiples of 8; [n_pages][heads][page][head_dim],
+     * [n_pages][page][heads][head_dim] or a slice of more; no two rows may overlap) */
+    void *k, *v;
+    int64_t page_stride, head_stride, pos_stride;
+} lf_paged;
+
+/* The pages of a batch of sequences: device buffers of 32-bit integers. */
+typedef struct {
+    int32_t n_seqs;          /* rows, 0 .. 8192 */
+    int32_t max_pages;       /* columns; max_pages * page <= 2^30 */
+    int32_t n_pages, page;   /* as in lf_paged */
+    int32_t *tables;         /* [n_seqs][max_pages] at table_stride elements; entries behind a row's length mean nothing */
+    int64_t table_stride;
+    int32_t *lens;           /* [n_seqs] positions that each row holds */
+    int32_t *free_pages;     /* [n_pages]: the first *n_free are the pages that no row owns */
+    int32_t *n_free;
+    int32_t *status;         /* 0; the first lf_status of a plan that failed, until the caller clears it */
+} lf_page_tables;
+
+/* Plans one step on the device: row i keeps min(lens[i], keep[i]) positions (keep
+ * NULL: all) and gives the pages behind them back, then gets the pages for
+ * n_new[i] more, and lens[i] becomes the sum.  keep 0 ends a sequence (or, with
+ * n_new, lets another take its row); a smaller keep takes drafted positions back.
+ * The new positions of all rows, packed in row order, get
+ *   slots[t]       where position positions[t] of its row lies (lf_paged_append)
+ *   offsets[i]     the first t of row i; offsets[n_seqs] is their number
+ * and the entries behind them, up to max_tokens, slot -1 and position 0.
+ * Pages are taken from the end of the free ones and given back there in the
+ * reverse order: a plan that takes back what the last one took finds the same
+ * pages again, and equal calls give equal results.
+ * All or nothing: where the pool has too few pages, a row would pass max_pages
+ * or the tokens max_tokens (CAPACITY), or a length, keep, n_new or *n_free is out
+ * of range (INVALID_ARG), the tables, lens and free pages stay as they are, all
+ * slots are -1, all offsets 0, and *status says why unless it already says
+ * something.  Entries of tables and free_pages are moved, never followed.
+ * Errors found on the host: INVALID_ARG (NULL, alignment: 4 bytes, 16 of slots
+ * and positions; negative sizes; table_stride < max_pages), NOT_SUPPORTED
+ * (n_seqs, page, sizes beyond the bounds above, max_tokens > 2^30), CUDA. */
+LF_API lf_status lf_paged_plan(const lf_page_tables *t, const int32_t *n_new, const int32_t *keep, int32_t *slots,
+                               int32_t *positions, int32_t *offsets, int32_t max_tokens, void *stream);
+
+/* Row t of k and v [n][n_kv_heads][head_dim] (both of the cache's dtype, or both
+ * FP32, rounded to nearest even) into slot slots[t] (device memory); a slot
+ * outside 0 .. n_pages * page - 1 stores nothing.  No two rows may have one slot.
+ * n = 0 does nothing.  Errors: INVALID_ARG (NULL, alignment, strides, negative n,
+ * dtypes that differ or are neither), NOT_SUPPORTED (sizes of the cache, dtype), CUDA. */
+LF_API lf_status lf_paged_append(const lf_paged *c, const lf_rows *k, const lf_rows *v, int32_t n, const int32_t *slots,
+                                 void *stream);
+
+/* Attention of one query row per sequence, its newest position's:
+ *   out[i][h] = sum_j softmax_j(scale * q[i][h] . K[j]) V[j]
+ * over the positions j < lens[i] of row i (window > 0: the `window` most recent of
+ * them), query head h reading KV head h / (n_heads / n_kv_heads).  A row that
+ * sees no position (lens[i] <= 0) gives zeros.  Positions behind table_width pages
+ * and positions on a page that the pool does not have (table entries outside
+ * 0 .. n_pages - 1) are left out.  What lies in pages behind a row's length, or on
+ * pages that no row sees, is not read.  The narrower the table, the better the
+ * launch fits (pass the columns that the longest row needs, not the allocation).
+ * Scores, softmax and sums are FP32; q and the probabilities enter the products
+ * with 16 bits or more (q as it is where it has the cache's dtype). */
+typedef struct {
+    lf_rows q, out;          /* [n_seqs][n_heads][head_dim], both of the cache's dtype or FP32; out must not overlap q */
+    int32_t n_seqs;          /* 0 does nothing */
+    int32_t n_heads;         /* a multiple of n_kv_heads */
+    const int32_t *tables;   /* device, [n_seqs][table_width] at table_stride elements (0: one table for all) */
+    int64_t table_stride;
+    int32_t table_width;     /* table_width * page <= 2^30 */
+    const int32_t *lens;     /* device, [n_seqs] */
+    int32_t window;          /* 0: no window */
+    float scale;             /* 0 selects 1 / sqrt(head_dim) */
+} lf_paged_query;
+
+/* Scratch bytes that lf_paged_attend needs for this query on the current device;
+ * of its tensors only the dtype is looked at. */
+LF_API lf_status lf_paged_workspace(const lf_paged *c, const lf_paged_query *q, int64_t *bytes);
+
+/* workspace: device scratch, 16-byte aligned, of at least the bytes that
+ * lf_paged_workspace names (NULL where it names 0), as in lf_kv4_attend: not
+ * initialised, one per call that may run at the same time.  Errors: INVALID_ARG
+ * (NULL, alignment, strides, negative sizes, a scale that is not finite, dtypes that
+ * differ or are neither, out = q, a workspace that is too small), NOT_SUPPORTED
+ * (sizes of the cache, n_heads no multiple of n_kv_heads, n_seqs * n_heads above
+ * 2^31 - 1, table_width, or 2^50 slabs of 16 positions over all heads), CUDA. */
+LF_API lf_status lf_paged_attend(const lf_paged *c, const lf_paged_query *q, void *workspace, int64_t workspace_bytes,
+                                 void *stream);
+
 /* Static string naming a status code. */
 LF_API const char *lf_error_string(lf_status s);
 

@@ -11,6 +11,7 @@ import ctypes as C
 import os
 
 from .kv4 import KV4Cache, lf_kv4, lf_kv4_query, lf_rows
+from .paged import PagedKVCache, PageTables, lf_page_tables, lf_paged, lf_paged_query
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "liblf.so")
@@ -29,7 +30,8 @@ TRACE_STAMPS = 9
 EXPORTS = ("lf_create", "lf_destroy", "lf_prefill", "lf_decode", "lf_generate", "lf_sync", "lf_reset",
            "lf_set_schedule", "lf_get_info", "lf_error_string", "lf_abi_version", "lf_generate_noalloc",
            "lf_enable_trace", "lf_read_trace", "lf_sync_latency", "lf_kv4_append", "lf_kv4_read", "lf_kv4_workspace",
-           "lf_kv4_attend", "lf_kv4_status", "lf_create_kv4")
+           "lf_kv4_attend", "lf_kv4_status", "lf_create_kv4", "lf_paged_plan", "lf_paged_append", "lf_paged_workspace",
+           "lf_paged_attend")
 
 
 class LFError(RuntimeError):
@@ -110,7 +112,13 @@ def lib() -> C.CDLL:
         L.lf_kv4_workspace.argtypes = [C.POINTER(lf_kv4), C.POINTER(lf_kv4_query), C.POINTER(C.c_int64)]
         L.lf_kv4_attend.argtypes = [C.POINTER(lf_kv4), C.POINTER(lf_kv4_query), vp, C.c_int64, vp]
         L.lf_kv4_status.argtypes = [vp]
-        for name in ("lf_kv4_status", "lf_kv4_append", "lf_kv4_read", "lf_kv4_workspace", "lf_kv4_attend"):
+        ints = vp   # device buffers of 32-bit integers
+        L.lf_paged_plan.argtypes = [C.POINTER(lf_page_tables), ints, ints, ints, ints, ints, C.c_int32, vp]
+        L.lf_paged_append.argtypes = [C.POINTER(lf_paged), C.POINTER(lf_rows), C.POINTER(lf_rows), C.c_int32, ints, vp]
+        L.lf_paged_workspace.argtypes = [C.POINTER(lf_paged), C.POINTER(lf_paged_query), C.POINTER(C.c_int64)]
+        L.lf_paged_attend.argtypes = [C.POINTER(lf_paged), C.POINTER(lf_paged_query), vp, C.c_int64, vp]
+        for name in ("lf_kv4_status", "lf_kv4_append", "lf_kv4_read", "lf_kv4_workspace", "lf_kv4_attend", "lf_paged_plan",
+                     "lf_paged_append", "lf_paged_workspace", "lf_paged_attend"):
             getattr(L, name).restype = C.c_int
         for name in ("lf_create", "lf_create_kv4", "lf_prefill", "lf_decode", "lf_generate", "lf_sync", "lf_reset",
                      "lf_set_schedule", "lf_get_info"):

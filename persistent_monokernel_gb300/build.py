@@ -26,7 +26,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "liblf.so")
 EXT, EXT_SOURCE = os.path.join(HERE, "_lft.so"), "lf_torch.cpp"
 SOURCES = ["lf_kernel.cu", "lf_api.cu", "lf_noalloc.cu", "lf_syncbench.cu", "lf_prefill.cu", "lf_gemm.cu", "lf_attn_tc.cu",
-           "lf_kv4.cu", "lf_kv4_tc.cu"]
+           "lf_kv4.cu", "lf_kv4_tc.cu", "lf_paged.cu", "lf_paged_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr"]

@@ -21,8 +21,11 @@
 #include "lf_kv4.cuh"
 #include "lf_internal.cuh"
 #include "lf_ptx.cuh"
+#include "lf_rows.cuh"
 
 namespace lfq {
+
+using lfr::launch;
 
 // ---------------------------------------------------------------- append and read
 
@@ -734,26 +737,6 @@ static dim3 row_grid(const Cache &c, int n, int shift, int per)
 {
     return dim3((unsigned)((((long long)n << shift) + per - 1) / per), (unsigned)(2 * c.Hkv));
 }
-// A launch as a programmatic dependent of the previous kernel on the stream (it waits for that kernel's end before
-// any access to global memory), in clusters of `cluster` CTAs along x.
-template <class... P, class... A>
-static cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t s, const A &...args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 template <class T>
 struct RunAppend {
     static cudaError_t run(Cache c, Rows k, Rows v, int n, int pos, cudaStream_t s)
@@ -831,19 +814,14 @@ cudaError_t launch_attn(const Attn &a, cudaStream_t s)
 namespace {
 
 using namespace lfq;
+using lfr::aligned16;
+using lfr::check_rows;
+using lfr::sm_count;
+using lfr::status_of;
 
 constexpr int kMaxKvHeads = 1024;
 constexpr int kMaxPositions = 1 << 30;   // positions rounded up to whole splits stay in 32 bits
 constexpr long long kMaxRows = 1ll << 32;   // rows of all heads (8 GB per dim in FP16): their tiles do too
-
-lf_status status_of(cudaError_t e)
-{
-    if (e == cudaSuccess) return LF_OK;
-    (void)cudaGetLastError();
-    return e == cudaErrorMemoryAllocation ? LF_ERR_OUT_OF_MEMORY : LF_ERR_CUDA;
-}
-
-bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 lf_status check_cache(const lf_kv4 *c)
 {
@@ -852,26 +830,6 @@ lf_status check_cache(const lf_kv4 *c)
     if (c->n_kv_heads > kMaxKvHeads || c->max_seq > kMaxPositions) return LF_ERR_NOT_SUPPORTED;
     if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
         return LF_ERR_INVALID_ARG;
-    return LF_OK;
-}
-
-// Rows [n][heads][hd]: type, alignment, strides; `written`: no two may overlap.
-lf_status check_rows(const lf_rows *r, int n, int heads, int hd, bool written)
-{
-    if (!r) return LF_ERR_INVALID_ARG;
-    if (r->dtype != LF_F16 && r->dtype != LF_BF16 && r->dtype != LF_F32) return LF_ERR_NOT_SUPPORTED;
-    const long long per16 = r->dtype == LF_F32 ? 4 : 8;   // elements in 16 bytes
-    if (!aligned16(r->data) || r->token_stride < 0 || r->head_stride < 0 || r->token_stride % per16 ||
-        r->head_stride % per16)
-        return LF_ERR_INVALID_ARG;
-    const long long most = 1ll << 40;   // elements: keeps every offset far inside 64 bits
-    if (r->token_stride > most || r->head_stride > most) return LF_ERR_INVALID_ARG;
-    if (written) {
-        const long long ts = r->token_stride, hs = r->head_stride;
-        const bool t_ok = n == 1 || ts >= hd, h_ok = heads == 1 || hs >= hd;
-        const bool apart = n == 1 || heads == 1 || ts >= (heads - 1ll) * hs + hd || hs >= (n - 1ll) * ts + hd;
-        if (!t_ok || !h_ok || !apart) return LF_ERR_INVALID_ARG;
-    }
     return LF_OK;
 }
 
@@ -893,23 +851,6 @@ lf_status check_copy(const lf_kv4 *c, const lf_rows *k, const lf_rows *v, int n,
     if (st == LF_OK) st = check_rows(v, n, c->n_kv_heads, c->head_dim, written);
     if (st == LF_OK && (k->dtype != v->dtype || (written && k->data == v->data))) st = LF_ERR_INVALID_ARG;
     return st;
-}
-
-// Device properties that the plan needs, read once per device.
-lf_status sm_count(int *out)
-{
-    static int cached[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return status_of(e);
-    if (dev < 64 && cached[dev]) {
-        *out = cached[dev];
-        return LF_OK;
-    }
-    e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return status_of(e);
-    if (dev < 64) cached[dev] = *out;
-    return LF_OK;
 }
 
 lf_status make_attn(const lf_kv4 *c, const lf_kv4_query *q, Attn *a, size_t *bytes)

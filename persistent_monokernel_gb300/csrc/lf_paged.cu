@@ -1,0 +1,380 @@
+// lf_paged.cu -- a KV cache of many sequences in pages: the plan of their pages
+// and slots, the append, and the C entry points of these and the attention.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "../../include/lf.h"
+#include "lf_kv4.cuh"
+#include "lf_paged.h"
+#include "lf_rows.cuh"
+
+namespace lfpg {
+
+// ---------------------------------------------------------------- plan
+
+// Row i keeps kept = min(lens, keep) positions and gives the pages behind them back, then takes n_new more.  With
+// stay, held, want the pages of kept, lens and kept + n_new positions:
+//   the pages stay .. held - 1 of all rows, rows in order, are the back entries 0 ..; entry k goes to
+//   free[top - 1 - k], top = n_free + (their number);
+//   the pages stay .. want - 1 of all rows are the need entries 0 ..; entry k comes from free[top - 1 - k].
+// So a plan that takes back exactly what the one before it took finds the same pages again.
+//
+// Three sums over the rows say where everything lies; after them every page and token finds its row by a search in
+// shared memory, however uneven the rows are.  Every CTA of the (only) cluster forms the sums for itself: they are
+// a read of a few KB, and nothing has to be handed over.  What is read and what is written overlaps (lens, n_free,
+// table entries given back and taken anew), hence one cluster barrier between reading and writing.
+//
+// Bound by latency: the loads of the rows, the sums' shuffles, a search and two dependent loads per token.
+__device__ __forceinline__ int row_of(const int *before, int n, int k)   // the last row with before[row] <= k
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] <= k) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(1024) plan_pages(const __grid_constant__ Plan p, int ctas, int shift)
+{
+    extern __shared__ int smem[];
+    int *const kept = smem, *const tok = kept + p.n, *const back = tok + p.n + 1, *const need = back + p.n + 1;
+    __shared__ long long wsum[3][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    lfq::dependents_may_launch();
+    lfq::wait_for_prerequisites();
+    auto page_of = [&](int x) { return shift >= 0 ? x >> shift : (int)((unsigned)x / (unsigned)p.page); };
+    auto pages = [&](int x) { return x ? page_of(x - 1) + 1 : 0; };
+
+    // ---- the rows' numbers, and their sums up to each row
+    const int per = (p.n + blockDim.x - 1) / blockDim.x;
+    const int r0 = min(tid * per, p.n), r1 = min(r0 + per, p.n);
+    const long long cap = (long long)p.max_pages * p.page;
+    const int n_free = lfq::ld(p.n_free);
+    int wrong = n_free < 0 || n_free > p.n_pages ? LF_ERR_INVALID_ARG : 0;
+    auto row = [&](int r, long long (&x)[3]) {
+        const int len = lfq::ld(p.lens + r), n_new = lfq::ld(p.n_new + r);
+        const int keep = p.keep ? lfq::ld(p.keep + r) : len, k = min(len, keep);
+        x[0] = x[1] = x[2] = 0;
+        if (len < 0 || len > cap || keep < 0 || n_new < 0) {
+            wrong = LF_ERR_INVALID_ARG;
+            return 0;
+        }
+        if ((long long)k + n_new > cap) {
+            if (!wrong) wrong = LF_ERR_CAPACITY;
+            return 0;
+        }
+        x[0] = n_new;
+        x[1] = pages(len) - pages(k);
+        x[2] = pages(k + n_new) - pages(k);
+        return k;
+    };
+    long long mine[3] = {0, 0, 0}, at[3];
+    for (int r = r0; r < r1; ++r) {
+        long long x[3];
+        row(r, x);
+        for (int i = 0; i < 3; ++i) mine[i] += x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        long long incl = mine[i];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += x;
+        }
+        if (lane == 31) wsum[i][warp] = incl;
+        at[i] = incl - mine[i];
+    }
+    __syncthreads();
+    long long sum[3] = {0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        for (int w = 0; w < warps; ++w) {
+            if (w == warp) at[i] += sum[i];
+            sum[i] += wsum[i][w];
+        }
+    for (int r = r0; r < r1; ++r) {
+        long long x[3];
+        kept[r] = row(r, x);
+        tok[r] = (int)at[0], back[r] = (int)at[1], need[r] = (int)at[2];
+        for (int i = 0; i < 3; ++i) at[i] += x[i];
+    }
+    if (tid == 0) tok[p.n] = (int)sum[0], back[p.n] = (int)sum[1], need[p.n] = (int)sum[2];
+    // all or nothing: more pages given back than the pool has (tables that are not a plan's), or too few for the rows
+    const long long top64 = n_free + sum[1];
+    if (!wrong && top64 > p.n_pages) wrong = LF_ERR_INVALID_ARG;
+    if (!wrong && (sum[2] > top64 || sum[0] > p.max_tokens)) wrong = LF_ERR_CAPACITY;
+    const bool invalid = __syncthreads_or(wrong == LF_ERR_INVALID_ARG), fails = __syncthreads_or(wrong != 0);
+    const int all = ctas * blockDim.x, me = blockIdx.x * blockDim.x + tid;
+    const int tokens = fails ? 0 : (int)sum[0], n_back = (int)sum[1], n_need = (int)sum[2], top = (int)top64;
+
+    // ---- pages given back
+    if (!fails) {
+        for (int k = me; k < n_back; k += all) {
+            const int r = row_of(back, p.n, k);
+            p.free[top - 1 - k] = lfq::ld(p.tables + r * p.tstride + pages(kept[r]) + k - back[r]);
+        }
+    }
+    if (ctas > 1) lfq::cluster_sync();
+    else __syncthreads();
+    // ---- pages taken, and the rows
+    if (!fails) {
+        for (int k = me; k < n_need; k += all) {
+            const int r = row_of(need, p.n, k);
+            p.tables[r * p.tstride + pages(kept[r]) + k - need[r]] = lfq::ld(p.free + top - 1 - k);
+        }
+        for (int r = me; r < p.n; r += all) p.lens[r] = kept[r] + tok[r + 1] - tok[r];
+        if (me == 0) *p.n_free = top - n_need;
+    } else if (me == 0 && lfq::ld(p.status) == 0) {
+        *p.status = invalid ? LF_ERR_INVALID_ARG : LF_ERR_CAPACITY;
+    }
+    for (int r = me; r <= p.n; r += all) p.offsets[r] = fails ? 0 : tok[r];
+    // ---- four tokens a thread
+    for (int t0 = me * 4; t0 < p.max_tokens; t0 += all * 4) {
+        int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
+        if (t0 < tokens) {
+            int r = row_of(tok, p.n, t0), j = -1, page = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = t0 + i;
+                if (t >= tokens) break;
+                while (t >= tok[r + 1]) ++r, j = -1;
+                const int x = kept[r] + t - tok[r], c = page_of(x), stay = pages(kept[r]);
+                if (c != j) {
+                    j = c;
+                    page = c < stay ? lfq::ld(p.tables + r * p.tstride + c) : lfq::ld(p.free + top - 1 - (need[r] + c - stay));
+                }
+                slot[i] = page * p.page + x - c * p.page;
+                pos[i] = x;
+            }
+        }
+        if (t0 + 4 <= p.max_tokens) {
+            *reinterpret_cast<int4 *>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+            for (int i = 0; t0 + i < p.max_tokens; ++i) {
+                p.slots[t0 + i] = slot[i];
+                p.positions[t0 + i] = pos[i];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- append
+
+// A thread moves 8 values (16 bytes of the cache); one grid row per KV head and K or V, so that no division but the
+// slot's finds a place.  Slots outside the pool store nothing.  Bound by memory, and by latency for few rows.
+template <class TI, class TO>
+__global__ void __launch_bounds__(256) append_rows(const __grid_constant__ Pool c, const __grid_constant__ Rows k,
+                                                   const __grid_constant__ Rows v, int n, const int *slots, int shift)
+{
+    lfq::dependents_may_launch();
+    lfq::wait_for_prerequisites();
+    const bool isv = blockIdx.y & 1;
+    const int h = blockIdx.y >> 1;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, t = i >> shift;   // 2^shift places per row
+    const int b = (int)(i & ((1 << shift) - 1));
+    if (t >= n) return;
+    const Rows &in = isv ? v : k;
+    const TI *src = static_cast<const TI *>(in.p) + t * in.ts + h * in.hs + b * 8;
+    const unsigned slot = (unsigned)lfq::ld(slots + t);
+    uint4 x;
+    if constexpr (sizeof(TI) == 2) {
+        x = lfq::ld(reinterpret_cast<const uint4 *>(src));
+    } else {
+        const float4 f = lfq::ld(reinterpret_cast<const float4 *>(src)), g = lfq::ld(reinterpret_cast<const float4 *>(src) + 1);
+        auto two = [](float lo, float hi) {
+            if constexpr (std::is_same_v<TO, __half>) {
+                const __half2 y = __floats2half2_rn(lo, hi);
+                return *reinterpret_cast<const unsigned *>(&y);
+            } else {
+                const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+                return *reinterpret_cast<const unsigned *>(&y);
+            }
+        };
+        x = make_uint4(two(f.x, f.y), two(f.z, f.w), two(g.x, g.y), two(g.z, g.w));
+    }
+    const unsigned page = slot / (unsigned)c.page;
+    if (page >= (unsigned)c.n_pages) return;
+    char *dst = (isv ? c.v : c.k) + page * c.page_b + (long long)(slot - page * c.page) * c.pos_b + h * c.head_b + b * 16;
+    *reinterpret_cast<uint4 *>(dst) = x;
+}
+
+// ---------------------------------------------------------------- launches
+
+cudaError_t launch_plan(const Plan &p, cudaStream_t s)
+{
+    // Up to 4,096 tokens a CTA, in one cluster.
+    const int ctas = std::max(1, std::min(8, (p.max_tokens + 4095) / 4096));
+    const int threads = p.n <= 256 && p.max_tokens <= 1024 ? 256 : 1024;
+    const int smem = (4 * p.n + 3) * (int)sizeof(int);
+    int shift = -1;
+    for (int i = 4; i < 31; ++i)
+        if (p.page == 1 << i) shift = i;
+    static bool ready[64] = {};
+    const cudaError_t e = lfr::allow_smem(plan_pages, (4 * MAX_ROWS + 3) * (int)sizeof(int), ready);
+    if (e != cudaSuccess) return e;
+    return lfr::launch(plan_pages, dim3((unsigned)ctas), threads, smem, ctas, s, p, ctas, shift);
+}
+
+cudaError_t launch_append(const Pool &c, const Rows &k, const Rows &v, int n, const int *slots, cudaStream_t s)
+{
+    const int shift = c.hd == 128 ? 4 : 3;
+    const dim3 grid((unsigned)((((long long)n << shift) + 255) / 256), (unsigned)(2 * c.Hkv));
+    if (k.dtype != LF_F32) return lfr::launch(append_rows<__half, __half>, grid, 256, 0, 1, s, c, k, v, n, slots, shift);
+    if (c.bf16) return lfr::launch(append_rows<float, __nv_bfloat16>, grid, 256, 0, 1, s, c, k, v, n, slots, shift);
+    return lfr::launch(append_rows<float, __half>, grid, 256, 0, 1, s, c, k, v, n, slots, shift);
+}
+
+}  // namespace lfpg
+
+// ---------------------------------------------------------------- C entry points
+
+namespace {
+
+using namespace lfpg;
+using lfr::aligned16;
+using lfr::check_rows;
+using lfr::status_of;
+
+constexpr int kMaxKvHeads = 1024;
+constexpr long long kMaxStride = 1ll << 40;   // elements: keeps every offset far inside 64 bits
+
+bool aligned4(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool page_ok(int page) { return page >= 16 && page % 16 == 0; }
+
+lf_status check_pool(const lf_paged *c)
+{
+    if (!c || c->n_pages < 1 || c->n_kv_heads < 1 || c->page < 1) return LF_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return LF_ERR_NOT_SUPPORTED;
+    if (c->dtype != LF_F16 && c->dtype != LF_BF16) return LF_ERR_NOT_SUPPORTED;
+    if (c->n_kv_heads > kMaxKvHeads || !page_ok(c->page) || (long long)c->n_pages * c->page > INT32_MAX) return LF_ERR_NOT_SUPPORTED;
+    if (!aligned16(c->k) || !aligned16(c->v) || c->k == c->v) return LF_ERR_INVALID_ARG;
+    struct Dim {
+        long long stride, size;
+    } dims[3] = {{c->page_stride, c->n_pages}, {c->head_stride, c->n_kv_heads}, {c->pos_stride, c->page}};
+    for (Dim &d : dims) {
+        if (d.size == 1) d.stride = 0;                 // (never used)
+        if (d.stride < 0 || d.stride % 8 || d.stride > kMaxStride) return LF_ERR_INVALID_ARG;
+    }
+    // no two rows overlap: each stride spans all that lies within it
+    std::sort(dims, dims + 3, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
+    long long extent = c->head_dim;
+    for (const Dim &d : dims) {
+        if (d.size == 1) continue;
+        if (d.stride < extent || d.stride > (INT64_MAX >> 2) / d.size) return LF_ERR_INVALID_ARG;
+        extent += d.stride * (d.size - 1);
+    }
+    return LF_OK;
+}
+
+Pool pool_of(const lf_paged *c)
+{
+    return {static_cast<char *>(c->k), static_cast<char *>(c->v), 2 * c->page_stride, 2 * c->head_stride, 2 * c->pos_stride,
+            c->n_pages, c->page, c->n_kv_heads, c->head_dim, c->dtype == LF_BF16};
+}
+Rows rows_of(const lf_rows *r) { return {r->data, r->dtype, r->token_stride, r->head_stride}; }
+
+lf_status make_attn(const lf_paged *c, const lf_paged_query *q, Attn *a, size_t *bytes)
+{
+    lf_status st = check_pool(c);
+    if (st != LF_OK) return st;
+    if (!q || q->n_seqs < 0 || q->n_heads < 1 || q->table_width < 0 || q->table_stride < 0 || q->table_stride > kMaxStride ||
+        q->window < 0 || !std::isfinite(q->scale))
+        return LF_ERR_INVALID_ARG;
+    if (q->n_heads % c->n_kv_heads) return LF_ERR_NOT_SUPPORTED;
+    if (q->q.dtype != LF_F16 && q->q.dtype != LF_BF16 && q->q.dtype != LF_F32) return LF_ERR_NOT_SUPPORTED;
+    if (q->q.dtype != LF_F32 && q->q.dtype != c->dtype) return LF_ERR_INVALID_ARG;
+    // positions, blocks of the join and the shares of a launch in their types
+    const long long seen = (long long)q->table_width * c->page;
+    if (seen > (1 << 30) || (long long)q->n_seqs * q->n_heads > INT32_MAX ||
+        (double)q->n_seqs * q->n_heads * (double)(seen / 16 + 1) > 0x1p50)
+        return LF_ERR_NOT_SUPPORTED;
+    a->c = pool_of(c);
+    a->q = rows_of(&q->q);
+    a->tables = q->tables;
+    a->tstride = q->table_stride;
+    a->lens = q->lens;
+    a->width = q->table_width;
+    a->n = q->n_seqs;
+    a->G = q->n_heads / c->n_kv_heads;
+    a->win = q->window;
+    a->scale = q->scale != 0.f ? q->scale : 1.0f / std::sqrt((float)c->head_dim);
+    *bytes = 0;
+    if (a->n == 0) return LF_OK;
+    int sms = 0;
+    st = lfr::sm_count(&sms);
+    if (st == LF_OK) *bytes = plan_attn(*a, sms);
+    return st;
+}
+
+}  // namespace
+
+extern "C" {
+
+lf_status lf_paged_plan(const lf_page_tables *t, const int32_t *n_new, const int32_t *keep, int32_t *slots,
+                        int32_t *positions, int32_t *offsets, int32_t max_tokens, void *stream)
+{
+    if (!t || t->n_seqs < 0 || t->max_pages < 1 || t->n_pages < 1 || t->page < 1 || max_tokens < 0 || t->table_stride < 0 ||
+        t->table_stride > kMaxStride || (t->n_seqs > 1 && t->table_stride < t->max_pages))
+        return LF_ERR_INVALID_ARG;
+    if (!page_ok(t->page) || t->n_seqs > MAX_ROWS || (long long)t->n_pages * t->page > INT32_MAX ||
+        (long long)t->max_pages * t->page > (1 << 30) || max_tokens > (1 << 30))
+        return LF_ERR_NOT_SUPPORTED;
+    if (!aligned4(t->n_free) || !aligned4(t->status) || !aligned4(t->free_pages) || !aligned4(offsets)) return LF_ERR_INVALID_ARG;
+    if (t->n_seqs && (!aligned4(t->tables) || !aligned4(t->lens) || !aligned4(n_new) || (keep && !aligned4(keep)))) return LF_ERR_INVALID_ARG;
+    if (max_tokens && (!aligned16(slots) || !aligned16(positions))) return LF_ERR_INVALID_ARG;
+    const Plan p = {t->tables, t->table_stride, t->lens, t->free_pages, t->n_free, t->status, t->n_seqs, t->max_pages, t->n_pages,
+                    t->page, n_new, keep, slots, positions, offsets, max_tokens};
+    return status_of(launch_plan(p, static_cast<cudaStream_t>(stream)));
+}
+
+lf_status lf_paged_append(const lf_paged *c, const lf_rows *k, const lf_rows *v, int32_t n, const int32_t *slots, void *stream)
+{
+    lf_status st = check_pool(c);
+    if (st != LF_OK) return st;
+    if (n < 0) return LF_ERR_INVALID_ARG;
+    if (n == 0) return LF_OK;
+    st = check_rows(k, n, c->n_kv_heads, c->head_dim, false);
+    if (st == LF_OK) st = check_rows(v, n, c->n_kv_heads, c->head_dim, false);
+    if (st != LF_OK) return st;
+    if (k->dtype != v->dtype || (k->dtype != LF_F32 && k->dtype != c->dtype) || !aligned4(slots)) return LF_ERR_INVALID_ARG;
+    return status_of(launch_append(pool_of(c), rows_of(k), rows_of(v), n, slots, static_cast<cudaStream_t>(stream)));
+}
+
+lf_status lf_paged_workspace(const lf_paged *c, const lf_paged_query *q, int64_t *bytes)
+{
+    if (!bytes) return LF_ERR_INVALID_ARG;
+    Attn a = {};
+    size_t need = 0;
+    const lf_status st = make_attn(c, q, &a, &need);
+    if (st == LF_OK) *bytes = (int64_t)need;
+    return st;
+}
+
+lf_status lf_paged_attend(const lf_paged *c, const lf_paged_query *q, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    Attn a = {};
+    size_t need = 0;
+    lf_status st = make_attn(c, q, &a, &need);
+    if (st != LF_OK || a.n == 0) return st;
+    st = check_rows(&q->q, a.n, q->n_heads, c->head_dim, false);
+    if (st == LF_OK) st = check_rows(&q->out, a.n, q->n_heads, c->head_dim, true);
+    if (st != LF_OK) return st;
+    if (q->q.dtype != q->out.dtype || q->q.data == q->out.data) return LF_ERR_INVALID_ARG;
+    if (!aligned4(q->lens) || (a.width && !aligned4(q->tables))) return LF_ERR_INVALID_ARG;
+    if (need && (!aligned16(workspace) || workspace_bytes < (int64_t)need)) return LF_ERR_INVALID_ARG;
+    a.o = rows_of(&q->out);
+    set_workspace(a, need ? workspace : nullptr);
+    return status_of(launch_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,656 @@
+// lf_paged_attn.cu -- attention of one new token per sequence over a paged KV
+// cache.
+//
+// For every sequence and query head: out = sum_j softmax_j(scale q . K[j]) V[j]
+// over the sequence's positions j, which lie in pages anywhere in the pools.
+// Each byte of K and V is needed once and meets 2 G products (G query heads
+// share a KV head): bound by memory, so all that counts is that loads never
+// pause.
+//
+// The unit of work is a slab: 16 positions of one KV head, a stretch of one
+// page (pages are whole slabs).  A warp works alone.  It copies its slabs into
+// a ring of its own in shared memory with asynchronous 16-byte copies, two of
+// three stages on the way at any time, forms
+//   S^T = K Q^T   (16 positions x 8 query heads, ldmatrix, warp-level products)
+//   O^T += V^T P^T (16 dims x 8 heads per step, ldmatrix transposed)
+// and carries its softmax state (reference, sum, O) in registers.  No barrier
+// joins the warps of a CTA on the way: 8 warps x 2 slabs of 8 KB are 128 KB on
+// the way per SM, twice what the memory's latency asks for.  Warp-level
+// products suit this shape (8 heads wide, 16 positions deep), and at 2 G
+// operations a byte the tensor cores wait for memory.
+//
+// Accuracy: scores, softmax and sums are FP32.  A query of the cache's type
+// enters the products as it is, one in FP32 as the sum of two FP16 terms (scaled
+// by a power of two: 22 bits) or three BF16 terms (24 bits).  P is split in the
+// same way, and in two terms where q is 16 bits wide: 16 (BF16) or 22 (FP16) bits,
+// so that the output's own rounding is the only one that counts.  The second
+// product of each step is free while memory is waited for.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "../../include/lf.h"
+#include "lf_kv4.cuh"
+#include "lf_paged.h"
+#include "lf_rows.cuh"
+
+namespace lfpg {
+
+using lfq::ex2;
+
+constexpr int NW = 8;             // warps of a CTA
+constexpr int PADF = 4;           // floats behind a partial state's O per row: m, l, and two that keep rows aligned
+
+template <class T>
+struct Half16;
+template <>
+struct Half16<__half> {
+    static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
+    static __device__ __forceinline__ float to(__half x) { return __half2float(x); }
+    static __device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], const unsigned (&b)[2])
+    {
+        lfk::mma16816(d, a[0], a[1], a[2], a[3], b[0], b[1]);
+    }
+};
+template <>
+struct Half16<__nv_bfloat16> {
+    static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
+    static __device__ __forceinline__ float to(__nv_bfloat16 x) { return __bfloat162float(x); }
+    static __device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], const unsigned (&b)[2])
+    {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+    }
+};
+template <class T>
+__device__ __forceinline__ unsigned pack(T lo, T hi)
+{
+    return (unsigned)*reinterpret_cast<unsigned short *>(&lo) | ((unsigned)*reinterpret_cast<unsigned short *>(&hi) << 16);
+}
+// x and y as sums of N terms of type T, the largest first: pairs (term of x, term of y)
+template <class T, int N>
+__device__ __forceinline__ void split_pair(float x, float y, unsigned (&out)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const T a = Half16<T>::from(x), b = Half16<T>::from(y);
+        out[i] = pack(a, b);
+        if (i + 1 < N) {
+            x -= Half16<T>::to(a);
+            y -= Half16<T>::to(b);
+        }
+    }
+}
+
+// 16 bytes global -> shared, zeros where `bytes` is 0 (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const char *src, unsigned bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const char *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Positions that a sequence's query sees, [lo, hi), and the slabs that hold them, [s0, s1).
+struct Seen {
+    int lo, hi, s0, s1;
+    __device__ __forceinline__ Seen(const Attn &a, int len)
+    {
+        hi = max(0, (int)min((long long)len, (long long)a.width * a.c.page));
+        lo = a.win > 0 && hi > a.win ? hi - a.win : 0;
+        s0 = lo >> 4;
+        s1 = (hi + 15) >> 4;
+    }
+    __device__ __forceinline__ int slabs() const { return s1 - s0; }
+};
+
+// What a warp is told about a slab in its ring.
+struct Told {
+    int row, ht, s, flags;
+    int lo, hi;
+};
+enum { BEGIN = 1, END = 2, FROM_START = 4, TO_END = 8 };   // of the warp's piece; which is (not) the sequence's begin, end
+
+template <int HD>
+struct Ring {
+    static constexpr int SLAB = 16 * HD * 2;                 // bytes of K, and of V
+    static constexpr int STAGES = 24576 / (2 * SLAB);        // 3 of 8 KB, 6 of 4
+    static constexpr int WARP = STAGES * 2 * SLAB + STAGES * 32;
+    static constexpr int BYTES = NW * WARP;
+};
+
+// A warp's softmax state and its products, for 8 NT query heads of one KV head.
+// QT: terms of q (1: it has the cache's type).
+template <int HD, int NT, class T, int QT>
+struct Work {
+    static constexpr int KS = HD / 16, PT = QT == 1 ? 2 : QT, RT = 8 * NT;
+    static constexpr float P_EXP = 7.f, P_SUM = 32768.f;
+    unsigned q[QT][NT][KS][2];
+    float f[NT][2], ref[NT][2], l[NT][2], o[NT][KS][4];
+
+    __device__ __forceinline__ void begin(const Attn &a, int row, int ht, int lane)
+    {
+        const int g = lane >> 2, t = lane & 3;
+        const int kvh = ht / a.tiles, h0 = (ht - kvh * a.tiles) * RT;
+        const float base = a.scale * 1.4426950408889634f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int hh = h0 + 8 * i + g;
+            const bool live = hh < a.G;
+            const size_t at = (size_t)row * a.q.ts + (size_t)(kvh * a.G + hh) * a.q.hs + 2 * t;
+            if (QT == 1) {
+                const T *src = static_cast<const T *>(a.q.p) + at;
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        q[0][i][k][u] = live ? lfq::ld(reinterpret_cast<const unsigned *>(src + 16 * k + 8 * u)) : 0u;
+                f[i][0] = f[i][1] = base;
+            } else {
+                const float *src = static_cast<const float *>(a.q.p) + at;
+                float2 x[KS][2];
+                float top = 0.f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        x[k][u] = live ? lfq::ld(reinterpret_cast<const float2 *>(src + 16 * k + 8 * u)) : make_float2(0.f, 0.f);
+                        top = fmaxf(top, fmaxf(fabsf(x[k][u].x), fabsf(x[k][u].y)));
+                    }
+                // a power of two brings the row to [1, 2): the terms' remainders stay in FP16's range, and BF16's
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float r = lfq::range_factor(top);
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        unsigned w[QT];
+                        split_pair<T, QT>(x[k][u].x * r, x[k][u].y * r, w);
+#pragma unroll
+                        for (int n = 0; n < QT; ++n) q[n][i][k][u] = w[n];
+                    }
+                f[i][0] = base / __shfl_sync(0xffffffffu, r, 8 * t);       // rows 2t and 2t + 1 of the tile
+                f[i][1] = base / __shfl_sync(0xffffffffu, r, 8 * t + 4);
+            }
+            ref[i][0] = ref[i][1] = -INFINITY;
+            l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) o[i][k][0] = o[i][k][1] = o[i][k][2] = o[i][k][3] = 0.f;
+        }
+    }
+
+    // One slab from position p on, of which [lo, hi) counts; ks, vs: its rows in shared memory, 16-byte groups XOR-ed
+    // with the position mod 8 (so that the 8 rows of a fragment lie in different banks).
+    __device__ __forceinline__ void slab(uint32_t ks, uint32_t vs, int p, int lo, int hi, int lane)
+    {
+        const int g = lane >> 2;
+        // ---- scores: position rows g, g + 8 by heads 2t, 2t + 1
+        float st[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) st[i][0] = st[i][1] = st[i][2] = st[i][3] = 0.f;
+        const uint32_t ka = ks + (lane & 15) * (HD * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            unsigned x[4];
+            lfk::ldsm_x4(x, ka ^ (k << 5));
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int n = 0; n < QT; ++n) Half16<T>::mma(st[i], x, q[n][i][k]);
+        }
+        // ---- P relative to the reference, and the lanes' sums.  No maximum is formed where a lane's P sum to no more
+        // than FP16 can hold; otherwise, and at the first position, the reference is put 2^P_EXP below the largest.
+        const bool whole = p >= lo && p + 16 <= hi;
+        const bool in0 = whole || (p + g >= lo && p + g < hi), in1 = whole || (p + g + 8 >= lo && p + g + 8 < hi);
+        float pr[NT][4], sum[NT][2];
+        auto probs = [&] {
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float neg = ref[i][e] == -INFINITY ? 0.f : -ref[i][e];
+                    const float x = ex2(fmaf(st[i][e], f[i][e], neg)), y = ex2(fmaf(st[i][2 + e], f[i][e], neg));
+                    pr[i][e] = in0 ? x : 0.f;
+                    pr[i][2 + e] = in1 ? y : 0.f;
+                    sum[i][e] = pr[i][e] + pr[i][2 + e];
+                    bad = bad || !(sum[i][e] <= P_SUM) || ref[i][e] == -INFINITY;
+                }
+            return bad;
+        };
+        if (__any_sync(0xffffffffu, probs())) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(in0 ? st[i][e] * f[i][e] : -INFINITY, in1 ? st[i][2 + e] * f[i][e] : -INFINITY);
+#pragma unroll
+                    for (int sh = 4; sh <= 16; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                    float &r = ref[i][e];
+                    if (mx > r && (r == -INFINITY || mx - r > P_EXP + 1.f)) {
+                        float n = mx - P_EXP;
+                        if (!(mx - n <= 15.f)) n = mx;     // scores so large that their steps are
+                        const float alpha = ex2(r - n);    // 0 from -inf
+                        l[i][e] *= alpha;
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            o[i][k][e] *= alpha;
+                            o[i][k][2 + e] *= alpha;
+                        }
+                        r = n;
+                    }
+                }
+            probs();
+        }
+        // ---- O^T += V^T P^T
+        unsigned pb[PT][NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            l[i][0] += sum[i][0];
+            l[i][1] += sum[i][1];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                unsigned w[PT];
+                split_pair<T, PT>(pr[i][2 * u], pr[i][2 * u + 1], w);
+#pragma unroll
+                for (int n = 0; n < PT; ++n) pb[n][i][u] = lfk::movm_t(w[n]);
+            }
+        }
+        const uint32_t va = vs + ((lane & 7) + (lane >> 4) * 8) * (HD * 2) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            unsigned x[4];
+            lfk::ldsm_x4_t(x, va ^ (k << 5));
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int n = 0; n < PT; ++n) Half16<T>::mma(o[i][k], x, pb[n][i]);
+        }
+    }
+
+    // The sums of all positions (each lane holds those of its rows).
+    __device__ __forceinline__ void sums()
+    {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int sh = 4; sh <= 16; sh <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], sh);
+    }
+    // The state as it lies in the lanes: O as [NT][KS][lane] x 4, then (reference, sum) of each head.
+    __device__ __forceinline__ void store_state(float *dst, int lane) const
+    {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+                *reinterpret_cast<float4 *>(dst + ((i * KS + k) * 32 + lane) * 4) =
+                    make_float4(o[i][k][0], o[i][k][1], o[i][k][2], o[i][k][3]);
+        if (lane < 4) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                *reinterpret_cast<float4 *>(dst + RT * HD + (8 * i + 2 * lane) * 2) =
+                    make_float4(ref[i][0], l[i][0], ref[i][1], l[i][1]);
+        }
+    }
+};
+
+// Two heads' outputs of dims 16 k + g and + 8, normalised: v = O of (head 0, head 1) at both dims.
+template <int HD, int NT, class O>
+__device__ __forceinline__ void store_out(const Attn &a, int row, int ht, int i, int k, int lane, float4 v, float l0, float l1)
+{
+    const int g = lane >> 2, t = lane & 3;
+    const int kvh = ht / a.tiles, hh = (ht - kvh * a.tiles) * 8 * NT + 8 * i + 2 * t;
+    const float r0 = l0 > 0.f ? 1.0f / l0 : (l0 == 0.f ? 0.f : l0), r1 = l1 > 0.f ? 1.0f / l1 : (l1 == 0.f ? 0.f : l1);
+    O *dst = static_cast<O *>(a.o.p) + (size_t)row * a.o.ts + (size_t)(kvh * a.G + hh) * a.o.hs + 16 * k + g;
+    auto put = [](O *p, float x) {
+        if constexpr (sizeof(O) == 4) *p = x;
+        else *p = Half16<O>::from(x);
+    };
+    if (hh < a.G) {
+        put(dst, v.x * r0);
+        put(dst + 8, v.z * r0);
+    }
+    if (hh + 1 < a.G) {
+        put(dst + a.o.hs, v.y * r1);
+        put(dst + a.o.hs + 8, v.w * r1);
+    }
+}
+
+// States of the same heads added up, relative to the largest reference so far; a thread holds two heads at two dims.
+struct Joined {
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    // ml: reference and sum of head 0, then of head 1
+    __device__ __forceinline__ void add(float4 ml, float4 x)
+    {
+        const float n0 = fmaxf(m0, ml.x), n1 = fmaxf(m1, ml.z);
+        const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
+        const float a0 = ex2(m0 - z0), b0 = ex2(ml.x - z0), a1 = ex2(m1 - z1), b1 = ex2(ml.z - z1);
+        m0 = n0;
+        m1 = n1;
+        l0 = fmaf(ml.y, b0, l0 * a0);
+        l1 = fmaf(ml.w, b1, l1 * a1);
+        v.x = fmaf(x.x, b0, v.x * a0);
+        v.z = fmaf(x.z, b0, v.z * a0);
+        v.y = fmaf(x.y, b1, v.y * a1);
+        v.w = fmaf(x.w, b1, v.w * a1);
+    }
+    __device__ __forceinline__ float4 ml() const { return make_float4(m0, l0, m1, l1); }
+};
+
+// The ring of one warp: where its slabs come from and what it is told of them.
+template <int HD>
+struct Feed {
+    using R = Ring<HD>;
+    uint32_t base;
+    Told *told;
+    long long place;   // this lane's entry of the next 32 slabs: byte offset in the pools, -1 for none
+    int lane;
+
+    // Looks the places of slabs s, s + step, .. (below end) up, one per lane.
+    __device__ __forceinline__ void look_up(const Attn &a, int row, int kvh, int s, int step, int end)
+    {
+        const int pp = a.c.page >> 4, mine = s + lane * step;
+        place = -1;
+        if (mine >= end) return;
+        const int col = mine / pp;
+        const int id = lfq::ld(a.tables + (size_t)row * a.tstride + col);
+        if ((unsigned)id < (unsigned)a.c.n_pages)
+            place = id * a.c.page_b + kvh * a.c.head_b + (long long)((mine - col * pp) * 16) * a.c.pos_b;
+    }
+    // Begins the copies of slab s, the j-th that was looked up, into stage `st`.
+    __device__ __forceinline__ void fetch(const Attn &a, int st, int j, const Told &w)
+    {
+        constexpr int CPR = HD / 8, RPI = 32 / CPR, N = 16 / RPI;   // 16-byte groups a row, rows per instruction
+        const long long at = __shfl_sync(0xffffffffu, place, j);
+        const uint32_t dst = base + st * 2 * R::SLAB;
+        const int r0 = lane / CPR, c = lane % CPR, p = w.s * 16;
+        const bool none = at < 0, whole = !none && p >= w.lo && p + 16 <= w.hi;
+        const char *k = a.c.k + (none ? 0 : at) + r0 * a.c.pos_b + c * 16, *v = k + (a.c.v - a.c.k);
+        const long long step = RPI * a.c.pos_b;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < N; ++i, k += step) {
+                const int r = i * RPI + r0;
+                copy16(dst + r * (HD * 2) + ((c ^ (r & 7)) << 4), k);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i, v += step) {
+                const int r = i * RPI + r0;
+                copy16(dst + R::SLAB + r * (HD * 2) + ((c ^ (r & 7)) << 4), v);
+            }
+        } else {
+            // rows that do not count become zeros (what they hold may be anything, and 0 x inf is not 0)
+            for (int i = 0; i < N; ++i, k += step, v += step) {
+                const int r = i * RPI + r0;
+                const bool in = !none && p + r >= w.lo && p + r < w.hi;
+                const uint32_t d = dst + r * (HD * 2) + ((c ^ (r & 7)) << 4);
+                copy16(d, in ? k : a.c.k, in ? 16u : 0u);
+                copy16(d + R::SLAB, in ? v : a.c.v, in ? 16u : 0u);
+            }
+        }
+        if (lane == 0) {
+            Told x = w;
+            if (none) x.hi = x.lo = 0;
+            told[st] = x;
+        }
+    }
+};
+
+// ---------------------------------------------------------------- all warps share all slabs
+
+// Warp w of W takes slabs [U w / W, U (w + 1) / W) of the U in all: the same bytes for each, however the lengths are
+// spread.  Its pieces that are a whole sequence's go out at once; at most two are not, and are left for the join.
+// W is known on the device alone: all warps of the launch, but each takes MIN_SHARE slabs at least.
+constexpr int MIN_SHARE = 2;
+__device__ __forceinline__ long long sharers(long long units, int warps)
+{
+    return min((long long)warps, (units + MIN_SHARE - 1) / MIN_SHARE);
+}
+__device__ __forceinline__ long long share_of(long long units, long long w, long long sharers) { return units * w / sharers; }
+
+template <int HD, int NT, class T, int QT>
+__global__ void __launch_bounds__(NW * 32, 1) attn_shared(const __grid_constant__ Attn a)
+{
+    using W = Work<HD, NT, T, QT>;
+    using R = Ring<HD>;
+    using O = std::conditional_t<QT == 1, T, float>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    lfq::dependents_may_launch();
+    lfq::wait_for_prerequisites();
+
+    // ---- slabs before each stretch of rows (one stretch a thread), in the ring's memory
+    long long *sums = reinterpret_cast<long long *>(smem);       // [256 + 1]
+    long long *wsum = sums + 257;                                // [NW]
+    const int per = (a.n + 255) / 256;
+    const int r0 = min(threadIdx.x * per, a.n), r1 = min(r0 + per, a.n);
+    long long mine = 0;
+    for (int r = r0; r < r1; ++r) mine += Seen(a, lfq::ld(a.lens + r)).slabs();
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += x;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += wsum[w];
+    sums[threadIdx.x + 1] = incl;
+    if (threadIdx.x == 0) sums[0] = 0;
+    if (blockIdx.x == 0) {       // for the join
+        long long at = incl - mine;
+        for (int r = r0; r < r1; ++r) {
+            a.first[r] = at;
+            at += Seen(a, lfq::ld(a.lens + r)).slabs();
+        }
+        if (threadIdx.x == 255) a.first[a.n] = incl;
+    }
+    __syncthreads();
+    const long long units = sums[256] * a.ht;
+    const int w = blockIdx.x * NW + warp;
+    long long u = 0, left = 0;
+    int row = 0, end_row = 0;
+    const long long all = sharers(units, a.warps);
+    if (w < all) {
+        u = share_of(units, w, all);
+        left = share_of(units, w + 1, all) - u;
+        // the stretch that holds unit u: the last whose first slab is not behind it
+        int lo = 0, hi = 255;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sums[mid] * a.ht <= u) lo = mid;
+            else hi = mid - 1;
+        }
+        row = lo * per;
+        end_row = a.n;
+        u -= sums[lo] * a.ht;
+    }
+    __syncthreads();             // the ring takes the memory
+    if (left == 0) return;
+
+    Feed<HD> feed;
+    feed.lane = lane;
+    feed.base = lfk::smem_u32(smem) + warp * (R::STAGES * 2 * R::SLAB);
+    feed.told = reinterpret_cast<Told *>(smem + NW * R::STAGES * 2 * R::SLAB) + warp * R::STAGES;
+    // rows from `row` on, 32 at a time: their lengths lie in the lanes
+    int rbase = row, len = rbase + lane < end_row ? lfq::ld(a.lens + rbase + lane) : 0;
+    auto seen_of = [&](int r) {
+        if (r - rbase >= 32) {
+            rbase = r;
+            len = r + lane < end_row ? lfq::ld(a.lens + r + lane) : 0;
+        }
+        return Seen(a, __shfl_sync(0xffffffffu, len, r - rbase));
+    };
+    Seen seen = seen_of(row);
+    while (u >= (long long)seen.slabs() * a.ht) {   // the row of the first slab
+        u -= (long long)seen.slabs() * a.ht;
+        seen = seen_of(++row);
+    }
+    int ht = (int)(u / seen.slabs()), s = seen.s0 + (int)(u - (long long)ht * seen.slabs()), ebase = s;
+    feed.look_up(a, row, ht / a.tiles, s, 1, seen.s1);
+    bool begin = true;
+    // the next slab of the share into stage st
+    auto issue = [&](int st) {
+        if (left > 0) {
+            if (s == seen.s1) {
+                if (++ht == a.ht) {
+                    ht = 0;
+                    do seen = seen_of(++row);
+                    while (seen.slabs() == 0);
+                }
+                s = seen.s0;
+                begin = true;
+                ebase = s;
+                feed.look_up(a, row, ht / a.tiles, s, 1, seen.s1);
+            } else if (s - ebase == 32) {
+                ebase = s;
+                feed.look_up(a, row, ht / a.tiles, s, 1, seen.s1);
+            }
+            --left;
+            const bool last = s + 1 == seen.s1, end = last || left == 0;
+            Told x = {row, ht, s, (begin ? BEGIN : 0) | (end ? END : 0) | (s == seen.s0 ? FROM_START : 0) | (last ? TO_END : 0),
+                      seen.lo, seen.hi};
+            feed.fetch(a, st, s - ebase, x);
+            begin = false;
+            ++s;
+        }
+        copies_commit();
+    };
+    long long todo = left;
+#pragma unroll 1
+    for (int i = 0; i < R::STAGES - 1; ++i) issue(i);
+    W work;
+    int st = 0;
+    bool from_start = false;
+#pragma unroll 1
+    for (; todo > 0; --todo) {
+        copies_wait<R::STAGES - 2>();
+        __syncwarp();
+        issue(st == 0 ? R::STAGES - 1 : st - 1);
+        const Told x = feed.told[st];
+        if (x.flags & BEGIN) {
+            work.begin(a, x.row, x.ht, lane);
+            from_start = x.flags & FROM_START;
+        }
+        const uint32_t ks = feed.base + st * 2 * R::SLAB;
+        work.slab(ks, ks + R::SLAB, x.s * 16, x.lo, x.hi, lane);
+        if (x.flags & END) {
+            work.sums();
+            if (from_start && (x.flags & TO_END)) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int k = 0; k < W::KS; ++k)
+                        store_out<HD, NT, O>(a, x.row, x.ht, i, k, lane,
+                                             make_float4(work.o[i][k][0], work.o[i][k][1], work.o[i][k][2], work.o[i][k][3]),
+                                             work.l[i][0], work.l[i][1]);
+            } else {
+                // a piece that goes on behind this warp's share lies second, one that came from before it first
+                work.store_state(a.part + ((size_t)w * 2 + (from_start ? 1 : 0)) * W::RT * (HD + PADF), lane);
+            }
+        }
+        st = st + 1 == R::STAGES ? 0 : st + 1;
+    }
+}
+
+// Joins the pieces of one sequence and tile; groups of NT * HD * 2 threads take every groups-th piece.
+template <int HD, int NT, class O>
+__global__ void __launch_bounds__(1024) attn_shared_join(const __grid_constant__ Attn a)
+{
+    constexpr int KS = HD / 16, F = NT * KS * 32, RT = 8 * NT;
+    __shared__ float4 sh[2][1024];
+    lfq::dependents_may_launch();
+    lfq::wait_for_prerequisites();
+    const int row = blockIdx.x / a.ht, ht = blockIdx.x % a.ht;
+    const long long first = lfq::ld(a.first + row), slabs = lfq::ld(a.first + row + 1) - first;
+    const long long units = lfq::ld(a.first + a.n) * a.ht;
+    const int f = threadIdx.x % F, grp = threadIdx.x / F, groups = blockDim.x / F;
+    const int i = f / (KS * 32), k = f / 32 % KS, lane = f % 32;
+    Joined j;
+    if (slabs > 0) {
+        // warp of unit x: the last whose share begins at or before it
+        const long long u0 = first * a.ht + slabs * ht, u1 = u0 + slabs - 1;
+        const long long all = sharers(units, a.warps);
+        const long long w0 = ((u0 + 1) * all - 1) / units, w1 = ((u1 + 1) * all - 1) / units;
+        if (w0 == w1) return;                                  // in one piece: it has its output
+#pragma unroll 4
+        for (long long w = w0 + grp; w <= w1; w += groups) {
+            const float *p = a.part + ((size_t)w * 2 + (w == w0 ? 1 : 0)) * RT * (HD + PADF);
+            j.add(lfq::ld(reinterpret_cast<const float4 *>(p + RT * HD + (8 * i + 2 * (lane & 3)) * 2)),
+                  lfq::ld(reinterpret_cast<const float4 *>(p + f * 4)));
+        }
+        if (groups > 1) {
+            sh[0][threadIdx.x] = j.ml();
+            sh[1][threadIdx.x] = j.v;
+            __syncthreads();
+            if (grp) return;
+            for (int x = 1; x < groups; ++x) j.add(sh[0][x * F + f], sh[1][x * F + f]);
+        }
+    } else if (grp) {
+        return;
+    }
+    store_out<HD, NT, O>(a, row, ht, i, k, lane, j.v, j.l0, j.l1);
+}
+
+// ---------------------------------------------------------------- launches
+
+template <int HD, int NT, class T, int QT>
+static cudaError_t run(const Attn &a, cudaStream_t s)
+{
+    using O = std::conditional_t<QT == 1, T, float>;
+    constexpr int smem = Ring<HD>::BYTES;
+    static bool ready[64] = {};
+    cudaError_t e = lfr::allow_smem(attn_shared<HD, NT, T, QT>, smem, ready);
+    if (e == cudaSuccess)
+        e = lfr::launch(attn_shared<HD, NT, T, QT>, dim3((unsigned)((a.warps + NW - 1) / NW)), NW * 32, smem, 1, s, a);
+    if (e != cudaSuccess) return e;
+    // few blocks: the pieces of a row are spread over a whole one; many: the rows have few pieces each
+    const long long blocks = (long long)a.n * a.ht;
+    constexpr int F = NT * (HD / 16) * 32;
+    return lfr::launch(attn_shared_join<HD, NT, O>, dim3((unsigned)blocks), blocks < 512 ? 1024 : F, 0, 1, s, a);
+}
+
+template <class T, int QT>
+static cudaError_t run(const Attn &a, cudaStream_t s)
+{
+    if (a.c.hd == 128) return a.rt == 8 ? run<128, 1, T, QT>(a, s) : run<128, 2, T, QT>(a, s);
+    return a.rt == 8 ? run<64, 1, T, QT>(a, s) : run<64, 2, T, QT>(a, s);
+}
+
+size_t plan_attn(Attn &a, int sms)
+{
+    a.rt = a.G <= 8 ? 8 : 16;
+    a.tiles = (a.G + a.rt - 1) / a.rt;
+    a.ht = a.c.Hkv * a.tiles;
+    a.cl = 0;
+    const long long most = (long long)a.n * a.ht * (((long long)a.width * a.c.page + 15) / 16);
+    a.warps = (int)std::min<long long>((long long)sms * NW, std::max(1ll, most));
+    return (size_t)a.warps * 2 * a.rt * (a.c.hd + PADF) * sizeof(float) + ((size_t)a.n + 1) * sizeof(long long);
+}
+
+void set_workspace(Attn &a, void *ws)
+{
+    a.part = static_cast<float *>(ws);
+    a.first = reinterpret_cast<long long *>(a.part + (size_t)a.warps * 2 * a.rt * (a.c.hd + PADF));
+}
+
+cudaError_t launch_attn(const Attn &a, cudaStream_t s)
+{
+    if (a.c.bf16) return a.q.dtype == LF_F32 ? run<__nv_bfloat16, 3>(a, s) : run<__nv_bfloat16, 1>(a, s);
+    return a.q.dtype == LF_F32 ? run<__half, 2>(a, s) : run<__half, 1>(a, s);
+}
+
+}  // namespace lfpg

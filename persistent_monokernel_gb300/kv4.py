@@ -51,14 +51,36 @@ def _load():
     if _lft.made_for != have:
         raise ImportError(f"_lft.so was built for torch {_lft.made_for[0]} and Python {_lft.made_for[1]:#x}, not for "
                           f"{have[0]} and {have[1]:#x}: {_BUILD}")
-    _lft.bind(*(C.cast(getattr(_lib, "lf_kv4_" + f), C.c_void_p).value for f in ("append", "read", "attend", "workspace")),
-              _fail)
+    names = ("kv4_append", "kv4_read", "kv4_attend", "kv4_workspace", "paged_plan", "paged_append", "paged_attend",
+             "paged_workspace")
+    _lft.bind(*(C.cast(getattr(_lib, "lf_" + f), C.c_void_p).value for f in names), _fail)
     _calls = _lft
     _codes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
     _torch = torch
 
 
-class KV4Cache:
+class OnStream:
+    """Tensors of one device (_parts, device), and calls that may be queued on any of its streams."""
+    _what = "cache"
+
+    def _elsewhere(self, call, stream, args):
+        """The call again with this device, and the stream if one is passed, current: what it allocates belongs to that
+        stream.  What the call reads and writes is marked as in use there, so that memory that the caller lets go of
+        before the stream is done is not given to another."""
+        if stream is None:
+            with _torch.cuda.device(self.device):
+                return call(*args)
+        if stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the {self._what} on {self.device}")
+        with _torch.cuda.stream(stream):
+            got = call(*args)
+        if not isinstance(stream, _torch.cuda.ExternalStream):   # (which may be gone when the memory is let go of)
+            for t in (*self._parts, *_tensors(args)):
+                t.record_stream(stream)
+        return got
+
+
+class KV4Cache(OnStream):
     """K and V of one layer for positions 0 .. max_seq - 1, `n_kv_heads` heads of `head_dim` (64 or 128) values.
 
     Tensors passed to the calls are CUDA tensors [n, heads, head_dim] on the cache's device with a contiguous last
@@ -111,22 +133,6 @@ class KV4Cache:
     @property
     def nbytes(self) -> int:
         return sum(t.numel() for t in self._parts)
-
-    def _elsewhere(self, call, stream, args):
-        """The call again with the cache's device, and the stream if one is passed, current: what it allocates belongs
-        to that stream.  What the call reads and writes is marked as in use there, so that memory that the caller lets
-        go of before the stream is done is not given to another."""
-        if stream is None:
-            with _torch.cuda.device(self.device):
-                return call(*args)
-        if stream.device != self.device:
-            raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
-        with _torch.cuda.stream(stream):
-            got = call(*args)
-        if not isinstance(stream, _torch.cuda.ExternalStream):   # (which may be gone when the memory is let go of)
-            for t in (*self._parts, *_tensors(args)):
-                t.record_stream(stream)
-        return got
 
     def append(self, k, v, pos: int, stream=None) -> None:
         """Quantise k, v [n, n_kv_heads, head_dim] into positions pos .. pos + n - 1."""
