@@ -271,18 +271,19 @@ def run(state):
     c = state["case"]
     kind = c["kind"]
     if own:
-        import persistent_monokernel_gb300 as pm
-        if "handles" not in state:   # what a program keeps: the batch's tables and the layer's cache, over its tensors
-            state["handles"] = (None if kind in ("append", "attend") else pm.PageTables.wrap(*(state[k] for k in ("tables", "lens", "free", "n_free")), c["page"]),
-                                None if kind == "plan" else pm.PagedKVCache.wrap(state["k"], state["v"]))
-        tables, cache = state["handles"]
+        if "handles" not in state:   # what a program keeps: the batch's tables and the layer's cache, over its tensors, and its bound of a step's tokens
+            import persistent_monokernel_gb300 as pm
+            plans = kind in ("plan", "step")
+            state["handles"] = (pm.PageTables.wrap(*(state[k] for k in ("tables", "lens", "free", "n_free")), c["page"]) if plans else None,
+                                None if kind == "plan" else pm.PagedKVCache.wrap(state["k"], state["v"]), _tokens(c) if plans else 0)
+        tables, cache, most = state["handles"]
         if kind == "append":
             k, v = _heads(state)
             cache.append(k, v, state["slots"])
             return state["k"], state["v"]
         if kind == "attend":
             return cache.attend(_heads(state)[0], state["tables"], state["lens"], window=c["window"])
-        plan = tables.plan(state["n_new"], _tokens(c), keep=state["keep"])
+        plan = tables.plan(state["n_new"], most, keep=state["keep"])
         if kind == "plan":
             return (*plan, state["tables"], state["lens"], state["free"], state["n_free"])
         q, k, v = _heads(state)
