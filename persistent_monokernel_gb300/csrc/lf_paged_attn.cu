@@ -124,8 +124,8 @@ template <int HD>
 struct Ring {
     static constexpr int SLAB = 16 * HD * 2;                 // bytes of K, and of V
     static constexpr int STAGES = 24576 / (2 * SLAB);        // 3 of 8 KB, 6 of 4
-    static constexpr int WARP = STAGES * 2 * SLAB + STAGES * 32;
-    static constexpr int BYTES = NW * WARP;
+    static constexpr int COPIES = STAGES * 2 * SLAB;         // bytes of a warp's slabs
+    static constexpr int bytes(int warps) { return warps * (COPIES + STAGES * (int)sizeof(Told)); }
 };
 
 // A warp's softmax state and its products, for 8 NT query heads of one KV head.
@@ -190,14 +190,20 @@ struct Work {
     }
 
     // One slab from position p on, of which [lo, hi) counts; ks, vs: its rows in shared memory, 16-byte groups XOR-ed
-    // with the position mod 8 (so that the 8 rows of a fragment lie in different banks).
-    __device__ __forceinline__ void slab(uint32_t ks, uint32_t vs, int p, int lo, int hi, int lane)
+    // with the position mod 8 (so that the 8 rows of a fragment lie in different banks).  `meanwhile` runs while the
+    // scores' products are on their way.
+    template <class M>
+    __device__ __forceinline__ void slab(uint32_t ks, uint32_t vs, int p, int lo, int hi, int lane, M meanwhile)
     {
         const int g = lane >> 2;
-        // ---- scores: position rows g, g + 8 by heads 2t, 2t + 1
-        float st[NT][4];
+        // ---- scores: position rows g, g + 8 by heads 2t, 2t + 1.  Each product waits for the one before it into the
+        // same sum: CH sums, by the terms of q or the dims' halves, are on their way at a time.
+        constexpr int CH = QT == 1 ? 2 : QT;
+        float st[NT][4], sc[CH][NT][4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) st[i][0] = st[i][1] = st[i][2] = st[i][3] = 0.f;
+        for (int n = 0; n < CH; ++n)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) sc[n][i][0] = sc[n][i][1] = sc[n][i][2] = sc[n][i][3] = 0.f;
         const uint32_t ka = ks + (lane & 15) * (HD * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
@@ -206,8 +212,17 @@ struct Work {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int n = 0; n < QT; ++n) Half16<T>::mma(st[i], x, q[n][i][k]);
+                for (int n = 0; n < QT; ++n) Half16<T>::mma(sc[QT == 1 ? k & 1 : n][i], x, q[n][i][k]);
         }
+        meanwhile();
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                st[i][e] = sc[CH - 1][i][e];                // the smallest terms first
+#pragma unroll
+                for (int n = CH - 2; n >= 0; --n) st[i][e] += sc[n][i][e];
+            }
         // ---- P relative to the reference, and the lanes' sums.  No maximum is formed where a lane's P sum to no more
         // than FP16 can hold; otherwise, and at the first position, the reference is put 2^P_EXP below the largest.
         const bool whole = p >= lo && p + 16 <= hi;
@@ -411,15 +426,15 @@ struct Feed {
 
 // ---------------------------------------------------------------- all warps share all slabs
 
-// Warp w of W takes slabs [U w / W, U (w + 1) / W) of the U in all: the same bytes for each, however the lengths are
-// spread.  Its pieces that are a whole sequence's go out at once; at most two are not, and are left for the join.
-// W is known on the device alone: all warps of the launch, but each takes MIN_SHARE slabs at least.
+// Warp w takes slabs [C w, C (w + 1)) of all: the same bytes for each, however the lengths are spread.  Its pieces that
+// are a whole sequence's go out at once; at most two are not, and are left for the join.  C is known on the device
+// alone: what all warps of the launch need to take, MIN_SHARE at least.
 constexpr int MIN_SHARE = 2;
-__device__ __forceinline__ long long sharers(long long units, int warps)
+__device__ __forceinline__ long long quotient(long long x, long long y)   // of numbers that are not negative
 {
-    return min((long long)warps, (units + MIN_SHARE - 1) / MIN_SHARE);
+    return ((x | y) >> 32) ? x / y : (long long)((unsigned)x / (unsigned)y);   // (64-bit division is ten times as long)
 }
-__device__ __forceinline__ long long share_of(long long units, long long w, long long sharers) { return units * w / sharers; }
+__device__ __forceinline__ long long share(long long units, int warps) { return max((long long)MIN_SHARE, quotient(units + warps - 1, warps)); }
 
 template <int HD, int NT, class T, int QT>
 __global__ void __launch_bounds__(NW * 32, 1) attn_shared(const __grid_constant__ Attn a)
@@ -463,10 +478,10 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_shared(const __grid_constant_
     const int w = blockIdx.x * NW + warp;
     long long u = 0, left = 0;
     int row = 0, end_row = 0;
-    const long long all = sharers(units, a.warps);
-    if (w < all) {
-        u = share_of(units, w, all);
-        left = share_of(units, w + 1, all) - u;
+    const long long each = share(units, a.warps);
+    if (w < a.warps && w * each < units) {
+        u = w * each;
+        left = min(each, units - u);
         // the stretch that holds unit u: the last whose first slab is not behind it
         int lo = 0, hi = 255;
         while (lo < hi) {
@@ -483,8 +498,8 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_shared(const __grid_constant_
 
     Feed<HD> feed;
     feed.lane = lane;
-    feed.base = lfk::smem_u32(smem) + warp * (R::STAGES * 2 * R::SLAB);
-    feed.told = reinterpret_cast<Told *>(smem + NW * R::STAGES * 2 * R::SLAB) + warp * R::STAGES;
+    feed.base = lfk::smem_u32(smem) + warp * R::COPIES;
+    feed.told = reinterpret_cast<Told *>(smem + NW * R::COPIES) + warp * R::STAGES;
     // rows from `row` on, 32 at a time: their lengths lie in the lanes
     int rbase = row, len = rbase + lane < end_row ? lfq::ld(a.lens + rbase + lane) : 0;
     auto seen_of = [&](int r) {
@@ -499,7 +514,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_shared(const __grid_constant_
         u -= (long long)seen.slabs() * a.ht;
         seen = seen_of(++row);
     }
-    int ht = (int)(u / seen.slabs()), s = seen.s0 + (int)(u - (long long)ht * seen.slabs()), ebase = s;
+    int ht = (int)quotient(u, seen.slabs()), s = seen.s0 + (int)(u - (long long)ht * seen.slabs()), ebase = s;
     feed.look_up(a, row, ht / a.tiles, s, 1, seen.s1);
     bool begin = true;
     // the next slab of the share into stage st
@@ -539,14 +554,13 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_shared(const __grid_constant_
     for (; todo > 0; --todo) {
         copies_wait<R::STAGES - 2>();
         __syncwarp();
-        issue(st == 0 ? R::STAGES - 1 : st - 1);
         const Told x = feed.told[st];
         if (x.flags & BEGIN) {
             work.begin(a, x.row, x.ht, lane);
             from_start = x.flags & FROM_START;
         }
         const uint32_t ks = feed.base + st * 2 * R::SLAB;
-        work.slab(ks, ks + R::SLAB, x.s * 16, x.lo, x.hi, lane);
+        work.slab(ks, ks + R::SLAB, x.s * 16, x.lo, x.hi, lane, [&] { issue(st == 0 ? R::STAGES - 1 : st - 1); });
         if (x.flags & END) {
             work.sums();
             if (from_start && (x.flags & TO_END)) {
@@ -566,43 +580,145 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_shared(const __grid_constant_
     }
 }
 
-// Joins the pieces of one sequence and tile; groups of NT * HD * 2 threads take every groups-th piece.
+// Joins the pieces of the sequences and tiles that were cut.  A block takes 256 / groups of the 16-byte places of a
+// state's O (dims and heads), `groups` threads each: thread `grp` adds every groups-th piece.  It fits beside a CTA of
+// the first launch, so that it is there when that ends.
+constexpr int JOIN_THREADS = 256;
 template <int HD, int NT, class O>
-__global__ void __launch_bounds__(1024) attn_shared_join(const __grid_constant__ Attn a)
+__global__ void __launch_bounds__(JOIN_THREADS) attn_shared_join(const __grid_constant__ Attn a, int groups)
 {
     constexpr int KS = HD / 16, F = NT * KS * 32, RT = 8 * NT;
-    __shared__ float4 sh[2][1024];
+    __shared__ float4 sh[2][JOIN_THREADS];
     lfq::dependents_may_launch();
     lfq::wait_for_prerequisites();
-    const int row = blockIdx.x / a.ht, ht = blockIdx.x % a.ht;
+    const int per = JOIN_THREADS / groups, blocks = F / per;    // places a block; blocks a tile
+    const int item = blockIdx.x / blocks, row = item / a.ht, ht = item - row * a.ht;
+    const int f = (blockIdx.x - item * blocks) * per + threadIdx.x % per, grp = threadIdx.x / per;
     const long long first = lfq::ld(a.first + row), slabs = lfq::ld(a.first + row + 1) - first;
     const long long units = lfq::ld(a.first + a.n) * a.ht;
-    const int f = threadIdx.x % F, grp = threadIdx.x / F, groups = blockDim.x / F;
     const int i = f / (KS * 32), k = f / 32 % KS, lane = f % 32;
     Joined j;
     if (slabs > 0) {
-        // warp of unit x: the last whose share begins at or before it
-        const long long u0 = first * a.ht + slabs * ht, u1 = u0 + slabs - 1;
-        const long long all = sharers(units, a.warps);
-        const long long w0 = ((u0 + 1) * all - 1) / units, w1 = ((u1 + 1) * all - 1) / units;
+        const long long u0 = first * a.ht + slabs * ht, each = share(units, a.warps);
+        const int w0 = (int)quotient(u0, each), w1 = (int)quotient(u0 + slabs - 1, each);
         if (w0 == w1) return;                                  // in one piece: it has its output
-#pragma unroll 4
-        for (long long w = w0 + grp; w <= w1; w += groups) {
-            const float *p = a.part + ((size_t)w * 2 + (w == w0 ? 1 : 0)) * RT * (HD + PADF);
-            j.add(lfq::ld(reinterpret_cast<const float4 *>(p + RT * HD + (8 * i + 2 * (lane & 3)) * 2)),
-                  lfq::ld(reinterpret_cast<const float4 *>(p + f * 4)));
+        constexpr int AHEAD = 8;                               // loads of pieces on the way at a time
+        for (int w = w0 + grp; w <= w1; w += AHEAD * groups) {
+            float4 ml[AHEAD], v[AHEAD];
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) {
+                const int y = w + x * groups;
+                if (y > w1) continue;
+                const float *p = a.part + ((size_t)y * 2 + (y == w0 ? 1 : 0)) * RT * (HD + PADF);
+                ml[x] = lfq::ld(reinterpret_cast<const float4 *>(p + RT * HD + (8 * i + 2 * (lane & 3)) * 2));
+                v[x] = lfq::ld(reinterpret_cast<const float4 *>(p + f * 4));
+            }
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x)
+                if (w + x * groups <= w1) j.add(ml[x], v[x]);
         }
-        if (groups > 1) {
+        // the groups, pairwise
+        for (int half = groups >> 1; half; half >>= 1) {
+            __syncthreads();
             sh[0][threadIdx.x] = j.ml();
             sh[1][threadIdx.x] = j.v;
             __syncthreads();
-            if (grp) return;
-            for (int x = 1; x < groups; ++x) j.add(sh[0][x * F + f], sh[1][x * F + f]);
+            if (grp < half) j.add(sh[0][threadIdx.x + half * per], sh[1][threadIdx.x + half * per]);
         }
+        if (grp) return;
     } else if (grp) {
         return;
     }
     store_out<HD, NT, O>(a, row, ht, i, k, lane, j.v, j.l0, j.l1);
+}
+
+// ---------------------------------------------------------------- a cluster for each sequence and tile
+
+// CTA `rank` of a cluster of `cl`, four warps each: the cluster's warps take the slabs in turn.  Their states are
+// joined in shared memory, the CTA's first, then the cluster's: one launch, nothing in between.
+constexpr int CW = 4;
+template <int HD, int NT, class T, int QT>
+__global__ void __launch_bounds__(CW * 32, 2) attn_cluster(const __grid_constant__ Attn a)
+{
+    using W = Work<HD, NT, T, QT>;
+    using R = Ring<HD>;
+    using O = std::conditional_t<QT == 1, T, float>;
+    constexpr int STATE = W::RT * (HD + PADF), KS = W::KS, F = NT * KS * 32;
+    static_assert((CW + 1) * STATE * 4 <= CW * R::COPIES, "the states take the ring's memory");
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    lfq::dependents_may_launch();
+    lfq::wait_for_prerequisites();
+    const int rank = blockIdx.x % a.cl, item = blockIdx.x / a.cl, row = item / a.ht, ht = item - row * a.ht;
+    const int nw = a.cl * CW, me = rank * CW + warp, kvh = ht / a.tiles;
+    Feed<HD> feed;
+    feed.lane = lane;
+    feed.base = lfk::smem_u32(smem) + warp * R::COPIES;
+    feed.told = reinterpret_cast<Told *>(smem + CW * R::COPIES) + warp * R::STAGES;
+    // Without a window the first slab is known before the length is: the table's entries are asked for at once.
+    const int len = lfq::ld(a.lens + row);
+    const int all = (int)(((long long)a.width * a.c.page) >> 4);
+    if (a.win == 0) feed.look_up(a, row, kvh, me, nw, all);
+    W work;
+    work.begin(a, row, ht, lane);
+    const Seen seen(a, len);
+    if (a.win) feed.look_up(a, row, kvh, seen.s0 + me, nw, seen.s1);
+    int s = seen.s0 + me, j = 0;
+    auto issue = [&](int st) {
+        if (s < seen.s1) {
+            if (j == 32) {
+                j = 0;
+                feed.look_up(a, row, kvh, s, nw, seen.s1);
+            }
+            feed.fetch(a, st, j, Told{row, ht, s, 0, seen.lo, seen.hi});
+            ++j;
+            s += nw;
+        }
+        copies_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < R::STAGES - 1; ++i) issue(i);
+    int st = 0;
+#pragma unroll 1
+    for (int x = seen.s0 + me; x < seen.s1; x += nw) {
+        copies_wait<R::STAGES - 2>();
+        __syncwarp();
+        const Told t = feed.told[st];
+        const uint32_t ks = feed.base + st * 2 * R::SLAB;
+        work.slab(ks, ks + R::SLAB, t.s * 16, t.lo, t.hi, lane, [&] { issue(st == 0 ? R::STAGES - 1 : st - 1); });
+        st = st + 1 == R::STAGES ? 0 : st + 1;
+    }
+    work.sums();
+    copies_wait<0>();
+    __syncthreads();             // the states take the ring's memory
+    float *states = reinterpret_cast<float *>(smem), *own = states + CW * STATE;
+    work.store_state(states + warp * STATE, lane);
+    __syncthreads();
+    for (int f = threadIdx.x; f < F; f += CW * 32) {
+        const int i = f / (KS * 32), k = f / 32 % KS, ln = f % 32, ml = W::RT * HD + (8 * i + 2 * (ln & 3)) * 2;
+        Joined x;
+#pragma unroll
+        for (int w = 0; w < CW; ++w)
+            x.add(*reinterpret_cast<const float4 *>(states + w * STATE + ml), *reinterpret_cast<const float4 *>(states + w * STATE + f * 4));
+        if (a.cl == 1) {
+            store_out<HD, NT, O>(a, row, ht, i, k, ln, x.v, x.l0, x.l1);
+        } else {
+            *reinterpret_cast<float4 *>(own + f * 4) = x.v;
+            if (k == 0 && ln < 4) *reinterpret_cast<float4 *>(own + ml) = x.ml();
+        }
+    }
+    if (a.cl == 1) return;
+    lfq::cluster_sync();
+    for (int f = rank * CW * 32 + threadIdx.x; f < F; f += nw * 32) {
+        const int i = f / (KS * 32), k = f / 32 % KS, ln = f % 32, ml = W::RT * HD + (8 * i + 2 * (ln & 3)) * 2;
+        Joined x;
+        for (int c = 0; c < a.cl; ++c) {
+            const uint32_t base = lfq::cluster_smem(own, c);
+            x.add(lfq::ld_cluster4(base + ml * 4), lfq::ld_cluster4(base + f * 16));
+        }
+        store_out<HD, NT, O>(a, row, ht, i, k, ln, x.v, x.l0, x.l1);
+    }
+    lfq::cluster_sync();         // no CTA leaves while its state may be read
 }
 
 // ---------------------------------------------------------------- launches
@@ -611,16 +727,23 @@ template <int HD, int NT, class T, int QT>
 static cudaError_t run(const Attn &a, cudaStream_t s)
 {
     using O = std::conditional_t<QT == 1, T, float>;
-    constexpr int smem = Ring<HD>::BYTES;
-    static bool ready[64] = {};
+    constexpr int smem = Ring<HD>::bytes(NW);
+    static bool ready[64] = {}, ready_cl[64] = {};
+    if (a.cl) {
+        constexpr int smem_cl = Ring<HD>::bytes(CW);
+        const cudaError_t e = lfr::allow_smem(attn_cluster<HD, NT, T, QT>, smem_cl, ready_cl);
+        if (e != cudaSuccess) return e;
+        return lfr::launch(attn_cluster<HD, NT, T, QT>, dim3((unsigned)(a.n * a.ht * a.cl)), CW * 32, smem_cl, a.cl, s, a);
+    }
     cudaError_t e = lfr::allow_smem(attn_shared<HD, NT, T, QT>, smem, ready);
     if (e == cudaSuccess)
         e = lfr::launch(attn_shared<HD, NT, T, QT>, dim3((unsigned)((a.warps + NW - 1) / NW)), NW * 32, smem, 1, s, a);
     if (e != cudaSuccess) return e;
-    // few blocks: the pieces of a row are spread over a whole one; many: the rows have few pieces each
-    const long long blocks = (long long)a.n * a.ht;
+    // few tiles: many pieces each; many: few
     constexpr int F = NT * (HD / 16) * 32;
-    return lfr::launch(attn_shared_join<HD, NT, O>, dim3((unsigned)blocks), blocks < 512 ? 1024 : F, 0, 1, s, a);
+    const long long items = (long long)a.n * a.ht;
+    const int groups = std::max(items < 32 ? 32 : items < 64 ? 16 : items < 256 ? 8 : items < 2048 ? 2 : 1, JOIN_THREADS / F);
+    return lfr::launch(attn_shared_join<HD, NT, O>, dim3((unsigned)(items * (F * groups / JOIN_THREADS))), JOIN_THREADS, 0, 1, s, a, groups);
 }
 
 template <class T, int QT>
@@ -636,7 +759,9 @@ size_t plan_attn(Attn &a, int sms)
     a.tiles = (a.G + a.rt - 1) / a.rt;
     a.ht = a.c.Hkv * a.tiles;
     a.cl = 0;
-    const long long most = (long long)a.n * a.ht * (((long long)a.width * a.c.page + 15) / 16);
+    const long long slabs = ((long long)a.width * a.c.page + 15) / 16, most = (long long)a.n * a.ht * slabs;
+    if (getenv("LF_CL")) a.cl = atoi(getenv("LF_CL"));
+    if (a.cl) return 0;
     a.warps = (int)std::min<long long>((long long)sms * NW, std::max(1ll, most));
     return (size_t)a.warps * 2 * a.rt * (a.c.hd + PADF) * sizeof(float) + ((size_t)a.n + 1) * sizeof(long long);
 }
