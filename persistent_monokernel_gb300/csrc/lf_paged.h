@@ -47,11 +47,9 @@ struct Attn {
     int rt;                 // 8 or 16
     int win;
     float scale;
-    // One launch: clusters of `cl` CTAs take a (sequence, KV head, tile) each.  Two (cl 0): `warps` warps share all
-    // slabs evenly, and a second launch joins what they cut.
-    int cl, warps;
-    float *part;            // [warps][2][rt * (hd + 4)] partial states (cl 0)
-    long long *first;       // [n + 1] slabs before each sequence
+    // launch: `parts` clusters of `cl` CTAs of `cw` warps (4 or 8) for each sequence and tile
+    int cl, cw, parts;
+    float *part;            // [n * ht][parts] partial states of rt * (hd + 4) floats (parts > 1)
 };
 
 // Fills a's choice of launch for `sms` SMs and returns the workspace it needs.

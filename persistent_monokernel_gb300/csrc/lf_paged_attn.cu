@@ -41,7 +41,6 @@ namespace lfpg {
 
 using lfq::ex2;
 
-constexpr int NW = 8;             // warps of a CTA
 constexpr int PADF = 4;           // floats behind a partial state's O per row: m, l, and two that keep rows aligned
 
 template <class T>
@@ -52,7 +51,9 @@ struct Half16<__half> {
     static __device__ __forceinline__ float to(__half x) { return __half2float(x); }
     static __device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], const unsigned (&b)[2])
     {
-        lfk::mma16816(d, a[0], a[1], a[2], a[3], b[0], b[1]);
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
     }
 };
 template <>
@@ -61,10 +62,9 @@ struct Half16<__nv_bfloat16> {
     static __device__ __forceinline__ float to(__nv_bfloat16 x) { return __bfloat162float(x); }
     static __device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], const unsigned (&b)[2])
     {
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%0, %1, %2, %3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
     }
 };
 template <class T>
@@ -115,10 +115,8 @@ struct Seen {
 
 // What a warp is told about a slab in its ring.
 struct Told {
-    int row, ht, s, flags;
-    int lo, hi;
+    int s, lo, hi;          // the slab, and the positions of it that count
 };
-enum { BEGIN = 1, END = 2, FROM_START = 4, TO_END = 8 };   // of the warp's piece; which is (not) the sequence's begin, end
 
 template <int HD>
 struct Ring {
@@ -132,7 +130,8 @@ struct Ring {
 // QT: terms of q (1: it has the cache's type).
 template <int HD, int NT, class T, int QT>
 struct Work {
-    static constexpr int KS = HD / 16, PT = QT == 1 ? 2 : QT, RT = 8 * NT;
+    static constexpr int KS = HD / 16, RT = 8 * NT;
+    static constexpr int PT = QT > 1 ? QT : std::is_same_v<T, __half> ? 1 : 2;   // terms of P
     static constexpr float P_EXP = 7.f, P_SUM = 32768.f;
     unsigned q[QT][NT][KS][2];
     float f[NT][2], ref[NT][2], l[NT][2], o[NT][KS][4];
@@ -198,21 +197,25 @@ struct Work {
         const int g = lane >> 2;
         // ---- scores: position rows g, g + 8 by heads 2t, 2t + 1.  Each product waits for the one before it into the
         // same sum: CH sums, by the terms of q or the dims' halves, are on their way at a time.
-        constexpr int CH = QT == 1 ? 2 : QT;
+        constexpr int CH = QT > 1 ? QT : NT == 1 ? 4 : 2;
         float st[NT][4], sc[CH][NT][4];
 #pragma unroll
         for (int n = 0; n < CH; ++n)
 #pragma unroll
             for (int i = 0; i < NT; ++i) sc[n][i][0] = sc[n][i][1] = sc[n][i][2] = sc[n][i][3] = 0.f;
         const uint32_t ka = ks + (lane & 15) * (HD * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
+        constexpr int KB = 4;                                // fragments loaded ahead of their products
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            unsigned x[4];
-            lfk::ldsm_x4(x, ka ^ (k << 5));
+        for (int k0 = 0; k0 < KS; k0 += KB) {
+            unsigned x[KB][4];
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int k = 0; k < KB; ++k) lfk::ldsm_x4(x[k], ka ^ ((k0 + k) << 5));
 #pragma unroll
-                for (int n = 0; n < QT; ++n) Half16<T>::mma(sc[QT == 1 ? k & 1 : n][i], x, q[n][i][k]);
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int n = 0; n < QT; ++n)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) Half16<T>::mma(sc[QT == 1 ? k % CH : n][i], x[k], q[n][i][k0 + k]);
         }
         meanwhile();
 #pragma unroll
@@ -271,25 +274,55 @@ struct Work {
         unsigned pb[PT][NT][2];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            l[i][0] += sum[i][0];
-            l[i][1] += sum[i][1];
+            if (PT > 1) {
+                l[i][0] += sum[i][0];
+                l[i][1] += sum[i][1];
+            }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 unsigned w[PT];
                 split_pair<T, PT>(pr[i][2 * u], pr[i][2 * u + 1], w);
+                if (PT == 1) {       // the sum of the rounded ones: weights that still add up to one
+                    const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&w[0]));
+                    l[i][0] += r.x;
+                    l[i][1] += r.y;
+                }
 #pragma unroll
                 for (int n = 0; n < PT; ++n) pb[n][i][u] = lfk::movm_t(w[n]);
             }
         }
         const uint32_t va = vs + ((lane & 7) + (lane >> 4) * 8) * (HD * 2) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            unsigned x[4];
-            lfk::ldsm_x4_t(x, va ^ (k << 5));
+        for (int k0 = 0; k0 < KS; k0 += KB) {
+            unsigned x[KB][4];
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int k = 0; k < KB; ++k) lfk::ldsm_x4_t(x[k], va ^ ((k0 + k) << 5));
+            if constexpr (QT == 1) {
 #pragma unroll
-                for (int n = 0; n < PT; ++n) Half16<T>::mma(o[i][k], x, pb[n][i]);
+                for (int n = 0; n < PT; ++n)
+#pragma unroll
+                    for (int k = 0; k < KB; ++k)
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) Half16<T>::mma(o[i][k0 + k], x[k], pb[n][i]);
+            } else {
+                // The products' own sums are cut off, not rounded, at each step: a slab's is formed from zero, and
+                // added with rounding (11,000 positions in one warp: 2.8e-6 off without).
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    float y[KB][4];
+#pragma unroll
+                    for (int n = PT - 1; n >= 0; --n)
+#pragma unroll
+                        for (int k = 0; k < KB; ++k) {
+                            if (n == PT - 1) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.f;
+                            Half16<T>::mma(y[k], x[k], pb[n][i]);
+                        }
+#pragma unroll
+                    for (int k = 0; k < KB; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][k0 + k][e] += y[k][e];
+                }
+            }
         }
     }
 
@@ -424,221 +457,21 @@ struct Feed {
     }
 };
 
-// ---------------------------------------------------------------- all warps share all slabs
+// ---------------------------------------------------------------- clusters
 
-// Warp w takes slabs [C w, C (w + 1)) of all: the same bytes for each, however the lengths are spread.  Its pieces that
-// are a whole sequence's go out at once; at most two are not, and are left for the join.  C is known on the device
-// alone: what all warps of the launch need to take, MIN_SHARE at least.
-constexpr int MIN_SHARE = 2;
-__device__ __forceinline__ long long quotient(long long x, long long y)   // of numbers that are not negative
+// A sequence's slabs for one tile of query heads (an item) are taken by `parts` clusters of `cl` CTAs of CW warps: a
+// stretch for each part, whose slabs the cluster's warps take in turn (neighbours in memory are read at the same time,
+// which DRAM rewards).  The warps' states are joined in shared memory, the CTA's first, then the cluster's; where
+// there is one part that is the output, in one launch, else a second one joins the parts.  How many parts a sequence
+// really needs, its length says: every warp gets MIN_SLABS slabs before there is another part.
+constexpr int MIN_SLABS = 4;
+__device__ __forceinline__ int parts_of(const Attn &a, int slabs)
 {
-    return ((x | y) >> 32) ? x / y : (long long)((unsigned)x / (unsigned)y);   // (64-bit division is ten times as long)
-}
-__device__ __forceinline__ long long share(long long units, int warps) { return max((long long)MIN_SHARE, quotient(units + warps - 1, warps)); }
-
-template <int HD, int NT, class T, int QT>
-__global__ void __launch_bounds__(NW * 32, 1) attn_shared(const __grid_constant__ Attn a)
-{
-    using W = Work<HD, NT, T, QT>;
-    using R = Ring<HD>;
-    using O = std::conditional_t<QT == 1, T, float>;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    lfq::dependents_may_launch();
-    lfq::wait_for_prerequisites();
-
-    // ---- slabs before each stretch of rows (one stretch a thread), in the ring's memory
-    long long *sums = reinterpret_cast<long long *>(smem);       // [256 + 1]
-    long long *wsum = sums + 257;                                // [NW]
-    const int per = (a.n + 255) / 256;
-    const int r0 = min(threadIdx.x * per, a.n), r1 = min(r0 + per, a.n);
-    long long mine = 0;
-    for (int r = r0; r < r1; ++r) mine += Seen(a, lfq::ld(a.lens + r)).slabs();
-    long long incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += x;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += wsum[w];
-    sums[threadIdx.x + 1] = incl;
-    if (threadIdx.x == 0) sums[0] = 0;
-    if (blockIdx.x == 0) {       // for the join
-        long long at = incl - mine;
-        for (int r = r0; r < r1; ++r) {
-            a.first[r] = at;
-            at += Seen(a, lfq::ld(a.lens + r)).slabs();
-        }
-        if (threadIdx.x == 255) a.first[a.n] = incl;
-    }
-    __syncthreads();
-    const long long units = sums[256] * a.ht;
-    const int w = blockIdx.x * NW + warp;
-    long long u = 0, left = 0;
-    int row = 0, end_row = 0;
-    const long long each = share(units, a.warps);
-    if (w < a.warps && w * each < units) {
-        u = w * each;
-        left = min(each, units - u);
-        // the stretch that holds unit u: the last whose first slab is not behind it
-        int lo = 0, hi = 255;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (sums[mid] * a.ht <= u) lo = mid;
-            else hi = mid - 1;
-        }
-        row = lo * per;
-        end_row = a.n;
-        u -= sums[lo] * a.ht;
-    }
-    __syncthreads();             // the ring takes the memory
-    if (left == 0) return;
-
-    Feed<HD> feed;
-    feed.lane = lane;
-    feed.base = lfk::smem_u32(smem) + warp * R::COPIES;
-    feed.told = reinterpret_cast<Told *>(smem + NW * R::COPIES) + warp * R::STAGES;
-    // rows from `row` on, 32 at a time: their lengths lie in the lanes
-    int rbase = row, len = rbase + lane < end_row ? lfq::ld(a.lens + rbase + lane) : 0;
-    auto seen_of = [&](int r) {
-        if (r - rbase >= 32) {
-            rbase = r;
-            len = r + lane < end_row ? lfq::ld(a.lens + r + lane) : 0;
-        }
-        return Seen(a, __shfl_sync(0xffffffffu, len, r - rbase));
-    };
-    Seen seen = seen_of(row);
-    while (u >= (long long)seen.slabs() * a.ht) {   // the row of the first slab
-        u -= (long long)seen.slabs() * a.ht;
-        seen = seen_of(++row);
-    }
-    int ht = (int)quotient(u, seen.slabs()), s = seen.s0 + (int)(u - (long long)ht * seen.slabs()), ebase = s;
-    feed.look_up(a, row, ht / a.tiles, s, 1, seen.s1);
-    bool begin = true;
-    // the next slab of the share into stage st
-    auto issue = [&](int st) {
-        if (left > 0) {
-            if (s == seen.s1) {
-                if (++ht == a.ht) {
-                    ht = 0;
-                    do seen = seen_of(++row);
-                    while (seen.slabs() == 0);
-                }
-                s = seen.s0;
-                begin = true;
-                ebase = s;
-                feed.look_up(a, row, ht / a.tiles, s, 1, seen.s1);
-            } else if (s - ebase == 32) {
-                ebase = s;
-                feed.look_up(a, row, ht / a.tiles, s, 1, seen.s1);
-            }
-            --left;
-            const bool last = s + 1 == seen.s1, end = last || left == 0;
-            Told x = {row, ht, s, (begin ? BEGIN : 0) | (end ? END : 0) | (s == seen.s0 ? FROM_START : 0) | (last ? TO_END : 0),
-                      seen.lo, seen.hi};
-            feed.fetch(a, st, s - ebase, x);
-            begin = false;
-            ++s;
-        }
-        copies_commit();
-    };
-    long long todo = left;
-#pragma unroll 1
-    for (int i = 0; i < R::STAGES - 1; ++i) issue(i);
-    W work;
-    int st = 0;
-    bool from_start = false;
-#pragma unroll 1
-    for (; todo > 0; --todo) {
-        copies_wait<R::STAGES - 2>();
-        __syncwarp();
-        const Told x = feed.told[st];
-        if (x.flags & BEGIN) {
-            work.begin(a, x.row, x.ht, lane);
-            from_start = x.flags & FROM_START;
-        }
-        const uint32_t ks = feed.base + st * 2 * R::SLAB;
-        work.slab(ks, ks + R::SLAB, x.s * 16, x.lo, x.hi, lane, [&] { issue(st == 0 ? R::STAGES - 1 : st - 1); });
-        if (x.flags & END) {
-            work.sums();
-            if (from_start && (x.flags & TO_END)) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int k = 0; k < W::KS; ++k)
-                        store_out<HD, NT, O>(a, x.row, x.ht, i, k, lane,
-                                             make_float4(work.o[i][k][0], work.o[i][k][1], work.o[i][k][2], work.o[i][k][3]),
-                                             work.l[i][0], work.l[i][1]);
-            } else {
-                // a piece that goes on behind this warp's share lies second, one that came from before it first
-                work.store_state(a.part + ((size_t)w * 2 + (from_start ? 1 : 0)) * W::RT * (HD + PADF), lane);
-            }
-        }
-        st = st + 1 == R::STAGES ? 0 : st + 1;
-    }
+    return min(a.parts, max(1, slabs / (a.cl * a.cw * MIN_SLABS)));
 }
 
-// Joins the pieces of the sequences and tiles that were cut.  A block takes 256 / groups of the 16-byte places of a
-// state's O (dims and heads), `groups` threads each: thread `grp` adds every groups-th piece.  It fits beside a CTA of
-// the first launch, so that it is there when that ends.
-constexpr int JOIN_THREADS = 256;
-template <int HD, int NT, class O>
-__global__ void __launch_bounds__(JOIN_THREADS) attn_shared_join(const __grid_constant__ Attn a, int groups)
-{
-    constexpr int KS = HD / 16, F = NT * KS * 32, RT = 8 * NT;
-    __shared__ float4 sh[2][JOIN_THREADS];
-    lfq::dependents_may_launch();
-    lfq::wait_for_prerequisites();
-    const int per = JOIN_THREADS / groups, blocks = F / per;    // places a block; blocks a tile
-    const int item = blockIdx.x / blocks, row = item / a.ht, ht = item - row * a.ht;
-    const int f = (blockIdx.x - item * blocks) * per + threadIdx.x % per, grp = threadIdx.x / per;
-    const long long first = lfq::ld(a.first + row), slabs = lfq::ld(a.first + row + 1) - first;
-    const long long units = lfq::ld(a.first + a.n) * a.ht;
-    const int i = f / (KS * 32), k = f / 32 % KS, lane = f % 32;
-    Joined j;
-    if (slabs > 0) {
-        const long long u0 = first * a.ht + slabs * ht, each = share(units, a.warps);
-        const int w0 = (int)quotient(u0, each), w1 = (int)quotient(u0 + slabs - 1, each);
-        if (w0 == w1) return;                                  // in one piece: it has its output
-        constexpr int AHEAD = 8;                               // loads of pieces on the way at a time
-        for (int w = w0 + grp; w <= w1; w += AHEAD * groups) {
-            float4 ml[AHEAD], v[AHEAD];
-#pragma unroll
-            for (int x = 0; x < AHEAD; ++x) {
-                const int y = w + x * groups;
-                if (y > w1) continue;
-                const float *p = a.part + ((size_t)y * 2 + (y == w0 ? 1 : 0)) * RT * (HD + PADF);
-                ml[x] = lfq::ld(reinterpret_cast<const float4 *>(p + RT * HD + (8 * i + 2 * (lane & 3)) * 2));
-                v[x] = lfq::ld(reinterpret_cast<const float4 *>(p + f * 4));
-            }
-#pragma unroll
-            for (int x = 0; x < AHEAD; ++x)
-                if (w + x * groups <= w1) j.add(ml[x], v[x]);
-        }
-        // the groups, pairwise
-        for (int half = groups >> 1; half; half >>= 1) {
-            __syncthreads();
-            sh[0][threadIdx.x] = j.ml();
-            sh[1][threadIdx.x] = j.v;
-            __syncthreads();
-            if (grp < half) j.add(sh[0][threadIdx.x + half * per], sh[1][threadIdx.x + half * per]);
-        }
-        if (grp) return;
-    } else if (grp) {
-        return;
-    }
-    store_out<HD, NT, O>(a, row, ht, i, k, lane, j.v, j.l0, j.l1);
-}
-
-// ---------------------------------------------------------------- a cluster for each sequence and tile
-
-// CTA `rank` of a cluster of `cl`, four warps each: the cluster's warps take the slabs in turn.  Their states are
-// joined in shared memory, the CTA's first, then the cluster's: one launch, nothing in between.
-constexpr int CW = 4;
-template <int HD, int NT, class T, int QT>
-__global__ void __launch_bounds__(CW * 32, 2) attn_cluster(const __grid_constant__ Attn a)
+template <int HD, int NT, class T, int QT, int CW>
+__global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_constant__ Attn a)
 {
     using W = Work<HD, NT, T, QT>;
     using R = Ring<HD>;
@@ -649,7 +482,8 @@ __global__ void __launch_bounds__(CW * 32, 2) attn_cluster(const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     lfq::dependents_may_launch();
     lfq::wait_for_prerequisites();
-    const int rank = blockIdx.x % a.cl, item = blockIdx.x / a.cl, row = item / a.ht, ht = item - row * a.ht;
+    const int rank = blockIdx.x % a.cl, cluster = blockIdx.x / a.cl;
+    const int item = cluster / a.parts, part = cluster - item * a.parts, row = item / a.ht, ht = item - row * a.ht;
     const int nw = a.cl * CW, me = rank * CW + warp, kvh = ht / a.tiles;
     Feed<HD> feed;
     feed.lane = lane;
@@ -658,11 +492,19 @@ __global__ void __launch_bounds__(CW * 32, 2) attn_cluster(const __grid_constant
     // Without a window the first slab is known before the length is: the table's entries are asked for at once.
     const int len = lfq::ld(a.lens + row);
     const int all = (int)(((long long)a.width * a.c.page) >> 4);
-    if (a.win == 0) feed.look_up(a, row, kvh, me, nw, all);
+    const bool early = a.win == 0 && a.parts == 1;
+    if (early) feed.look_up(a, row, kvh, me, nw, all);
     W work;
     work.begin(a, row, ht, lane);
-    const Seen seen(a, len);
-    if (a.win) feed.look_up(a, row, kvh, seen.s0 + me, nw, seen.s1);
+    Seen seen(a, len);
+    const int parts = parts_of(a, seen.slabs());
+    if (part >= parts) return;   // (all CTAs of the cluster)
+    if (parts > 1) {
+        const int n = seen.slabs(), s0 = seen.s0;
+        seen.s0 = s0 + (int)((long long)n * part / parts);
+        seen.s1 = s0 + (int)((long long)n * (part + 1) / parts);
+    }
+    if (!early) feed.look_up(a, row, kvh, seen.s0 + me, nw, seen.s1);
     int s = seen.s0 + me, j = 0;
     auto issue = [&](int st) {
         if (s < seen.s1) {
@@ -670,7 +512,7 @@ __global__ void __launch_bounds__(CW * 32, 2) attn_cluster(const __grid_constant
                 j = 0;
                 feed.look_up(a, row, kvh, s, nw, seen.s1);
             }
-            feed.fetch(a, st, j, Told{row, ht, s, 0, seen.lo, seen.hi});
+            feed.fetch(a, st, j, Told{s, seen.lo, seen.hi});
             ++j;
             s += nw;
         }
@@ -692,6 +534,15 @@ __global__ void __launch_bounds__(CW * 32, 2) attn_cluster(const __grid_constant
     copies_wait<0>();
     __syncthreads();             // the states take the ring's memory
     float *states = reinterpret_cast<float *>(smem), *own = states + CW * STATE;
+    float *const out = parts > 1 ? a.part + ((size_t)item * a.parts + part) * STATE : nullptr;   // a partial state
+    auto finish = [&](const Joined &x, int f, int i, int k, int ln, int ml) {
+        if (out) {
+            *reinterpret_cast<float4 *>(out + f * 4) = x.v;
+            if (k == 0 && ln < 4) *reinterpret_cast<float4 *>(out + ml) = x.ml();
+        } else {
+            store_out<HD, NT, O>(a, row, ht, i, k, ln, x.v, x.l0, x.l1);
+        }
+    };
     work.store_state(states + warp * STATE, lane);
     __syncthreads();
     for (int f = threadIdx.x; f < F; f += CW * 32) {
@@ -701,7 +552,7 @@ __global__ void __launch_bounds__(CW * 32, 2) attn_cluster(const __grid_constant
         for (int w = 0; w < CW; ++w)
             x.add(*reinterpret_cast<const float4 *>(states + w * STATE + ml), *reinterpret_cast<const float4 *>(states + w * STATE + f * 4));
         if (a.cl == 1) {
-            store_out<HD, NT, O>(a, row, ht, i, k, ln, x.v, x.l0, x.l1);
+            finish(x, f, i, k, ln, ml);
         } else {
             *reinterpret_cast<float4 *>(own + f * 4) = x.v;
             if (k == 0 && ln < 4) *reinterpret_cast<float4 *>(own + ml) = x.ml();
@@ -716,9 +567,52 @@ __global__ void __launch_bounds__(CW * 32, 2) attn_cluster(const __grid_constant
             const uint32_t base = lfq::cluster_smem(own, c);
             x.add(lfq::ld_cluster4(base + ml * 4), lfq::ld_cluster4(base + f * 16));
         }
-        store_out<HD, NT, O>(a, row, ht, i, k, ln, x.v, x.l0, x.l1);
+        finish(x, f, i, k, ln, ml);
     }
     lfq::cluster_sync();         // no CTA leaves while its state may be read
+}
+
+// Joins the parts of the items that have more than one.  A block takes 256 / groups of the 16-byte places of a state's O
+// (dims and heads), `groups` threads each: thread `grp` adds every groups-th part.
+constexpr int JOIN_THREADS = 256;
+template <int HD, int NT, class O>
+__global__ void __launch_bounds__(JOIN_THREADS, 4) attn_join(const __grid_constant__ Attn a, int groups)
+{
+    constexpr int KS = HD / 16, F = NT * KS * 32, RT = 8 * NT, STATE = RT * (HD + PADF);
+    __shared__ float4 sh[2][JOIN_THREADS];
+    lfq::dependents_may_launch();
+    lfq::wait_for_prerequisites();
+    const int per = JOIN_THREADS / groups, blocks = F / per;    // places a block; blocks an item
+    const int item = blockIdx.x / blocks, row = item / a.ht, ht = item - row * a.ht;
+    const int f = (blockIdx.x - item * blocks) * per + threadIdx.x % per, grp = threadIdx.x / per;
+    const int parts = parts_of(a, Seen(a, lfq::ld(a.lens + row)).slabs());
+    if (parts == 1) return;                                    // it has its output
+    const int i = f / (KS * 32), k = f / 32 % KS, lane = f % 32;
+    Joined j;
+    constexpr int AHEAD = 4;                                   // loads on the way at a time
+    for (int p0 = grp; p0 < parts; p0 += AHEAD * groups) {
+        float4 ml[AHEAD], v[AHEAD];
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) {
+            const int p = p0 + x * groups;
+            if (p >= parts) continue;
+            const float *src = a.part + ((size_t)item * a.parts + p) * STATE;
+            ml[x] = lfq::ld(reinterpret_cast<const float4 *>(src + RT * HD + (8 * i + 2 * (lane & 3)) * 2));
+            v[x] = lfq::ld(reinterpret_cast<const float4 *>(src + f * 4));
+        }
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x)
+            if (p0 + x * groups < parts) j.add(ml[x], v[x]);
+    }
+    // the groups, pairwise
+    for (int half = groups >> 1; half; half >>= 1) {
+        __syncthreads();
+        sh[0][threadIdx.x] = j.ml();
+        sh[1][threadIdx.x] = j.v;
+        __syncthreads();
+        if (grp < half) j.add(sh[0][threadIdx.x + half * per], sh[1][threadIdx.x + half * per]);
+    }
+    if (grp == 0) store_out<HD, NT, O>(a, row, ht, i, k, lane, j.v, j.l0, j.l1);
 }
 
 // ---------------------------------------------------------------- launches
@@ -727,23 +621,19 @@ template <int HD, int NT, class T, int QT>
 static cudaError_t run(const Attn &a, cudaStream_t s)
 {
     using O = std::conditional_t<QT == 1, T, float>;
-    constexpr int smem = Ring<HD>::bytes(NW);
-    static bool ready[64] = {}, ready_cl[64] = {};
-    if (a.cl) {
-        constexpr int smem_cl = Ring<HD>::bytes(CW);
-        const cudaError_t e = lfr::allow_smem(attn_cluster<HD, NT, T, QT>, smem_cl, ready_cl);
+    static bool ready[2][64] = {};
+    auto go = [&](auto warps, bool (&ready)[64]) {
+        constexpr int CW = decltype(warps)::value, smem = Ring<HD>::bytes(CW);
+        const cudaError_t e = lfr::allow_smem(attn_cluster<HD, NT, T, QT, CW>, smem, ready);
         if (e != cudaSuccess) return e;
-        return lfr::launch(attn_cluster<HD, NT, T, QT>, dim3((unsigned)(a.n * a.ht * a.cl)), CW * 32, smem_cl, a.cl, s, a);
-    }
-    cudaError_t e = lfr::allow_smem(attn_shared<HD, NT, T, QT>, smem, ready);
-    if (e == cudaSuccess)
-        e = lfr::launch(attn_shared<HD, NT, T, QT>, dim3((unsigned)((a.warps + NW - 1) / NW)), NW * 32, smem, 1, s, a);
-    if (e != cudaSuccess) return e;
-    // few tiles: many pieces each; many: few
+        return lfr::launch(attn_cluster<HD, NT, T, QT, CW>, dim3((unsigned)(a.n * a.ht * a.parts * a.cl)), CW * 32, smem, a.cl, s, a);
+    };
+    const cudaError_t e = a.cw == 4 ? go(std::integral_constant<int, 4>(), ready[0]) : go(std::integral_constant<int, 8>(), ready[1]);
+    if (e != cudaSuccess || a.parts == 1) return e;
     constexpr int F = NT * (HD / 16) * 32;
-    const long long items = (long long)a.n * a.ht;
-    const int groups = std::max(items < 32 ? 32 : items < 64 ? 16 : items < 256 ? 8 : items < 2048 ? 2 : 1, JOIN_THREADS / F);
-    return lfr::launch(attn_shared_join<HD, NT, O>, dim3((unsigned)(items * (F * groups / JOIN_THREADS))), JOIN_THREADS, 0, 1, s, a, groups);
+    int groups = JOIN_THREADS / F > 1 ? JOIN_THREADS / F : 1;
+    while (groups < 16 && groups * 4 < a.parts) groups *= 2;
+    return lfr::launch(attn_join<HD, NT, O>, dim3((unsigned)(a.n * a.ht * (F * groups / JOIN_THREADS))), JOIN_THREADS, 0, 1, s, a, groups);
 }
 
 template <class T, int QT>
@@ -758,19 +648,14 @@ size_t plan_attn(Attn &a, int sms)
     a.rt = a.G <= 8 ? 8 : 16;
     a.tiles = (a.G + a.rt - 1) / a.rt;
     a.ht = a.c.Hkv * a.tiles;
-    a.cl = 0;
-    const long long slabs = ((long long)a.width * a.c.page + 15) / 16, most = (long long)a.n * a.ht * slabs;
+    a.cl = 4, a.cw = 4, a.parts = 1;
     if (getenv("LF_CL")) a.cl = atoi(getenv("LF_CL"));
-    if (a.cl) return 0;
-    a.warps = (int)std::min<long long>((long long)sms * NW, std::max(1ll, most));
-    return (size_t)a.warps * 2 * a.rt * (a.c.hd + PADF) * sizeof(float) + ((size_t)a.n + 1) * sizeof(long long);
+    if (a.cl > 1000) a.parts = a.cl / 1000, a.cl %= 1000;
+    if (a.cl > 100) a.cw = 8, a.cl -= 100;
+    return a.parts > 1 ? (size_t)a.n * a.ht * a.parts * a.rt * (a.c.hd + PADF) * sizeof(float) : 0;
 }
 
-void set_workspace(Attn &a, void *ws)
-{
-    a.part = static_cast<float *>(ws);
-    a.first = reinterpret_cast<long long *>(a.part + (size_t)a.warps * 2 * a.rt * (a.c.hd + PADF));
-}
+void set_workspace(Attn &a, void *ws) { a.part = static_cast<float *>(ws); }
 
 cudaError_t launch_attn(const Attn &a, cudaStream_t s)
 {
