@@ -484,19 +484,12 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
     lfq::wait_for_prerequisites();
     const int rank = blockIdx.x % a.cl, cluster = blockIdx.x / a.cl;
     const int item = cluster / a.parts, part = cluster - item * a.parts, row = item / a.ht, ht = item - row * a.ht;
-    const int nw = a.cl * CW, me = rank * CW + warp, kvh = ht / a.tiles;
+    const int me = rank * CW + warp, kvh = ht / a.tiles;
     Feed<HD> feed;
     feed.lane = lane;
     feed.base = lfk::smem_u32(smem) + warp * R::COPIES;
     feed.told = reinterpret_cast<Told *>(smem + CW * R::COPIES) + warp * R::STAGES;
-    // Without a window the first slab is known before the length is: the table's entries are asked for at once.
-    const int len = lfq::ld(a.lens + row);
-    const int all = (int)(((long long)a.width * a.c.page) >> 4);
-    const bool early = a.win == 0 && a.parts == 1;
-    if (early) feed.look_up(a, row, kvh, me, nw, all);
-    W work;
-    work.begin(a, row, ht, lane);
-    Seen seen(a, len);
+    Seen seen(a, lfq::ld(a.lens + row));
     const int parts = parts_of(a, seen.slabs());
     if (part >= parts) return;   // (all CTAs of the cluster)
     if (parts > 1) {
@@ -504,7 +497,12 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
         seen.s0 = s0 + (int)((long long)n * part / parts);
         seen.s1 = s0 + (int)((long long)n * (part + 1) / parts);
     }
-    if (!early) feed.look_up(a, row, kvh, seen.s0 + me, nw, seen.s1);
+    // A short row needs fewer CTAs: the others leave, and the cluster's barriers count those that are left.
+    const int cl = max(1, min(a.cl, seen.slabs() / (CW * 2))), nw = cl * CW;
+    if (rank >= cl) return;
+    feed.look_up(a, row, kvh, seen.s0 + me, nw, seen.s1);
+    W work;
+    work.begin(a, row, ht, lane);
     int s = seen.s0 + me, j = 0;
     auto issue = [&](int st) {
         if (s < seen.s1) {
@@ -551,19 +549,19 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
 #pragma unroll
         for (int w = 0; w < CW; ++w)
             x.add(*reinterpret_cast<const float4 *>(states + w * STATE + ml), *reinterpret_cast<const float4 *>(states + w * STATE + f * 4));
-        if (a.cl == 1) {
+        if (cl == 1) {
             finish(x, f, i, k, ln, ml);
         } else {
             *reinterpret_cast<float4 *>(own + f * 4) = x.v;
             if (k == 0 && ln < 4) *reinterpret_cast<float4 *>(own + ml) = x.ml();
         }
     }
-    if (a.cl == 1) return;
+    if (cl == 1) return;
     lfq::cluster_sync();
     for (int f = rank * CW * 32 + threadIdx.x; f < F; f += nw * 32) {
         const int i = f / (KS * 32), k = f / 32 % KS, ln = f % 32, ml = W::RT * HD + (8 * i + 2 * (ln & 3)) * 2;
         Joined x;
-        for (int c = 0; c < a.cl; ++c) {
+        for (int c = 0; c < cl; ++c) {
             const uint32_t base = lfq::cluster_smem(own, c);
             x.add(lfq::ld_cluster4(base + ml * 4), lfq::ld_cluster4(base + f * 16));
         }
@@ -643,16 +641,37 @@ static cudaError_t run(const Attn &a, cudaStream_t s)
     return a.rt == 8 ? run<64, 1, T, QT>(a, s) : run<64, 2, T, QT>(a, s);
 }
 
+// The lengths are known on the device alone, so the launch goes by what the host knows: the items (sequences x tiles)
+// and the slabs that the widest row may have.  Two CTAs of four warps fit an SM (304 places on 152).
+//   * Clusters as large as the items leave places for, with two slabs a warp at least (a sixth CTA per place costs
+//     more than the warps it adds: 16 x 5 heads of 512 positions take 6.2 us in clusters of two, 8.3 of four, 13.3 of
+//     eight).  Beyond the places only where a warp still has 8 cl slabs: smaller shares even out rows of different
+//     lengths (64 x 8 heads of up to 16,384: 331 us in single CTAs, 310 in twos, 298 in fours, 303 in eights).
+//   * Few items of many slabs leave SMs idle in one cluster each: up to 17 items of 12,288 positions or more are cut into
+//     parts, as many clusters of four as fit (280 CTAs: the last clusters find no group of SMs that is free), and a second
+//     launch joins them (3 us; one sequence of 5 heads at 32,768: 19.8 us in parts, 23.4 in clusters of eight CTAs of
+//     eight warps; at 8,192 9.7 and 9.7; of 8 heads at 131,071: 80.5 and 88).
+//   * Otherwise, where clusters of eight leave half the places empty, CTAs of eight warps (5 heads at 8,192: 9.7 us,
+//     10.8 with four; at 2,048 6.1 either way).
 size_t plan_attn(Attn &a, int sms)
 {
     a.rt = a.G <= 8 ? 8 : 16;
     a.tiles = (a.G + a.rt - 1) / a.rt;
     a.ht = a.c.Hkv * a.tiles;
-    a.cl = 4, a.cw = 4, a.parts = 1;
-    if (getenv("LF_CL")) a.cl = atoi(getenv("LF_CL"));
-    if (a.cl > 1000) a.parts = a.cl / 1000, a.cl %= 1000;
-    if (a.cl > 100) a.cw = 8, a.cl -= 100;
-    return a.parts > 1 ? (size_t)a.n * a.ht * a.parts * a.rt * (a.c.hd + PADF) * sizeof(float) : 0;
+    const long long items = (long long)a.n * a.ht, places = 2 * sms;
+    long long slabs = ((long long)a.width * a.c.page + 15) / 16;
+    if (a.win > 0) slabs = std::min<long long>(slabs, a.win / 16 + 2);
+    a.cl = 1, a.cw = 4, a.parts = 1;
+    for (int cl = 2; cl <= 8; cl *= 2)
+        if (slabs >= 8 * cl && (items * cl <= places || slabs >= 32 * cl * cl)) a.cl = cl;
+    const long long parts = places * 280 / 304 / (4 * items);
+    if (slabs >= 768 && parts >= 4) {
+        a.cl = 4;
+        a.parts = (int)parts;
+    } else if (a.cl == 8 && items * 8 <= sms && slabs >= 256) {
+        a.cw = 8;
+    }
+    return a.parts > 1 ? (size_t)items * a.parts * a.rt * (a.c.hd + PADF) * sizeof(float) : 0;
 }
 
 void set_workspace(Attn &a, void *ws) { a.part = static_cast<float *>(ws); }
