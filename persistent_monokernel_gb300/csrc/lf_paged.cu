@@ -27,7 +27,8 @@ namespace lfpg {
 // Three sums over the rows say where everything lies; after them every page and token finds its row by a search in
 // shared memory, however uneven the rows are.  Every CTA of the (only) cluster forms the sums for itself: they are
 // a read of a few KB, and nothing has to be handed over.  What is read and what is written overlaps (lens, n_free,
-// table entries given back and taken anew), hence one cluster barrier between reading and writing.
+// table entries given back and taken anew), hence one cluster barrier between reading and writing.  Many tokens are
+// left to a second launch, which needs no more than the tables and offsets that the first one wrote.
 //
 // Bound by latency: the loads of the rows, the sums' shuffles, a search and two dependent loads per token.
 __device__ __forceinline__ int row_of(const int *before, int n, int k)   // the last row with before[row] <= k
@@ -41,16 +42,53 @@ __device__ __forceinline__ int row_of(const int *before, int n, int k)   // the 
     return lo;
 }
 
-__global__ void __launch_bounds__(1024) plan_pages(const __grid_constant__ Plan p, int ctas, int shift)
+// Position to page: a shift where the page is a power of two.
+__device__ __forceinline__ int page_of(const Plan &p, int shift, int x)
+{
+    return shift >= 0 ? x >> shift : (int)((unsigned)x / (unsigned)p.page);
+}
+
+// Slots and positions of tokens t0 .. t0 + 3 (and nothing behind max_tokens).  tok: tokens before each row;
+// first(r): position of row r's first; page(r, c): its c-th page.
+template <class First, class Page>
+__device__ __forceinline__ void four_tokens(const Plan &p, int t0, int tokens, const int *tok, int shift, First first, Page page)
+{
+    int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
+    if (t0 < tokens) {
+        int r = row_of(tok, p.n, t0), base = first(r), have = -1, id = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + i;
+            if (t >= tokens) break;
+            while (t >= tok[r + 1]) base = first(++r), have = -1;
+            const int x = base + t - tok[r], c = page_of(p, shift, x);
+            if (c != have) have = c, id = page(r, c);
+            slot[i] = id * p.page + x - c * p.page;
+            pos[i] = x;
+        }
+    }
+    if (t0 + 4 <= p.max_tokens) {
+        *reinterpret_cast<int4 *>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (t0 + i < p.max_tokens) {
+                p.slots[t0 + i] = slot[i];
+                p.positions[t0 + i] = pos[i];
+            }
+    }
+}
+
+__global__ void __launch_bounds__(1024) plan_pages(const __grid_constant__ Plan p, int ctas, int shift, bool with_tokens)
 {
     extern __shared__ int smem[];
     int *const kept = smem, *const tok = kept + p.n, *const back = tok + p.n + 1, *const need = back + p.n + 1;
-    __shared__ long long wsum[3][32];
+    __shared__ long long wsum[3][33];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     lfq::dependents_may_launch();
     lfq::wait_for_prerequisites();
-    auto page_of = [&](int x) { return shift >= 0 ? x >> shift : (int)((unsigned)x / (unsigned)p.page); };
-    auto pages = [&](int x) { return x ? page_of(x - 1) + 1 : 0; };
+    auto pages = [&](int x) { return x ? page_of(p, shift, x - 1) + 1 : 0; };
 
     // ---- the rows' numbers, and their sums up to each row
     const int per = (p.n + blockDim.x - 1) / blockDim.x;
@@ -93,13 +131,24 @@ __global__ void __launch_bounds__(1024) plan_pages(const __grid_constant__ Plan 
         at[i] = incl - mine[i];
     }
     __syncthreads();
-    long long sum[3] = {0, 0, 0};
+    if (warp < 3) {                                  // the sums of the warps before each, and of all
+        const long long x = lane < warps ? wsum[warp][lane] : 0;
+        long long incl = x;
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-        for (int w = 0; w < warps; ++w) {
-            if (w == warp) at[i] += sum[i];
-            sum[i] += wsum[i][w];
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += y;
         }
+        wsum[warp][lane] = incl - x;
+        if (lane == 31) wsum[warp][32] = incl;
+    }
+    __syncthreads();
+    long long sum[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        at[i] += wsum[i][warp];
+        sum[i] = wsum[i][32];
+    }
     for (int r = r0; r < r1; ++r) {
         long long x[3];
         kept[r] = row(r, x);
@@ -124,47 +173,40 @@ __global__ void __launch_bounds__(1024) plan_pages(const __grid_constant__ Plan 
     }
     if (ctas > 1) lfq::cluster_sync();
     else __syncthreads();
-    // ---- pages taken, and the rows
+    // ---- pages taken, and the rows; the last threads take these, the first ones the tokens
+    const int last = all - 1 - me;
+    for (int r = last; r <= p.n; r += all) p.offsets[r] = fails ? 0 : tok[r];
     if (!fails) {
-        for (int k = me; k < n_need; k += all) {
+        for (int r = last; r < p.n; r += all) p.lens[r] = kept[r] + tok[r + 1] - tok[r];
+        if (last == 0) *p.n_free = top - n_need;
+        for (int k = last; k < n_need; k += all) {
             const int r = row_of(need, p.n, k);
             p.tables[r * p.tstride + pages(kept[r]) + k - need[r]] = lfq::ld(p.free + top - 1 - k);
         }
-        for (int r = me; r < p.n; r += all) p.lens[r] = kept[r] + tok[r + 1] - tok[r];
-        if (me == 0) *p.n_free = top - n_need;
-    } else if (me == 0 && lfq::ld(p.status) == 0) {
+    } else if (last == 0 && lfq::ld(p.status) == 0) {
         *p.status = invalid ? LF_ERR_INVALID_ARG : LF_ERR_CAPACITY;
     }
-    for (int r = me; r <= p.n; r += all) p.offsets[r] = fails ? 0 : tok[r];
-    // ---- four tokens a thread
-    for (int t0 = me * 4; t0 < p.max_tokens; t0 += all * 4) {
-        int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
-        if (t0 < tokens) {
-            int r = row_of(tok, p.n, t0), j = -1, page = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = t0 + i;
-                if (t >= tokens) break;
-                while (t >= tok[r + 1]) ++r, j = -1;
-                const int x = kept[r] + t - tok[r], c = page_of(x), stay = pages(kept[r]);
-                if (c != j) {
-                    j = c;
-                    page = c < stay ? lfq::ld(p.tables + r * p.tstride + c) : lfq::ld(p.free + top - 1 - (need[r] + c - stay));
-                }
-                slot[i] = page * p.page + x - c * p.page;
-                pos[i] = x;
-            }
-        }
-        if (t0 + 4 <= p.max_tokens) {
-            *reinterpret_cast<int4 *>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-            *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-        } else {
-            for (int i = 0; t0 + i < p.max_tokens; ++i) {
-                p.slots[t0 + i] = slot[i];
-                p.positions[t0 + i] = pos[i];
-            }
-        }
-    }
+    if (!with_tokens) return;
+    for (int t0 = me * 4; t0 < p.max_tokens; t0 += all * 4)
+        four_tokens(p, t0, tokens, tok, shift, [&](int r) { return kept[r]; },
+                    [&](int r, int c) {
+                        const int stay = pages(kept[r]);
+                        return c < stay ? lfq::ld(p.tables + r * p.tstride + c) : lfq::ld(p.free + top - 1 - (need[r] + c - stay));
+                    });
+}
+
+// The slots and positions of many tokens, from what the first launch wrote.
+__global__ void __launch_bounds__(256) plan_tokens(const __grid_constant__ Plan p, int shift)
+{
+    extern __shared__ int smem[];
+    lfq::dependents_may_launch();
+    lfq::wait_for_prerequisites();
+    for (int r = threadIdx.x; r <= p.n; r += 256) smem[r] = lfq::ld(p.offsets + r);
+    __syncthreads();
+    const int t0 = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (t0 < p.max_tokens)
+        four_tokens(p, t0, smem[p.n], smem, shift, [&](int r) { return lfq::ld(p.lens + r) - (smem[r + 1] - smem[r]); },
+                    [&](int r, int c) { return lfq::ld(p.tables + r * p.tstride + c); });
 }
 
 // ---------------------------------------------------------------- append
@@ -211,17 +253,19 @@ __global__ void __launch_bounds__(256) append_rows(const __grid_constant__ Pool 
 
 cudaError_t launch_plan(const Plan &p, cudaStream_t s)
 {
-    // Up to 4,096 tokens a CTA, in one cluster.
-    const int ctas = std::max(1, std::min(8, (p.max_tokens + 4095) / 4096));
-    const int threads = p.n <= 256 && p.max_tokens <= 1024 ? 256 : 1024;
-    const int smem = (4 * p.n + 3) * (int)sizeof(int);
+    // One CTA, or a cluster of them where there may be thousands of pages to move: new tokens' and given back ones.
+    const bool with_tokens = p.max_tokens <= 4096;
+    const long long moves = (long long)p.max_tokens / p.page + p.n;
+    const int ctas = moves <= 2048 ? 1 : moves <= 8192 ? 4 : 8, threads = p.n <= 256 && p.max_tokens <= 1024 ? 256 : 1024;
     int shift = -1;
     for (int i = 4; i < 31; ++i)
         if (p.page == 1 << i) shift = i;
     static bool ready[64] = {};
-    const cudaError_t e = lfr::allow_smem(plan_pages, (4 * MAX_ROWS + 3) * (int)sizeof(int), ready);
+    cudaError_t e = lfr::allow_smem(plan_pages, (4 * MAX_ROWS + 3) * (int)sizeof(int), ready);
     if (e != cudaSuccess) return e;
-    return lfr::launch(plan_pages, dim3((unsigned)ctas), threads, smem, ctas, s, p, ctas, shift);
+    e = lfr::launch(plan_pages, dim3((unsigned)ctas), threads, (4 * p.n + 3) * (int)sizeof(int), ctas, s, p, ctas, shift, with_tokens);
+    if (e != cudaSuccess || with_tokens) return e;
+    return lfr::launch(plan_tokens, dim3((unsigned)((p.max_tokens + 1023) / 1024)), 256, (p.n + 1) * (int)sizeof(int), 1, s, p, shift);
 }
 
 cudaError_t launch_append(const Pool &c, const Rows &k, const Rows &v, int n, const int *slots, cudaStream_t s)

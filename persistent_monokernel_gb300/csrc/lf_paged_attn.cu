@@ -204,7 +204,7 @@ struct Work {
 #pragma unroll
             for (int i = 0; i < NT; ++i) sc[n][i][0] = sc[n][i][1] = sc[n][i][2] = sc[n][i][3] = 0.f;
         const uint32_t ka = ks + (lane & 15) * (HD * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
-        constexpr int KB = 4;                                // fragments loaded ahead of their products
+        constexpr int KB = QT * NT < 6 ? 4 : 2;              // fragments loaded ahead of their products (registers run out)
 #pragma unroll
         for (int k0 = 0; k0 < KS; k0 += KB) {
             unsigned x[KB][4];
