@@ -595,7 +595,7 @@ LF_API lf_status lf_paged_workspace(const lf_paged *c, const lf_paged_query *q, 
  * (NULL, alignment, strides, negative sizes, a scale that is not finite, dtypes that
  * differ or are neither, out = q, a workspace that is too small), NOT_SUPPORTED
  * (sizes of the cache, n_heads no multiple of n_kv_heads, n_seqs * n_heads above
- * 2^31 - 1, table_width, or 2^50 slabs of 16 positions over all heads), CUDA. */
+ * 2^27, table_width * page above 2^30), CUDA. */
 LF_API lf_status lf_paged_attend(const lf_paged *c, const lf_paged_query *q, void *workspace, int64_t workspace_bytes,
                                  void *stream);
 

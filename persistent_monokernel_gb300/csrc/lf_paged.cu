@@ -337,11 +337,8 @@ lf_status make_attn(const lf_paged *c, const lf_paged_query *q, Attn *a, size_t 
     if (q->n_heads % c->n_kv_heads) return LF_ERR_NOT_SUPPORTED;
     if (q->q.dtype != LF_F16 && q->q.dtype != LF_BF16 && q->q.dtype != LF_F32) return LF_ERR_NOT_SUPPORTED;
     if (q->q.dtype != LF_F32 && q->q.dtype != c->dtype) return LF_ERR_INVALID_ARG;
-    // positions, blocks of the join and the shares of a launch in their types
-    const long long seen = (long long)q->table_width * c->page;
-    if (seen > (1 << 30) || (long long)q->n_seqs * q->n_heads > INT32_MAX ||
-        (double)q->n_seqs * q->n_heads * (double)(seen / 16 + 1) > 0x1p50)
-        return LF_ERR_NOT_SUPPORTED;
+    // positions and blocks of a launch (at most 8 per row and head) in 32 bits
+    if ((long long)q->table_width * c->page > (1 << 30) || (long long)q->n_seqs * q->n_heads > (1 << 27)) return LF_ERR_NOT_SUPPORTED;
     a->c = pool_of(c);
     a->q = rows_of(&q->q);
     a->tables = q->tables;

@@ -100,13 +100,14 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Positions that a sequence's query sees, [lo, hi), and the slabs that hold them, [s0, s1).
+// Positions that a sequence's query sees and the table has, [lo, hi), and the slabs that hold them, [s0, s1).
 struct Seen {
     int lo, hi, s0, s1;
     __device__ __forceinline__ Seen(const Attn &a, int len)
     {
-        hi = max(0, (int)min((long long)len, (long long)a.width * a.c.page));
-        lo = a.win > 0 && hi > a.win ? hi - a.win : 0;
+        lo = a.win > 0 && len > a.win ? len - a.win : 0;
+        hi = (int)min((long long)len, (long long)a.width * a.c.page);
+        if (hi <= lo) lo = hi = 0;
         s0 = lo >> 4;
         s1 = (hi + 15) >> 4;
     }
