@@ -49,6 +49,7 @@ struct Attn {
     float scale;
     // launch: `parts` clusters of `cl` CTAs of `cw` warps (4 or 8) for each sequence and tile
     int cl, cw, parts;
+    int sorted;             // the clusters take long sequences first (parts 1)
     float *part;            // [n * ht][parts] partial states of rt * (hd + 4) floats (parts > 1)
 };
 

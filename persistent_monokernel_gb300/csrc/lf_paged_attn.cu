@@ -87,6 +87,12 @@ __device__ __forceinline__ void split_pair(float x, float y, unsigned (&out)[N])
     }
 }
 
+__device__ __forceinline__ void sts(uint32_t at, unsigned x) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory"); }
+__device__ __forceinline__ void lds2(unsigned (&x)[2], uint32_t at)
+{
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(at));
+}
+
 // 16 bytes global -> shared, zeros where `bytes` is 0 (nothing is read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const char *src, unsigned bytes)
 {
@@ -134,10 +140,14 @@ struct Work {
     static constexpr int KS = HD / 16, RT = 8 * NT;
     static constexpr int PT = QT > 1 ? QT : std::is_same_v<T, __half> ? 1 : 2;   // terms of P
     static constexpr float P_EXP = 7.f, P_SUM = 32768.f;
-    unsigned q[QT][NT][KS][2];
+    // q's fragments: in registers, or where they would take 96 of them in shared memory, one copy for the CTA
+    static constexpr bool QS = QT * NT >= 6;
+    static constexpr int Q_BYTES = QS ? NT * KS * 32 * QT * 8 : 0;
+    unsigned q[QS ? 1 : QT][QS ? 1 : NT][QS ? 1 : KS][2];
+    uint32_t qs;
     float f[NT][2], ref[NT][2], l[NT][2], o[NT][KS][4];
 
-    __device__ __forceinline__ void begin(const Attn &a, int row, int ht, int lane)
+    __device__ __forceinline__ void begin(const Attn &a, int row, int ht, int warp, int warps, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
         const int kvh = ht / a.tiles, h0 = (ht - kvh * a.tiles) * RT;
@@ -177,7 +187,10 @@ struct Work {
                         unsigned w[QT];
                         split_pair<T, QT>(x[k][u].x * r, x[k][u].y * r, w);
 #pragma unroll
-                        for (int n = 0; n < QT; ++n) q[n][i][k][u] = w[n];
+                        for (int n = 0; n < QT; ++n) {
+                            if constexpr (!QS) q[n][i][k][u] = w[n];
+                            else if (k % warps == warp) sts(q_at(n, i, k, lane) + 4 * u, w[n]);
+                        }
                     }
                 f[i][0] = base / __shfl_sync(0xffffffffu, r, 8 * t);       // rows 2t and 2t + 1 of the tile
                 f[i][1] = base / __shfl_sync(0xffffffffu, r, 8 * t + 4);
@@ -188,6 +201,9 @@ struct Work {
             for (int k = 0; k < KS; ++k) o[i][k][0] = o[i][k][1] = o[i][k][2] = o[i][k][3] = 0.f;
         }
     }
+
+    // Where term n of fragment (i, k) of this lane lies.
+    __device__ __forceinline__ uint32_t q_at(int n, int i, int k, int lane) const { return qs + (((n * NT + i) * KS + k) * 32 + lane) * 8; }
 
     // One slab from position p on, of which [lo, hi) counts; ks, vs: its rows in shared memory, 16-byte groups XOR-ed
     // with the position mod 8 (so that the 8 rows of a fragment lie in different banks).  `meanwhile` runs while the
@@ -205,7 +221,7 @@ struct Work {
 #pragma unroll
             for (int i = 0; i < NT; ++i) sc[n][i][0] = sc[n][i][1] = sc[n][i][2] = sc[n][i][3] = 0.f;
         const uint32_t ka = ks + (lane & 15) * (HD * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
-        constexpr int KB = QT * NT < 6 ? 4 : 2;              // fragments loaded ahead of their products (registers run out)
+        constexpr int KB = 4;                                // fragments loaded ahead of their products
 #pragma unroll
         for (int k0 = 0; k0 < KS; k0 += KB) {
             unsigned x[KB][4];
@@ -216,7 +232,15 @@ struct Work {
 #pragma unroll
                 for (int n = 0; n < QT; ++n)
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) Half16<T>::mma(sc[QT == 1 ? k % CH : n][i], x[k], q[n][i][k0 + k]);
+                    for (int i = 0; i < NT; ++i) {
+                        if constexpr (QS) {
+                            unsigned b[2];
+                            lds2(b, q_at(n, i, k0 + k, lane));
+                            Half16<T>::mma(sc[n][i], x[k], b);
+                        } else {
+                            Half16<T>::mma(sc[QT == 1 ? k % CH : n][i], x[k], q[n][i][k0 + k]);
+                        }
+                    }
         }
         meanwhile();
 #pragma unroll
@@ -471,6 +495,52 @@ __device__ __forceinline__ int parts_of(const Attn &a, int slabs)
     return min(a.parts, max(1, slabs / (a.cl * a.cw * MIN_SLABS)));
 }
 
+// The row that comes `rank`-th where long ones come first: in classes of like numbers of slabs (two per octave), in row
+// order within one.  Where the clusters come in several rounds the last one then is of short rows (200 rows of up to
+// 20,000 positions, most of them short, FP32 queries: 182 us, 202 in row order).  Called by all threads; `scratch`: 65 words
+// of shared memory, free again after the next barrier.
+__device__ __forceinline__ int row_by_length(const Attn &a, int rank, int *scratch)
+{
+    auto class_of = [&](int r) {
+        const int n = Seen(a, lfq::ld(a.lens + r)).slabs();
+        if (n == 0) return 0;
+        const int top = 31 - __clz(n);                       // 0 .. 26
+        return 2 * top + 1 + (top ? n >> (top - 1) & 1 : 0);  // 1 .. 54
+    };
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 64) scratch[threadIdx.x] = 0;
+    __syncthreads();
+    for (int r = threadIdx.x; r < a.n; r += blockDim.x) atomicAdd(scratch + class_of(r), 1);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        // lane l: classes 63 - 2 l and 62 - 2 l, the longest first
+        const int x = scratch[63 - 2 * lane], y = scratch[62 - 2 * lane];
+        int incl = x + y;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += z;
+        }
+        const int at = __ffs(__ballot_sync(0xffffffffu, incl > rank)) - 1;    // (all rows are counted: there is one)
+        const int before = __shfl_sync(0xffffffffu, incl - x - y, at), first = __shfl_sync(0xffffffffu, x, at);
+        int left = rank - before, cls = 63 - 2 * at;
+        if (left >= first) left -= first, --cls;
+        for (int base = 0; base < a.n; base += 32) {
+            const bool mine = base + lane < a.n && class_of(base + lane) == cls;
+            unsigned set = __ballot_sync(0xffffffffu, mine);
+            const int count = __popc(set);
+            if (left < count) {
+                while (left--) set &= set - 1;
+                if (lane == 0) scratch[64] = base + __ffs(set) - 1;
+                break;
+            }
+            left -= count;
+        }
+    }
+    __syncthreads();
+    return scratch[64];
+}
+
 template <int HD, int NT, class T, int QT, int CW>
 __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_constant__ Attn a)
 {
@@ -484,7 +554,9 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
     lfq::dependents_may_launch();
     lfq::wait_for_prerequisites();
     const int rank = blockIdx.x % a.cl, cluster = blockIdx.x / a.cl;
-    const int item = cluster / a.parts, part = cluster - item * a.parts, row = item / a.ht, ht = item - row * a.ht;
+    const int item = cluster / a.parts, part = cluster - item * a.parts, ht = item % a.ht;
+    const int row = a.sorted ? row_by_length(a, item / a.ht, reinterpret_cast<int *>(smem)) : item / a.ht;
+    if (a.sorted) __syncthreads();
     const int me = rank * CW + warp, kvh = ht / a.tiles;
     Feed<HD> feed;
     feed.lane = lane;
@@ -503,7 +575,9 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
     if (rank >= cl) return;
     feed.look_up(a, row, kvh, seen.s0 + me, nw, seen.s1);
     W work;
-    work.begin(a, row, ht, lane);
+    work.qs = lfk::smem_u32(feed.told + (CW - warp) * R::STAGES);
+    work.begin(a, row, ht, warp, CW, lane);
+    if (W::QS) __syncthreads();
     int s = seen.s0 + me, j = 0;
     auto issue = [&](int st) {
         if (s < seen.s1) {
@@ -622,7 +696,7 @@ static cudaError_t run(const Attn &a, cudaStream_t s)
     using O = std::conditional_t<QT == 1, T, float>;
     static bool ready[2][64] = {};
     auto go = [&](auto warps, bool (&ready)[64]) {
-        constexpr int CW = decltype(warps)::value, smem = Ring<HD>::bytes(CW);
+        constexpr int CW = decltype(warps)::value, smem = Ring<HD>::bytes(CW) + Work<HD, NT, T, QT>::Q_BYTES;
         const cudaError_t e = lfr::allow_smem(attn_cluster<HD, NT, T, QT, CW>, smem, ready);
         if (e != cudaSuccess) return e;
         return lfr::launch(attn_cluster<HD, NT, T, QT, CW>, dim3((unsigned)(a.n * a.ht * a.parts * a.cl)), CW * 32, smem, a.cl, s, a);
@@ -644,10 +718,14 @@ static cudaError_t run(const Attn &a, cudaStream_t s)
 
 // The lengths are known on the device alone, so the launch goes by what the host knows: the items (sequences x tiles)
 // and the slabs that the widest row may have.  Two CTAs of four warps fit an SM (304 places on 152).
-//   * Clusters as large as the items leave places for, with two slabs a warp at least (a sixth CTA per place costs
-//     more than the warps it adds: 16 x 5 heads of 512 positions take 6.2 us in clusters of two, 8.3 of four, 13.3 of
-//     eight).  Beyond the places only where a warp still has 8 cl slabs: smaller shares even out rows of different
-//     lengths (64 x 8 heads of up to 16,384: 331 us in single CTAs, 310 in twos, 298 in fours, 303 in eights).
+//   * Clusters as large as the items leave places for, with two slabs a warp at least (16 x 5 heads of 512 positions:
+//     6.2 us in clusters of two, 8.3 in fours, 13.3 in eights, of which most places have to wait for).
+//   * Beyond the places larger clusters only where rows are so long that the last ones would run alone: a row is then
+//     not one CTA's (16 x 8 heads of up to 32,768: 232 us in single CTAs, 91 in clusters of four, 80 of eight).
+//   * More items than places, of 4,096 positions or more, are taken long ones first, which costs each CTA half a
+//     microsecond (up to 256 rows) and does with smaller clusters: 64 x 8 heads of up to 16,384 positions 295 us in
+//     twos (302 in fours, in row order), of 4,096 81 in single CTAs (84 in twos, in row order), 200 x 2 heads of 16
+//     queries each, most of them short, a few of 20,000, 138 in fours (144).
 //   * Few items of many slabs leave SMs idle in one cluster each: up to 17 items of 12,288 positions or more are cut into
 //     parts, as many clusters of four as fit (280 CTAs: the last clusters find no group of SMs that is free), and a second
 //     launch joins them (3 us; one sequence of 5 heads at 32,768: 19.8 us in parts, 23.4 in clusters of eight CTAs of
@@ -663,8 +741,9 @@ size_t plan_attn(Attn &a, int sms)
     long long slabs = ((long long)a.width * a.c.page + 15) / 16;
     if (a.win > 0) slabs = std::min<long long>(slabs, a.win / 16 + 2);
     a.cl = 1, a.cw = 4, a.parts = 1;
+    a.sorted = items > places && slabs >= 256 && a.n > 1 && a.n <= 256;
     for (int cl = 2; cl <= 8; cl *= 2)
-        if (slabs >= 8 * cl && (items * cl <= places || slabs >= 32 * cl * cl)) a.cl = cl;
+        if (slabs >= 8 * cl && (items * cl <= places || slabs >= (a.sorted ? 72 : 32) * cl * cl)) a.cl = cl;
     const long long parts = places * 280 / 304 / (4 * items);
     if (slabs >= 768 && parts >= 4) {
         a.cl = 4;

@@ -446,13 +446,13 @@ PyObject *paged_attend(PyObject *, PyObject *const *args, Py_ssize_t n_args)
                 made = empty(x.sizes(), x.scalar_type(), c.device);
                 q.out = {made.mutable_data_ptr(), q.q.dtype, q.n_heads * (int64_t)cache.head_dim, cache.head_dim};
             }
-            // scratch of this call alone: no two streams or captured graphs share it
-            at::Tensor ws;
+            // Scratch, where a call needs some (few long sequences do), is that call's alone: no two streams or captured
+            // graphs share it.
+            st = g_paged_attend(&cache, &q, nullptr, 0, stream);
             int64_t need = 0;
-            st = g_paged_workspace(&cache, &q, &need);
-            if (st == LF_OK) {
-                if (need) ws = empty({need}, at::kByte, c.device);
-                st = g_paged_attend(&cache, &q, need ? ws.mutable_data_ptr() : nullptr, need, stream);
+            if (st == LF_ERR_INVALID_ARG && g_paged_workspace(&cache, &q, &need) == LF_OK && need > 0) {
+                const at::Tensor ws = empty({need}, at::kByte, c.device);
+                st = g_paged_attend(&cache, &q, ws.mutable_data_ptr(), need, stream);
             }
         }
         return out == Py_None ? THPVariable_Wrap(std::move(made)) : Py_NewRef(out);
