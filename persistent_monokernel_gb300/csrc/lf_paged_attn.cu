@@ -138,7 +138,7 @@ struct Ring {
 template <int HD, int NT, class T, int QT>
 struct Work {
     static constexpr int KS = HD / 16, RT = 8 * NT;
-    static constexpr int PT = QT > 1 ? QT : std::is_same_v<T, __half> ? 1 : 2;   // terms of P
+    static constexpr int PT = QT > 1 ? QT : 2;               // terms of P
     static constexpr float P_EXP = 7.f, P_SUM = 32768.f;
     // q's fragments: in registers, or where they would take 96 of them in shared memory, one copy for the CTA
     static constexpr bool QS = QT * NT >= 6;
@@ -299,19 +299,12 @@ struct Work {
         unsigned pb[PT][NT][2];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            if (PT > 1) {
-                l[i][0] += sum[i][0];
-                l[i][1] += sum[i][1];
-            }
+            l[i][0] += sum[i][0];
+            l[i][1] += sum[i][1];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 unsigned w[PT];
                 split_pair<T, PT>(pr[i][2 * u], pr[i][2 * u + 1], w);
-                if (PT == 1) {       // the sum of the rounded ones: weights that still add up to one
-                    const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&w[0]));
-                    l[i][0] += r.x;
-                    l[i][1] += r.y;
-                }
 #pragma unroll
                 for (int n = 0; n < PT; ++n) pb[n][i][u] = lfk::movm_t(w[n]);
             }
@@ -717,15 +710,17 @@ static cudaError_t run(const Attn &a, cudaStream_t s)
 }
 
 // The lengths are known on the device alone, so the launch goes by what the host knows: the items (sequences x tiles)
-// and the slabs that the widest row may have.  Two CTAs of four warps fit an SM (304 places on 152).
+// and the slabs that the widest row may have (of 8 KB: narrow heads' count half).  Two CTAs of four warps fit an SM (304
+// places on 152).
 //   * Clusters as large as the items leave places for, with two slabs a warp at least (16 x 5 heads of 512 positions:
-//     6.2 us in clusters of two, 8.3 in fours, 13.3 in eights, of which most places have to wait for).
-//   * Beyond the places larger clusters only where rows are so long that the last ones would run alone: a row is then
-//     not one CTA's (16 x 8 heads of up to 32,768: 232 us in single CTAs, 91 in clusters of four, 80 of eight).
-//   * More items than places, of 4,096 positions or more, are taken long ones first, which costs each CTA half a
-//     microsecond (up to 256 rows) and does with smaller clusters: 64 x 8 heads of up to 16,384 positions 295 us in
-//     twos (302 in fours, in row order), of 4,096 81 in single CTAs (84 in twos, in row order), 200 x 2 heads of 16
-//     queries each, most of them short, a few of 20,000, 138 in fours (144).
+//     6.2 us in clusters of two, 8.3 in fours, 13.3 in eights, of which most have to wait for places).
+//   * More items than places: long ones first, which costs each CTA half a microsecond (up to 256 rows, where one has
+//     2,048 positions or more).  Clusters then only up to three rounds of items, and only where a warp still has 40 slabs
+//     of a row: 64 x 8 heads of up to 16,384 positions take 295 us in twos (310 in single CTAs, 302 in fours and in row
+//     order), of 4,096 81 in single CTAs (86 in twos); 200 x 2 heads of 16 FP32 queries each, skewed to 20,000,
+//     167 in fours (200 in twos, 368 in single CTAs, 202 in fours and in row order).
+//   * Fewer items whose clusters need rounds: as large as leaves 8 cl slabs a warp (16 x 8 heads skewed to 32,768:
+//     232 us in single CTAs, 91 in fours, 80 in eights).
 //   * Few items of many slabs leave SMs idle in one cluster each: up to 17 items of 12,288 positions or more are cut into
 //     parts, as many clusters of four as fit (280 CTAs: the last clusters find no group of SMs that is free), and a second
 //     launch joins them (3 us; one sequence of 5 heads at 32,768: 19.8 us in parts, 23.4 in clusters of eight CTAs of
@@ -741,9 +736,12 @@ size_t plan_attn(Attn &a, int sms)
     long long slabs = ((long long)a.width * a.c.page + 15) / 16;
     if (a.win > 0) slabs = std::min<long long>(slabs, a.win / 16 + 2);
     a.cl = 1, a.cw = 4, a.parts = 1;
-    a.sorted = items > places && slabs >= 256 && a.n > 1 && a.n <= 256;
-    for (int cl = 2; cl <= 8; cl *= 2)
-        if (slabs >= 8 * cl && (items * cl <= places || slabs >= (a.sorted ? 72 : 32) * cl * cl)) a.cl = cl;
+    const long long wide = slabs * a.c.hd / 128;
+    a.sorted = items > places && wide >= 128 && a.n > 1 && a.n <= 256;
+    for (int cl = 2; cl <= 8; cl *= 2) {
+        const bool rounds = a.sorted ? items * cl / 2 < 3 * places && wide >= 160 * cl : wide >= 32 * cl * cl;
+        if (slabs >= 8 * cl && (items * cl <= places || rounds)) a.cl = cl;
+    }
     const long long parts = places * 280 / 304 / (4 * items);
     if (slabs >= 768 && parts >= 4) {
         a.cl = 4;

@@ -60,7 +60,7 @@ def attend(q, k, v, tables, lens, window=0, scale=0.0):
       - the score's error: head_dim products summed in 32 bits with cut sums, 2^-23 of sum |q_d k_d| a step; q as the sum
         of two FP16 terms (2^-22, and 2^-25 of the row's largest value where a term runs out of exponents) or three
         BF16 ones (2^-24); the exponent's arithmetic, 2^-22 of the score and its largest; exp2 itself, 2^-21;
-      - the rounding of P: one FP16 term 2^-11, two BF16 terms 2^-16, with FP32 queries 2^-22.
+      - the rounding of P: two FP16 terms 2^-22, two BF16 terms 2^-16 (three with FP32 queries, 2^-24).
     FP16 terms of P end at 2^-24, half a step 2^-25 of a largest P of 2^6 at least: n 2^-31 max|v|.  O's own sum:
     n / 8 steps of 2^-23 of sum p_j |v_j| (and 64 for the joins); then the output's half step."""
     n_pages, hkv, page, hd = k.shape
@@ -69,7 +69,7 @@ def attend(q, k, v, tables, lens, window=0, scale=0.0):
     scale = scale or 1 / math.sqrt(hd)
     out = torch.zeros(n, heads, hd, dtype=torch.float64, device=q.device)
     bound = torch.zeros_like(out)
-    p_step = 2.0 ** -22 if f32 else 2.0 ** -11 if k.dtype == torch.float16 else 2.0 ** -16
+    p_step = 2.0 ** -22 if f32 or k.dtype == torch.float16 else 2.0 ** -16
     for i in range(n):
         pages, places = visible(tables, lens, i, page, window, n_pages)
         if not len(pages):
