@@ -84,28 +84,29 @@ __global__ void __launch_bounds__(1024) plan_pages(const __grid_constant__ Plan 
 {
     extern __shared__ int smem[];
     int *const kept = smem, *const tok = kept + p.n, *const back = tok + p.n + 1, *const need = back + p.n + 1;
-    __shared__ long long wsum[3][33];
+    __shared__ unsigned wsum[4][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     lfq::dependents_may_launch();
     lfq::wait_for_prerequisites();
     auto pages = [&](int x) { return x ? page_of(p, shift, x - 1) + 1 : 0; };
 
-    // ---- the rows' numbers, and their sums up to each row
+    // ---- the rows' numbers (new tokens, pages back, pages needed), and their sums up to each row.  The sums saturate:
+    // one that leaves 32 bits is more than any pool or max_tokens.
     const int per = (p.n + blockDim.x - 1) / blockDim.x;
     const int r0 = min(tid * per, p.n), r1 = min(r0 + per, p.n);
     const long long cap = (long long)p.max_pages * p.page;
     const int n_free = lfq::ld(p.n_free);
-    int wrong = n_free < 0 || n_free > p.n_pages ? LF_ERR_INVALID_ARG : 0;
-    auto row = [&](int r, long long (&x)[3]) {
+    unsigned wrong = n_free < 0 || n_free > p.n_pages ? 1u : 0u;         // bit 0: INVALID_ARG, bit 1: CAPACITY
+    auto row = [&](int r, unsigned (&x)[3]) {
         const int len = lfq::ld(p.lens + r), n_new = lfq::ld(p.n_new + r);
         const int keep = p.keep ? lfq::ld(p.keep + r) : len, k = min(len, keep);
         x[0] = x[1] = x[2] = 0;
         if (len < 0 || len > cap || keep < 0 || n_new < 0) {
-            wrong = LF_ERR_INVALID_ARG;
+            wrong |= 1u;
             return 0;
         }
         if ((long long)k + n_new > cap) {
-            if (!wrong) wrong = LF_ERR_CAPACITY;
+            wrong |= 2u;
             return 0;
         }
         x[0] = n_new;
@@ -113,54 +114,54 @@ __global__ void __launch_bounds__(1024) plan_pages(const __grid_constant__ Plan 
         x[2] = pages(k + n_new) - pages(k);
         return k;
     };
-    long long mine[3] = {0, 0, 0}, at[3];
+    auto plus = [](unsigned x, unsigned y) { return x + y < x ? 0xffffffffu : x + y; };
+    unsigned x[3] = {0, 0, 0}, mine[3] = {0, 0, 0}, at[3], sum[3];
+    int k0 = 0;
     for (int r = r0; r < r1; ++r) {
-        long long x[3];
-        row(r, x);
-        for (int i = 0; i < 3; ++i) mine[i] += x[i];
+        k0 = row(r, x);
+        for (int i = 0; i < 3; ++i) mine[i] = plus(mine[i], x[i]);
     }
+    auto scan = [&](unsigned (&v)[3]) {              // inclusive, over the lanes
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        long long incl = mine[i];
+        for (int d = 1; d < 32; d <<= 1)
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += x;
-        }
-        if (lane == 31) wsum[i][warp] = incl;
-        at[i] = incl - mine[i];
+            for (int i = 0; i < 3; ++i) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, v[i], d);
+                if (lane >= d) v[i] = plus(v[i], y);
+            }
+    };
+    unsigned incl[3] = {mine[0], mine[1], mine[2]}, all_w[3];
+    scan(incl);
+    const unsigned some = __reduce_or_sync(0xffffffffu, wrong);
+    if (lane == 31) wsum[0][warp] = incl[0], wsum[1][warp] = incl[1], wsum[2][warp] = incl[2], wsum[3][warp] = some;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {                    // up to this thread's rows
+        const unsigned before = __shfl_up_sync(0xffffffffu, incl[i], 1);
+        at[i] = lane ? before : 0u;
     }
     __syncthreads();
-    if (warp < 3) {                                  // the sums of the warps before each, and of all
-        const long long x = lane < warps ? wsum[warp][lane] : 0;
-        long long incl = x;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += y;
-        }
-        wsum[warp][lane] = incl - x;
-        if (lane == 31) wsum[warp][32] = incl;
-    }
-    __syncthreads();
-    long long sum[3];
+    for (int i = 0; i < 3; ++i) all_w[i] = lane < warps ? wsum[i][lane] : 0u;
+    const unsigned all_wrong = __reduce_or_sync(0xffffffffu, lane < warps ? wsum[3][lane] : 0u);
+    scan(all_w);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        at[i] += wsum[i][warp];
-        sum[i] = wsum[i][32];
+        const unsigned before = __shfl_sync(0xffffffffu, all_w[i], max(warp - 1, 0));
+        at[i] = plus(at[i], warp ? before : 0u);
+        sum[i] = __shfl_sync(0xffffffffu, all_w[i], 31);
     }
     for (int r = r0; r < r1; ++r) {
-        long long x[3];
-        kept[r] = row(r, x);
-        tok[r] = (int)at[0], back[r] = (int)at[1], need[r] = (int)at[2];
-        for (int i = 0; i < 3; ++i) at[i] += x[i];
+        if (per > 1) k0 = row(r, x);
+        kept[r] = k0;
+        tok[r] = at[0], back[r] = at[1], need[r] = at[2];
+        for (int i = 0; i < 3; ++i) at[i] = plus(at[i], x[i]);
     }
-    if (tid == 0) tok[p.n] = (int)sum[0], back[p.n] = (int)sum[1], need[p.n] = (int)sum[2];
+    if (tid == 0) tok[p.n] = sum[0], back[p.n] = sum[1], need[p.n] = sum[2];
+    __syncthreads();
     // all or nothing: more pages given back than the pool has (tables that are not a plan's), or too few for the rows
-    const long long top64 = n_free + sum[1];
-    if (!wrong && top64 > p.n_pages) wrong = LF_ERR_INVALID_ARG;
-    if (!wrong && (sum[2] > top64 || sum[0] > p.max_tokens)) wrong = LF_ERR_CAPACITY;
-    const bool invalid = __syncthreads_or(wrong == LF_ERR_INVALID_ARG), fails = __syncthreads_or(wrong != 0);
+    const long long top64 = (long long)n_free + sum[1];
+    const bool invalid = (all_wrong & 1u) || top64 > p.n_pages;
+    const bool fails = invalid || (all_wrong & 2u) || sum[2] > top64 || sum[0] > (unsigned)p.max_tokens;
     const int all = ctas * blockDim.x, me = blockIdx.x * blockDim.x + tid;
     const int tokens = fails ? 0 : (int)sum[0], n_back = (int)sum[1], n_need = (int)sum[2], top = (int)top64;
 
@@ -256,7 +257,7 @@ cudaError_t launch_plan(const Plan &p, cudaStream_t s)
     // One CTA, or a cluster of them where there may be thousands of pages to move: new tokens' and given back ones.
     const bool with_tokens = p.max_tokens <= 4096;
     const long long moves = (long long)p.max_tokens / p.page + p.n;
-    const int ctas = moves <= 2048 ? 1 : moves <= 8192 ? 4 : 8, threads = p.n <= 256 && p.max_tokens <= 1024 ? 256 : 1024;
+    const int ctas = moves <= 1024 ? 1 : moves <= 2048 ? 2 : moves <= 4096 ? 4 : 8, threads = p.n <= 256 && p.max_tokens <= 1024 ? 256 : 1024;
     int shift = -1;
     for (int i = 4; i < 31; ++i)
         if (p.page == 1 << i) shift = i;
