@@ -48,41 +48,49 @@ struct Half16;
 template <>
 struct Half16<__half> {
     static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
-    static __device__ __forceinline__ float to(__half x) { return __half2float(x); }
-    static __device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], const unsigned (&b)[2])
+    static __device__ __forceinline__ unsigned pair(float x, float y)
     {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const unsigned *>(&h);
+    }
+    static __device__ __forceinline__ float2 values(unsigned p) { return __half22float2(*reinterpret_cast<const __half2 *>(&p)); }
+    // d = a b + (d, or 0)
+    static __device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], const unsigned (&b)[2], bool first = false)
+    {
+        const float c[4] = {first ? 0.f : d[0], first ? 0.f : d[1], first ? 0.f : d[2], first ? 0.f : d[3]};
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
     }
 };
 template <>
 struct Half16<__nv_bfloat16> {
     static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
-    static __device__ __forceinline__ float to(__nv_bfloat16 x) { return __bfloat162float(x); }
-    static __device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], const unsigned (&b)[2])
+    static __device__ __forceinline__ unsigned pair(float x, float y)
     {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const unsigned *>(&h);
+    }
+    static __device__ __forceinline__ float2 values(unsigned p) { return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)); }
+    static __device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], const unsigned (&b)[2], bool first = false)
+    {
+        const float c[4] = {first ? 0.f : d[0], first ? 0.f : d[1], first ? 0.f : d[2], first ? 0.f : d[3]};
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
     }
 };
-template <class T>
-__device__ __forceinline__ unsigned pack(T lo, T hi)
-{
-    return (unsigned)*reinterpret_cast<unsigned short *>(&lo) | ((unsigned)*reinterpret_cast<unsigned short *>(&hi) << 16);
-}
 // x and y as sums of N terms of type T, the largest first: pairs (term of x, term of y)
 template <class T, int N>
 __device__ __forceinline__ void split_pair(float x, float y, unsigned (&out)[N])
 {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const T a = Half16<T>::from(x), b = Half16<T>::from(y);
-        out[i] = pack(a, b);
+        out[i] = Half16<T>::pair(x, y);
         if (i + 1 < N) {
-            x -= Half16<T>::to(a);
-            y -= Half16<T>::to(b);
+            const float2 v = Half16<T>::values(out[i]);
+            x -= v.x;
+            y -= v.y;
         }
     }
 }
@@ -140,8 +148,8 @@ struct Work {
     static constexpr int KS = HD / 16, RT = 8 * NT;
     static constexpr int PT = QT > 1 ? QT : 2;               // terms of P
     static constexpr float P_EXP = 7.f, P_SUM = 32768.f;
-    // q's fragments: in registers, or where they would take 96 of them in shared memory, one copy for the CTA
-    static constexpr bool QS = QT * NT >= 6;
+    // q's fragments: in registers, or where they would take 64 of them or 96 in shared memory, one copy for the CTA
+    static constexpr bool QS = QT * NT >= 4;
     static constexpr int Q_BYTES = QS ? NT * KS * 32 * QT * 8 : 0;
     unsigned q[QS ? 1 : QT][QS ? 1 : NT][QS ? 1 : KS][2];
     uint32_t qs;
@@ -216,10 +224,6 @@ struct Work {
         // same sum: CH sums, by the terms of q or the dims' halves, are on their way at a time.
         constexpr int CH = QT > 1 ? QT : NT == 1 ? 4 : 2;
         float st[NT][4], sc[CH][NT][4];
-#pragma unroll
-        for (int n = 0; n < CH; ++n)
-#pragma unroll
-            for (int i = 0; i < NT; ++i) sc[n][i][0] = sc[n][i][1] = sc[n][i][2] = sc[n][i][3] = 0.f;
         const uint32_t ka = ks + (lane & 15) * (HD * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
         constexpr int KB = 4;                                // fragments loaded ahead of their products
 #pragma unroll
@@ -233,12 +237,14 @@ struct Work {
                 for (int n = 0; n < QT; ++n)
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
+                        const int to = QT == 1 ? k % CH : n;
+                        const bool first = QT == 1 ? k0 + k < CH : k0 + k == 0;
                         if constexpr (QS) {
                             unsigned b[2];
                             lds2(b, q_at(n, i, k0 + k, lane));
-                            Half16<T>::mma(sc[n][i], x[k], b);
+                            Half16<T>::mma(sc[to][i], x[k], b, first);
                         } else {
-                            Half16<T>::mma(sc[QT == 1 ? k % CH : n][i], x[k], q[n][i][k0 + k]);
+                            Half16<T>::mma(sc[to][i], x[k], q[n][i][k0 + k], first);
                         }
                     }
         }
@@ -331,10 +337,7 @@ struct Work {
 #pragma unroll
                     for (int n = PT - 1; n >= 0; --n)
 #pragma unroll
-                        for (int k = 0; k < KB; ++k) {
-                            if (n == PT - 1) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.f;
-                            Half16<T>::mma(y[k], x[k], pb[n][i]);
-                        }
+                        for (int k = 0; k < KB; ++k) Half16<T>::mma(y[k], x[k], pb[n][i], n == PT - 1);
 #pragma unroll
                     for (int k = 0; k < KB; ++k)
 #pragma unroll
@@ -441,30 +444,26 @@ struct Feed {
     {
         constexpr int CPR = HD / 8, RPI = 32 / CPR, N = 16 / RPI;   // 16-byte groups a row, rows per instruction
         const long long at = __shfl_sync(0xffffffffu, place, j);
-        const uint32_t dst = base + st * 2 * R::SLAB;
         const int r0 = lane / CPR, c = lane % CPR, p = w.s * 16;
+        // row r = i RPI + r0, and (r mod 8) = (i RPI mod 8) xor r0
+        const uint32_t dst = base + st * 2 * R::SLAB + r0 * (HD * 2), swz = (uint32_t)(c ^ r0) << 4;
+        auto to = [&](int i) { return dst + i * RPI * (HD * 2) + (swz ^ (i * RPI % 8 << 4)); };
         const bool none = at < 0, whole = !none && p >= w.lo && p + 16 <= w.hi;
         const char *k = a.c.k + (none ? 0 : at) + r0 * a.c.pos_b + c * 16, *v = k + (a.c.v - a.c.k);
         const long long step = RPI * a.c.pos_b;
         if (whole) {
 #pragma unroll
-            for (int i = 0; i < N; ++i, k += step) {
-                const int r = i * RPI + r0;
-                copy16(dst + r * (HD * 2) + ((c ^ (r & 7)) << 4), k);
-            }
+            for (int i = 0; i < N; ++i, k += step) copy16(to(i), k);
 #pragma unroll
-            for (int i = 0; i < N; ++i, v += step) {
-                const int r = i * RPI + r0;
-                copy16(dst + R::SLAB + r * (HD * 2) + ((c ^ (r & 7)) << 4), v);
-            }
+            for (int i = 0; i < N; ++i, v += step) copy16(to(i) + R::SLAB, v);
         } else {
             // rows that do not count become zeros (what they hold may be anything, and 0 x inf is not 0)
+#pragma unroll
             for (int i = 0; i < N; ++i, k += step, v += step) {
                 const int r = i * RPI + r0;
                 const bool in = !none && p + r >= w.lo && p + r < w.hi;
-                const uint32_t d = dst + r * (HD * 2) + ((c ^ (r & 7)) << 4);
-                copy16(d, in ? k : a.c.k, in ? 16u : 0u);
-                copy16(d + R::SLAB, in ? v : a.c.v, in ? 16u : 0u);
+                copy16(to(i), in ? k : a.c.k, in ? 16u : 0u);
+                copy16(to(i) + R::SLAB, in ? v : a.c.v, in ? 16u : 0u);
             }
         }
         if (lane == 0) {
