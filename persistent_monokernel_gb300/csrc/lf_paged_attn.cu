@@ -719,8 +719,9 @@ static cudaError_t run(const Attn &a, cudaStream_t s)
 //     order), of 4,096 81 in single CTAs (86 in twos); 200 x 2 heads of 16 FP32 queries each, skewed to 20,000,
 //     167 in fours (200 in twos, 368 in single CTAs, 202 in fours and in row order).
 //   * Fewer items whose clusters need rounds: as large as leaves 8 cl slabs a warp (16 x 8 heads skewed to 32,768:
-//     232 us in single CTAs, 91 in fours, 80 in eights).
-//   * Few items of many slabs leave SMs idle in one cluster each: up to 17 items of 12,288 positions or more are cut into
+//     232 us in single CTAs, 91 in fours, 80 in eights), long ones first from 4,096 positions on (48 x 5 heads of up to
+//     4,096: 41.8 us, 45.3 in row order).
+//   * Few items of many slabs leave SMs idle in one cluster each: up to 23 items of 12,288 positions or more are cut into
 //     parts, as many clusters of four as fit (280 CTAs: the last clusters find no group of SMs that is free), and a second
 //     launch joins them (3 us; one sequence of 5 heads at 32,768: 19.8 us in parts, 23.4 in clusters of eight CTAs of
 //     eight warps; at 8,192 9.7 and 9.7; of 8 heads at 131,071: 80.5 and 88).
@@ -742,12 +743,13 @@ size_t plan_attn(Attn &a, int sms)
         if (slabs >= 8 * cl && (items * cl <= places || rounds)) a.cl = cl;
     }
     const long long parts = places * 280 / 304 / (4 * items);
-    if (slabs >= 768 && parts >= 4) {
+    if (slabs >= 768 && parts >= 3) {
         a.cl = 4;
         a.parts = (int)parts;
     } else if (a.cl == 8 && items * 8 <= sms && slabs >= 256) {
         a.cw = 8;
     }
+    if (a.parts == 1 && items * a.cl > places && wide >= 256 && a.n > 1 && a.n <= 256) a.sorted = 1;
     return a.parts > 1 ? (size_t)items * a.parts * a.rt * (a.c.hd + PADF) * sizeof(float) : 0;
 }
 
