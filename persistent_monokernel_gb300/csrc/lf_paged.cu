@@ -30,7 +30,9 @@ namespace lfpg {
 // table entries given back and taken anew), hence one cluster barrier between reading and writing.  Many tokens are
 // left to a second launch, which needs no more than the tables and offsets that the first one wrote.
 //
-// Bound by latency: the loads of the rows, the sums' shuffles, a search and two dependent loads per token.
+// Bound by latency: the loads of the rows, the sums' shuffles, a search and two dependent loads per token.  64 rows of one
+// token: 4.1 us; 500 rows, 71,360 tokens: 8.7 us (13.9 with all tokens in the one cluster, 10.0 with clusters of four
+// for the 5,000 pages), 8,000 rows: 25 us.
 __device__ __forceinline__ int row_of(const int *before, int n, int k)   // the last row with before[row] <= k
 {
     int lo = 0, hi = n - 1;
@@ -213,7 +215,8 @@ __global__ void __launch_bounds__(256) plan_tokens(const __grid_constant__ Plan 
 // ---------------------------------------------------------------- append
 
 // A thread moves 8 values (16 bytes of the cache); one grid row per KV head and K or V, so that no division but the
-// slot's finds a place.  Slots outside the pool store nothing.  Bound by memory, and by latency for few rows.
+// slot's finds a place.  Slots outside the pool store nothing.  Bound by memory (8,191 rows of 5 x 128, FP32 to FP16: 10.6 us,
+// 5.9 TB/s), and by the launch for few rows (64 of 8 x 128: 1.2 us).
 template <class TI, class TO>
 __global__ void __launch_bounds__(256) append_rows(const __grid_constant__ Pool c, const __grid_constant__ Rows k,
                                                    const __grid_constant__ Rows v, int n, const int *slots, int shift)
