@@ -226,7 +226,7 @@ struct Work {
     {
         const int g = lane >> 2;
         // ---- scores: position rows g, g + 8 by heads 2t, 2t + 1.  Each product waits for the one before it into the
-        // same sum: CH sums, by the terms of q or the dims' halves, are on their way at a time.
+        // same sum: CH sums, by the terms of q or by the dims in turn, are on their way at a time.
         constexpr int CH = QT > 1 ? QT : NT == 1 ? 4 : 2;
         float st[NT][4], sc[CH][NT][4];
         const uint32_t ka = ks + (lane & 15) * (HD * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
@@ -494,7 +494,7 @@ __device__ __forceinline__ int parts_of(const Attn &a, int slabs)
 
 // The row that comes `rank`-th where long ones come first: in classes of like numbers of slabs (two per octave), in row
 // order within one.  Where the clusters come in several rounds the last one then is of short rows (200 rows of up to
-// 20,000 positions, most of them short, FP32 queries: 182 us, 202 in row order).  Called by all threads; `scratch`: 65 words
+// 20,000 positions, most of them short, FP32 queries: 167 us, 202 in row order).  Called by all threads; `scratch`: 65 words
 // of shared memory, free again after the next barrier.
 __device__ __forceinline__ int row_by_length(const Attn &a, int rank, int *scratch)
 {

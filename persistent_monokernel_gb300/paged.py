@@ -82,9 +82,9 @@ class PageTables(OnStream):
         [n_seqs]).  keep[i] = 0 ends sequence i, and with n_new[i] lets another take its row; keep[i] < lens[i] takes
         drafted positions back.
 
-        Returns (slots, positions, offsets), int32: the new positions of all rows, packed in row order, slots
-        [max_tokens] for PagedKVCache.append, positions [max_tokens] within their sequences, and where each row's begin
-        [n_seqs + 1].  Behind the last one slots are -1 and positions 0.
+        Returns (slots, positions, offsets), int32 parts of one new allocation: the new positions of all rows, packed in
+        row order, slots [max_tokens] for PagedKVCache.append, positions [max_tokens] within their sequences, and where
+        each row's begin [n_seqs + 1].  Behind the last one slots are -1 and positions 0.
 
         All or nothing: where the pages, the rows' max_pages or max_tokens do not suffice, nothing changes, all slots
         are -1 and all offsets 0, and sync() tells."""
