@@ -133,17 +133,11 @@ struct Seen {
     __device__ __forceinline__ int slabs() const { return s1 - s0; }
 };
 
-// What a warp is told about a slab in its ring.
-struct Told {
-    int s, lo, hi;          // the slab, and the positions of it that count
-};
-
 template <int HD>
 struct Ring {
     static constexpr int SLAB = 16 * HD * 2;                 // bytes of K, and of V
     static constexpr int STAGES = 24576 / (2 * SLAB);        // 3 of 8 KB, 6 of 4
     static constexpr int COPIES = STAGES * 2 * SLAB;         // bytes of a warp's slabs
-    static constexpr int bytes(int warps) { return warps * (COPIES + STAGES * (int)sizeof(Told)); }
 };
 
 // A warp's softmax state and its products, for 8 NT query heads of one KV head.
@@ -424,58 +418,57 @@ struct Joined {
     __device__ __forceinline__ float4 ml() const { return make_float4(m0, l0, m1, l1); }
 };
 
-// The ring of one warp: where its slabs come from and what it is told of them.
+// The ring of one warp, and where its slabs come from.
 template <int HD>
 struct Feed {
     using R = Ring<HD>;
+    static constexpr int CPR = HD / 8, RPI = 32 / CPR, N = 16 / RPI;   // 16-byte groups a row, rows per instruction, instructions
     uint32_t base;
-    Told *told;
-    long long place;   // this lane's entry of the next 32 slabs: byte offset in the pools, -1 for none
     int lane;
+    long long place;   // this lane's entry of the next 32 slabs: byte offset in the pools, -1 for none
+    long long next;    // the next slab's (looked up ahead: a shuffle takes as long as two copies)
+    unsigned none;     // bit st: stage st holds zeros, its slab lies on no page of the pool
 
     // Looks the places of slabs s, s + step, .. (below end) up, one per lane.
     __device__ __forceinline__ void look_up(const Attn &a, int row, int kvh, int s, int step, int end)
     {
         const int pp = a.c.page >> 4, mine = s + lane * step;
         place = -1;
-        if (mine >= end) return;
-        const int col = mine / pp;
-        const int id = lfq::ld(a.tables + (size_t)row * a.tstride + col);
-        if ((unsigned)id < (unsigned)a.c.n_pages)
-            place = id * a.c.page_b + kvh * a.c.head_b + (long long)((mine - col * pp) * 16) * a.c.pos_b;
+        if (mine < end) {
+            const int col = mine / pp;
+            const int id = lfq::ld(a.tables + (size_t)row * a.tstride + col);
+            if ((unsigned)id < (unsigned)a.c.n_pages)
+                place = id * a.c.page_b + kvh * a.c.head_b + (long long)((mine - col * pp) * 16) * a.c.pos_b;
+        }
+        next = __shfl_sync(0xffffffffu, place, 0);
     }
-    // Begins the copies of slab s, the j-th that was looked up, into stage `st`.
-    __device__ __forceinline__ void fetch(const Attn &a, int st, int j, const Told &w)
+    // Begins the copies of the slab at position p, of which [lo, hi) counts, into stage `st`; it is the j-th that was
+    // looked up.
+    __device__ __forceinline__ void fetch(const Attn &a, int st, int j, int p, int lo, int hi)
     {
-        constexpr int CPR = HD / 8, RPI = 32 / CPR, N = 16 / RPI;   // 16-byte groups a row, rows per instruction
-        const long long at = __shfl_sync(0xffffffffu, place, j);
-        const int r0 = lane / CPR, c = lane % CPR, p = w.s * 16;
+        const int r0 = lane / CPR, c = lane % CPR;
         // row r = i RPI + r0, and (r mod 8) = (i RPI mod 8) xor r0
         const uint32_t dst = base + st * 2 * R::SLAB + r0 * (HD * 2), swz = (uint32_t)(c ^ r0) << 4;
         auto to = [&](int i) { return dst + i * RPI * (HD * 2) + (swz ^ (i * RPI % 8 << 4)); };
-        const bool none = at < 0, whole = !none && p >= w.lo && p + 16 <= w.hi;
-        const char *k = a.c.k + (none ? 0 : at) + r0 * a.c.pos_b + c * 16, *v = k + (a.c.v - a.c.k);
+        const bool gone = next < 0;
+        const char *k = a.c.k + next + r0 * a.c.pos_b + c * 16, *v = k + (a.c.v - a.c.k);
         const long long step = RPI * a.c.pos_b;
-        if (whole) {
+        none = gone ? none | 1u << st : none & ~(1u << st);
+        if (!gone && p >= lo && p + 16 <= hi) {
 #pragma unroll
-            for (int i = 0; i < N; ++i, k += step) copy16(to(i), k);
+            for (int i = 0; i < N; ++i) copy16(to(i), k + i * step);
 #pragma unroll
-            for (int i = 0; i < N; ++i, v += step) copy16(to(i) + R::SLAB, v);
+            for (int i = 0; i < N; ++i) copy16(to(i) + R::SLAB, v + i * step);
         } else {
             // rows that do not count become zeros (what they hold may be anything, and 0 x inf is not 0)
-#pragma unroll
-            for (int i = 0; i < N; ++i, k += step, v += step) {
+            for (int i = 0; i < N; ++i) {
                 const int r = i * RPI + r0;
-                const bool in = !none && p + r >= w.lo && p + r < w.hi;
-                copy16(to(i), in ? k : a.c.k, in ? 16u : 0u);
-                copy16(to(i) + R::SLAB, in ? v : a.c.v, in ? 16u : 0u);
+                const bool in = !gone && p + r >= lo && p + r < hi;
+                copy16(to(i), in ? k + i * step : a.c.k, in ? 16u : 0u);
+                copy16(to(i) + R::SLAB, in ? v + i * step : a.c.v, in ? 16u : 0u);
             }
         }
-        if (lane == 0) {
-            Told x = w;
-            if (none) x.hi = x.lo = 0;
-            told[st] = x;
-        }
+        next = __shfl_sync(0xffffffffu, place, j + 1);
     }
 };
 
@@ -558,7 +551,7 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
     Feed<HD> feed;
     feed.lane = lane;
     feed.base = lfk::smem_u32(smem) + warp * R::COPIES;
-    feed.told = reinterpret_cast<Told *>(smem + CW * R::COPIES) + warp * R::STAGES;
+    feed.none = 0;
     Seen seen(a, lfq::ld(a.lens + row));
     const int parts = parts_of(a, seen.slabs());
     if (part >= parts) return;   // (all CTAs of the cluster)
@@ -572,7 +565,7 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
     if (rank >= cl) return;
     feed.look_up(a, row, kvh, seen.s0 + me, nw, seen.s1);
     W work;
-    work.qs = lfk::smem_u32(feed.told + (CW - warp) * R::STAGES);
+    work.qs = lfk::smem_u32(smem) + CW * R::COPIES;
     work.begin(a, row, ht, warp, CW, lane);
     if (W::QS) __syncthreads();
     int s = seen.s0 + me, j = 0;
@@ -582,7 +575,7 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
                 j = 0;
                 feed.look_up(a, row, kvh, s, nw, seen.s1);
             }
-            feed.fetch(a, st, j, Told{s, seen.lo, seen.hi});
+            feed.fetch(a, st, j, s * 16, seen.lo, seen.hi);
             ++j;
             s += nw;
         }
@@ -595,9 +588,8 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
     for (int x = seen.s0 + me; x < seen.s1; x += nw) {
         copies_wait<R::STAGES - 2>();
         __syncwarp();
-        const Told t = feed.told[st];
         const uint32_t ks = feed.base + st * 2 * R::SLAB;
-        work.slab(ks, ks + R::SLAB, t.s * 16, t.lo, t.hi, lane, [&] { issue(st == 0 ? R::STAGES - 1 : st - 1); });
+        work.slab(ks, ks + R::SLAB, x * 16, seen.lo, feed.none >> st & 1 ? 0 : seen.hi, lane, [&] { issue(st == 0 ? R::STAGES - 1 : st - 1); });
         st = st + 1 == R::STAGES ? 0 : st + 1;
     }
     work.sums();
@@ -693,7 +685,7 @@ static cudaError_t run(const Attn &a, cudaStream_t s)
     using O = std::conditional_t<QT == 1, T, float>;
     static bool ready[2][64] = {};
     auto go = [&](auto warps, bool (&ready)[64]) {
-        constexpr int CW = decltype(warps)::value, smem = Ring<HD>::bytes(CW) + Work<HD, NT, T, QT>::Q_BYTES;
+        constexpr int CW = decltype(warps)::value, smem = CW * Ring<HD>::COPIES + Work<HD, NT, T, QT>::Q_BYTES;
         const cudaError_t e = lfr::allow_smem(attn_cluster<HD, NT, T, QT, CW>, smem, ready);
         if (e != cudaSuccess) return e;
         return lfr::launch(attn_cluster<HD, NT, T, QT, CW>, dim3((unsigned)(a.n * a.ht * a.parts * a.cl)), CW * 32, smem, a.cl, s, a);
