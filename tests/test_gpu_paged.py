@@ -79,6 +79,23 @@ def test_parts_with_windows_and_short_rows(pm):
         attend(pm, c, window=window)
 
 
+LONG_FIRST = [(4, 128, [2100, 0, 5, 16, 17, 700, 700, 1999] * 10), (2, 64, [4100] + [i % 40 for i in range(199)]),
+              (4, 128, [0] * 30 + [4200, 1] + [33] * 18), (1, 64, [0] * 255 + [5000])]
+
+
+@pytest.mark.parametrize("cache,dtype", TYPES)
+@pytest.mark.parametrize("hkv,hd,lens", LONG_FIRST)
+def test_long_rows_first(pm, hkv, hd, lens, cache, dtype):
+    """More rows than run at a time, of few or many lengths, equal ones and none among them: each is taken once."""
+    attend(pm, ref.case(lens, hkv * (9 if hkv == 2 else 2), hkv, hd, 64, cache, dtype, seed=hkv))
+
+
+@pytest.mark.parametrize("lens", [[33000, 40, 0, 1500] + [100] * 36])
+def test_clusters_of_eight_in_rounds(pm, lens):
+    attend(pm, ref.case(lens, 8, 4, 64, 128, F16, F16, seed=8))
+    attend(pm, ref.case(lens, 8, 4, 64, 128, F16, F16, seed=8), window=20000)
+
+
 @pytest.mark.parametrize("lens", [[40, 33], [13000, 12999]])
 def test_tables_narrower_than_the_lengths_and_wider(pm, lens):
     q, k, v, tables, ln = ref.case(lens, 4, 2, 64, 16, F16, F16, width=900)
