@@ -574,7 +574,8 @@ LF_API lf_status lf_paged_append(const lf_paged *c, const lf_rows *k, const lf_r
  * Scores, softmax and sums are FP32; q and the probabilities enter the products
  * with 16 bits or more (q as it is where it has the cache's dtype).  q must be
  * finite; infinities and NaN in K or V spoil the heads and rows that see them, and
- * no others. */
+ * no others.  So do scores that FP32 does not hold, and sums of V that leave it
+ * with weights of up to 2^15. */
 typedef struct {
     lf_rows q, out;          /* [n_seqs][n_heads][head_dim], both of the cache's dtype or FP32; out must not overlap q */
     int32_t n_seqs;          /* 0 does nothing */

@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "../../include/lf.h"
@@ -152,13 +153,15 @@ struct Work {
     static constexpr int Q_BYTES = QS ? NT * KS * 32 * QT * 8 : 0;
     unsigned q[QS ? 1 : QT][QS ? 1 : NT][QS ? 1 : KS][2];
     uint32_t qs;
+    // Score = f st in log2 units, f >= 0 (q carries the scale's sign).  The reference is a value of st, subtracted before
+    // f multiplies, so that equal scores differ by 0 and the largest one from itself, however far apart FP32's steps are.
     float f[NT][2], ref[NT][2], l[NT][2], o[NT][KS][4];
 
     __device__ __forceinline__ void begin(const Attn &a, int row, int ht, int warp, int warps, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
         const int kvh = ht / a.tiles, h0 = (ht - kvh * a.tiles) * RT;
-        const float base = a.scale * 1.4426950408889634f;
+        const float base = fminf(fabsf(a.scale) * 1.4426950408889634f, FLT_MAX);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int hh = h0 + 8 * i + g;
@@ -186,26 +189,39 @@ struct Work {
                 // a power of two brings the row to [1, 2): the terms' remainders stay in FP16's range, and BF16's
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float r = lfq::range_factor(top);
+                const float r = lfq::range_factor(top), rq = a.scale < 0.f ? -r : r;
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         unsigned w[QT];
-                        split_pair<T, QT>(x[k][u].x * r, x[k][u].y * r, w);
+                        split_pair<T, QT>(x[k][u].x * rq, x[k][u].y * rq, w);
 #pragma unroll
                         for (int n = 0; n < QT; ++n) {
                             if constexpr (!QS) q[n][i][k][u] = w[n];
                             else if (k % warps == warp) sts(q_at(n, i, k, lane) + 4 * u, w[n]);
                         }
                     }
-                f[i][0] = base / __shfl_sync(0xffffffffu, r, 8 * t);       // rows 2t and 2t + 1 of the tile
-                f[i][1] = base / __shfl_sync(0xffffffffu, r, 8 * t + 4);
+                f[i][0] = fminf(base / __shfl_sync(0xffffffffu, r, 8 * t), FLT_MAX);       // rows 2t and 2t + 1 of the tile
+                f[i][1] = fminf(base / __shfl_sync(0xffffffffu, r, 8 * t + 4), FLT_MAX);
             }
             ref[i][0] = ref[i][1] = -INFINITY;
             l[i][0] = l[i][1] = 0.f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) o[i][k][0] = o[i][k][1] = o[i][k][2] = o[i][k][3] = 0.f;
+        }
+    }
+
+    // The scale's sign on a 16-bit q, once the first copies are on their way: begin() does not wait for its loads.
+    __device__ __forceinline__ void sign(const Attn &a)
+    {
+        if constexpr (QT == 1) {
+            if (a.scale < 0.f) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) q[0][i][k][0] ^= 0x80008000u, q[0][i][k][1] ^= 0x80008000u;
+            }
         }
     }
 
@@ -257,7 +273,7 @@ struct Work {
                 for (int n = CH - 2; n >= 0; --n) st[i][e] += sc[n][i][e];
             }
         // ---- P relative to the reference, and the lanes' sums.  No maximum is formed where a lane's P sum to no more
-        // than FP16 can hold; otherwise, and at the first position, the reference is put 2^P_EXP below the largest.
+        // than FP16 can hold; otherwise, and at the first position, the reference becomes the largest, whose P is 2^P_EXP.
         const bool whole = p >= lo && p + 16 <= hi;
         const bool in0 = whole || (p + g >= lo && p + g < hi), in1 = whole || (p + g + 8 >= lo && p + g + 8 < hi);
         float pr[NT][4], sum[NT][2];
@@ -267,8 +283,8 @@ struct Work {
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float neg = ref[i][e] == -INFINITY ? 0.f : -ref[i][e];
-                    const float x = ex2(fmaf(st[i][e], f[i][e], neg)), y = ex2(fmaf(st[i][2 + e], f[i][e], neg));
+                    const float r = ref[i][e] == -INFINITY ? 0.f : ref[i][e];
+                    const float x = ex2(fmaf(st[i][e] - r, f[i][e], P_EXP)), y = ex2(fmaf(st[i][2 + e] - r, f[i][e], P_EXP));
                     pr[i][e] = in0 ? x : 0.f;
                     pr[i][2 + e] = in1 ? y : 0.f;
                     sum[i][e] = pr[i][e] + pr[i][2 + e];
@@ -281,21 +297,19 @@ struct Work {
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(in0 ? st[i][e] * f[i][e] : -INFINITY, in1 ? st[i][2 + e] * f[i][e] : -INFINITY);
+                    float mx = fmaxf(in0 ? st[i][e] : -INFINITY, in1 ? st[i][2 + e] : -INFINITY);
 #pragma unroll
                     for (int sh = 4; sh <= 16; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
                     float &r = ref[i][e];
-                    if (mx > r && (r == -INFINITY || mx - r > P_EXP + 1.f)) {
-                        float n = mx - P_EXP;
-                        if (!(mx - n <= 15.f)) n = mx;     // scores so large that their steps are
-                        const float alpha = ex2(r - n);    // 0 from -inf
+                    if (mx > r && (r == -INFINITY || (mx - r) * f[i][e] > P_EXP + 1.f)) {
+                        const float alpha = r == -INFINITY ? 0.f : ex2((r - mx) * f[i][e]);
                         l[i][e] *= alpha;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
                             o[i][k][e] *= alpha;
                             o[i][k][2 + e] *= alpha;
                         }
-                        r = n;
+                        r = mx;
                     }
                 }
             probs();
@@ -346,15 +360,17 @@ struct Work {
         }
     }
 
-    // The sums of all positions (each lane holds those of its rows).
+    // The sums of all positions (each lane holds those of its rows), and the references in log2 units.
     __device__ __forceinline__ void sums()
     {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int sh = 4; sh <= 16; sh <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], sh);
+                if (ref[i][e] != -INFINITY) ref[i][e] *= f[i][e];
+            }
     }
     // The state as it lies in the lanes: O as [NT][KS][lane] x 4, then (reference, sum) of each head.
     __device__ __forceinline__ void store_state(float *dst, int lane) const
@@ -583,6 +599,7 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
     };
 #pragma unroll 1
     for (int i = 0; i < R::STAGES - 1; ++i) issue(i);
+    work.sign(a);
     int st = 0;
 #pragma unroll 1
     for (int x = seen.s0 + me; x < seen.s1; x += nw) {

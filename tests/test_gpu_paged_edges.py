@@ -1,0 +1,66 @@
+"""The paged KV cache's operators where they can go wrong."""
+import pytest
+import torch
+
+import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+TYPES = [(F16, F16), (BF16, BF16), (F16, F32), (BF16, F32)]
+
+
+@pytest.fixture(scope="module")
+def pm():
+    import persistent_monokernel_gb300 as pm
+    pm.lib()
+    torch.cuda.set_device(0)
+    return pm
+
+
+# ---------------------------------------------------------------- large scores
+
+def planted(lens, places, cache, dtype, sign, hd, factor=1.0):
+    """One query head per KV head, and K = sign q at the places (of those, the ones that a row has), which therefore have
+    the largest scores by far: hd or so, against 6 sqrt(hd) at most."""
+    q, k, v, tables, ln = ref.case(lens, 2, 2, hd, 32, cache, dtype, seed=hd)
+    q = (q.to(cache) * factor).to(dtype)                  # (values that the cache's type has)
+    k.mul_(factor)
+    at = [[p for p in places if p < n] for n in lens]
+    for i, ps in enumerate(at):
+        for p in ps:
+            k[int(tables[i, p // 32]), :, p % 32] = (sign * q[i]).to(cache)
+    return q, k, v, tables, ln, at
+
+
+@pytest.mark.parametrize("cache,dtype", TYPES)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("scale", [1e3, 1e6, 1e7, 1.3e8, 1e10, 1e20])
+@pytest.mark.parametrize("lens,places", [([700, 31, 1, 0, 17], [0, 3]), ([700, 300, 64], [0, 17, 40, 41, 255, 640]), ([13001], [12]),
+                                         ([13001], [7, 16, 5000, 5001, 12999])])
+def test_scores_far_beyond_their_steps(pm, lens, places, scale, sign, cache, dtype):
+    """The largest score has all the weight, equal ones share it.  Scores of 1e5 to 1e22 are steps of up to 1e15 apart; equal rows
+    of K have equal scores to the bit, all others' weight is 0, so that only the mean of the rows of V (m of them, added
+    up and divided in 32 bits) and the output's half step are left."""
+    for hd in (64, 128):
+        q, k, v, tables, ln, at = planted(lens, places, cache, dtype, sign, hd)
+        got = pm.PagedKVCache.wrap(k, v).attend(q, tables, ln, scale=sign * scale)
+        for i, ps in enumerate(at):
+            if not ps:
+                assert not got[i].any()
+                continue
+            rows = torch.stack([v[int(tables[i, p // 32]), :, p % 32] for p in ps]).double()
+            want, size = rows.mean(0), rows.abs().mean(0)
+            bound = ref.HALF_STEP[dtype] * want.abs() + (len(ps) + 4) * 2.0 ** -23 * size + (2.0 ** -25 if dtype == F16 else 0)
+            ref.check(got[i], want, bound)
+
+
+@pytest.mark.parametrize("cache,dtype", TYPES)
+def test_large_queries_and_keys(pm, cache, dtype):
+    """The same by values of some ten thousand each, at the usual scale."""
+    q, k, v, tables, ln, at = planted([700, 64, 5], [2, 33, 690], cache, dtype, 1, 128, 2.0 ** 13)
+    got = pm.PagedKVCache.wrap(k, v).attend(q, tables, ln)
+    for i, ps in enumerate(at):
+        rows = torch.stack([v[int(tables[i, p // 32]), :, p % 32] for p in ps]).double()
+        want, size = rows.mean(0), rows.abs().mean(0)
+        ref.check(got[i], want, ref.HALF_STEP[dtype] * want.abs() + (len(ps) + 4) * 2.0 ** -23 * size + (2.0 ** -25 if dtype == F16 else 0))
