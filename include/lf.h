@@ -566,7 +566,7 @@ LF_API lf_status lf_paged_append(const lf_paged *c, const lf_rows *k, const lf_r
  *   out[i][h] = sum_j softmax_j(scale * q[i][h] . K[j]) V[j]
  * over the positions j < lens[i] of row i (window > 0: the `window` most recent of
  * them), query head h reading KV head h / (n_heads / n_kv_heads).  A row that
- * sees no position (lens[i] <= 0) gives zeros.  Positions behind table_width pages
+ * sees no position (lens[i] <= 0) gives zeros, one whose scores are all -inf NaN.  Positions behind table_width pages
  * and positions on a page that the pool does not have (table entries outside
  * 0 .. n_pages - 1) are left out.  What lies in pages behind a row's length, or on
  * pages that no row sees, is not read.  The narrower the table, the better the

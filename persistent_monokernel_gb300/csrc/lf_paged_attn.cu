@@ -297,7 +297,8 @@ struct Work {
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(in0 ? st[i][e] : -INFINITY, in1 ? st[i][2 + e] : -INFINITY);
+                    // (a score of -inf is a position seen all the same: the reference -inf is for none)
+                    float mx = fmaxf(in0 ? fmaxf(st[i][e], -FLT_MAX) : -INFINITY, in1 ? fmaxf(st[i][2 + e], -FLT_MAX) : -INFINITY);
 #pragma unroll
                     for (int sh = 4; sh <= 16; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
                     float &r = ref[i][e];
@@ -369,7 +370,7 @@ struct Work {
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int sh = 4; sh <= 16; sh <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], sh);
-                if (ref[i][e] != -INFINITY) ref[i][e] *= f[i][e];
+                if (ref[i][e] != -INFINITY) ref[i][e] = fmaxf(ref[i][e] * f[i][e], -FLT_MAX);
             }
     }
     // The state as it lies in the lanes: O as [NT][KS][lane] x 4, then (reference, sum) of each head.
@@ -390,13 +391,15 @@ struct Work {
     }
 };
 
-// Two heads' outputs of dims 16 k + g and + 8, normalised: v = O of (head 0, head 1) at both dims.
+// Two heads' outputs of dims 16 k + g and + 8, normalised: v = O of (head 0, head 1) at both dims; ml: reference and sum of
+// head 0, then of head 1.  A head that saw no position (reference -inf) gives zeros, one whose scores were all -inf NaN.
 template <int HD, int NT, class O>
-__device__ __forceinline__ void store_out(const Attn &a, int row, int ht, int i, int k, int lane, float4 v, float l0, float l1)
+__device__ __forceinline__ void store_out(const Attn &a, int row, int ht, int i, int k, int lane, float4 v, float4 ml)
 {
     const int g = lane >> 2, t = lane & 3;
     const int kvh = ht / a.tiles, hh = (ht - kvh * a.tiles) * 8 * NT + 8 * i + 2 * t;
-    const float r0 = l0 > 0.f ? 1.0f / l0 : (l0 == 0.f ? 0.f : l0), r1 = l1 > 0.f ? 1.0f / l1 : (l1 == 0.f ? 0.f : l1);
+    auto inverse = [](float m, float l) { return l > 0.f ? 1.0f / l : m == -INFINITY ? 0.f : NAN; };
+    const float r0 = inverse(ml.x, ml.y), r1 = inverse(ml.z, ml.w);
     O *dst = static_cast<O *>(a.o.p) + (size_t)row * a.o.ts + (size_t)(kvh * a.G + hh) * a.o.hs + 16 * k + g;
     auto put = [](O *p, float x) {
         if constexpr (sizeof(O) == 4) *p = x;
@@ -619,7 +622,7 @@ __global__ void __launch_bounds__(CW * 32, 8 / CW) attn_cluster(const __grid_con
             *reinterpret_cast<float4 *>(out + f * 4) = x.v;
             if (k == 0 && ln < 4) *reinterpret_cast<float4 *>(out + ml) = x.ml();
         } else {
-            store_out<HD, NT, O>(a, row, ht, i, k, ln, x.v, x.l0, x.l1);
+            store_out<HD, NT, O>(a, row, ht, i, k, ln, x.v, x.ml());
         }
     };
     work.store_state(states + warp * STATE, lane);
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) attn_join(const __grid_consta
         __syncthreads();
         if (grp < half) j.add(sh[0][threadIdx.x + half * per], sh[1][threadIdx.x + half * per]);
     }
-    if (grp == 0) store_out<HD, NT, O>(a, row, ht, i, k, lane, j.v, j.l0, j.l1);
+    if (grp == 0) store_out<HD, NT, O>(a, row, ht, i, k, lane, j.v, j.ml());
 }
 
 // ---------------------------------------------------------------- launches

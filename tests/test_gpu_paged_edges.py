@@ -1,4 +1,6 @@
 """The paged KV cache's operators where they can go wrong."""
+import math
+
 import pytest
 import torch
 
@@ -64,3 +66,23 @@ def test_large_queries_and_keys(pm, cache, dtype):
         rows = torch.stack([v[int(tables[i, p // 32]), :, p % 32] for p in ps]).double()
         want, size = rows.mean(0), rows.abs().mean(0)
         ref.check(got[i], want, ref.HALF_STEP[dtype] * want.abs() + (len(ps) + 4) * 2.0 ** -23 * size + (2.0 ** -25 if dtype == F16 else 0))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("n", [1, 16, 100, 13000])
+def test_rows_of_infinitely_low_scores_are_not_empty(pm, n, dtype):
+    """Every score -inf: there is no softmax (-inf minus -inf), and zeros are for rows that see no position.  Next to finite
+    scores they have no weight."""
+    q, k, v, tables, lens = ref.case([n, n, 0], 2, 2, 64, 16, dtype, dtype, seed=n)
+    q[:] = 1.0
+    for j in range(ref.cdiv(n, 16)):
+        k[int(tables[0, j]), 0, :, 5] = -math.inf
+        k[int(tables[1, j]), 1, :, 5] = -math.inf
+    out = pm.PagedKVCache.wrap(k, v).attend(q, tables, lens)
+    assert out[0, 0].isnan().all() and out[1, 1].isnan().all() and not out[2].any()
+    want, bound = ref.attend(q, k.nan_to_num(0.0, neginf=0.0), v, tables, lens)
+    ref.check(out[0, 1], want[0, 1], bound[0, 1])
+    ref.check(out[1, 0], want[1, 0], bound[1, 0])
+    last = int(tables[0, (n - 1) // 16]), 0, (n - 1) % 16
+    k[last][5] = 1.0                                      # one finite score: it has all the weight
+    assert torch.equal(pm.PagedKVCache.wrap(k, v).attend(q, tables, lens)[0, 0], v[last])
