@@ -86,3 +86,28 @@ def test_rows_of_infinitely_low_scores_are_not_empty(pm, n, dtype):
     last = int(tables[0, (n - 1) // 16]), 0, (n - 1) % 16
     k[last][5] = 1.0                                      # one finite score: it has all the weight
     assert torch.equal(pm.PagedKVCache.wrap(k, v).attend(q, tables, lens)[0, 0], v[last])
+
+
+# ---------------------------------------------------------------- long sums
+
+@pytest.mark.parametrize("dtype,n", [(F16, 2 ** 14), (BF16, 2 ** 17)])
+def test_a_long_row_keeps_small_addends(pm, dtype, n):
+    """One warp adds n slabs: a first sum S, then by turns 1/4 and 3/4 of a step of S in 32 bits.  Rounded to nearest they
+    come to half a step each, cut off to nothing.  n steps are a step of the output's type, or its half."""
+    head = 2.0 ** 15                                      # S = 2^7 16 head; its step in units of P = 2^7: 16 head 2^-23
+    step = 16 * head * 2.0 ** -23
+    k = torch.zeros(2, 8, 128, 64, dtype=dtype, device="cuda")
+    v = torch.zeros_like(k)
+    v[0, :, :64] = head                                   # four warps, a slab each
+    v[0, :, 64::16], v[1, :, 64::16], v[1, :, :64:16] = 0.25 * step, 0.25 * step, 0.75 * step
+    positions = 64 * n
+    tables = torch.ones(1, positions // 128, dtype=torch.int32, device="cuda")
+    tables[0, 0] = 0
+    lens = torch.zeros(256, dtype=torch.int32, device="cuda")
+    lens[0] = positions
+    q = torch.zeros(256, 8, 64, dtype=dtype, device="cuda")
+    out = pm.PagedKVCache.wrap(k, v).attend(q, tables.expand(256, -1), lens)
+    want = (64 * head + 4 * step * (0.25 + (n - 2) / 2)) / positions
+    low = 64 * head / positions
+    assert torch.tensor(want, dtype=dtype) > torch.tensor(low, dtype=dtype)
+    assert torch.equal(out[0], torch.full_like(out[0], want)) and not out[1:].any()
