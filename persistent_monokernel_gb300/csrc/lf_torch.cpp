@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -42,6 +43,15 @@ PyObject *g_fail;   // raises the library's error: fail(status, entry point)
 struct Refused : std::runtime_error {
     using std::runtime_error::runtime_error;
 };
+
+// These calls form no derivatives: what asks for some is refused, backward ones and forward ones (a tangent).
+void no_derivatives(const at::Tensor &t, const char *what)
+{
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        throw Refused(std::string(what) + " requires a gradient, and these calls form none: detach it, or call under torch.no_grad()");
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+        throw Refused(std::string(what) + " has a tangent, and these calls form none: pass its primal, or call under torch.inference_mode()");
+}
 
 // A cache as the library has it, its tensors (k_codes, k_scales, v_codes, v_scales) and device, and the scratch that
 // the last query that needed some did.
@@ -92,8 +102,8 @@ struct Paged {
     {
         if (!fits(k, c, device) || !fits(v, c, device) || !alike(k, v))
             throw Refused("a tensor of the cache is no longer what the cache was made with");
-        if (c10::GradMode::is_enabled() && (k.requires_grad() || v.requires_grad()))
-            throw Refused("a tensor of the cache requires a gradient, and these calls form none");
+        no_derivatives(k, "k of the cache");
+        no_derivatives(v, "v of the cache");
         c.page_stride = k.stride(0);
         c.head_stride = k.stride(1);
         c.pos_stride = k.stride(2);
@@ -166,8 +176,7 @@ lf_rows rows_of(PyObject *o, const H &c, int64_t n, int64_t heads, const char *w
           << "] float16, bfloat16 or float32 with a contiguous last dimension on cuda:" << (int)c.device << " is needed";
         throw Refused(s.str());
     }
-    if (t.requires_grad() && c10::GradMode::is_enabled())
-        throw Refused(std::string(what) + " requires a gradient, and these calls form none: detach it, or call under torch.no_grad()");
+    no_derivatives(t, what);
     // the stride of a dimension of one is never used (and may be anything)
     return {const_cast<void *>(t.const_data_ptr()), code, n > 1 ? t.stride(0) : 0, heads > 1 ? t.stride(1) : 0};
 }

@@ -110,7 +110,7 @@ class PagedKVCache(OnStream):
 
     Rows passed to the calls are CUDA tensors [n, heads, head_dim] on the cache's device, of the cache's dtype or
     float32, with a contiguous last dimension, 16-byte aligned rows and any other strides; what the library refuses
-    raises LFError.  The calls form no gradients and take a stream as KV4Cache's do.
+    raises LFError.  The calls form no derivatives and take a stream as KV4Cache's do.
     """
 
     def __init__(self, n_pages: int, n_kv_heads: int, head_dim: int, page: int = 64, dtype=None, device="cuda"):

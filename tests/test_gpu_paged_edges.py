@@ -20,6 +20,10 @@ def pm():
     return pm
 
 
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
 # ---------------------------------------------------------------- large scores
 
 def planted(lens, places, cache, dtype, sign, hd, factor=1.0):
@@ -111,3 +115,28 @@ def test_a_long_row_keeps_small_addends(pm, dtype, n):
     low = 64 * head / positions
     assert torch.tensor(want, dtype=dtype) > torch.tensor(low, dtype=dtype)
     assert torch.equal(out[0], torch.full_like(out[0], want)) and not out[1:].any()
+
+
+# ---------------------------------------------------------------- what torch has to know
+
+def test_forward_mode_derivatives_are_refused(pm):
+    import torch.autograd.forward_ad as fwad
+    q, k, v, tables, lens = ref.case([20, 5], 4, 2, 64, 16, F16, F16)
+    cache, kv4 = pm.PagedKVCache.wrap(k, v), pm.KV4Cache(2, 64, 16)
+    x = torch.zeros(3, 2, 64, dtype=F16, device="cuda")
+    slots = ints([1, 2, 3])
+    kv4.append(x, x, 0)
+    want = cache.attend(q, tables, lens)
+    with fwad.dual_level():
+        dual = fwad.make_dual(q, torch.ones_like(q))
+        dx = fwad.make_dual(x, torch.ones_like(x))
+        pool = fwad.make_dual(k.clone(), torch.ones_like(k))
+        for call in (lambda: cache.attend(dual, tables, lens), lambda: cache.append(dx, x, slots), lambda: cache.append(x, dx, slots),
+                     lambda: pm.PagedKVCache.wrap(pool, v).attend(q, tables, lens), lambda: kv4.append(dx, x, 0),
+                     lambda: kv4.attend(dual[:, :2], 0), lambda: cache.attend(q, tables, lens, out=fwad.make_dual(q.clone(), q)),
+                     lambda: kv4.read(0, 3, out=(dx.clone(), x.clone()))):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+        with torch.inference_mode():                      # no derivatives are asked for
+            assert torch.equal(cache.attend(dual, tables, lens), want)
+        assert torch.equal(cache.attend(fwad.unpack_dual(dual).primal, tables, lens), want)
