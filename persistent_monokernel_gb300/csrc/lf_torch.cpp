@@ -53,6 +53,13 @@ void no_derivatives(const at::Tensor &t, const char *what)
         throw Refused(std::string(what) + " has a tangent, and these calls form none: pass its primal, or call under torch.inference_mode()");
 }
 
+// A call writes t: its version says so to a backward pass that has kept it.  (Tensors made in inference mode have none.)
+void written(const at::Tensor &t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject *o) { written(THPVariable_Unpack(o)); }
+
 // A cache as the library has it, its tensors (k_codes, k_scales, v_codes, v_scales) and device, and the scratch that
 // the last query that needed some did.
 struct Cache {
@@ -249,6 +256,7 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n_args)
         sizes_of(args[1], n, heads, "k");
         const lf_rows k = rows_of(args[1], c, n, c.c.n_kv_heads, "k"), v = rows_of(args[2], c, n, c.c.n_kv_heads, "v");
         st = g_append(&c.c, &k, &v, n, pos, stream_of(c));
+        for (const at::Tensor &t : c.parts) written(t);
         Py_RETURN_NONE;
     });
 }
@@ -287,6 +295,8 @@ PyObject *read(PyObject *, PyObject *const *args, Py_ssize_t n_args)
         try {
             const lf_rows a = rows_of(k, c, rows, heads, "k"), b = rows_of(v, c, rows, heads, "v");
             st = g_read(&c.c, &a, &b, n, pos, stream_of(c));
+            written(k);
+            written(v);
         } catch (...) {
             Py_DECREF(out);
             throw;
@@ -339,6 +349,7 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n_args)
             }
         }
         if (need > had) c.n = q.n, c.heads = q.n_heads, c.scratch = need;
+        if (out != Py_None) written(out);
         return out == Py_None ? THPVariable_Wrap(std::move(made)) : Py_NewRef(out);
     });
 }
@@ -414,6 +425,8 @@ PyObject *paged_append(PyObject *, PyObject *const *args, Py_ssize_t n_args)
         sizes_of(args[1], n, heads, "k");
         const lf_rows k = rows_of(args[1], c, n, c.c.n_kv_heads, "k"), v = rows_of(args[2], c, n, c.c.n_kv_heads, "v");
         st = g_paged_append(&c.c, &k, &v, n, ints_of(args[3], n, c.device, "slots"), stream_of(c));
+        written(c.k);
+        written(c.v);
         Py_RETURN_NONE;
     });
 }
@@ -464,6 +477,7 @@ PyObject *paged_attend(PyObject *, PyObject *const *args, Py_ssize_t n_args)
                 st = g_paged_attend(&cache, &q, ws.mutable_data_ptr(), need, stream);
             }
         }
+        if (out != Py_None) written(out);
         return out == Py_None ? THPVariable_Wrap(std::move(made)) : Py_NewRef(out);
     });
 }
@@ -526,6 +540,7 @@ PyObject *plan(PyObject *, PyObject *const *args, Py_ssize_t n_args)
             int32_t *const p = all.mutable_data_ptr<int32_t>();
             st = g_plan(&tables, n_new, keep, p, p + pitch, p + 2 * pitch, most, stream);
         }
+        for (const at::Tensor &t : c.parts) written(t);
         for (int i = 0; i < 3; ++i) {
             made[i] = at::detail::make_tensor<at::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
             made[i].unsafeGetTensorImpl()->set_sizes_contiguous(size[i]);

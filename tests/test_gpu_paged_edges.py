@@ -140,3 +140,40 @@ def test_forward_mode_derivatives_are_refused(pm):
         with torch.inference_mode():                      # no derivatives are asked for
             assert torch.equal(cache.attend(dual, tables, lens), want)
         assert torch.equal(cache.attend(fwad.unpack_dual(dual).primal, tables, lens), want)
+
+
+def test_writes_are_seen_by_autograd(pm):
+    """A tensor that a backward pass has kept and a call has written since is an error, as with any write in place."""
+    k, v = (torch.zeros(2, 2, 16, 64, dtype=F16, device="cuda") for _ in range(2))
+    cache = pm.PagedKVCache.wrap(k, v)
+    x = torch.ones(3, 2, 64, dtype=F16, device="cuda")
+    t = pm.PageTables(2, 1, 2, 16)
+    lens, tables = ints([3, 0]), ints([[0], [1]])
+    for kept in (k, v):
+        w = torch.ones_like(kept, requires_grad=True)
+        y = (kept * w).sum()
+        cache.append(x, x, ints([0, 1, 2]))
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+
+    def bumped(call, *tensors):
+        was = [a._version for a in tensors]
+        call()
+        return all(a._version > b for a, b in zip(tensors, was))
+
+    q, out = torch.ones(2, 4, 64, dtype=F16, device="cuda"), torch.empty(2, 4, 64, dtype=F16, device="cuda")
+    assert bumped(lambda: cache.append(x, x, ints([0, 1, 2])), k, v)
+    assert bumped(lambda: cache.attend(q, tables, lens, out=out), out)
+    assert not any(bumped(lambda: cache.attend(q, tables, lens), a) for a in (k, v, q, tables, lens))
+    assert bumped(lambda: t.plan(ints([1, 1]), 2), t.tables, t.lens, t.free, t.n_free, t.status)
+    kv4 = pm.KV4Cache(2, 64, 16)
+    a, b = x.clone(), x.clone()
+    assert bumped(lambda: kv4.append(x, x, 0), kv4.k_codes, kv4.k_scales, kv4.v_codes, kv4.v_scales)
+    assert bumped(lambda: kv4.read(0, 3, out=(a, b)), a, b)
+    assert bumped(lambda: kv4.attend(x, 0, out=a), a)
+    with torch.inference_mode():                          # tensors without a version
+        free = [torch.zeros_like(k) for _ in range(2)]
+        o = torch.empty_like(q)
+    pm.PagedKVCache.wrap(*free).append(x, x, ints([0, 1, 2]))
+    pm.PagedKVCache.wrap(*free).attend(q, tables, lens, out=o)
+    assert torch.equal(o, out)
