@@ -204,6 +204,15 @@ at::Tensor empty(at::IntArrayRef size, at::ScalarType type, c10::DeviceIndex dev
 {
     return at::Tensor(at::detail::empty_cuda(size, type, at::Device(at::kCUDA, device), std::nullopt));
 }
+// A new output of n rows, as q says and not its tensor (which another thread may resize meanwhile), and q.out for it.
+template <class Q>
+at::Tensor output(int64_t n, Q &q, int64_t hd, c10::DeviceIndex device)
+{
+    const at::ScalarType type = q.q.dtype == LF_F16 ? at::kHalf : q.q.dtype == LF_BF16 ? at::kBFloat16 : at::kFloat;
+    at::Tensor t = empty({n, q.n_heads, hd}, type, device);
+    q.out = {t.mutable_data_ptr(), q.q.dtype, q.n_heads * hd, hd};
+    return t;
+}
 // A contiguous tensor of n 32-bit integers.
 const int32_t *ints_of(PyObject *o, int64_t n, c10::DeviceIndex device, const char *what)
 {
@@ -335,11 +344,7 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n_args)
         const lf_kv4 cache = c.c;                         // (c is another thread's to change meanwhile)
         {
             NoGil free;
-            if (out == Py_None) {
-                const at::Tensor &t = THPVariable_Unpack(args[1]);
-                made = empty(t.sizes(), t.scalar_type(), c.device);
-                q.out = {made.mutable_data_ptr(), q.q.dtype, q.n_heads * (int64_t)c.c.head_dim, c.c.head_dim};
-            }
+            if (out == Py_None) made = output(q.n, q, cache.head_dim, c.device);
             at::Tensor ws;
             if (had) ws = empty({had}, at::kByte, c.device);
             st = g_attend(&cache, &q, had ? ws.mutable_data_ptr() : nullptr, had, stream);
@@ -463,11 +468,7 @@ PyObject *paged_attend(PyObject *, PyObject *const *args, Py_ssize_t n_args)
         const lf_paged cache = c.c;                       // (c is another thread's to change meanwhile)
         {
             NoGil free;
-            if (out == Py_None) {
-                const at::Tensor &x = THPVariable_Unpack(args[1]);
-                made = empty(x.sizes(), x.scalar_type(), c.device);
-                q.out = {made.mutable_data_ptr(), q.q.dtype, q.n_heads * (int64_t)cache.head_dim, cache.head_dim};
-            }
+            if (out == Py_None) made = output(q.n_seqs, q, cache.head_dim, c.device);
             // Scratch, where a call needs some (few long sequences do), is that call's alone: no two streams or captured
             // graphs share it.
             st = g_paged_attend(&cache, &q, nullptr, 0, stream);
