@@ -87,16 +87,19 @@ class PageTables(OnStream):
         each row's begin [n_seqs + 1].  Behind the last one slots are -1 and positions 0.
 
         All or nothing: where the pages, the rows' max_pages or max_tokens do not suffice, nothing changes, all slots
-        are -1 and all offsets 0, and sync() tells."""
+        are -1 and all offsets 0, and sync() on the same stream tells."""
         if stream is None:
             got = kv4._calls.plan(self._handle, n_new, max_tokens, keep)
             if got is not NotImplemented:
                 return got
         return self._elsewhere(self.plan, stream, (n_new, max_tokens, keep))
 
-    def sync(self) -> int:
-        """Synchronise the current stream of the tables' device: 0, or why a plan since the last sync changed nothing,
-        LF_ERR_CAPACITY (3) or LF_ERR_INVALID_ARG (1), the first where there were several."""
+    def sync(self, stream=None) -> int:
+        """Synchronise `stream`, or the current stream of the tables' device: 0, or why a plan since the last sync changed
+        nothing, LF_ERR_CAPACITY (3) or LF_ERR_INVALID_ARG (1), the first where there were several.  Plans that are
+        still to run on other streams are not waited for."""
+        if stream is not None:
+            return self._elsewhere(self.sync, stream, ())
         with kv4._torch.cuda.device(self.device):
             status = int(self.status.item())
             if status:

@@ -177,3 +177,20 @@ def test_writes_are_seen_by_autograd(pm):
     pm.PagedKVCache.wrap(*free).append(x, x, ints([0, 1, 2]))
     pm.PagedKVCache.wrap(*free).attend(q, tables, lens, out=o)
     assert torch.equal(o, out)
+
+
+def test_sync_of_another_stream(pm):
+    """A plan on a stream of its own: sync on that stream waits for it."""
+    t = pm.PageTables(2, 4, 6, 16)
+    s = torch.cuda.Stream()
+    new = ints([100, 0])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    t.plan(new, 200, stream=s)
+    assert t.sync(stream=s) == 3
+    assert t.sync() == 0 and t.sync(stream=s) == 0
+    with pytest.raises(ValueError, match="stream"):
+        class Elsewhere:
+            device = torch.device("cuda", 99)
+        t.sync(stream=Elsewhere())
