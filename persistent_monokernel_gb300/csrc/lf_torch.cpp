@@ -111,6 +111,10 @@ struct Paged {
             throw Refused("a tensor of the cache is no longer what the cache was made with");
         no_derivatives(k, "k of the cache");
         no_derivatives(v, "v of the cache");
+        place();
+    }
+    void place()
+    {
         c.page_stride = k.stride(0);
         c.head_stride = k.stride(1);
         c.pos_stride = k.stride(2);
@@ -385,7 +389,7 @@ PyObject *cache(PyObject *, PyObject *args)
     return o;
 }
 
-// paged(k, v): the pools [n_pages, n_kv_heads, page, head_dim] (their checks are the binding's and the library's)
+// paged(k, v): the pools [n_pages, n_kv_heads, page, head_dim] (their checks are here and in the library)
 PyObject *paged(PyObject *, PyObject *args)
 {
     PyObject *k, *v;
@@ -412,6 +416,12 @@ PyObject *paged(PyObject *, PyObject *args)
         if (!ok)
             throw Refused("k and v must be CUDA tensors [n_pages, n_kv_heads, page, head_dim] in float16 or bfloat16, alike in type, "
                           "device and strides, with a contiguous last dimension");
+        c->place();
+        // what else the library refuses, at once: an append of no rows checks the pools and does nothing
+        if (const lf_status st = g_paged_append(&c->c, nullptr, nullptr, 0, nullptr, nullptr); st != LF_OK) {
+            Py_XDECREF(PyObject_CallFunction(g_fail, "is", (int)st, "lf_paged"));
+            return nullptr;
+        }
         PyObject *o = PyCapsule_New(c.get(), Paged::name, drop<Paged>);
         if (o) c.release();
         return o;

@@ -107,6 +107,21 @@ class PageTables(OnStream):
         return status
 
 
+def _check_pool(shape, dtype) -> None:
+    """Raise LFError for contiguous pools [n_pages, n_kv_heads, page, head_dim] that the library refuses: an append of no
+    rows checks them and does nothing else (the addresses are any)."""
+    if kv4._torch is None:
+        kv4._load()
+    code = kv4._codes.get(dtype)
+    if code not in (kv4.F16, kv4.BF16) or max(shape) >= 2 ** 31:
+        raise ValueError(f"pools {list(shape)} of {dtype}: sizes of 32 bits, float16 or bfloat16 are needed")
+    n_pages, heads, page, hd = shape
+    pools = lf_paged(n_pages, heads, page, hd, code, 16, 32, heads * page * hd, page * hd, hd)
+    status = kv4._lib.lf_paged_append(C.byref(pools), None, None, 0, None, None)
+    if status:
+        kv4._fail(status, "lf_paged")
+
+
 class PagedKVCache(OnStream):
     """K and V of one layer in `n_pages` pages of `page` positions (a multiple of 16), `n_kv_heads` heads of `head_dim`
     (64 or 128) values in float16 or bfloat16.
@@ -119,7 +134,9 @@ class PagedKVCache(OnStream):
     def __init__(self, n_pages: int, n_kv_heads: int, head_dim: int, page: int = 64, dtype=None, device="cuda"):
         import torch
         shape = int(n_pages), int(n_kv_heads), int(page), int(head_dim)
-        self._set(*(torch.zeros(shape, dtype=dtype or torch.float16, device=device) for _ in range(2)))
+        dtype = dtype or torch.float16
+        _check_pool(shape, dtype)                          # before any memory is asked for
+        self._set(*(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)))
 
     @classmethod
     def wrap(cls, k, v) -> "PagedKVCache":

@@ -194,3 +194,18 @@ def test_sync_of_another_stream(pm):
         class Elsewhere:
             device = torch.device("cuda", 99)
         t.sync(stream=Elsewhere())
+
+
+def test_caches_that_cannot_be_are_refused_at_once(pm):
+    for args in ((4, 2, 64, 8), (4, 2, 96), (0, 2, 64), (4, 0, 64), (4, 1025, 64), (2 ** 27, 1, 64), (4, 2, 64, 24), (4, 2, 64, 0),
+                 (4, 2, 64, 2 ** 31)):
+        was = torch.cuda.memory_allocated(), torch.cuda.max_memory_allocated()
+        with pytest.raises((pm.LFError, ValueError)):
+            pm.PagedKVCache(*args)
+        assert (torch.cuda.memory_allocated(), torch.cuda.max_memory_allocated()) == was
+    with pytest.raises(ValueError):
+        pm.PagedKVCache(4, 2, 64, dtype=F32)
+    k, v = (torch.zeros(4, 2, 24, 64, dtype=F16, device="cuda") for _ in range(2))
+    for bad in ((k, v), (k[:, :, :16, :32], v[:, :, :16, :32]), (k[:, :, :16], k[:, :, :16])):
+        with pytest.raises(pm.LFError):
+            pm.PagedKVCache.wrap(*bad)
