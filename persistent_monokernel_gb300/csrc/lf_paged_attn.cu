@@ -47,8 +47,6 @@ namespace lfpg {
 
 using lfq::ex2;
 
-constexpr int PADF = 4;           // floats behind a partial state's O per row: m, l, and two that keep rows aligned
-
 template <class T>
 struct Half16;
 template <>
@@ -714,51 +712,6 @@ static cudaError_t run(const Attn &a, cudaStream_t s)
 {
     if (a.c.hd == 128) return a.rt == 8 ? run<128, 1, T, QT>(a, s) : run<128, 2, T, QT>(a, s);
     return a.rt == 8 ? run<64, 1, T, QT>(a, s) : run<64, 2, T, QT>(a, s);
-}
-
-// The lengths are known on the device alone, so the launch goes by what the host knows: the items (sequences x tiles)
-// and the slabs that the widest row may have (of 8 KB: narrow heads' count half).  Two CTAs of four warps fit an SM (304
-// places on 152).
-//   * Clusters as large as the items leave places for, with two slabs a warp at least (16 x 5 heads of 512 positions:
-//     6.2 us in clusters of two, 8.3 in fours, 13.3 in eights, of which most have to wait for places).
-//   * More items than places: long ones first, which costs each CTA half a microsecond (up to 256 rows, where one has
-//     2,048 positions or more).  Clusters then only up to three rounds of items, and only where a warp still has 40 slabs
-//     of a row: 64 x 8 heads of up to 16,384 positions take 295 us in twos (310 in single CTAs, 302 in fours and in row
-//     order), of 4,096 81 in single CTAs (86 in twos); 200 x 2 heads of 16 FP32 queries each, skewed to 20,000,
-//     167 in fours (200 in twos, 368 in single CTAs, 202 in fours and in row order).
-//   * Fewer items whose clusters need rounds: as large as leaves 8 cl slabs a warp (16 x 8 heads skewed to 32,768:
-//     232 us in single CTAs, 91 in fours, 80 in eights), long ones first from 4,096 positions on (48 x 5 heads of up to
-//     4,096: 41.8 us, 45.3 in row order).
-//   * Few items of many slabs leave SMs idle in one cluster each: up to 23 items of 12,288 positions or more are cut into
-//     parts, as many clusters of four as fit (280 CTAs: the last clusters find no group of SMs that is free), and a second
-//     launch joins them (3 us; one sequence of 5 heads at 32,768: 19.8 us in parts, 23.4 in clusters of eight CTAs of
-//     eight warps; at 8,192 9.7 and 9.7; of 8 heads at 131,071: 80.5 and 88).
-//   * Otherwise, where clusters of eight leave half the places empty, CTAs of eight warps (5 heads at 8,192: 9.7 us,
-//     10.8 with four; at 2,048 6.1 either way).
-size_t plan_attn(Attn &a, int sms)
-{
-    a.rt = a.G <= 8 ? 8 : 16;
-    a.tiles = (a.G + a.rt - 1) / a.rt;
-    a.ht = a.c.Hkv * a.tiles;
-    const long long items = (long long)a.n * a.ht, places = 2 * sms;
-    long long slabs = ((long long)a.width * a.c.page + 15) / 16;
-    if (a.win > 0) slabs = std::min<long long>(slabs, a.win / 16 + 2);
-    a.cl = 1, a.cw = 4, a.parts = 1;
-    const long long wide = slabs * a.c.hd / 128;
-    a.sorted = items > places && wide >= 128 && a.n > 1 && a.n <= 256;
-    for (int cl = 2; cl <= 8; cl *= 2) {
-        const bool rounds = a.sorted ? items * cl / 2 < 3 * places && wide >= 160 * cl : wide >= 32 * cl * cl;
-        if (slabs >= 8 * cl && (items * cl <= places || rounds)) a.cl = cl;
-    }
-    const long long parts = places * 280 / 304 / (4 * items);
-    if (slabs >= 768 && parts >= 3) {
-        a.cl = 4;
-        a.parts = (int)parts;
-    } else if (a.cl == 8 && items * 8 <= sms && slabs >= 256) {
-        a.cw = 8;
-    }
-    if (a.parts == 1 && items * a.cl > places && wide >= 256 && a.n > 1 && a.n <= 256) a.sorted = 1;
-    return a.parts > 1 ? (size_t)items * a.parts * a.rt * (a.c.hd + PADF) * sizeof(float) : 0;
 }
 
 void set_workspace(Attn &a, void *ws) { a.part = static_cast<float *>(ws); }
