@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import paged_ref as ref
+from paged_launch import launches
 
 pytestmark = pytest.mark.gpu
 
@@ -115,6 +116,101 @@ def test_a_long_row_keeps_small_addends(pm, dtype, n):
     low = 64 * head / positions
     assert torch.tensor(want, dtype=dtype) > torch.tensor(low, dtype=dtype)
     assert torch.equal(out[0], torch.full_like(out[0], want)) and not out[1:].any()
+
+
+# ---------------------------------------------------------------- every position once
+
+def marked(lens, group, hkv, hd, page, cache, dtype):
+    """Queries of zeros (equal weights), and V that marks positions: dim d of KV head 0 those whose slab of 16 is d modulo
+    hd, of head 1 those that are d modulo hd, of head 2 those whose stretch of 64 slabs is; then the same again."""
+    q, k, v, tables, ln = ref.case(lens, group * hkv, hkv, hd, page, cache, dtype, seed=1)
+    v.zero_()
+    for i, n in enumerate(lens):
+        j = torch.arange(n, device="cuda")
+        ids = tables[i].long()[j // page]
+        for h in range(hkv):
+            v[ids, h, j % page, (j // (16, 1, 1024)[h % 3]) % hd] = 1.0
+    return torch.zeros_like(q), k, v, tables, ln
+
+
+def shares(n, group, hkv, hd, window=0, left_out=()):
+    """[heads, hd]: what share of a row's positions each dim marks; left_out: slabs that do not count."""
+    j = torch.arange(max(0, n - window) if window else 0, n)
+    for s in left_out:
+        j = j[j // 16 != s]
+    return torch.stack([torch.bincount((j // d) % hd, minlength=hd) for d in (16, 1, 1024)]).double()[[h % 3 for h in range(hkv)]] \
+        .repeat_interleave(group, 0) / max(len(j), 1)
+
+
+def mark_bound(want, dtype):
+    """Weights are a power of two, so that all sums are exact: 1 / n and the product with it round, and the output."""
+    return (ref.HALF_STEP[dtype] + 2.0 ** -22) * want + (2.0 ** -25 if dtype == F16 else 0)
+
+
+def check_marks(pm, c, group, lens, window):
+    q, k, v, tables, ln = c
+    got = pm.PagedKVCache.wrap(k, v).attend(q, tables, ln, window=window)
+    want = torch.stack([shares(n, group, k.shape[1], k.shape[3], window) for n in lens]).cuda()
+    ref.check(got, want, mark_bound(want, q.dtype))
+
+
+MARKED = [[40000], [30000, 29999], [13001, 0, 5], [5000], [4097, 1024], [1023] * 5, [300] * 40, [8000] * 4, list(range(1, 2400, 37)),
+          [20000] + [17] * 90, [33000] + [40] * 39]
+
+
+@pytest.mark.parametrize("cache,dtype", TYPES)
+@pytest.mark.parametrize("lens", MARKED, ids=lambda x: f"{len(x)}x{max(x)}")
+def test_every_position_counts_once(pm, lens, cache, dtype):
+    """A slab (or a position, or a part) left out or counted twice shows, whatever the row's length."""
+    for hd in (64, 128):
+        c = marked(lens, 2, 3, hd, 64, cache, dtype)
+        for window in (0, max(lens) - 3, 1000):
+            check_marks(pm, c, 2, lens, window)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_marks_tell_of_one_slab(dtype):
+    """What the two tests around this one would see if a kernel left one slab out: more than they let pass."""
+    for n in (40000, 66000):
+        want = shares(n, 1, 3, 64)
+        for s in (0, 7, n // 32, n // 16 - 1):
+            assert bool(((shares(n, 1, 3, 64, 0, [s]) - want).abs() > 2 * mark_bound(want, dtype)).any())
+
+
+# lengths, heads per KV head, KV heads, head_dim, page; the launch (clusters, warps, parts, long rows first)
+REACHED = [([66000, 40, 0, 1500] + [100] * 36, 2, 4, 64, 128, (8, 4, 1, 1)), ([33000, 40, 0, 1500] + [100] * 36, 1, 4, 128, 128, (8, 4, 1, 1)),
+           ([0] * 255 + [6000], 2, 2, 128, 64, (2, 4, 1, 1)), ([4200] + [33, 0] * 127 + [16], 1, 2, 128, 64, (1, 4, 1, 1)),
+           ([12000, 0, 900, 15] * 50, 9, 2, 128, 64, (4, 4, 1, 1)), ([2100, 7, 0, 700] * 40, 1, 3, 128, 64, (1, 4, 1, 1)),
+           ([4100] + [50, 0, 1, 300] * 64, 4, 2, 128, 64, (2, 4, 1, 0)), ([9000] + [80] * 298 + [0], 2, 2, 128, 64, (4, 4, 1, 0)),
+           ([40000] + [20] * 279, 3, 1, 128, 256, (8, 4, 1, 0)), ([500] * 400, 2, 2, 64, 32, (1, 4, 1, 0)), ([8000], 4, 5, 128, 64, (8, 8, 1, 0)),
+           ([40000], 17, 3, 64, 64, (4, 4, 11, 0)), ([13000] * 4, 8, 1, 128, 16, (4, 4, 17, 0)), ([1000] * 24, 4, 5, 128, 64, (2, 4, 1, 0))]
+
+
+@pytest.mark.parametrize("cache,dtype", TYPES)
+@pytest.mark.parametrize("lens,group,hkv,hd,page,launch", REACHED, ids=lambda x: f"{len(x)}x{max(x)}" if isinstance(x, list) else None)
+def test_each_kind_of_launch(pm, tmp_path, lens, group, hkv, hd, page, launch, cache, dtype):
+    """Rows that need all CTAs of their launch, few and none, with the launch that the rule chooses for them."""
+    width = ref.cdiv(max(lens), page)
+    chosen, = launches([(len(lens), group, hkv, hd, page, width, 0)], str(tmp_path),
+                       torch.cuda.get_device_properties(0).multi_processor_count)
+    assert chosen == launch
+    c = marked(lens, group, hkv, hd, page, cache, dtype)
+    for window in (0, max(lens) - 3):
+        check_marks(pm, c, group, lens, window)
+    # Equal weights of random values.  What rounds is the sum of V: half a step of 32 bits for each slab of a warp, a step
+    # for each of a slab's two times 17 addends, which the products cut, and the joins' 40 half ones.
+    q, k, v, tables, ln = ref.case(lens, group * hkv, hkv, hd, page, cache, dtype, seed=2)
+    got = pm.PagedKVCache.wrap(k, v).attend(q.zero_(), tables, ln)
+    for i, n in enumerate(lens):
+        if not n:
+            assert not got[i].any()
+            continue
+        j = torch.arange(n, device="cuda")
+        rows = v[tables[i].long()[j // page], :, j % page].double()
+        want, size = (x.mean(0).repeat_interleave(group, 0) for x in (rows, rows.abs()))
+        chain = n // (16 * chosen.cl * chosen.cw * chosen.parts) + 8
+        bound = (chain / 2 + 64) * 2.0 ** -23 * size
+        ref.check(got[i], want, bound + ref.HALF_STEP[dtype] * (want.abs() + bound) + (2.0 ** -25 if dtype == F16 else 0))
 
 
 # ---------------------------------------------------------------- what torch has to know
