@@ -460,7 +460,8 @@ LF_API lf_status lf_kv4_read(const lf_kv4 *c, const lf_rows *k, const lf_rows *v
  * into FP16's range by a power of two (exact down to 2^-17 of its largest value).
  * With q in FP32, q and the probabilities enter the products as an FP16 head and
  * remainder: about 22 bits, small values to 2^-25 of the row's largest.
- * q must be finite. */
+ * q must be finite, and scores (scale * q . K) stay below 2^25 in magnitude:
+ * beyond, their FP32 steps may spoil a row. */
 typedef struct {
     lf_rows q, out;          /* [n][n_heads][head_dim], one dtype; out must not overlap q */
     int32_t n_heads;         /* a multiple of n_kv_heads */
