@@ -118,6 +118,24 @@ def test_a_long_row_keeps_small_addends(pm, dtype, n):
     assert torch.equal(out[0], torch.full_like(out[0], want)) and not out[1:].any()
 
 
+@pytest.mark.parametrize("cache,dtype", TYPES)
+def test_weights_that_cancel(pm, cache, dtype):
+    """Two positions whose scores differ by d, V = 1 and -e^d (rounded): their weights cancel up to that rounding, which shows the
+    weights' own error.  Exponents below 8 round to 2^-22, exp2 adds 2^-22 and the terms of P 2^-24: 2^-21 in each weight, and
+    the larger one's share, 0.67, of both in the output."""
+    d = (0.2 + torch.arange(256, dtype=torch.float64) / 512).to(cache).double()
+    far = torch.exp(d).to(cache).double()
+    k, v = (torch.zeros(256, 1, 16, 64, dtype=cache, device="cuda") for _ in range(2))
+    k[:, 0, 1, 0] = -d.cuda()
+    v[:, 0, 0], v[:, 0, 1] = 1.0, -far.cuda()[:, None]
+    q = torch.zeros(256, 1, 64, dtype=dtype, device="cuda")
+    q[:, :, 0] = 1.0
+    tables, lens = torch.arange(256, dtype=torch.int32, device="cuda")[:, None], torch.full((256,), 2, dtype=torch.int32, device="cuda")
+    got = pm.PagedKVCache.wrap(k, v).attend(q, tables, lens, scale=1.0)
+    want = ((1 - far * torch.exp(-d)) / (1 + torch.exp(-d))).cuda()[:, None, None].expand_as(got)
+    ref.check(got, want, ref.HALF_STEP[dtype] * want.abs() + 2.0 ** -20)
+
+
 # ---------------------------------------------------------------- every position once
 
 def marked(lens, group, hkv, hd, page, cache, dtype):
