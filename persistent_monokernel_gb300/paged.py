@@ -8,7 +8,10 @@ nothing on the host:
 
     slots, positions, offsets = tables.plan(n_new, max_tokens)     # once, for all layers
     cache.append(k, v, slots)                                      # per layer
-    out = cache.attend(q, tables.tables, tables.lens)
+    out = cache.attend(q, tables.tables[:, :pages], tables.lens)
+
+`pages` is a bound of what any row needs that the host knows (all columns are one, too): the lengths are the device's,
+and the attention's launch goes by the table's width.
 """
 from __future__ import annotations
 
@@ -110,6 +113,7 @@ class PageTables(OnStream):
 def _check_pool(shape, dtype) -> None:
     """Raise LFError for contiguous pools [n_pages, n_kv_heads, page, head_dim] that the library refuses: an append of no
     rows checks them and does nothing else (the addresses are any)."""
+    from . import lib
     if kv4._torch is None:
         kv4._load()
     code = kv4._codes.get(dtype)
@@ -117,7 +121,7 @@ def _check_pool(shape, dtype) -> None:
         raise ValueError(f"pools {list(shape)} of {dtype}: sizes of 32 bits, float16 or bfloat16 are needed")
     n_pages, heads, page, hd = shape
     pools = lf_paged(n_pages, heads, page, hd, code, 16, 32, heads * page * hd, page * hd, hd)
-    status = kv4._lib.lf_paged_append(C.byref(pools), None, None, 0, None, None)
+    status = lib().lf_paged_append(C.byref(pools), None, None, 0, None, None)
     if status:
         kv4._fail(status, "lf_paged")
 
@@ -170,9 +174,9 @@ class PagedKVCache(OnStream):
         """Attention of one query row per sequence, q [n_seqs, n_heads, head_dim], over its first lens[i] positions, which
         lie in the pages tables[i] (int32 [n_seqs, pages], [n_seqs]); window W > 0 leaves the W most recent; scale 0
         selects 1 / sqrt(head_dim).  A row that sees nothing gives zeros; positions behind the table's columns or on
-        pages that the pool does not have are left out.  A table no wider than the longest row needs
-        (tables[:, :pages]) makes the best launch.  Returns [n_seqs, n_heads, head_dim] in q's dtype: a new tensor, or
-        `out`, which must not overlap q."""
+        pages that the pool does not have are left out.  The launch goes by the table's
+        width: pass the columns that a bound of the longest row needs (tables[:, :pages]).  Returns [n_seqs, n_heads,
+        head_dim] in q's dtype: a new tensor, or `out`, which must not overlap q."""
         if stream is None:
             got = kv4._calls.paged_attend(self._handle, q, tables, lens, window, scale, out)
             if got is not NotImplemented:
