@@ -29,7 +29,7 @@
 //
 // Measured (one GB300): 64 sequences of up to 16,384 positions, 32/8 heads x
 // 128, BF16: 291-296 us, 7.4 TB/s (a copy's rate is 6.8); one of 131,071 81 us,
-// 6.6 TB/s; one of 512, 20/5 heads x 128 4.8 us.  With FP32 queries on BF16 and
+// 6.6 TB/s; one of 512, 20/5 heads x 128 4.9 us.  With FP32 queries on BF16 and
 // 16 heads per KV head the instructions count: 5.2 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -496,7 +496,7 @@ __device__ __forceinline__ int parts_of(const Attn &a, int slabs)
 
 // The row that comes `rank`-th where long ones come first: in classes of like numbers of slabs (two per octave), in row
 // order within one.  Where the clusters come in several rounds the last one then is of short rows (200 rows of up to
-// 20,000 positions, most of them short, FP32 queries: 167 us, 202 in row order).  Called by all threads; `scratch`: 65 words
+// 20,000 positions, most of them short, FP32 queries: 160 us, 191 in row order).  Called by all threads; `scratch`: 65 words
 // of shared memory, free again after the next barrier.
 __device__ __forceinline__ int row_by_length(const Attn &a, int rank, int *scratch)
 {
