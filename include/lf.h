@@ -573,7 +573,7 @@ LF_API lf_status lf_paged_append(const lf_paged *c, const lf_rows *k, const lf_r
  * pages that no row sees, is not read.  The narrower the table, the better the
  * launch fits (pass the columns that the longest row needs, not the allocation).
  * Scores, softmax and sums are FP32; q and the probabilities enter the products
- * with 16 bits or more (q as it is where it has the cache's dtype).  q must be
+ * with 22 bits or more (q as it is where it has the cache's dtype).  q must be
  * finite; infinities and NaN in K or V spoil the heads and rows that see them, and
  * no others.  So do scores that FP32 does not hold, and sums of V that leave it
  * with weights of up to 2^15. */
